@@ -1,0 +1,470 @@
+"""The operators of a full-attention decoder layer beside the sparse path: their cases, plain forms and work.
+
+Three operators, each called as a serving program calls it:
+
+* ``paged_gqa``: attention of one to eight new tokens per request over the whole paged K/V cache
+  (``msa.paged_gqa_decode``), K/V in bf16, FP8 E4M3 or NVFP4;
+* ``build_step``: a step's block tables, slot map and positions from the requests' lengths
+  (``msa.build_step``);
+* ``mrope``: the step in front of the attention with rotary positions on several axes
+  (``msa.qk_norm_mrope_insert``).
+
+``own`` selects the framework's kernels; otherwise ``run`` computes the plain forms in elementary torch
+operations.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+BLOCK, DIM = 128, 128
+FP8_SCALE = 6.0 / 448.0             # K/V per-tensor scale: six standard deviations on E4M3's largest value
+FP4_SCALE = 6.0 / (6.0 * 448.0)     # NVFP4 global scale: the same over E2M1's times E4M3's largest value
+KV_BYTES = {"bf16": 256.0, "fp8": 128.0, "nvfp4": 72.0}      # one K or V row of one head
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+EPS, THETA = 1e-6, 10000.0
+SECTIONS = (16, 24, 24)             # rotary pairs of the time, height and width axes
+
+
+# ---------------------------------------------------------------------------------------------- cases --
+def _gqa(name, batch, lo, hi, q_len=1, kv_heads=4, group=16, kv="bf16", empty=0):
+    c = {"op": "paged_gqa", "batch": batch, "lo": lo, "hi": hi, "q_len": q_len, "kv_heads": kv_heads,
+         "group": group, "kv": kv, "empty": empty}
+    return dict(c, name=name) if name else c
+
+
+def _step(name, batch, ctx_lo, ctx_hi, new_lo, new_hi, axes=3, pad=0):
+    c = {"op": "build_step", "batch": batch, "ctx_lo": ctx_lo, "ctx_hi": ctx_hi, "new_lo": new_lo,
+         "new_hi": new_hi, "axes": axes, "pad": pad}
+    return dict(c, name=name) if name else c
+
+
+def _mrope(name, tokens, kv="bf16", kv_heads=4, image=False):
+    c = {"op": "mrope", "tokens": tokens, "kv": kv, "kv_heads": kv_heads, "image": image}
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # two chats of 4K tokens: the smallest decode step, where latency counts
+        _gqa("gqa 2x4k bf16", 2, 4096, 4096),
+        # the batch decode of the benchmark, on a full-attention layer
+        _gqa("gqa 32x32k bf16", 32, 32768, 32768),
+        # the ragged batch of the benchmark: every length another, none a multiple of the block
+        _gqa("gqa 64 ragged 8k-128k bf16", 64, 8193, 131071),
+        # speculative verification: 7 draft tokens and one more per request
+        _gqa("gqa 32x64k 8 positions bf16", 32, 65536, 65536, q_len=8),
+        # the batch decode on an FP8 cache
+        _gqa("gqa 32x32k fp8", 32, 32768, 32768, kv="fp8"),
+        # long contexts on an NVFP4 cache
+        _gqa("gqa 16x256k nvfp4", 16, 262144, 262144, kv="nvfp4"),
+        # one long request on one tensor-parallel rank of eight: one KV head, 8 query heads
+        _gqa("gqa 1x128k fp8 one head", 1, 131071, 131071, kv_heads=1, group=8, kv="fp8"),
+        # many short requests of odd lengths with three positions, some slots of the batch unused
+        _gqa("gqa 96 short q3 fp8", 96, 1, 2047, q_len=3, kv_heads=2, group=8, kv="fp8", empty=5),
+        # a decode step's metadata: one new token for each of 64 requests
+        _step("step 64 decode", 64, 8193, 131071, 1, 1),
+        # a chunk of prompts: long new parts behind cached prefixes, padded to the captured token count
+        _step("step 16 prefill", 16, 0, 16000, 1, 65535, pad=1000),
+        # one new text token for each of 64 requests
+        _mrope("mrope 64 decode", 64),
+        # a chunk of a video prompt into an FP8 cache
+        _mrope("mrope 8191 video fp8", 8191, kv="fp8", image=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def draw(rng):
+    op = rng.choice(("paged_gqa", "paged_gqa", "paged_gqa", "build_step", "mrope"))
+    if op == "paged_gqa":
+        kv = rng.choice(("bf16", "fp8", "nvfp4"))
+        batch = _log(rng, 1, 96)
+        kv_heads = rng.choice((1, 2, 3, 4, 8))
+        group = rng.choice((1, 2, 4, 5, 8, 16))
+        q_len = rng.choice((1, 1, 1, 2, 3, 4, 8))
+        hi = _log(rng, 1, max(1, min(262144, 8_000_000 // (batch * kv_heads))))
+        lo = rng.choice((hi, max(1, hi // 16), 1))
+        return _gqa(None, batch, lo, hi, q_len, kv_heads, group, kv, rng.choice((0, 0, batch // 8)))
+    if op == "build_step":
+        batch = _log(rng, 1, 512)
+        if rng.random() < 0.5:
+            return _step(None, batch, 1, _log(rng, 128, 131072), 1, rng.choice((1, 2, 8)), rng.choice((1, 3)),
+                         rng.randint(0, 64))
+        new_hi = _log(rng, 1, max(1, min(65535, 500_000 // batch)))
+        return _step(None, batch, 0, _log(rng, 1, 16000), rng.choice((0, 1, new_hi)), new_hi, rng.choice((1, 3)),
+                     rng.randint(0, 1000))
+    return _mrope(None, _log(rng, 1, 8190), rng.choice(("bf16", "fp8")), rng.choice((1, 2, 4)), rng.random() < 0.5)
+
+
+def _spread(lo, hi, n):
+    """n lengths evenly over [lo, hi]."""
+    return [lo + (hi - lo) * i // max(1, n - 1) for i in range(n)] if n > 1 else [hi]
+
+
+def _gqa_lens(case):
+    n = case["batch"] - case["empty"]
+    return _spread(case["lo"], case["hi"], n) + [0] * case["empty"]
+
+
+def _step_lens(case):
+    """(tokens cached, tokens added) of every request."""
+    ctx = _spread(case["ctx_lo"], case["ctx_hi"], case["batch"])
+    new = _spread(case["new_lo"], case["new_hi"], case["batch"])
+    return ctx, new
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def work(case):
+    if case["op"] == "paged_gqa":
+        lens = _gqa_lens(case)
+        tokens, rows = sum(lens), case["batch"] * case["q_len"] * case["kv_heads"] * case["group"]
+        # every cached K and V row once, the queries and outputs once, the block table's live entries
+        b = tokens * case["kv_heads"] * 2 * KV_BYTES[case["kv"]] + rows * (2 * 2 * DIM + 4)
+        b += 4.0 * sum(_blocks(n) for n in lens) + 4.0 * case["batch"]
+        # q.k and p.v over the tokens each position sees
+        seen = sum(max(0, n - case["q_len"] + j + 1) for n in lens for j in range(case["q_len"]))
+        return {"bytes": b, "flops": 4.0 * DIM * seen * case["kv_heads"] * case["group"]}
+    if case["op"] == "build_step":
+        ctx, new = _step_lens(case)
+        pages = sum(_blocks(c + n) - _blocks(c) for c, n in zip(ctx, new))
+        t = sum(new) + case["pad"]
+        # lengths and offsets in, page ids in and out, slots and positions out
+        return {"bytes": case["batch"] * 4.0 * 5 + pages * 8.0 + t * (8.0 + 4.0 * case["axes"]), "flops": 0}
+    t, g = case["tokens"], case["kv_heads"]
+    rows_in, q_rows = 18 * g * t, 16 * g * t
+    out = q_rows * 2.0 * DIM + 2 * g * t * (2.0 * DIM if case["kv"] == "bf16" else 1.0 * DIM)
+    return {"bytes": rows_in * 2.0 * DIM + out + t * (8.0 + 12.0), "flops": 12.0 * 17 * g * t * DIM}
+
+
+# --------------------------------------------------------------------------------------------- inputs --
+def _fp4_rows(x):
+    """fp32 [..., 128] -> packed E2M1 codes [..., 64] and E4M3 scales [..., 8], one per 16 values."""
+    v = x.reshape(*x.shape[:-1], 8, 16)
+    sb = (v.abs().amax(-1) / 6.0 / FP4_SCALE).clamp(max=448.0).to(torch.float8_e4m3fn)
+    den = sb.float()[..., None] * FP4_SCALE
+    y = torch.where(den > 0, v / den.clamp(min=1e-30), torch.zeros_like(v))
+    edges = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=x.device)
+    code = torch.bucketize(y.abs(), edges).to(torch.uint8) | ((y < 0).to(torch.uint8) << 3)
+    code = code.reshape(*x.shape[:-1], 64, 2)
+    return code[..., 0] | (code[..., 1] << 4), sb.view(torch.uint8)
+
+
+def _fill(kind, pages, heads, gen, std=1.0):
+    """A K or V cache of N(0, std) values: (codes or values, scales or None)."""
+    if kind == "bf16":
+        x = torch.empty((pages, heads, BLOCK, DIM), dtype=torch.bfloat16, device="cuda")
+        return x.normal_(0.0, std, generator=gen), None
+    if kind == "fp8":
+        code = torch.empty((pages, heads, BLOCK, DIM), dtype=torch.uint8, device="cuda")
+    else:
+        code = torch.empty((pages, heads, BLOCK, DIM // 2), dtype=torch.uint8, device="cuda")
+        scale = torch.empty((pages, heads, BLOCK, DIM // 16), dtype=torch.uint8, device="cuda")
+    for at in range(0, pages, 4096):
+        n = min(4096, pages - at)
+        x = torch.empty((n, heads, BLOCK, DIM), dtype=torch.float32, device="cuda").normal_(0.0, std, generator=gen)
+        if kind == "fp8":
+            code[at:at + n] = (x / FP8_SCALE).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+        else:
+            code[at:at + n], scale[at:at + n] = _fp4_rows(x)
+    return code, None if kind == "fp8" else scale
+
+
+def _global(kind):
+    return {"bf16": 1.0, "fp8": FP8_SCALE, "nvfp4": FP4_SCALE}[kind]
+
+
+def prepare(case, seed):
+    rng = random.Random(seed * 7919 + 17)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed * 7919 + 17)
+    s = {"case": dict(case), "flags": torch.zeros(1, dtype=torch.int32, device="cuda")}
+    if case["op"] == "paged_gqa":
+        lens = _gqa_lens(case)
+        rng.shuffle(lens)
+        B, Q, G, H = case["batch"], case["q_len"], case["kv_heads"], case["kv_heads"] * case["group"]
+        nb = [_blocks(n) for n in lens]
+        cols, pages = max(1, max(nb)), max(1, sum(nb))
+        s["k"], s["k_scale"] = _fill(case["kv"], pages, G, gen)
+        s["v"], s["v_scale"] = _fill(case["kv"], pages, G, gen)
+        lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        nb_d = torch.tensor(nb, dtype=torch.int64, device="cuda")
+        col = torch.arange(cols, device="cuda")[None, :]
+        rank = (nb_d.cumsum(0) - nb_d)[:, None] + col
+        perm = torch.randperm(pages, generator=gen, device="cuda")
+        s["block_table"] = torch.where(col < nb_d[:, None], perm[rank.clamp(max=pages - 1)], -1).to(torch.int32)
+        s["seq_lens"], s["pages"] = lens_d, pages
+        s["q"] = torch.empty((B, Q, H, DIM), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+        s["out"] = torch.empty_like(s["q"])
+        s["lse"] = torch.empty((B, Q, H), dtype=torch.float32, device="cuda")
+    elif case["op"] == "build_step":
+        ctx, new = _step_lens(case)
+        both = list(zip(ctx, new))
+        rng.shuffle(both)
+        ctx, new = [c for c, _ in both], [n for _, n in both]
+        used = [_blocks(c) for c in ctx]
+        need = sum(_blocks(c + n) - _blocks(c) for c, n in both)
+        pages = sum(used) + need + 64
+        perm = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+        cols = max(_blocks(c + n) for c, n in both) + 2
+        u = torch.tensor(used, device="cuda")
+        col = torch.arange(cols, device="cuda")[None, :]
+        rank = (u.cumsum(0) - u)[:, None] + col
+        s["block_table"] = torch.where(col < u[:, None], perm[rank.clamp(max=pages - 1)], -1).to(torch.int32)
+        s["free_pages"] = perm[sum(used):].contiguous()
+        s["free_head"] = torch.tensor([rng.randint(0, 32)], dtype=torch.int32, device="cuda")
+        s["ctx_lens"] = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        s["new_lens"] = torch.tensor(new, dtype=torch.int32, device="cuda")
+        s["pos_offset"] = torch.tensor([-rng.randint(0, min(c, 500)) for c in ctx], dtype=torch.int32, device="cuda")
+        t = max(1, sum(new) + case["pad"])
+        s["seq_lens"] = torch.empty(case["batch"], dtype=torch.int32, device="cuda")
+        s["token_starts"] = torch.empty(case["batch"] + 1, dtype=torch.int32, device="cuda")
+        s["slots"] = torch.empty(t, dtype=torch.int64, device="cuda")
+        s["positions"] = torch.empty((case["axes"], t), dtype=torch.int32, device="cuda")
+        s["free_head_out"] = torch.empty(1, dtype=torch.int32, device="cuda")
+        s["pages"] = pages
+    else:
+        T, G = case["tokens"], case["kv_heads"]
+        H = 16 * G
+        pages = _blocks(T) if case["image"] else T          # a prompt fills pages, decode tokens lie in one each
+        for n, h in (("q", H), ("k", G), ("v", G)):
+            s[n] = torch.empty((T, h, DIM), dtype=torch.bfloat16, device="cuda").normal_(0.0, 2.0, generator=gen)
+        for n in ("wq", "wk"):
+            s[n] = 1.0 + 0.1 * torch.randn(DIM, generator=gen, device="cuda")
+        t = torch.arange(T, device="cuda")
+        if case["image"]:
+            base, side = rng.randint(0, 4096), 24              # frames of 24 x 24 patches behind some text
+            s["positions"] = torch.stack((base + t // (side * side), base + t // side % side,
+                                          base + t % side)).to(torch.int32)
+            perm = torch.randperm(pages, generator=gen, device="cuda")
+            s["slots"] = perm[t // BLOCK] * BLOCK + t % BLOCK
+        else:
+            p = torch.randint(0, 262144, (T,), generator=gen, device="cuda")
+            s["positions"] = p[None].expand(3, T).to(torch.int32).contiguous()
+            perm = torch.randperm(pages, generator=gen, device="cuda")
+            s["slots"] = perm[t] * BLOCK + p % BLOCK
+        s["pages"] = pages
+        kind = torch.bfloat16 if case["kv"] == "bf16" else torch.uint8
+        s["k_cache"] = torch.zeros((pages, G, BLOCK, DIM), dtype=kind, device="cuda")
+        s["v_cache"] = torch.zeros((pages, G, BLOCK, DIM), dtype=kind, device="cuda")
+        s["q_out"] = torch.empty_like(s["q"])
+    return s
+
+
+# ----------------------------------------------------------------------------------------- plain forms --
+def _values(kind, code, scale):
+    """Cache values in fp32 from what the cache holds."""
+    if kind == "bf16":
+        return code.float()
+    if kind == "fp8":
+        return code.view(torch.float8_e4m3fn).float() * FP8_SCALE
+    grid = torch.tensor(E2M1 + tuple(-x for x in E2M1), device=code.device)
+    x = torch.stack((grid[(code & 15).long()], grid[(code >> 4).long()]), -1)
+    x = x.reshape(*code.shape[:-1], DIM // 16, 16) * scale.view(torch.float8_e4m3fn).float()[..., None]
+    return x.reshape(*code.shape[:-1], DIM) * FP4_SCALE
+
+
+def _gathered(s, name):
+    """[B, G, tokens, D] fp32: a cache in the order of the requests' block tables."""
+    kind = s["case"]["kv"]
+    at = s["block_table"].clamp(min=0).long()
+    B, cols = at.shape
+    code = s[name][at].transpose(1, 2)
+    scale = None if s[name + "_scale"] is None else s[name + "_scale"][at].transpose(1, 2)
+    return _values(kind, code, scale).reshape(B, -1, cols * BLOCK, DIM)
+
+
+def _plain_gqa(s):
+    c = s["case"]
+    B, Q, G, n = c["batch"], c["q_len"], c["kv_heads"], c["group"]
+    q = s["q"].float().reshape(B, Q, G, n, DIM).permute(0, 2, 1, 3, 4).reshape(B, G, Q * n, DIM)
+    x = torch.matmul(q, _gathered(s, "k").transpose(2, 3)) * (1.0 / math.sqrt(DIM))
+    x = x.reshape(B, G, Q, n, -1)
+    last = s["seq_lens"][:, None] - Q + torch.arange(Q, device="cuda")[None, :]             # [B, Q]
+    seen = torch.arange(x.shape[-1], device="cuda")[None, None, :] <= last[:, :, None]       # [B, Q, tokens]
+    x = x.masked_fill_(~seen[:, None, :, None, :], -math.inf)
+    top = x.amax(-1, keepdim=True)
+    live = top > -math.inf
+    x = x.sub_(torch.where(live, top, torch.zeros_like(top))).exp_()
+    total = x.sum(-1, keepdim=True)
+    o = torch.matmul(x.reshape(B, G, Q * n, -1), _gathered(s, "v")).reshape(B, G, Q, n, DIM)
+    o = torch.where(live, o / total.clamp(min=1e-37), torch.zeros_like(o))
+    lse = torch.where(live, top + total.clamp(min=1e-37).log(), top)[..., 0]
+    return (o.permute(0, 2, 1, 3, 4).reshape(B, Q, G * n, DIM).to(torch.bfloat16),
+            lse.permute(0, 2, 1, 3).reshape(B, Q, G * n))
+
+
+def _plain_step(s):
+    ctx, new = s["ctx_lens"].long(), s["new_lens"].long()
+    B, T = ctx.numel(), s["slots"].numel()
+    seq = ctx + new
+    starts = torch.cat((torch.zeros_like(new[:1]), new.cumsum(0)))
+    old, now = (ctx + BLOCK - 1) // BLOCK, (seq + BLOCK - 1) // BLOCK
+    need = now - old
+    first = need.cumsum(0) - need + s["free_head"].long()
+    col = torch.arange(s["block_table"].shape[1], device="cuda")[None, :]
+    take = (first[:, None] + col - old[:, None]).clamp(0, s["free_pages"].numel() - 1)
+    table = torch.where((col >= old[:, None]) & (col < now[:, None]), s["free_pages"][take], s["block_table"])
+    i = torch.arange(T, device="cuda")
+    b = torch.searchsorted(starts[1:], i, right=True).clamp(max=B - 1)
+    live = i < starts[-1]
+    pos = ctx[b] + i - starts[b]
+    page = table[b, (pos // BLOCK).clamp(max=table.shape[1] - 1)].long()
+    slots = torch.where(live, page * BLOCK + pos % BLOCK, -1)
+    positions = torch.where(live, pos + s["pos_offset"].long()[b], 0).to(torch.int32)
+    head = s["free_head"] + need.sum().to(torch.int32)
+    return (table, seq.to(torch.int32), starts.to(torch.int32), slots,
+            positions[None].expand(s["positions"].shape[0], T), head)
+
+
+def _axis(device):
+    return torch.repeat_interleave(torch.arange(3, device=device), torch.tensor(SECTIONS, device=device),
+                                   output_size=DIM // 2)
+
+
+def _rotated(x, w, positions):
+    x = x.float()
+    y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + EPS) * w
+    inv = THETA ** (-2.0 * torch.arange(DIM // 2, device=x.device, dtype=torch.float64) / DIM)
+    angle = positions[_axis(x.device)].T.double() * inv                                     # [T, D/2]
+    cos, sin = angle.cos().float()[:, None], angle.sin().float()[:, None]
+    a, b = y[..., :DIM // 2], y[..., DIM // 2:]
+    return torch.cat((a * cos - b * sin, a * sin + b * cos), -1).to(torch.bfloat16)
+
+
+def _held(kind, x):
+    """What a cache holds of bf16 values."""
+    if kind == "bf16":
+        return x
+    return (x.float() / FP8_SCALE).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _cache_view(c, x):
+    return x if c["kv"] == "bf16" else x.view(torch.float8_e4m3fn)
+
+
+def _plain_mrope(s):
+    c = s["case"]
+    k = _rotated(s["k"], s["wk"], s["positions"])
+    page, off = s["slots"] // BLOCK, s["slots"] % BLOCK
+    s["k_cache"][page, :, off] = _held(c["kv"], k)
+    s["v_cache"][page, :, off] = _held(c["kv"], s["v"])
+    return _rotated(s["q"], s["wq"], s["positions"]), _cache_view(c, s["k_cache"]), _cache_view(c, s["v_cache"])
+
+
+# ------------------------------------------------------------------------------------- the framework's --
+def _own_call(s):
+    """The marshalled call a decode loop keeps for its buffers and issues every step."""
+    from block_sparse_attention_07_gb300 import msa
+    c = s["case"]
+    kind = {"bf16": msa.BF16, "fp8": msa.FP8_E4M3, "nvfp4": msa.NVFP4}
+    if c["op"] == "paged_gqa":
+        d = msa.make_dims(c["batch"], c["q_len"], c["kv_heads"] * c["group"], c["kv_heads"], c["kv_heads"],
+                          max_blocks_per_seq=s["block_table"].shape[1], num_pages=s["pages"])
+        g = _global(c["kv"])
+        cache = msa.KVCache(kind[c["kv"]], s["k"], s["v"], s["k_scale"], s["v_scale"], g, g)
+        s["ws"] = torch.empty(msa.paged_gqa_workspace_size(d, cache.dtype), dtype=torch.uint8, device="cuda")
+        return msa.paged_gqa_decode(d, s["q"], cache, s["block_table"], s["seq_lens"], s["out"], s["lse"], s["ws"],
+                                    s["flags"], prepare=True)
+    if c["op"] == "build_step":
+        d = msa.make_dims(c["batch"], 1, max_blocks_per_seq=s["block_table"].shape[1], num_pages=s["pages"])
+        return msa.build_step(d, s["ctx_lens"], s["new_lens"], s["free_pages"], s["free_head"], s["block_table"],
+                              s["seq_lens"], s["token_starts"], s["slots"], s["positions"], s["free_head_out"],
+                              s["flags"], pos_offset=s["pos_offset"], prepare=True)
+    G = c["kv_heads"]
+    d = msa.make_dims(1, 1, 16 * G, G, G, max_blocks_per_seq=s["pages"], num_pages=s["pages"])
+    g = _global(c["kv"])
+    cache = msa.KVCache(kind[c["kv"]], s["k_cache"], s["v_cache"], None, None, g, g)
+    nr = msa.make_norm_rope(s["wq"], s["wk"], eps=EPS, rope_theta=THETA)
+    return msa.qk_norm_mrope_insert(d, s["q"], s["k"], s["v"], None, None, s["positions"], s["slots"], nr,
+                                    msa.make_rope_axes(SECTIONS), s["q_out"], None, cache, None, s["flags"],
+                                    prepare=True)
+
+
+def run(s):
+    c = s["case"]
+    if own:
+        if "call" not in s:
+            s["call"] = _own_call(s)
+        s["call"]()
+        if c["op"] == "paged_gqa":
+            return s["out"], s["lse"]
+        if c["op"] == "build_step":
+            return s["block_table"], s["seq_lens"], s["token_starts"], s["slots"], s["positions"], s["free_head_out"]
+        return s["q_out"], _cache_view(c, s["k_cache"]), _cache_view(c, s["v_cache"])
+    if c["op"] == "paged_gqa":
+        return _plain_gqa(s)
+    if c["op"] == "build_step":
+        return _plain_step(s)
+    return _plain_mrope(s)
+
+
+# ---------------------------------------------------------------------------------------------- exact --
+def _exact_rows(kind, code, scale):
+    """fp64 values of cache rows [..., bytes], decoded from the formats' bit fields."""
+    if kind == "bf16":
+        return code.double()
+    byte = torch.arange(256, device=code.device)
+    sign, e, m = 1.0 - 2.0 * (byte >> 7), (byte >> 3) & 15, (byte & 7).double()
+    table = sign * torch.where(e > 0, (1.0 + m / 8.0) * torch.pow(2.0, (e - 7).double()), m * 2.0 ** -9)
+    if kind == "fp8":
+        return table[code.long()] * FP8_SCALE
+    nib = torch.stack((code & 15, code >> 4), -1).reshape(*code.shape[:-1], DIM).long()
+    mag, e2 = (nib & 1).double(), (nib >> 1) & 3
+    x = torch.where(e2 > 0, (1.0 + mag / 2.0) * torch.pow(2.0, (e2 - 1).double()), mag * 0.5)
+    x = torch.where(nib >= 8, -x, x)
+    return x * table[scale.long()].repeat_interleave(16, -1) * FP4_SCALE
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "paged_gqa":
+        B, Q, G, n = case["batch"], case["q_len"], case["kv_heads"], case["group"]
+        out = torch.zeros((B, Q, G * n, DIM), dtype=torch.float64, device="cuda")
+        lse = torch.full((B, Q, G * n), -math.inf, dtype=torch.float64, device="cuda")
+        lens = s["seq_lens"].tolist()
+        for b in range(B):
+            L = lens[b]
+            if L == 0:
+                continue
+            pages = s["block_table"][b, :_blocks(L)].long()
+            for g in range(G):
+                rows = [_exact_rows(case["kv"], s[x][pages, g].reshape(-1, s[x].shape[-1])[:L],
+                                    None if s[x + "_scale"] is None else
+                                    s[x + "_scale"][pages, g].reshape(-1, DIM // 16)[:L]) for x in ("k", "v")]
+                for j in range(max(0, Q - L), Q):
+                    m = L - Q + j + 1
+                    x = s["q"][b, j, g * n:(g + 1) * n].double() @ rows[0][:m].T / math.sqrt(DIM)
+                    lse[b, j, g * n:(g + 1) * n] = torch.logsumexp(x, -1)
+                    out[b, j, g * n:(g + 1) * n] = torch.softmax(x, -1) @ rows[1][:m]
+        return out, lse
+    if case["op"] == "build_step":
+        return None
+    # a complex number turned by its angle, one per pair
+    inv = torch.pow(torch.tensor(THETA, dtype=torch.float64, device="cuda"),
+                    -torch.arange(0, DIM, 2, dtype=torch.float64, device="cuda") / DIM)
+    lo, turns = 0, []
+    for axis, width in enumerate(SECTIONS):
+        turns.append(s["positions"][axis].double()[:, None] * inv[None, lo:lo + width])
+        lo += width
+    turn = torch.polar(torch.ones((), dtype=torch.float64, device="cuda").expand(case["tokens"], DIM // 2),
+                       torch.cat(turns, 1))[:, None]
+    got = []
+    for x, w in (("q", "wq"), ("k", "wk")):
+        y = s[x].double()
+        y = y * (y.square().sum(-1, keepdim=True) / DIM + EPS).rsqrt() * s[w].double()
+        z = torch.complex(y[..., :DIM // 2], y[..., DIM // 2:]) * turn
+        got.append(torch.cat((z.real, z.imag), -1))
+    caches = []
+    for x in (got[1], s["v"].double()):
+        cache = torch.zeros(s["k_cache"].shape, dtype=torch.float64, device="cuda")
+        cache[s["slots"] // BLOCK, :, s["slots"] % BLOCK] = x if case["kv"] == "bf16" else (x / FP8_SCALE).clamp(-448, 448)
+        caches.append(cache)
+    return got[0], caches[0], caches[1]
