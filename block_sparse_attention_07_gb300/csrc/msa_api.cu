@@ -52,6 +52,22 @@ static msa_status_t check_dims(const msa_dims_t* d) {
   return MSA_OK;
 }
 
+// Shape rules of the full-attention layer's calls: any grouping of up to 16
+// query heads per KV head. The sparse path's fields are not looked at.
+static msa_status_t check_dense_dims(const msa_dims_t* d) {
+  if (d == nullptr) return MSA_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->q_len < 1 || d->n_heads < 1 || d->n_kv_heads < 1 || d->head_dim < 1 || d->block_size < 1 ||
+      d->max_blocks_per_seq < 1 || d->num_pages < 1)
+    return MSA_ERR_INVALID_ARG;
+  if (d->head_dim != kDim || d->block_size != kBlock) return MSA_ERR_UNSUPPORTED;
+  if (d->n_heads % d->n_kv_heads != 0 || d->n_heads / d->n_kv_heads > kGroup || d->n_kv_heads > 64)
+    return MSA_ERR_UNSUPPORTED;
+  if (d->q_len > 8 || d->batch > 4096) return MSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->max_blocks_per_seq) * kBlock > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->num_pages) * d->n_kv_heads * kBlock > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
 static msa_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 }  // namespace msa
@@ -382,6 +398,150 @@ msa_status_t msa_select_sparse_gqa_decode(const msa_dims_t* dims, const void* q,
   if (scores == nullptr) return MSA_ERR_INVALID_ARG;
   return sparse_gqa_common(dims, q, cache, block_table, seq_lens, selected, scores, out, lse, workspace,
                            workspace_bytes, dev_flags, stream);
+}
+
+msa_status_t msa_build_step(const msa_dims_t* dims, const int32_t* ctx_lens, const int32_t* new_lens,
+                            const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                            const int32_t* pos_offset, int32_t* block_table, int32_t* seq_lens,
+                            int32_t* token_starts, int64_t* slot_mapping, int32_t* positions, int32_t num_axes,
+                            int64_t position_stride, int32_t max_tokens, int32_t* free_head_out,
+                            uint32_t* dev_flags, void* stream) {
+  if (dims == nullptr) return MSA_ERR_INVALID_ARG;
+  if (dims->batch < 1 || dims->block_size < 1 || dims->max_blocks_per_seq < 1 || dims->num_pages < 1)
+    return MSA_ERR_INVALID_ARG;
+  if (dims->block_size != kBlock || dims->batch > 4096) return MSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(dims->max_blocks_per_seq) * kBlock > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  if (num_free < 0 || max_tokens < 1 || num_axes < 1 || position_stride < max_tokens) return MSA_ERR_INVALID_ARG;
+  if (num_axes > 4) return MSA_ERR_UNSUPPORTED;
+  if (ctx_lens == nullptr || new_lens == nullptr || (free_pages == nullptr && num_free > 0) || free_head == nullptr ||
+      block_table == nullptr || seq_lens == nullptr || token_starts == nullptr || slot_mapping == nullptr ||
+      positions == nullptr || free_head_out == nullptr || dev_flags == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  if (!aligned16(slot_mapping)) return MSA_ERR_INVALID_ARG;
+  if (seq_lens == ctx_lens || seq_lens == new_lens || free_head_out == free_head) return MSA_ERR_INVALID_ARG;
+  StepArgs a{ctx_lens, new_lens, free_pages, free_head, pos_offset, block_table, seq_lens, token_starts,
+             slot_mapping, positions, free_head_out, dev_flags, position_stride, dims->batch,
+             dims->max_blocks_per_seq, dims->num_pages, num_free, num_axes, max_tokens};
+  return cuda_status(launch_build_step(a, static_cast<cudaStream_t>(stream), &g_record));
+}
+
+msa_status_t msa_qk_norm_mrope_insert(const msa_dims_t* dims, const void* q, const void* k, const void* v,
+                                      const void* idx_q, const void* idx_k, const int32_t* positions,
+                                      int64_t position_stride, const int64_t* slot_mapping, int32_t num_tokens,
+                                      const msa_norm_rope_t* nr, const msa_rope_axes_t* axes, void* q_out,
+                                      void* idx_q_out, const msa_kv_cache_t* cache,
+                                      const msa_index_cache_t* idx_cache, uint32_t* dev_flags, void* stream) {
+  msa_status_t st = check_dense_dims(dims);
+  if (st != MSA_OK) return st;
+  if (num_tokens < 0 || nr == nullptr || axes == nullptr || cache == nullptr || dev_flags == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  const bool with_idx = idx_q != nullptr || idx_k != nullptr;
+  if (with_idx && (idx_q == nullptr || idx_k == nullptr || idx_q_out == nullptr || nr->idx_q_weight == nullptr ||
+                   nr->idx_k_weight == nullptr || dims->n_idx_heads < 1))
+    return MSA_ERR_INVALID_ARG;
+  if (with_idx && dims->n_idx_heads != dims->n_kv_heads) return MSA_ERR_UNSUPPORTED;
+  if (!(nr->eps >= 0.f) || nr->eps > 1.f || !(nr->rope_theta > 1.f) || nr->rope_theta > 3.0e38f)
+    return MSA_ERR_INVALID_ARG;
+  if (axes->num_axes < 1) return MSA_ERR_INVALID_ARG;
+  if (axes->num_axes > 4) return MSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < kDim / 2; ++i)
+    if (axes->axis[i] >= axes->num_axes) return MSA_ERR_INVALID_ARG;
+  if (num_tokens == 0) {
+    g_record.set("qk_norm_mrope_insert empty");
+    return MSA_OK;
+  }
+  if (position_stride < num_tokens) return MSA_ERR_INVALID_ARG;
+  if (q == nullptr || k == nullptr || v == nullptr || positions == nullptr || slot_mapping == nullptr ||
+      q_out == nullptr || nr->q_weight == nullptr || nr->k_weight == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  const void* ptrs16[] = {q, k, v, q_out, nr->q_weight, nr->k_weight};
+  for (const void* ptr : ptrs16)
+    if (!aligned16(ptr)) return MSA_ERR_INVALID_ARG;
+  if (with_idx && (!aligned16(idx_q) || !aligned16(idx_k) || !aligned16(idx_q_out) || !aligned16(nr->idx_q_weight) ||
+                   !aligned16(nr->idx_k_weight)))
+    return MSA_ERR_INVALID_ARG;
+  if (with_idx && idx_cache != nullptr && idx_cache->dtype == MSA_F32) return MSA_ERR_UNSUPPORTED;
+  PrologueArgs a;
+  memset(&a, 0, sizeof(a));
+  st = insert_targets(dims, with_idx, MSA_BF16, cache, idx_cache, dev_flags, a.ins);
+  if (st != MSA_OK) return st;
+  a.ins.k_new = k;
+  a.ins.v_new = v;
+  a.ins.idx_new = idx_k;
+  a.ins.idx_new_bf16 = 1;
+  a.ins.slots = slot_mapping;
+  a.ins.T = num_tokens;
+  a.q = q;
+  a.idx_q = with_idx ? idx_q : nullptr;
+  a.q_out = q_out;
+  a.idx_q_out = with_idx ? idx_q_out : nullptr;
+  a.positions = positions;
+  a.wq = nr->q_weight;
+  a.wk = nr->k_weight;
+  a.wiq = nr->idx_q_weight;
+  a.wik = nr->idx_k_weight;
+  a.eps = nr->eps;
+  a.theta = nr->rope_theta;
+  a.H = dims->n_heads;
+  a.I = dims->n_idx_heads;
+  return cuda_status(
+      launch_qk_norm_mrope_insert(a, *axes, position_stride, static_cast<cudaStream_t>(stream), &g_record));
+}
+
+size_t msa_paged_gqa_workspace_size(const msa_dims_t* dims, msa_dtype_t kv_dtype) {
+  (void)kv_dtype;
+  if (check_dense_dims(dims) != MSA_OK) return 0;
+  return paged_gqa_workspace_bytes(dims->q_len, dims->n_heads, dims->n_kv_heads);
+}
+
+msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const msa_kv_cache_t* cache,
+                                  const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, uint32_t* dev_flags, void* stream) {
+  msa_status_t st = check_dense_dims(dims);
+  if (st != MSA_OK) return st;
+  if (!(dims->softmax_scale > 0.f) || dims->softmax_scale > 3.0e38f) return MSA_ERR_INVALID_ARG;
+  if (q == nullptr || cache == nullptr || cache->k == nullptr || cache->v == nullptr || block_table == nullptr ||
+      seq_lens == nullptr || out == nullptr || dev_flags == nullptr)
+    return MSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(cache->k) || !aligned16(cache->v)) return MSA_ERR_INVALID_ARG;
+  PagedArgs a;
+  memset(&a, 0, sizeof(a));
+  a.kv = cache->dtype;
+  a.k_global = a.v_global = 1.f;
+  if (cache->dtype == MSA_NVFP4 || cache->dtype == MSA_FP8_E4M3) {
+    if (!(cache->k_global > 0.f) || !(cache->v_global > 0.f) || cache->k_global > 3.0e38f ||
+        cache->v_global > 3.0e38f)
+      return MSA_ERR_INVALID_ARG;
+    if (cache->dtype == MSA_NVFP4 && (cache->k_scale == nullptr || cache->v_scale == nullptr ||
+                                      !aligned16(cache->k_scale) || !aligned16(cache->v_scale)))
+      return MSA_ERR_INVALID_ARG;
+    a.k_global = cache->k_global;
+    a.v_global = cache->v_global;
+  } else if (cache->dtype != MSA_BF16) {
+    return MSA_ERR_UNSUPPORTED;
+  }
+  if (workspace == nullptr || workspace_bytes < paged_gqa_workspace_bytes(dims->q_len, dims->n_heads, dims->n_kv_heads) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MSA_ERR_WORKSPACE;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = static_cast<const uint8_t*>(cache->k_scale);
+  a.v_scale = static_cast<const uint8_t*>(cache->v_scale);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.workspace = workspace;
+  a.flags = dev_flags;
+  a.B = dims->batch;
+  a.Q = dims->q_len;
+  a.H = dims->n_heads;
+  a.G = dims->n_kv_heads;
+  a.NB = dims->max_blocks_per_seq;
+  a.P = dims->num_pages;
+  a.softmax_scale = dims->softmax_scale;
+  return cuda_status(launch_paged_gqa(a, static_cast<cudaStream_t>(stream), &g_record));
 }
 
 msa_status_t msa_selftest_bounded_wait(uint32_t* dev_flags, void* stream) {

@@ -160,6 +160,51 @@ cudaError_t launch_qk_norm_rope_insert(const PrologueArgs& a, cudaStream_t strea
 // ins: the step's insert run inside the same launch (FP8 / NVFP4 index keys,
 // one query position, token t = request t's token at position L_t - 1), or null.
 cudaError_t launch_index_score(const IndexArgs& a, const InsertArgs* ins, cudaStream_t stream, DispatchRecord* rec);
+// Step metadata (msa_build_step).
+struct StepArgs {
+  const int32_t* ctx_lens;      // [B]
+  const int32_t* new_lens;      // [B]
+  const int32_t* free_pages;    // [F]
+  const int32_t* free_head;     // [1]
+  const int32_t* pos_offset;    // [B] or null
+  int32_t* block_table;         // [B, NB]
+  int32_t* seq_lens;            // [B]
+  int32_t* token_starts;        // [B + 1]
+  int64_t* slots;               // [T]
+  int32_t* positions;           // [A] rows of T, pos_stride apart
+  int32_t* free_head_out;       // [1]
+  uint32_t* flags;
+  int64_t pos_stride;
+  int B, NB, P, F, A, T;
+};
+cudaError_t launch_build_step(const StepArgs& a, cudaStream_t stream, DispatchRecord* rec);
+
+// QK-norm + rotary on several axes + insert: the prologue's arguments (whose
+// `positions` holds num_axes rows) and the axis of each rotary pair.
+cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_axes_t& axes, int64_t pos_stride,
+                                        cudaStream_t stream, DispatchRecord* rec);
+
+// Dense GQA decode over the paged cache (msa_paged_gqa_decode).
+struct PagedArgs {
+  const uint16_t* q;            // bf16 [B, Q, H, D]
+  msa_dtype_t kv;
+  const void* k;
+  const void* v;
+  const uint8_t* k_scale;       // nvfp4 [P, G, BS, D/16]
+  const uint8_t* v_scale;
+  float k_global, v_global;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  uint16_t* out;                // bf16 [B, Q, H, D]
+  float* lse;                   // [B, Q, H] or null
+  void* workspace;
+  uint32_t* flags;
+  int B, Q, H, G, NB, P;
+  float softmax_scale;
+};
+size_t paged_gqa_workspace_bytes(int Q, int H, int G);
+cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRecord* rec);
+
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, DispatchRecord* rec);
 cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRecord* rec);
 

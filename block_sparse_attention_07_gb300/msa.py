@@ -19,14 +19,15 @@ F32, BF16, FP8_E4M3, NVFP4 = 0, 1, 2, 3
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_DEVICE_FLAG = range(6)
 
-FLAG_BAD_PAGE, FLAG_BAD_BLOCK, FLAG_BAD_SEQLEN, FLAG_BAD_SLOT, FLAG_TIMEOUT, FLAG_Q_RANGE = (
-    0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
+FLAG_BAD_PAGE, FLAG_BAD_BLOCK, FLAG_BAD_SEQLEN, FLAG_BAD_SLOT, FLAG_TIMEOUT, FLAG_Q_RANGE, FLAG_NO_PAGES = (
+    0x1, 0x2, 0x4, 0x8, 0x10, 0x20, 0x40)
 
 # Every function include/msa.h declares.
 EXPORTED = ("msa_abi_version", "msa_status_string", "msa_get_last_dispatch", "msa_kv_insert_quant",
             "msa_index_score", "msa_insert_index_score", "msa_select_blocks", "msa_sparse_gqa_workspace_size",
             "msa_sparse_gqa_decode", "msa_sparse_gqa_decode_noalloc", "msa_read_device_flags",
-            "msa_qk_norm_rope_insert", "msa_select_sparse_gqa_decode", "msa_selftest_bounded_wait")
+            "msa_qk_norm_rope_insert", "msa_select_sparse_gqa_decode", "msa_selftest_bounded_wait",
+            "msa_build_step", "msa_qk_norm_mrope_insert", "msa_paged_gqa_workspace_size", "msa_paged_gqa_decode")
 
 
 class Dims(ctypes.Structure):
@@ -52,6 +53,11 @@ class NormRope(ctypes.Structure):
     """msa_norm_rope_t: device fp32 [D] RMSNorm weights (pointers), eps, rotary base."""
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("idx_q_weight", ctypes.c_void_p),
                 ("idx_k_weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("rope_theta", ctypes.c_float)]
+
+
+class RopeAxes(ctypes.Structure):
+    """msa_rope_axes_t: the number of position axes and the axis of each of the 64 rotary pairs."""
+    _fields_ = [("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
 
 
 class MSAError(RuntimeError):
@@ -89,8 +95,18 @@ def _load():
     lib.msa_qk_norm_rope_insert.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, vp, vp, vp, vp, i32,
                                             ctypes.POINTER(NormRope), vp, vp, ctypes.POINTER(_KVCache),
                                             ctypes.POINTER(_IndexCache), vp, vp]
+    lib.msa_build_step.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, i32,
+                                   ctypes.c_int64, i32, vp, vp, vp]
+    lib.msa_qk_norm_mrope_insert.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, i32,
+                                             ctypes.POINTER(NormRope), ctypes.POINTER(RopeAxes), vp, vp,
+                                             ctypes.POINTER(_KVCache), ctypes.POINTER(_IndexCache), vp, vp]
+    lib.msa_paged_gqa_workspace_size.restype = sz
+    lib.msa_paged_gqa_workspace_size.argtypes = [ctypes.POINTER(Dims), ctypes.c_int]
+    lib.msa_paged_gqa_decode.argtypes = [ctypes.POINTER(Dims), vp, ctypes.POINTER(_KVCache), vp, vp, vp, vp, vp, sz,
+                                         vp, vp]
     for name in EXPORTED:       # every other entry point returns msa_status_t
-        if name not in ("msa_abi_version", "msa_status_string", "msa_sparse_gqa_workspace_size"):
+        if name not in ("msa_abi_version", "msa_status_string", "msa_sparse_gqa_workspace_size",
+                        "msa_paged_gqa_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -268,6 +284,115 @@ def sparse_gqa_decode_noalloc(dims: Dims, q, cache: KVCache, block_table, seq_le
                                            _ptr(seq_lens), _ptr(selected), _ptr(out), _ptr(lse), _ptr(flags),
                                            _stream(stream))
     _check(st, "msa_sparse_gqa_decode_noalloc")
+
+
+def _want(what: str, name: str, t, dtype: str, shape, strided_rows=False):
+    """Refuses (ERR_INVALID_ARG) a tensor of another type, shape, layout or device than the call reads."""
+    import torch
+    ok = t.dtype == getattr(torch, dtype) and tuple(t.shape) == tuple(shape)
+    ok = ok and (t.is_contiguous() or (strided_rows and t.stride(-1) == 1))
+    ok = ok and (t.device.type != "cuda" or t.device.index == torch.cuda.current_device())
+    if not ok:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be {dtype} {list(shape)}, contiguous, on the current "
+                                        f"device (got {t.dtype} {list(t.shape)} strides {t.stride()} on {t.device})")
+
+
+def _want_cache(what: str, dims: Dims, cache: KVCache):
+    P, G, BS, D = dims.num_pages, dims.n_kv_heads, dims.block_size, dims.head_dim
+    kind, row = {BF16: ("bfloat16", D), FP8_E4M3: ("uint8", D), NVFP4: ("uint8", D // 2)}.get(cache.dtype, (None, 0))
+    if kind is None:
+        raise MSAError(ERR_UNSUPPORTED, f"{what}: no K/V cache of dtype {cache.dtype}")
+    for name in ("k", "v"):
+        _want(what, "cache." + name, getattr(cache, name), kind, (P, G, BS, row))
+        if cache.dtype == NVFP4:
+            if getattr(cache, name + "_scale") is None:
+                raise MSAError(ERR_INVALID_ARG, f"{what}: an NVFP4 cache needs {name}_scale")
+            _want(what, f"cache.{name}_scale", getattr(cache, name + "_scale"), "uint8", (P, G, BS, D // 16))
+
+
+def build_step(dims: Dims, ctx_lens, new_lens, free_pages, free_head, block_table, seq_lens, token_starts,
+               slot_mapping, positions, free_head_out, flags, pos_offset=None, stream=None, prepare=False):
+    """msa_build_step: block tables, slot map and positions ([axes, tokens]) of a step from its
+    requests' lengths. ``slot_mapping``'s length is the step's token capacity."""
+    what, B = "msa_build_step", dims.batch
+    T = int(slot_mapping.shape[0])
+    for name, t, shape in (("ctx_lens", ctx_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("free_pages", free_pages, (free_pages.numel(),)), ("free_head", free_head, (1,)),
+                           ("block_table", block_table, (B, dims.max_blocks_per_seq)), ("seq_lens", seq_lens, (B,)),
+                           ("token_starts", token_starts, (B + 1,)), ("free_head_out", free_head_out, (1,))):
+        _want(what, name, t, "int32", shape)
+    _want(what, "slot_mapping", slot_mapping, "int64", (T,))
+    _want(what, "positions", positions, "int32", (positions.shape[0], T), strided_rows=True)
+    if pos_offset is not None:
+        _want(what, "pos_offset", pos_offset, "int32", (B,))
+    axes = int(positions.shape[0])
+    pos_stride = int(positions.stride(0)) if axes > 1 else T
+    args = (ctypes.byref(dims), _ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), int(free_pages.numel()),
+            _ptr(free_head), _ptr(pos_offset), _ptr(block_table), _ptr(seq_lens), _ptr(token_starts),
+            _ptr(slot_mapping), _ptr(positions), axes, pos_stride, T, _ptr(free_head_out), _ptr(flags),
+            _stream(stream))
+    return _call(lib.msa_build_step, args, (dims,), what, prepare)
+
+
+def make_rope_axes(sections, interleaved: bool = False) -> RopeAxes:
+    """msa_rope_axes_t from the number of rotary pairs of each axis (sections sum to 64). Contiguous: the first
+    sections[0] pairs turn with axis 0, the next with axis 1, and so on. Interleaved: pair i turns with axis
+    i mod A while i // A < sections[i mod A], and with axis 0 otherwise, so axis 0 takes what the others leave."""
+    A = len(sections)
+    if not 1 <= A <= 4 or sum(sections) != 64 or min(sections) < 0:
+        raise MSAError(ERR_INVALID_ARG, "make_rope_axes: 1 to 4 sections that sum to 64")
+    if interleaved:
+        axis = [i % A if i // A < sections[i % A] else 0 for i in range(64)]
+        if any(axis.count(a) != n for a, n in enumerate(sections)):
+            raise MSAError(ERR_INVALID_ARG, f"make_rope_axes: sections {tuple(sections)} do not interleave over 64 pairs")
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return RopeAxes(A, (ctypes.c_uint8 * 64)(*axis))
+
+
+def qk_norm_mrope_insert(dims: Dims, q, k, v, idx_q, idx_k, positions, slot_mapping, nr: NormRope, axes: RopeAxes,
+                         q_out, idx_q_out, cache: KVCache, idx_cache: IndexCache | None, flags, stream=None,
+                         prepare=False):
+    """msa_qk_norm_mrope_insert: ``positions`` [axes.num_axes, T]; otherwise as qk_norm_rope_insert."""
+    what, T, D = "msa_qk_norm_mrope_insert", int(q.shape[0]), dims.head_dim
+    for name, t, h in (("q", q, dims.n_heads), ("k", k, dims.n_kv_heads), ("v", v, dims.n_kv_heads),
+                       ("q_out", q_out, dims.n_heads), ("idx_q", idx_q, dims.n_idx_heads),
+                       ("idx_k", idx_k, dims.n_idx_heads), ("idx_q_out", idx_q_out, dims.n_idx_heads)):
+        if t is not None:
+            _want(what, name, t, "bfloat16", (T, h, D))
+    _want(what, "positions", positions, "int32", (axes.num_axes, T), strided_rows=True)
+    _want(what, "slot_mapping", slot_mapping, "int64", (T,))
+    _want_cache(what, dims, cache)
+    kc = cache.c()
+    ic = idx_cache.c() if idx_cache is not None else None
+    pos_stride = int(positions.stride(0)) if axes.num_axes > 1 else T
+    args = (ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(idx_q), _ptr(idx_k), _ptr(positions), pos_stride,
+            _ptr(slot_mapping), T, ctypes.byref(nr), ctypes.byref(axes), _ptr(q_out), _ptr(idx_q_out),
+            ctypes.byref(kc), ctypes.byref(ic) if ic is not None else None, _ptr(flags), _stream(stream))
+    return _call(lib.msa_qk_norm_mrope_insert, args, (dims, nr, axes, kc, ic), what, prepare)
+
+
+def paged_gqa_workspace_size(dims: Dims, kv_dtype: int) -> int:
+    return int(lib.msa_paged_gqa_workspace_size(ctypes.byref(dims), kv_dtype))
+
+
+def paged_gqa_decode(dims: Dims, q, cache: KVCache, block_table, seq_lens, out, lse, workspace, flags, stream=None,
+                     prepare=False):
+    """msa_paged_gqa_decode: attention of the step's tokens over every cached token."""
+    what = "msa_paged_gqa_decode"
+    shape = (dims.batch, dims.q_len, dims.n_heads, dims.head_dim)
+    _want(what, "q", q, "bfloat16", shape)
+    _want(what, "out", out, "bfloat16", shape)
+    if lse is not None:
+        _want(what, "lse", lse, "float32", shape[:3])
+    _want(what, "block_table", block_table, "int32", (dims.batch, dims.max_blocks_per_seq))
+    _want(what, "seq_lens", seq_lens, "int32", (dims.batch,))
+    _want_cache(what, dims, cache)
+    kc = cache.c()
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = (ctypes.byref(dims), _ptr(q), ctypes.byref(kc), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse),
+            _ptr(workspace), nbytes, _ptr(flags), _stream(stream))
+    return _call(lib.msa_paged_gqa_decode, args, (dims, kc), what, prepare)
 
 
 def selftest_bounded_wait(flags, stream=None):

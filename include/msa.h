@@ -85,6 +85,7 @@ typedef enum {
 #define MSA_FLAG_BAD_SLOT      0x8u  /* slot_mapping entry >= num_pages * BS */
 #define MSA_FLAG_TIMEOUT       0x10u /* a bounded wait inside a kernel gave up */
 #define MSA_FLAG_Q_RANGE       0x20u /* an index-query row too large for the fp16 operand path */
+#define MSA_FLAG_NO_PAGES      0x40u /* msa_build_step: the free list does not cover a request's new blocks */
 
 /* Problem shape (host struct). block_size must be 128, head_dim 128,
  * local_blocks 1, n_idx_heads == n_kv_heads, n_heads % n_kv_heads == 0,
@@ -368,6 +369,114 @@ msa_status_t msa_sparse_gqa_decode_noalloc(const msa_dims_t* dims, const void* q
                                            const int32_t* block_table, const int32_t* seq_lens,
                                            const int32_t* selected, void* out, float* lse, uint32_t* dev_flags,
                                            void* stream);
+
+/*
+ * Step metadata: a step's block tables, slot map and positions from the
+ * requests' lengths, so that a step whose lengths live on the GPU needs no host
+ * work ("MiniMax M3 vLLM サポート：…", section "KV キャッシュ統合": an ordinary
+ * paged cache; the pages give no allocator, so the rule is this library's).
+ * Request b has ctx_lens[b] cached tokens and adds new_lens[b]:
+ *   seq_lens[b]     = ctx_lens[b] + new_lens[b];
+ *   token_starts[b] = the sum of new_lens before b; token_starts[B] the total;
+ *   the blocks from ceil(ctx/128) up to ceil(seq/128) take the next pages of
+ *   free_pages, from entry free_head on, in request order, and are written to
+ *   block_table[b]; its other columns are left as they are;
+ *   token i of request b (position p = ctx_lens[b] + i) gets
+ *   slot_mapping[token_starts[b] + i] = block_table[b, p/128] * 128 + p % 128
+ *   and positions[a, token_starts[b] + i] = p + pos_offset[b] on every axis a;
+ *   tokens from the total up to max_tokens (padding of a captured step) get
+ *   slot -1, which the inserts skip, and position 0;
+ *   free_head_out   = free_head plus the pages taken.
+ * Refused requests: one with a negative length, more than NB * 128 tokens or
+ * tokens past max_tokens (MSA_FLAG_BAD_SEQLEN), and one whose blocks go past
+ * the end of the free list (MSA_FLAG_NO_PAGES; a later request that needs pages
+ * then goes past it too), takes no page and keeps its blocks; its tokens keep
+ * their places with slot -1, and its seq_lens entry is ctx_lens[b] (held to
+ * 0 .. NB * 128). token_starts never exceeds max_tokens. A page id outside
+ * [0, P) gives slot -1, a table entry of -1 and MSA_FLAG_BAD_PAGE.
+ * dims: batch (up to 4096), block_size, max_blocks_per_seq and num_pages are
+ * used. ctx_lens, new_lens: int32 [B]. free_pages: int32 [num_free].
+ * free_head: int32 [1]. pos_offset: int32 [B] or NULL (0): the difference
+ * between rotary and cache positions after image or video tokens. block_table:
+ * int32 [B, NB], in and out. seq_lens: int32 [B]. token_starts: int32 [B + 1].
+ * slot_mapping: int64 [max_tokens], 16-byte aligned. positions: int32, num_axes
+ * (1 to 4) rows of max_tokens, position_stride elements apart. free_head_out:
+ * int32 [1]. No output may overlap an input or another output: the inputs are
+ * read while the outputs are written (take turns with two buffers to advance
+ * ctx_lens and free_head on the device).
+ */
+msa_status_t msa_build_step(const msa_dims_t* dims, const int32_t* ctx_lens, const int32_t* new_lens,
+                            const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                            const int32_t* pos_offset, int32_t* block_table, int32_t* seq_lens,
+                            int32_t* token_starts, int64_t* slot_mapping, int32_t* positions, int32_t num_axes,
+                            int64_t position_stride, int32_t max_tokens, int32_t* free_head_out,
+                            uint32_t* dev_flags, void* stream);
+
+/* Rotary axes of msa_qk_norm_mrope_insert (host struct): pair i (dims i and
+ * i + 64) turns with the position on axis[i], 0 <= axis[i] < num_axes. */
+typedef struct {
+  int32_t num_axes;            /* 1 to 4 */
+  uint8_t axis[64];
+} msa_rope_axes_t;
+
+/*
+ * msa_qk_norm_rope_insert with rotary positions on several axes, for image and
+ * video tokens ("MiniMax M3 vLLM サポート：…", the section on multimodal input;
+ * the pages give no formula): a token has one position per axis (time, height,
+ * width), and each rotary pair turns with the axis it is given,
+ *   phi_i = positions[axis[i], t] * rope_theta^(-2i/D),
+ * its phase reduced exactly modulo one turn, whatever the position. Text tokens
+ * have equal positions on all axes and get the one-axis rotation. Norm,
+ * rounding, quantisation, outputs and the index branch are those of
+ * msa_qk_norm_rope_insert. A token with a negative slot is skipped by the
+ * caches and still writes its q_out row.
+ * Shapes: n_heads and n_kv_heads as in dims, any n_heads up to 16 n_kv_heads
+ * that n_kv_heads divides, n_kv_heads up to 64; n_idx_heads rows in the index
+ * branch. positions: int32, axes->num_axes rows of num_tokens, position_stride
+ * elements apart. q_out may be q, idx_q_out may be idx_q.
+ */
+msa_status_t msa_qk_norm_mrope_insert(const msa_dims_t* dims, const void* q, const void* k, const void* v,
+                                      const void* idx_q, const void* idx_k, const int32_t* positions,
+                                      int64_t position_stride, const int64_t* slot_mapping, int32_t num_tokens,
+                                      const msa_norm_rope_t* nr, const msa_rope_axes_t* axes, void* q_out,
+                                      void* idx_q_out, const msa_kv_cache_t* cache,
+                                      const msa_index_cache_t* idx_cache, uint32_t* dev_flags, void* stream);
+
+/* Bytes of device workspace msa_paged_gqa_decode needs for this shape; 0 for a
+ * shape that it refuses. */
+size_t msa_paged_gqa_workspace_size(const msa_dims_t* dims, msa_dtype_t kv_dtype);
+
+/*
+ * Dense GQA decode over the paged cache, for the layers without block
+ * selection ("vLLM、AMD Instinct MI355X上で…": 57 of the 60 decoder layers are
+ * sparse, the others attend over every token). For every query head h of
+ * position j of request b, with KV head h / (H / G), over the tokens
+ * t <= p = seq_lens[b] - Q + j:
+ *   out[b, j, h] = sum_t softmax_t(softmax_scale * q . k_t) * v_t
+ *   lse[b, j, h] = log sum_t exp(softmax_scale * q . k_t)
+ * A position without a token (seq_lens[b] = 0, an unused place of the batch, or
+ * p < 0) gets out = 0 and lse = -inf. A length below 0 or above NB * 128 raises
+ * MSA_FLAG_BAD_SEQLEN and counts as 0; a block whose page id is outside [0, P)
+ * is skipped and raises MSA_FLAG_BAD_PAGE.
+ * The blocks of all requests are split evenly over the SMs; a (request, KV
+ * head) whose blocks fall to several CTAs leaves partial results (running
+ * maximum, sum, unnormalised output, fp32) in the workspace, and a second
+ * launch joins them in their order: results do not depend on timing.
+ * Cache slots past the last token may hold any bytes, NaN patterns included. A
+ * later draft token's K is masked from earlier positions, but its V has to be
+ * finite: it enters their sums with weight 0.
+ * dims: q_len 1 to 8, any n_heads that n_kv_heads divides with 1 to 16 query
+ * heads per KV head, n_kv_heads up to 64, batch up to 4096; n_idx_heads, topk
+ * and local_blocks are not used. q: bf16 [B, Q, H, D]. cache: bf16, FP8 E4M3 or
+ * NVFP4. block_table: int32 [B, NB]. seq_lens: int32 [B]. out: bf16
+ * [B, Q, H, D]. lse: fp32 [B, Q, H] or NULL. workspace: at least
+ * msa_paged_gqa_workspace_size bytes, 256-byte aligned; its contents need no
+ * initialisation and mean nothing after the call; calls that overlap on the
+ * GPU, replays of captured graphs among them, must not share it.
+ */
+msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const msa_kv_cache_t* cache,
+                                  const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, uint32_t* dev_flags, void* stream);
 
 /*
  * Diagnostic of the bounded waits (the pages have no counterpart). Launches
