@@ -531,6 +531,645 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
   }
 }
 
+// ---------------------------------------------------------------------------
+// FP8 and NVFP4 K/V on the fifth-generation tensor cores. mma.sync needs the
+// values as f16 register fragments, and expanding them is what bounds it; here
+// both products take the tokens (then the dims) as the 128 rows of A,
+//   S^T = K Q^T   (M = 128 tokens, N = NR query rows, K = 128 dims)
+//   O^T = V^T P^T (M = 128 dims,   N = NR query rows, K = 128 tokens)
+// so that K and V are A operands read from shared memory.
+//   FP8: the stage is the operand: nothing is converted. Q and P are split into
+//   8-bit parts that are accumulated one after the other: Q = two E4M3 parts
+//   after a power-of-two scaling of its row (4 significant bits each, a bf16
+//   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
+//   parts of its f16 value (3 significant bits each, rounded at 2^-10 relative).
+//   NVFP4: eight warps expand each block (e2m1 x e4m3, exact in f16) into swizzled
+//   f16 tiles; Q is scaled into f16's range and P rounded to f16.
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2 and 3 bring the next row's
+// queries into shared memory, then 4 softmax warps per row group (a thread owns a
+// token of S and a dim of O), then the expanding warps. The softmax warps agree on
+// a rescale with one barrier-with-vote per block; a row's reference is raised only
+// when a logit exceeds it by 2^8, so that after a row's first block they hardly
+// ever have to. P's columns are written token by token (MN-major, unswizzled: a
+// thread's rows are 16-byte runs). Every wait on memory is bounded; a warp whose
+// wait ran out still votes, so its group leaves together.
+constexpr int kTcS = 2;                 // S buffers in tensor memory
+constexpr int kInfos = 16;              // ring of block descriptions, longer than anything in flight
+
+struct BlockInfo {
+  int live, lim0;                       // cached tokens of the block; last token of position 0, both from its start
+  int b, g, flags, pad0, pad1, pad2;    // 1 first of a segment, 2 last, 4 starts its row, 8 ends its row
+};
+
+template <int kKv, int NR>
+struct TcCfg {
+  static constexpr bool kFp8 = kKv == MSA_FP8_E4M3;
+  static constexpr int kGroups = NR > 32 ? 2 : 1;
+  static constexpr int kRG = NR / kGroups;                     // rows per softmax group
+  static constexpr int kConv = kFp8 ? 0 : 8;                   // expanding warps
+  static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
+  static constexpr int kWarpsAll = kConv0 + kConv;
+  static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
+  static constexpr int kPBufs = NR > 64 ? 1 : 2;
+  static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
+  static constexpr uint32_t kPPart = NR * (kFp8 ? 128 : 256);
+  static constexpr uint32_t kStage = raw_bytes<kKv>();
+  static constexpr uint32_t kTiles = kFp8 ? 0 : 8 * kHalfBox;  // K[2], V[2] in f16
+  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPParts * kPPart;
+  static constexpr uint32_t kSmall = 4096 + NR * 64;
+  static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr uint32_t kCols = 3 * NR <= 64 ? 64 : 3 * NR <= 128 ? 128 : 3 * NR <= 256 ? 256 : 512;
+  static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
+  // shared memory
+  static constexpr uint32_t oStage = 0;
+  static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
+  static constexpr uint32_t oQ = oTiles + kTiles;
+  static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
+  static constexpr uint32_t oInfo = oP + kPBufs * kPParts * kPPart;
+  static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
+  static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [NR] kOff - reference
+  static constexpr uint32_t oAlpha = oRef + NR * 4;                      // [NR]
+  static constexpr uint32_t oRed = oAlpha + NR * 4;                      // [4][NR]
+  static constexpr uint32_t oPos = oRed + 4 * NR * 4;                    // [NR] position of a row
+  static constexpr uint32_t oBars = oPos + NR * 4;
+  static constexpr int kBars = 2 * kStages + kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 1;
+  static constexpr uint32_t oSlot = oBars + kBars * 8;
+  static constexpr uint32_t kTotal = oSlot + 16;
+  static_assert(kStages >= 3, "at least three stages");
+  static_assert(kTotal - oInfo <= kSmall, "small area");
+};
+
+// Shared-memory matrix descriptors (leading and stride byte offsets in 16-byte
+// units, descriptor version 1). Swizzled 128 B: as the tensor maps write. Plain:
+// core matrices of 8 rows of 16 bytes.
+__device__ __forceinline__ uint64_t mat_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(swizzle) << 61);
+}
+constexpr uint32_t kSwz128 = 2, kSwzNone = 0;
+
+// Instruction descriptor: fp32 accumulator, operand types, majorness (0 K, 1 MN), N / 8, M / 16.
+__host__ __device__ constexpr uint32_t mma_idesc(int a_type, int b_type, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) |
+         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// kind::f16 operand types: 0 f16, 1 bf16. kind::f8f6f4: 0 E4M3, 1 E5M2.
+
+template <bool kFp8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if (kFp8)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+               : "r"(a));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const float* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+               ::"r"(a), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+                 "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Barrier of a softmax group (128 threads) that returns whether any thread voted yes.
+__device__ __forceinline__ bool group_any(int id, bool vote) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred q, a;\n setp.ne.u32 q, %2, 0;\n barrier.cta.red.or.pred a, %1, 128, q;\n selp.u32 %0, 1, 0, a;\n}"
+               : "=r"(r) : "r"(id), "r"(vote ? 1u : 0u) : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint2 fp8_parts(const float (&x)[4], float f) {
+  const float y0 = x[0] * f, y1 = x[1] * f, y2 = x[2] * f, y3 = x[3] * f;
+  const uint32_t a = f32x2_to_e4m3x2(y0, y1), b = f32x2_to_e4m3x2(y2, y3);
+  const uint32_t ha = e4m3x2_to_f16x2(static_cast<uint16_t>(a)), hb = e4m3x2_to_f16x2(static_cast<uint16_t>(b));
+  const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
+  const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
+  const uint32_t la = f32x2_to_e4m3x2(y0 - fa.x, y1 - fa.y), lb = f32x2_to_e4m3x2(y2 - fb.x, y3 - fb.y);
+  return make_uint2(a | (b << 16), la | (lb << 16));
+}
+
+template <int kKv, int NR>
+__global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
+    paged_gqa_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                        const __grid_constant__ PagedParams p) {
+  using C = TcCfg<kKv, NR>;
+  constexpr bool kFp8 = C::kFp8;
+  constexpr int kAllThreads = 32 * C::kWarpsAll;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Range shared_range;
+  __shared__ int64_t warp_sums[C::kWarpsAll];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + C::oInfo);
+  float* row_mul = reinterpret_cast<float*>(sm + C::oRow);
+  float* row_ref = reinterpret_cast<float*>(sm + C::oRef);
+  float* row_alpha = reinterpret_cast<float*>(sm + C::oAlpha);
+  float* red = reinterpret_cast<float*>(sm + C::oRed);
+  int* row_pos = reinterpret_cast<int*>(sm + C::oPos);
+  const uint32_t bars = base + C::oBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
+  constexpr int b0 = 2 * C::kStages;
+  auto s_full = [&](int i) { return bars + 8u * (b0 + i); };                       // S of a block is there
+  auto p_full = [&](int i) { return bars + 8u * (b0 + kTcS + i); };                // P is written
+  auto p_free = [&](int i) { return bars + 8u * (b0 + kTcS + C::kPBufs + i); };    // P V is done
+  constexpr int b1 = b0 + kTcS + 2 * C::kPBufs;
+  auto q_full = [&](int i) { return bars + 8u * (b1 + i); };
+  auto q_free = [&](int i) { return bars + 8u * (b1 + 2 + i); };
+  auto k_full = [&](int i) { return bars + 8u * (b1 + 4 + i); };                   // NVFP4: f16 tiles
+  auto k_free = [&](int i) { return bars + 8u * (b1 + 6 + i); };
+  auto v_full = [&](int i) { return bars + 8u * (b1 + 8 + i); };
+  auto v_free = [&](int i) { return bars + 8u * (b1 + 10 + i); };
+  const uint32_t done_bar = bars + 8u * (C::kBars - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kFp8 ? 1 : C::kConv);
+    }
+    for (int i = 0; i < kTcS; ++i) mbar_init(s_full(i), 2);          // the commit, and the issuing thread's own arrival
+    for (int i = 0; i < C::kPBufs; ++i) {
+      mbar_init(p_full(i), 4 * C::kGroups);
+      mbar_init(p_free(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 2);
+      mbar_init(q_free(i), 1 + 4 * C::kGroups);                      // S is done with Q, softmax with its multipliers
+      if (!kFp8) {
+        mbar_init(k_full(i), C::kConv);
+        mbar_init(k_free(i), 1);
+        mbar_init(v_full(i), C::kConv);
+        mbar_init(v_free(i), 1);
+      }
+    }
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+    if (kFp8) {
+      prefetch_tensormap(&tk);
+      prefetch_tensormap(&tv);
+    }
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  for (int r = threadIdx.x; r < NR; r += kAllThreads) row_pos[r] = r < p.R ? r / p.group : 0;
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
+  const uint32_t tO = tmem + kTcS * NR;
+  griddep_wait();
+
+  const int cta = blockIdx.x;
+  Range rg;
+  find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
+  paged_empty_requests(p, kAllThreads);
+  if (threadIdx.x == 0) paged_describe_cut(p, rg, cta);
+  const int items = static_cast<int>(rg.x1 - rg.x0);
+  bool ok = true;
+
+  if (items > 0 && warp == 0) {
+    // ----------------------------------------------------------- copies --
+    if (lane == 0) {
+      constexpr int kAhead = 4;                     // page ids are fetched this many blocks ahead
+      int page[kAhead];
+      Walk far = rg.at, cur = rg.at;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        page[i] = i < items ? paged_page(p, far, true) : -1;
+        if (i < items) far.next(p);
+      }
+      const uint64_t policy = l2_evict_first_policy();
+      int s = 0;
+      uint32_t ph = 0;
+      bool first = true, from_start = cur.blk == 0;
+      for (int n = 0; n < items && ok; ++n) {
+        const int pg = page[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) page[i] = page[i + 1];
+        if (n + kAhead < items) {
+          page[kAhead - 1] = paged_page(p, far, true);
+          far.next(p);
+        }
+        if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
+        const bool ends = cur.blk == cur.nb - 1;
+        BlockInfo& bi = infos[n & (kInfos - 1)];
+        const int left = cur.L - cur.blk * kBlock;
+        bi.live = pg < 0 ? 0 : left < kBlock ? left : kBlock;
+        bi.lim0 = pg < 0 ? -kBlock : left - p.Q;
+        bi.b = cur.b;
+        bi.g = cur.g;
+        bi.flags = (first ? 1 : 0) | (ends || n + 1 == items ? 2 : 0) | (from_start ? 4 : 0) | (ends ? 8 : 0);
+        first = ends;
+        from_start = from_start || ends;             // only the CTA's first segment may start inside a row
+        const int64_t slab = static_cast<int64_t>(pg < 0 ? 0 : pg) * p.G + cur.g;     // a bad page's place is taken by page 0
+        const uint32_t dst = base + C::oStage + s * C::kStage;
+        mbar_arrive_expect_tx(full(s), C::kStage);
+        if (kFp8) {
+          tma_load_2d(dst, &tk, 0, static_cast<int>(slab * kBlock), full(s));
+          tma_load_2d(dst + kBlock * kDim, &tv, 0, static_cast<int>(slab * kBlock), full(s));
+        } else {
+          constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
+          bulk_g2s(dst, p.k + slab * codes, codes, full(s), policy);
+          bulk_g2s(dst + codes, p.v + slab * codes, codes, full(s), policy);
+          bulk_g2s(dst + 2 * codes, p.ks + slab * scales, scales, full(s), policy);
+          bulk_g2s(dst + 2 * codes + scales, p.vs + slab * scales, scales, full(s), policy);
+        }
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        cur.next(p);
+      }
+      // no copy may be in flight when the CTA ends, whatever the others did
+      for (int k = 0; k < C::kStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
+      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (items > 0 && warp == 1) {
+    // ------------------------------------------------------------- MMAs --
+    if (lane == 0) {
+      constexpr uint32_t id_s = mma_idesc(0, 0, NR, 0, 0);
+      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, NR, 1, 1);
+      int s_stage = 0, v_stage = 0;
+      uint32_t s_ph = 0;
+      int seg_q = -1;                               // segment whose queries S uses
+      auto issue_s = [&](int n) -> bool {
+        if (kFp8 ? !mbar_wait(full(s_stage), s_ph) : !mbar_wait(k_full(n & 1), (n >> 1) & 1)) return false;
+        const int fl = infos[n & (kInfos - 1)].flags;
+        if (fl & 1) {
+          ++seg_q;
+          if (!mbar_wait(q_full(seg_q & 1), (seg_q >> 1) & 1)) return false;
+        }
+        tmem_fence_after();
+        const uint32_t q = base + C::oQ + (seg_q & 1) * (C::kQParts * C::kQPart);
+        const uint32_t d = tmem + (n & 1) * NR;
+        if (kFp8) {
+          const uint32_t k = base + C::oStage + s_stage * C::kStage;
+#pragma unroll
+          for (int part = 0; part < C::kQParts; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss<true>(d, mat_desc(k + kk * 32, 16, 1024, kSwz128),
+                           mat_desc(q + part * C::kQPart + kk * 32, 16, 1024, kSwz128), id_s, part + kk > 0);
+        } else {
+          const uint32_t k = base + C::oTiles + (n & 1) * 2 * kHalfBox;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss<false>(d, mat_desc(k + (kk >> 2) * kHalfBox + (kk & 3) * 32, 16, 1024, kSwz128),
+                          mat_desc(q + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024, kSwz128), id_s, kk > 0);
+          mma_commit(k_free(n & 1));
+        }
+        mma_commit(s_full(n & 1));
+        mbar_arrive(s_full(n & 1));
+        if (fl & 2) mma_commit(q_free(seg_q & 1));
+        if (++s_stage == C::kStages) { s_stage = 0; s_ph ^= 1u; }
+        return true;
+      };
+      auto issue_pv = [&](int n) -> bool {
+        const int pb = n % C::kPBufs;
+        if (!mbar_wait(p_full(pb), (n / C::kPBufs) & 1)) return false;
+        if (!kFp8 && !mbar_wait(v_full(n & 1), (n >> 1) & 1)) return false;
+        const bool fresh = (infos[n & (kInfos - 1)].flags & 1) != 0;
+        tmem_fence_after();
+        const uint32_t pt = base + C::oP + pb * (C::kPParts * C::kPPart);
+        if (kFp8) {
+          const uint32_t v = base + C::oStage + v_stage * C::kStage + kBlock * kDim;
+#pragma unroll
+          for (int part = 0; part < C::kPParts; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss<true>(tO, mat_desc(v + kk * 4096, 16384, 1024, kSwz128),
+                           mat_desc(pt + part * C::kPPart + kk * 512, 128, 2048, kSwzNone), id_o, !(fresh && part + kk == 0));
+          mma_commit(empty(v_stage));
+        } else {
+          const uint32_t v = base + C::oTiles + 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss<false>(tO, mat_desc(v + kk * 2048, kHalfBox, 1024, kSwz128),
+                          mat_desc(pt + kk * 256, 128, 2048, kSwzNone), id_o, !(fresh && kk == 0));
+          mma_commit(v_free(n & 1));
+        }
+        mma_commit(p_free(pb));
+        if (++v_stage == C::kStages) v_stage = 0;
+        return true;
+      };
+      ok = issue_s(0);
+      if (ok && items > 1) ok = issue_s(1);
+      for (int n = 0; n < items && ok; ++n) {
+        ok = issue_pv(n);
+        if (ok && n + 2 < items) ok = issue_s(n + 2);
+      }
+      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+      mma_commit(done_bar);                         // every MMA has finished before tensor memory is freed
+      mbar_wait(done_bar, 0);
+    }
+    __syncwarp();
+  } else if (items > 0 && warp < C::kSoft0) {
+    // ---------------------------------------------------------- queries --
+    Walk w = rg.at;
+    int64_t left = items;
+    for (int seg = 0; left > 0; ++seg) {
+      const int qb = seg & 1;
+      if (seg >= 2 && !mbar_wait(q_free(qb), ((seg >> 1) - 1) & 1)) { ok = false; break; }
+      uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
+      for (int r = warp - 2; r < NR; r += 2) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < p.R) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p.q + paged_head(p, w.b, w.g, r) * kDim + 4 * lane);
+          x[0] = bf16_bits_to_f32(v.x & 0xFFFF); x[1] = bf16_bits_to_f32(v.x >> 16);
+          x[2] = bf16_bits_to_f32(v.y & 0xFFFF); x[3] = bf16_bits_to_f32(v.y >> 16);
+        }
+        float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, o));
+        // a power of two that brings the row's largest value to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
+        int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
+        sh = sh < -126 ? -126 : sh;
+        const float f = exp2_int(sh);
+        if (kFp8) {
+          const uint2 parts = fp8_parts(x, f);
+          const uint32_t at = r * 128 + ((((lane >> 2) ^ r) & 7) << 4) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(q + at) = parts.x;
+          *reinterpret_cast<uint32_t*>(q + C::kQPart + at) = parts.y;
+        } else {
+          const uint32_t at = (lane >> 4) * (NR * 128) + r * 128 + (((((lane & 15) >> 1) ^ r) & 7) << 4) + (lane & 1) * 8;
+          *reinterpret_cast<uint2*>(q + at) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
+        }
+        if (lane == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+      }
+      smem_to_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(qb));
+      left -= w.nb - w.blk;
+      w.blk = w.nb - 1;
+      if (left > 0) w.next(p);
+    }
+  } else if (items > 0 && warp < C::kConv0) {
+    // ---------------------------------------------------------- softmax --
+    constexpr int RG = C::kRG;
+    const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
+    const int t = 32 * wl + lane;                   // token of S, dim of O
+    const int r0 = grp * RG;
+    const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
+    float l[RG];
+    int stage = 0, seg = -1;
+    bool first = false;                             // no block of the segment has set the references yet
+    for (int n = 0; n < items; ++n) {
+      const int sb = n & 1, pb = n % C::kPBufs;
+      ok = mbar_wait(s_full(sb), (n >> 1) & 1);
+      if (n >= C::kPBufs) ok = mbar_wait(p_free(pb), ((n / C::kPBufs) - 1) & 1) && ok;
+      const BlockInfo bi = infos[n & (kInfos - 1)];
+      if (bi.flags & 1) {
+        ++seg;
+        first = true;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) l[r] = 0.f;
+      }
+      const float* mul = row_mul + (seg & 1) * NR + r0;
+      float x[RG];
+      tmem_fence_after();
+#pragma unroll
+      for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * NR + r0 + 16 * i, x + 16 * i);
+      tmem_wait_ld();
+      const bool edge = bi.lim0 < kBlock - 1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < RG; r += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(mul + r);
+        const float4 f4 = *reinterpret_cast<const float4*>(row_ref + r0 + r);
+        const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ff[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[r + e] = first ? x[r + e] * mm[e] : fmaf(x[r + e], mm[e], ff[e]);
+          if (edge && t > bi.lim0 + row_pos[r0 + r + e]) x[r + e] = -INFINITY;
+          top = fmaxf(top, x[r + e]);
+        }
+      }
+      if (group_any(bar_id, first || !ok || top > C::kOff + kSlack)) {
+        // the block's maxima over all tokens; rows that rise by more than the slack get a new reference
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          float v = x[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kEvery, v, o));
+          if (lane == 0) red[wl * NR + r0 + r] = v;
+        }
+        if (!first && n >= 1) ok = mbar_wait(p_free((n - 1) % C::kPBufs), ((n - 1) / C::kPBufs) & 1) && ok;   // O is complete
+        if (group_any(bar_id, !ok)) { ok = false; break; }
+        if (t < RG) {
+          // x = s - reference + kOff, s itself in a first block; row_ref holds kOff - reference. A row that its
+          // first block masks is masked by every later one: its reference stays -inf and its x with it
+          const int r = r0 + t;
+          const float v = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
+          float alpha = 1.f, delta = 0.f;
+          if (first) {
+            delta = v == -INFINITY ? -INFINITY : C::kOff - v;
+            row_ref[r] = delta;
+          } else if (v > C::kOff + kSlack) {
+            delta = C::kOff - v;
+            alpha = ex2_approx(delta);
+            row_ref[r] += delta;
+          }
+          row_alpha[r] = alpha;
+          red[r] = delta;                            // (no other thread reads this row's maxima)
+        }
+        group_any(bar_id, false);
+        tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < RG / 16; ++i) {
+          float o[16];
+          if (!first) {
+            tmem_ld16(tO + lanes + r0 + 16 * i, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float alpha = row_alpha[r0 + 16 * i + e];
+            x[16 * i + e] += red[r0 + 16 * i + e];
+            l[16 * i + e] *= alpha;
+            if (!first) o[e] *= alpha;
+          }
+          if (!first) tmem_st16(tO + lanes + r0 + 16 * i, o);
+        }
+        tmem_wait_st();
+        if (bi.live > 0) first = false;              // (a block whose page is bad sets nothing)
+        group_any(bar_id, false);                    // `red` may change again
+      }
+      // probabilities
+      const uint32_t pt = C::oP + pb * (C::kPParts * C::kPPart) + (t >> 3) * 128 + (t & 7) * 16;
+#pragma unroll
+      for (int i = 0; i < RG / 16; ++i) {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = ex2_approx(x[16 * i + 2 * e]), b = ex2_approx(x[16 * i + 2 * e + 1]);
+          l[16 * i + 2 * e] += a;
+          l[16 * i + 2 * e + 1] += b;
+          h[e] = pack_f16x2(a, b);
+        }
+        if (kFp8) {
+          // an E5M2 byte is the upper byte of an f16: three bytes of 3 significant bits, the last rounded
+          uint8_t* d = sm + pt + ((r0 >> 4) + i) * 2048;
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (part == 2) { h[2 * e] += 0x00800080u; h[2 * e + 1] += 0x00800080u; }
+              w[e] = __byte_perm(h[2 * e], h[2 * e + 1], 0x7531);
+              if (part < 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t hi = h[2 * e + k] & 0xFF00FF00u;
+                  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * e + k]), *reinterpret_cast<const __half2*>(&hi));
+                  h[2 * e + k] = *reinterpret_cast<const uint32_t*>(&rest);
+                }
+              }
+            }
+            *reinterpret_cast<uint4*>(d + part * C::kPPart) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint8_t* d = sm + pt + ((r0 >> 3) + 2 * i) * 2048;
+          *reinterpret_cast<uint4*>(d) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(d + 2048) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      if (kFp8 && grp == 0 && t >= bi.live) {
+        // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
+        uint4* v = reinterpret_cast<uint4*>(sm + C::oStage + stage * C::kStage + kBlock * kDim + t * kDim);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (++stage == C::kStages) stage = 0;
+      smem_to_async();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(pb));
+
+      if (bi.flags & 2) {
+        // the segment's output: this thread's dim of every row
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          float v = l[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kEvery, v, o);
+          if (lane == 0) red[wl * NR + r0 + r] = v;
+        }
+        ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1);
+        if (group_any(bar_id, !ok)) { ok = false; break; }
+        tmem_fence_after();
+        const bool whole = (bi.flags & 12) == 12;
+        float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < RG / 16; ++i) {
+          float o[16];
+          tmem_ld16(tO + lanes + r0 + 16 * i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = r0 + 16 * i + e;
+            if (r >= p.R) continue;
+            const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
+            const float M = L > 0.f ? -row_ref[r] : -INFINITY;      // L and O are in units of 2^M
+            if (whole) {
+              const float inv = L > 0.f ? p.v_global / L : 0.f;
+              const int64_t head = paged_head(p, bi.b, bi.g, r);
+              p.out[head * kDim + t] = static_cast<uint16_t>(pack_bf16x2(L > 0.f ? o[e] * inv : 0.f, 0.f) & 0xFFFF);
+              if (p.lse != nullptr && t == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
+            } else {
+              part[r * kDim + t] = L > 0.f ? o[e] : 0.f;
+              if (t == 0) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = L; }
+            }
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_free(seg & 1));
+        group_any(bar_id, false);                     // `red` and the references may change again
+      }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+  } else if (items > 0 && C::kConv > 0) {
+    // -------------------------------------------------- NVFP4 expansion --
+    const int ct = threadIdx.x - 32 * C::kConv0;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int n = 0; n < items; ++n) {
+      ok = mbar_wait(full(s), ph);
+      const int live = infos[n & (kInfos - 1)].live;
+      const uint8_t* st = sm + C::oStage + s * C::kStage;
+#pragma unroll 1
+      for (int isv = 0; isv < 2 && ok; ++isv) {
+        if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1);
+        if (!ok) break;
+        constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
+        uint8_t* tile = sm + C::oTiles + isv * 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
+        // 32 values (two scale groups) at a time; eight lanes take 4 rows x 2 runs, so that their 16-byte
+        // stores fall to different banks
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int task = ct + 256 * i;
+          const int row = ((task >> 4) << 2) + ((task >> 1) & 3), run = (task & 1) + ((task >> 3) & 1) * 2;
+          const uint4 w = *reinterpret_cast<const uint4*>(st + isv * codes + row * (kDim / 2) + 16 * run);
+          const uint32_t sc = *reinterpret_cast<const uint16_t*>(st + 2 * codes + isv * scales + row * (kDim / 16) + 2 * run);
+          const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+          const bool dead = isv && row >= live;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            e2m1x8_to_f16x2x4(words[k], h);
+            const uint32_t b = (sc >> (8 * (k >> 1))) & 0xFF;
+            const uint32_t s2 = e4m3x2_to_f16x2(static_cast<uint16_t>(b | (b << 8)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[j]), *reinterpret_cast<const __half2*>(&s2));
+              h[j] = dead ? 0u : *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const int c = 4 * run + k;
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalfBox + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        smem_to_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(empty(s));
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+  }
+
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  }
+}
+
 // Joins the partials of a cut row, in CTA order. One CTA per (cut, group of
 // rows); with few rows the eight warps share a row's partials.
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
@@ -604,6 +1243,54 @@ static cudaError_t launch_rows(const PagedParams& p, int mt, int ctas, cudaStrea
   return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
 }
 
+// cuTensorMapEncodeTiled from the driver, looked up through the runtime (the
+// library does not link libcuda).
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool got = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                         cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return got ? reinterpret_cast<EncodeFn>(ptr) : nullptr;
+  }();
+  return fn;
+}
+
+// 2-D map over a cache [P * G * 128 rows][128 dims]: boxes of 128 rows x 128 bytes, 128-byte swizzle.
+static cudaError_t cache_map(CUtensorMap* map, const void* base, int64_t rows, bool bf16) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kDim) * (bf16 ? 2 : 1)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 128u, static_cast<cuuint32_t>(kBlock)};
+  const cuuint32_t ones[2] = {1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                        const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int kKv, int NR>
+static cudaError_t launch_tc(const PagedParams& p, int ctas, cudaStream_t stream) {
+  using C = TcCfg<kKv, NR>;
+  CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
+  cudaError_t err;
+  if (C::kFp8) {
+    const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
+    if ((err = cache_map(&tk, p.k, rows, false)) != cudaSuccess) return err;
+    if ((err = cache_map(&tv, p.v, rows, false)) != cudaSuccess) return err;
+  }
+  constexpr size_t smem = C::kTotal + 1024;
+  err = cudaFuncSetAttribute(paged_gqa_tc_kernel<kKv, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  return launch_pdl(paged_gqa_tc_kernel<kKv, NR>, dim3(ctas), dim3(32 * C::kWarpsAll), smem, stream, tk, tv, p);
+}
+
 cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRecord* rec) {
   PagedParams p;
   memset(&p, 0, sizeof(p));
@@ -631,9 +1318,18 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   if (most < ctas) ctas = static_cast<int>(most);
   const int tiles = (p.R + 15) / 16;
   const int mt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
-  cudaError_t err = a.kv == MSA_BF16 ? launch_rows<MSA_BF16>(p, mt, ctas, stream)
-                  : a.kv == MSA_FP8_E4M3 ? launch_rows<MSA_FP8_E4M3>(p, mt, ctas, stream)
-                                         : launch_rows<MSA_NVFP4>(p, mt, ctas, stream);
+  cudaError_t err;
+  const char* form = "mma";
+  if (a.kv == MSA_FP8_E4M3) {
+    form = "tcgen05";
+    err = mt == 1 ? launch_tc<MSA_FP8_E4M3, 16>(p, ctas, stream) : mt == 2 ? launch_tc<MSA_FP8_E4M3, 32>(p, ctas, stream)
+        : mt == 4 ? launch_tc<MSA_FP8_E4M3, 64>(p, ctas, stream) : launch_tc<MSA_FP8_E4M3, 128>(p, ctas, stream);
+  } else if (a.kv == MSA_NVFP4 && mt <= 2) {
+    form = "tcgen05";
+    err = mt == 1 ? launch_tc<MSA_NVFP4, 16>(p, ctas, stream) : launch_tc<MSA_NVFP4, 32>(p, ctas, stream);
+  } else {
+    err = a.kv == MSA_BF16 ? launch_rows<MSA_BF16>(p, mt, ctas, stream) : launch_rows<MSA_NVFP4>(p, mt, ctas, stream);
+  }
   if (err != cudaSuccess) return err;
   if (ctas > 1) {
     const int rpc = p.R <= 16 ? 1 : 8;
@@ -641,8 +1337,8 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
     err = launch_pdl(paged_join_kernel, dim3((ctas - 1) * chunks), dim3(kThreads), 0, stream, p, rpc);
     if (err != cudaSuccess) return err;
   }
-  rec->set("paged_gqa %s mma rows=%d tiles=%d grid=%d block=%d + join", a.kv == MSA_BF16 ? "bf16"
-           : a.kv == MSA_FP8_E4M3 ? "fp8" : "nvfp4", p.R, mt, ctas, kThreads);
+  rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"
+           : a.kv == MSA_FP8_E4M3 ? "fp8" : "nvfp4", form, p.R, 16 * mt, ctas);
   return cudaGetLastError();
 }
 
