@@ -579,7 +579,13 @@ struct TcCfg {
   static constexpr uint32_t kSmall = 4096 + NR * 64;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr uint32_t kCols = 3 * NR <= 64 ? 64 : 3 * NR <= 128 ? 128 : 3 * NR <= 256 ? 256 : 512;
+  // The parts of Q and P side by side as columns of one MMA (fewer, wider MMAs;
+  // the sums of the parts are taken where S and O are read), or one after the
+  // other into the same columns where tensor memory is too small for that.
+  static constexpr bool kStacked = kFp8 && NR <= 32;
+  static constexpr int kSCols = kStacked ? kQParts * NR : NR, kOCols = kStacked ? kPParts * NR : NR;
+  static constexpr int kUsedCols = kTcS * kSCols + kOCols;
+  static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
   // shared memory
   static constexpr uint32_t oStage = 0;
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
-  const uint32_t tO = tmem + kTcS * NR;
+  const uint32_t tO = tmem + kTcS * C::kSCols;
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -809,8 +815,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   } else if (items > 0 && warp == 1) {
     // ------------------------------------------------------------- MMAs --
     if (lane == 0) {
-      constexpr uint32_t id_s = mma_idesc(0, 0, NR, 0, 0);
-      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, NR, 1, 1);
+      constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0);
+      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
+      constexpr int q_passes = C::kStacked ? 1 : C::kQParts, p_passes = C::kStacked ? 1 : C::kPParts;
       int s_stage = 0, v_stage = 0;
       uint32_t s_ph = 0;
       int seg_q = -1;                               // segment whose queries S uses
@@ -823,11 +830,11 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         }
         tmem_fence_after();
         const uint32_t q = base + C::oQ + (seg_q & 1) * (C::kQParts * C::kQPart);
-        const uint32_t d = tmem + (n & 1) * NR;
+        const uint32_t d = tmem + (n & 1) * C::kSCols;
         if (kFp8) {
           const uint32_t k = base + C::oStage + s_stage * C::kStage;
 #pragma unroll
-          for (int part = 0; part < C::kQParts; ++part)
+          for (int part = 0; part < q_passes; ++part)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ss<true>(d, mat_desc(k + kk * 32, 16, 1024, kSwz128),
@@ -856,7 +863,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         if (kFp8) {
           const uint32_t v = base + C::oStage + v_stage * C::kStage + kBlock * kDim;
 #pragma unroll
-          for (int part = 0; part < C::kPParts; ++part)
+          for (int part = 0; part < p_passes; ++part)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ss<true>(tO, mat_desc(v + kk * 4096, 16384, 1024, kSwz128),
@@ -893,30 +900,37 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       const int qb = seg & 1;
       if (seg >= 2 && !mbar_wait(q_free(qb), ((seg >> 1) - 1) & 1)) { ok = false; break; }
       uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
-      for (int r = warp - 2; r < NR; r += 2) {
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < p.R) {
-          const uint2 v = *reinterpret_cast<const uint2*>(p.q + paged_head(p, w.b, w.g, r) * kDim + 4 * lane);
-          x[0] = bf16_bits_to_f32(v.x & 0xFFFF); x[1] = bf16_bits_to_f32(v.x >> 16);
-          x[2] = bf16_bits_to_f32(v.y & 0xFFFF); x[3] = bf16_bits_to_f32(v.y >> 16);
-        }
-        float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      for (int rb = warp - 2; rb < NR; rb += 16) {
+        // eight rows at a time, all loads before the first use
+        uint2 v[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, o));
-        // a power of two that brings the row's largest value to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
-        int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
-        sh = sh < -126 ? -126 : sh;
-        const float f = exp2_int(sh);
-        if (kFp8) {
-          const uint2 parts = fp8_parts(x, f);
-          const uint32_t at = r * 128 + ((((lane >> 2) ^ r) & 7) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(q + at) = parts.x;
-          *reinterpret_cast<uint32_t*>(q + C::kQPart + at) = parts.y;
-        } else {
-          const uint32_t at = (lane >> 4) * (NR * 128) + r * 128 + (((((lane & 15) >> 1) ^ r) & 7) << 4) + (lane & 1) * 8;
-          *reinterpret_cast<uint2*>(q + at) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
+        for (int i = 0; i < 8; ++i) {
+          const int r = rb + 2 * i;
+          v[i] = r < p.R ? *reinterpret_cast<const uint2*>(p.q + paged_head(p, w.b, w.g, r) * kDim + 4 * lane) : make_uint2(0u, 0u);
         }
-        if (lane == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = rb + 2 * i;
+          const float x[4] = {bf16_bits_to_f32(v[i].x & 0xFFFF), bf16_bits_to_f32(v[i].x >> 16),
+                              bf16_bits_to_f32(v[i].y & 0xFFFF), bf16_bits_to_f32(v[i].y >> 16)};
+          // the largest magnitude: for values without sign, the order of the bits is the order of the values
+          const float amax = __uint_as_float(__reduce_max_sync(
+              kEvery, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
+          // a power of two that brings it to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
+          int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
+          sh = sh < -126 ? -126 : sh;
+          const float f = exp2_int(sh);
+          if (kFp8) {
+            const uint2 parts = fp8_parts(x, f);
+            const uint32_t at = r * 128 + ((((lane >> 2) ^ r) & 7) << 4) + (lane & 3) * 4;
+            *reinterpret_cast<uint32_t*>(q + at) = parts.x;
+            *reinterpret_cast<uint32_t*>(q + C::kQPart + at) = parts.y;
+          } else {
+            const uint32_t at = (lane >> 4) * (NR * 128) + r * 128 + (((((lane & 15) >> 1) ^ r) & 7) << 4) + (lane & 1) * 8;
+            *reinterpret_cast<uint2*>(q + at) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
+          }
+          if (lane == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+        }
       }
       smem_to_async();
       __syncwarp();
@@ -950,7 +964,15 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       float x[RG];
       tmem_fence_after();
 #pragma unroll
-      for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * NR + r0 + 16 * i, x + 16 * i);
+      for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * C::kSCols + r0 + 16 * i, x + 16 * i);
+      if (C::kStacked) {
+        float lo[RG];
+#pragma unroll
+        for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * C::kSCols + NR + r0 + 16 * i, lo + 16 * i);
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < RG; ++r) x[r] += lo[r];
+      }
       tmem_wait_ld();
       const bool edge = bi.lim0 < kBlock - 1;
       float top = -INFINITY;
@@ -997,22 +1019,23 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         group_any(bar_id, false);
         tmem_fence_after();
 #pragma unroll
-        for (int i = 0; i < RG / 16; ++i) {
-          float o[16];
-          if (!first) {
-            tmem_ld16(tO + lanes + r0 + 16 * i, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float alpha = row_alpha[r0 + 16 * i + e];
-            x[16 * i + e] += red[r0 + 16 * i + e];
-            l[16 * i + e] *= alpha;
-            if (!first) o[e] *= alpha;
-          }
-          if (!first) tmem_st16(tO + lanes + r0 + 16 * i, o);
+        for (int r = 0; r < RG; ++r) {
+          x[r] += red[r0 + r];
+          l[r] *= row_alpha[r0 + r];
         }
-        tmem_wait_st();
+        if (!first) {
+#pragma unroll
+          for (int i = 0; i < (C::kOCols / NR) * (RG / 16); ++i) {
+            const int at = (i / (RG / 16)) * NR + r0 + 16 * (i % (RG / 16));
+            float o[16];
+            tmem_ld16(tO + lanes + at, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= row_alpha[r0 + 16 * (i % (RG / 16)) + e];
+            tmem_st16(tO + lanes + at, o);
+          }
+          tmem_wait_st();
+        }
         if (bi.live > 0) first = false;              // (a block whose page is bad sets nothing)
         group_any(bar_id, false);                    // `red` may change again
       }
@@ -1085,6 +1108,14 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         for (int i = 0; i < RG / 16; ++i) {
           float o[16];
           tmem_ld16(tO + lanes + r0 + 16 * i, o);
+          if (C::kStacked) {
+            float o1[16], o2[16];
+            tmem_ld16(tO + lanes + NR + r0 + 16 * i, o1);
+            tmem_ld16(tO + lanes + 2 * NR + r0 + 16 * i, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += o1[e] + o2[e];
+          }
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
