@@ -603,6 +603,7 @@ struct TcCfg {
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
+  static_assert(kPBufs * kPParts * kPPart >= kGroups * 16 * kDim * 4, "P's space holds the staged output rows");
   static_assert(kTotal - oInfo <= kSmall, "small area");
 };
 
@@ -671,6 +672,32 @@ __device__ __forceinline__ uint2 fp8_parts(const float (&x)[4], float f) {
   const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
   const uint32_t la = f32x2_to_e4m3x2(y0 - fa.x, y1 - fa.y), lb = f32x2_to_e4m3x2(y2 - fb.x, y3 - fb.y);
   return make_uint2(a | (b << 16), la | (lb << 16));
+}
+
+// Reduces N values per lane over the warp, all of them at once: each step halves
+// the values a lane keeps. Lane i ends with value i mod N (N = 16, 32) in v[0],
+// and value 32 + i in v[1] for N = 64.
+template <int N, bool kMax>
+__device__ __forceinline__ void warp_reduce_rows(float (&v)[N]) {
+  auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+  if (N == 16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = op(v[i], __shfl_xor_sync(kEvery, v[i], 16));
+  }
+  constexpr int kSets = N == 64 ? 2 : 1, kTop = N == 16 ? 8 : 16;
+#pragma unroll
+  for (int set = 0; set < kSets; ++set) {
+#pragma unroll
+    for (int o = kTop; o > 0; o >>= 1) {
+      const bool up = (threadIdx.x & o) != 0;
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const float a = v[32 * set + i], b = v[32 * set + i + o];
+        v[32 * set + i] = op(up ? b : a, __shfl_xor_sync(kEvery, up ? a : b, o));
+      }
+    }
+  }
+  if (N == 64) v[1] = v[32];
 }
 
 template <int kKv, int NR>
@@ -990,12 +1017,13 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       }
       if (group_any(bar_id, first || !ok || top > C::kOff + kSlack)) {
         // the block's maxima over all tokens; rows that rise by more than the slack get a new reference
+        {
+          float v[RG];
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          float v = x[r];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kEvery, v, o));
-          if (lane == 0) red[wl * NR + r0 + r] = v;
+          for (int r = 0; r < RG; ++r) v[r] = x[r];
+          warp_reduce_rows<RG, true>(v);
+          if (lane < RG) red[wl * NR + r0 + lane] = v[0];
+          if (RG == 64) red[wl * NR + r0 + 32 + lane] = v[1];
         }
         if (!first && n >= 1) ok = mbar_wait(p_free((n - 1) % C::kPBufs), ((n - 1) / C::kPBufs) & 1) && ok;   // O is complete
         if (group_any(bar_id, !ok)) { ok = false; break; }
@@ -1091,21 +1119,19 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (lane == 0) mbar_arrive(p_full(pb));
 
       if (bi.flags & 2) {
-        // the segment's output: this thread's dim of every row
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          float v = l[r];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kEvery, v, o);
-          if (lane == 0) red[wl * NR + r0 + r] = v;
-        }
+        // the segment's output: 16 rows at a time through shared memory (P's, which no MMA reads now), so that
+        // the stores are whole rows and the code is short
+        warp_reduce_rows<RG, false>(l);
+        if (lane < RG) red[wl * NR + r0 + lane] = l[0];
+        if (RG == 64) red[wl * NR + r0 + 32 + lane] = l[1];
         ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1);
         if (group_any(bar_id, !ok)) { ok = false; break; }
         tmem_fence_after();
         const bool whole = (bi.flags & 12) == 12;
         float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
-#pragma unroll
-        for (int i = 0; i < RG / 16; ++i) {
+        float* stg = reinterpret_cast<float*>(sm + C::oP + grp * (16 * kDim * 4));
+#pragma unroll 1
+        for (int i = 0; i < RG / 16 && r0 + 16 * i < p.R; ++i) {
           float o[16];
           tmem_ld16(tO + lanes + r0 + 16 * i, o);
           if (C::kStacked) {
@@ -1117,20 +1143,27 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
             for (int e = 0; e < 16; ++e) o[e] += o1[e] + o2[e];
           }
           tmem_wait_ld();
+          if (i > 0) group_any(bar_id, false);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 16; ++e) stg[e * kDim + t] = o[e];
+          group_any(bar_id, false);
+#pragma unroll 1
+          for (int e = wl; e < 16; e += 4) {
             const int r = r0 + 16 * i + e;
-            if (r >= p.R) continue;
+            if (r >= p.R) break;
             const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
             const float M = L > 0.f ? -row_ref[r] : -INFINITY;      // L and O are in units of 2^M
+            const float4 v = *reinterpret_cast<const float4*>(stg + e * kDim + 4 * lane);
             if (whole) {
               const float inv = L > 0.f ? p.v_global / L : 0.f;
-              const int64_t head = paged_head(p, bi.b, bi.g, r);
-              p.out[head * kDim + t] = static_cast<uint16_t>(pack_bf16x2(L > 0.f ? o[e] * inv : 0.f, 0.f) & 0xFFFF);
-              if (p.lse != nullptr && t == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
+              const int j = row_pos[r];
+              const int64_t head = (static_cast<int64_t>(bi.b) * p.Q + j) * p.H + bi.g * p.group + (r - j * p.group);
+              *reinterpret_cast<uint2*>(p.out + head * kDim + 4 * lane) =
+                  L > 0.f ? make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
+              if (p.lse != nullptr && lane == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
             } else {
-              part[r * kDim + t] = L > 0.f ? o[e] : 0.f;
-              if (t == 0) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = L; }
+              *reinterpret_cast<float4*>(part + r * kDim + 4 * lane) = L > 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+              if (lane == 0) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = L; }
             }
           }
         }
@@ -1218,20 +1251,30 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   const bool live = row < p.R;
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-    for (int i = sub; i < cut.n; i += wpr) {
-      const float* part = i == 0 ? paged_part(p, cta - 1, 1) : paged_part(p, cta - 1 + i, 0);
-      M = fmaxf(M, part[p.R * kDim + row]);
-    }
-    if (M != -INFINITY) {
-#pragma unroll 4
-      for (int i = sub; i < cut.n; i += wpr) {
-        const float* part = i == 0 ? paged_part(p, cta - 1, 1) : paged_part(p, cta - 1 + i, 0);
-        const float f = ex2_approx(part[p.R * kDim + row] - M);
-        const float4 x = *reinterpret_cast<const float4*>(part + row * kDim + 4 * lane);
-        L += f * part[p.R * (kDim + 1) + row];
-        acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-      }
+  auto part_of = [&](int i) { return i == 0 ? paged_part(p, cta - 1, 1) : paged_part(p, cta - 1 + i, 0); };
+  // 32 partials at a time: their maxima and sums by lane, then their rows
+  for (int base = sub; live && base < cut.n; base += 32 * wpr) {
+    const int mine = base + lane * wpr;
+    const float* part = part_of(mine < cut.n ? mine : 0);
+    const float m = mine < cut.n ? part[p.R * kDim + row] : -INFINITY;
+    const float l = mine < cut.n ? part[p.R * (kDim + 1) + row] : 0.f;
+    float top = fmaxf(M, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kEvery, top, o));
+    if (top == -INFINITY) continue;                  // every partial so far is empty
+    const float was = ex2_approx(M - top), f = ex2_approx(m - top);
+    float ls = f * l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(kEvery, ls, o);
+    M = top;
+    L = L * was + ls;
+    acc.x *= was; acc.y *= was; acc.z *= was; acc.w *= was;
+    const int count = (cut.n - base + wpr - 1) / wpr < 32 ? (cut.n - base + wpr - 1) / wpr : 32;
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(part_of(base + i * wpr) + row * kDim + 4 * lane);
+      const float fi = __shfl_sync(kEvery, f, i);
+      acc.x += fi * x.x; acc.y += fi * x.y; acc.z += fi * x.z; acc.w += fi * x.w;
     }
   }
   if (wpr > 1) {
