@@ -1176,52 +1176,70 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   } else if (items > 0 && C::kConv > 0) {
     // -------------------------------------------------- NVFP4 expansion --
+    // K runs one block ahead of V: a K tile is free as soon as its S is done, a V
+    // tile only after the softmax and P V.
     const int ct = threadIdx.x - 32 * C::kConv0;
-    int s = 0;
-    uint32_t ph = 0;
-    for (int n = 0; n < items; ++n) {
-      ok = mbar_wait(full(s), ph);
-      const int live = infos[n & (kInfos - 1)].live;
+    constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
+    // 32 values (two scale groups) per thread and turn; eight lanes take 4 rows x 2 runs, so that their
+    // 16-byte stores fall to different banks
+    const int row = ((ct >> 4) << 2) + ((ct >> 1) & 3), run = (ct & 1) + ((ct >> 3) & 1) * 2;
+    const uint32_t src = row * (kDim / 2) + 16 * run, ssrc = 2 * codes + row * (kDim / 16) + 2 * run;
+    uint32_t dst[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = 4 * run + k;
+      dst[k] = (c >> 3) * kHalfBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    }
+    auto expand = [&](int s, int n, int isv) {
       const uint8_t* st = sm + C::oStage + s * C::kStage;
-#pragma unroll 1
-      for (int isv = 0; isv < 2 && ok; ++isv) {
-        if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1);
-        if (!ok) break;
-        constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
-        uint8_t* tile = sm + C::oTiles + isv * 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
-        // 32 values (two scale groups) at a time; eight lanes take 4 rows x 2 runs, so that their 16-byte
-        // stores fall to different banks
+      uint8_t* tile = sm + C::oTiles + isv * 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
+      const int live = isv ? infos[n & (kInfos - 1)].live : kBlock;
+      uint4 w[2];
+      uint32_t sc[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int task = ct + 256 * i;
-          const int row = ((task >> 4) << 2) + ((task >> 1) & 3), run = (task & 1) + ((task >> 3) & 1) * 2;
-          const uint4 w = *reinterpret_cast<const uint4*>(st + isv * codes + row * (kDim / 2) + 16 * run);
-          const uint32_t sc = *reinterpret_cast<const uint16_t*>(st + 2 * codes + isv * scales + row * (kDim / 16) + 2 * run);
-          const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-          const bool dead = isv && row >= live;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h[4];
-            e2m1x8_to_f16x2x4(words[k], h);
-            const uint32_t b = (sc >> (8 * (k >> 1))) & 0xFF;
-            const uint32_t s2 = e4m3x2_to_f16x2(static_cast<uint16_t>(b | (b << 8)));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[j]), *reinterpret_cast<const __half2*>(&s2));
-              h[j] = dead ? 0u : *reinterpret_cast<const uint32_t*>(&y);
-            }
-            const int c = 4 * run + k;
-            *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalfBox + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
-        }
-        smem_to_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
+      for (int i = 0; i < 2; ++i) {
+        w[i] = *reinterpret_cast<const uint4*>(st + isv * codes + src + i * 64 * (kDim / 2));
+        sc[i] = *reinterpret_cast<const uint16_t*>(st + isv * scales + ssrc + i * 64 * (kDim / 16));
       }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(empty(s));
-      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (row + 64 * i >= live) { w[i] = make_uint4(0u, 0u, 0u, 0u); sc[i] = 0u; }
+        const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[i]));
+        const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
+        const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[4];
+          e2m1x8_to_f16x2x4(words[k], h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[j]), s2[k >> 1]);
+            h[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          *reinterpret_cast<uint4*>(tile + dst[k] + i * 64 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      smem_to_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
+    };
+    int sk = 0, sv = 0;
+    uint32_t ph = 0;
+    for (int n = -1; n < items; ++n) {
+      if (n + 1 < items) {
+        ok = mbar_wait(full(sk), ph);
+        if (n + 1 >= 2) ok = mbar_wait(k_free((n + 1) & 1), (((n + 1) >> 1) - 1) & 1) && ok;
+        if (!ok) break;
+        expand(sk, n + 1, 0);
+        if (++sk == C::kStages) { sk = 0; ph ^= 1u; }
+      }
+      if (n >= 0) {
+        if (n >= 2 && !mbar_wait(v_free(n & 1), ((n >> 1) - 1) & 1)) { ok = false; break; }
+        expand(sv, n, 1);
+        if (lane == 0) mbar_arrive(empty(sv));
+        if (++sv == C::kStages) sv = 0;
+      }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   }
