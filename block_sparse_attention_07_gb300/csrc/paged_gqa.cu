@@ -656,6 +656,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const float* r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
+// A wait of a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(kEvery, mbar_wait(bar, parity)) != 0;
+}
+
 // Barrier of a softmax group (128 threads) that returns whether any thread voted yes.
 __device__ __forceinline__ bool group_any(int id, bool vote) {
   uint32_t r;
@@ -841,7 +853,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     __syncwarp();
   } else if (items > 0 && warp == 1) {
     // ------------------------------------------------------------- MMAs --
-    if (lane == 0) {
+    // The whole warp runs the loop and one elected lane issues: the descriptors then stay in uniform registers
+    // (68 cycles per MMA from a lane's branch against 40 here, which is the operand's 4 KB at 128 bytes a cycle).
+    {
+      const bool lead = elect_one();
       constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0);
       constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
       constexpr int q_passes = C::kStacked ? 1 : C::kQParts, p_passes = C::kStacked ? 1 : C::kPParts;
@@ -849,16 +864,17 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       uint32_t s_ph = 0;
       int seg_q = -1;                               // segment whose queries S uses
       auto issue_s = [&](int n) -> bool {
-        if (kFp8 ? !mbar_wait(full(s_stage), s_ph) : !mbar_wait(k_full(n & 1), (n >> 1) & 1)) return false;
+        if (kFp8 ? !warp_wait(full(s_stage), s_ph) : !warp_wait(k_full(n & 1), (n >> 1) & 1)) return false;
         const int fl = infos[n & (kInfos - 1)].flags;
         if (fl & 1) {
           ++seg_q;
-          if (!mbar_wait(q_full(seg_q & 1), (seg_q >> 1) & 1)) return false;
+          if (!warp_wait(q_full(seg_q & 1), (seg_q >> 1) & 1)) return false;
         }
         tmem_fence_after();
         const uint32_t q = base + C::oQ + (seg_q & 1) * (C::kQParts * C::kQPart);
         const uint32_t d = tmem + (n & 1) * C::kSCols;
-        if (kFp8) {
+        if (!lead) {
+        } else if (kFp8) {
           const uint32_t k = base + C::oStage + s_stage * C::kStage;
 #pragma unroll
           for (int part = 0; part < q_passes; ++part)
@@ -874,20 +890,24 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
                           mat_desc(q + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024, kSwz128), id_s, kk > 0);
           mma_commit(k_free(n & 1));
         }
-        mma_commit(s_full(n & 1));
-        mbar_arrive(s_full(n & 1));
-        if (fl & 2) mma_commit(q_free(seg_q & 1));
+        if (lead) {
+          mma_commit(s_full(n & 1));
+          mbar_arrive(s_full(n & 1));
+          if (fl & 2) mma_commit(q_free(seg_q & 1));
+        }
+        __syncwarp();
         if (++s_stage == C::kStages) { s_stage = 0; s_ph ^= 1u; }
         return true;
       };
       auto issue_pv = [&](int n) -> bool {
         const int pb = n % C::kPBufs;
-        if (!mbar_wait(p_full(pb), (n / C::kPBufs) & 1)) return false;
-        if (!kFp8 && !mbar_wait(v_full(n & 1), (n >> 1) & 1)) return false;
+        if (!warp_wait(p_full(pb), (n / C::kPBufs) & 1)) return false;
+        if (!kFp8 && !warp_wait(v_full(n & 1), (n >> 1) & 1)) return false;
         const bool fresh = (infos[n & (kInfos - 1)].flags & 1) != 0;
         tmem_fence_after();
         const uint32_t pt = base + C::oP + pb * (C::kPParts * C::kPPart);
-        if (kFp8) {
+        if (!lead) {
+        } else if (kFp8) {
           const uint32_t v = base + C::oStage + v_stage * C::kStage + kBlock * kDim;
 #pragma unroll
           for (int part = 0; part < p_passes; ++part)
@@ -904,7 +924,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
                           mat_desc(pt + kk * 256, 128, 2048, kSwzNone), id_o, !(fresh && kk == 0));
           mma_commit(v_free(n & 1));
         }
-        mma_commit(p_free(pb));
+        if (lead) mma_commit(p_free(pb));
+        __syncwarp();
         if (++v_stage == C::kStages) v_stage = 0;
         return true;
       };
@@ -914,8 +935,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         ok = issue_pv(n);
         if (ok && n + 2 < items) ok = issue_s(n + 2);
       }
-      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
-      mma_commit(done_bar);                         // every MMA has finished before tensor memory is freed
+      if (!ok && lead) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+      if (lead) mma_commit(done_bar);               // every MMA has finished before tensor memory is freed
+      __syncwarp();
       mbar_wait(done_bar, 0);
     }
     __syncwarp();
