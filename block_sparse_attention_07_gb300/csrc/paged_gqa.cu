@@ -543,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   after a power-of-two scaling of its row (4 significant bits each, a bf16
 //   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
 //   parts of its f16 value (3 significant bits each, rounded at 2^-10 relative).
-//   NVFP4: eight warps expand each block (e2m1 x e4m3, exact in f16) into swizzled
-//   f16 tiles; Q is scaled into f16's range and P rounded to f16.
+//   NVFP4: eight warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
+//   memory, V into swizzled shared memory (its rows are tokens, and as A it is
+//   needed by dims). Q is scaled into f16's range and P rounded to f16.
 // Roles: warp 0 copies, warp 1 issues the MMAs, warps 2 and 3 bring the next row's
 // queries into shared memory, then 4 softmax warps per row group (a thread owns a
 // token of S and a dim of O), then the expanding warps. The softmax warps agree on
@@ -574,7 +575,7 @@ struct TcCfg {
   static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
   static constexpr uint32_t kPPart = NR * (kFp8 ? 128 : 256);
   static constexpr uint32_t kStage = raw_bytes<kKv>();
-  static constexpr uint32_t kTiles = kFp8 ? 0 : 8 * kHalfBox;  // K[2], V[2] in f16
+  static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
   static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPParts * kPPart;
   static constexpr uint32_t kSmall = 4096 + NR * 64;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
@@ -584,7 +585,8 @@ struct TcCfg {
   // other into the same columns where tensor memory is too small for that.
   static constexpr bool kStacked = kFp8 && NR <= 32;
   static constexpr int kSCols = kStacked ? kQParts * NR : NR, kOCols = kStacked ? kPParts * NR : NR;
-  static constexpr int kUsedCols = kTcS * kSCols + kOCols;
+  static constexpr int kKCols = kFp8 ? 0 : 2 * (kDim / 2);     // NVFP4: K[2] in f16, two dims per column
+  static constexpr int kUsedCols = kTcS * kSCols + kOCols + kKCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
   // shared memory
@@ -634,6 +636,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
 }
+// A from tensor memory (kind::f16).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -651,6 +658,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const float* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                ::"r"(a), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
                  "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+               "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+               ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                 "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                 "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -762,18 +778,16 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       mbar_init(q_full(i), 2);
       mbar_init(q_free(i), 1 + 4 * C::kGroups);                      // S is done with Q, softmax with its multipliers
       if (!kFp8) {
-        mbar_init(k_full(i), C::kConv);
+        mbar_init(k_full(i), C::kConv / 2);
         mbar_init(k_free(i), 1);
-        mbar_init(v_full(i), C::kConv);
+        mbar_init(v_full(i), C::kConv / 2);
         mbar_init(v_free(i), 1);
       }
     }
     mbar_init(done_bar, 1);
     fence_mbar_init();
-    if (kFp8) {
-      prefetch_tensormap(&tk);
-      prefetch_tensormap(&tv);
-    }
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(C::kCols)
@@ -785,7 +799,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
-  const uint32_t tO = tmem + kTcS * C::kSCols;
+  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kOCols;
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -838,8 +852,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           tma_load_2d(dst + kBlock * kDim, &tv, 0, static_cast<int>(slab * kBlock), full(s));
         } else {
           constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
-          bulk_g2s(dst, p.k + slab * codes, codes, full(s), policy);
-          bulk_g2s(dst + codes, p.v + slab * codes, codes, full(s), policy);
+          tma_load_2d(dst, &tk, 0, static_cast<int>(slab * kBlock), full(s));
+          tma_load_2d(dst + codes, &tv, 0, static_cast<int>(slab * kBlock), full(s));
           bulk_g2s(dst + 2 * codes, p.ks + slab * scales, scales, full(s), policy);
           bulk_g2s(dst + 2 * codes + scales, p.vs + slab * scales, scales, full(s), policy);
         }
@@ -883,11 +897,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
               mma_ss<true>(d, mat_desc(k + kk * 32, 16, 1024, kSwz128),
                            mat_desc(q + part * C::kQPart + kk * 32, 16, 1024, kSwz128), id_s, part + kk > 0);
         } else {
-          const uint32_t k = base + C::oTiles + (n & 1) * 2 * kHalfBox;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss<false>(d, mat_desc(k + (kk >> 2) * kHalfBox + (kk & 3) * 32, 16, 1024, kSwz128),
-                          mat_desc(q + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024, kSwz128), id_s, kk > 0);
+            mma_ts(d, tK + (n & 1) * (kDim / 2) + 8 * kk,
+                   mat_desc(q + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024, kSwz128), id_s, kk > 0);
           mma_commit(k_free(n & 1));
         }
         if (lead) {
@@ -917,7 +930,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
                            mat_desc(pt + part * C::kPPart + kk * 512, 128, 2048, kSwzNone), id_o, !(fresh && part + kk == 0));
           mma_commit(empty(v_stage));
         } else {
-          const uint32_t v = base + C::oTiles + 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
+          const uint32_t v = base + C::oTiles + (n & 1) * 2 * kHalfBox;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ss<false>(tO, mat_desc(v + kk * 2048, kHalfBox, 1024, kSwz128),
@@ -1198,70 +1211,75 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   } else if (items > 0 && C::kConv > 0) {
     // -------------------------------------------------- NVFP4 expansion --
-    // K runs one block ahead of V: a K tile is free as soon as its S is done, a V
-    // tile only after the softmax and P V.
-    const int ct = threadIdx.x - 32 * C::kConv0;
+    // Four warps expand K into tensor memory, four expand V into shared memory; a
+    // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of
+    // eight rows in eight banks, and so does the V tile's for the stores.
+    const bool isv = warp >= C::kConv0 + 4;
+    const int row = 32 * (warp & 3) + lane;
     constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
-    // 32 values (two scale groups) per thread and turn; eight lanes take 4 rows x 2 runs, so that their
-    // 16-byte stores fall to different banks
-    const int row = ((ct >> 4) << 2) + ((ct >> 1) & 3), run = (ct & 1) + ((ct >> 3) & 1) * 2;
-    const uint32_t src = row * (kDim / 2) + 16 * run, ssrc = 2 * codes + row * (kDim / 16) + 2 * run;
-    uint32_t dst[4];
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int n = 0; n < items; ++n) {
+      ok = mbar_wait(full(s), ph);
+      if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1) && ok;
+      ok = __all_sync(kEvery, ok);
+      if (!ok) break;
+      const uint8_t* st = sm + C::oStage + s * C::kStage + (isv ? codes : 0);
+      uint4 w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = 4 * run + k;
-      dst[k] = (c >> 3) * kHalfBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-    }
-    auto expand = [&](int s, int n, int isv) {
-      const uint8_t* st = sm + C::oStage + s * C::kStage;
-      uint8_t* tile = sm + C::oTiles + isv * 4 * kHalfBox + (n & 1) * 2 * kHalfBox;
-      const int live = isv ? infos[n & (kInfos - 1)].live : kBlock;
-      uint4 w[2];
-      uint32_t sc[2];
+      for (int c = 0; c < 4; ++c)
+        w[c] = *reinterpret_cast<const uint4*>(st + row * (kDim / 2) + ((c ^ ((row >> 1) & 3)) << 4));
+      uint2 sc = *reinterpret_cast<const uint2*>(sm + C::oStage + s * C::kStage + 2 * codes + (isv ? scales : 0) + row * (kDim / 16));
+      if (isv && row >= infos[n & (kInfos - 1)].live) {
+        // a row that was never written may hold NaN patterns, and 0 x NaN is NaN
+        sc = make_uint2(0u, 0u);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[i] = *reinterpret_cast<const uint4*>(st + isv * codes + src + i * 64 * (kDim / 2));
-        sc[i] = *reinterpret_cast<const uint16_t*>(st + isv * scales + ssrc + i * 64 * (kDim / 16));
+        for (int c = 0; c < 4; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+      if (!isv) tmem_fence_after();
+      uint8_t* tile = sm + C::oTiles + (n & 1) * 2 * kHalfBox + row * 128;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (row + 64 * i >= live) { w[i] = make_uint4(0u, 0u, 0u, 0u); sc[i] = 0u; }
-        const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[i]));
-        const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
-        const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+      for (int half = 0; half < 2; ++half) {
+        uint32_t h[32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h[4];
-          e2m1x8_to_f16x2x4(words[k], h);
+        for (int q = 0; q < 2; ++q) {
+          const int c = 2 * half + q;
+          const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>((half ? sc.y : sc.x) >> (16 * q)));
+          const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
+          const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[j]), s2[k >> 1]);
-            h[j] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t e[4];
+            e2m1x8_to_f16x2x4(words[k], e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&e[j]), s2[k >> 1]);
+              h[16 * q + 4 * k + j] = *reinterpret_cast<const uint32_t*>(&y);
+            }
           }
-          *reinterpret_cast<uint4*>(tile + dst[k] + i * 64 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (isv) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(tile + half * kHalfBox + ((c ^ (row & 7)) << 4)) =
+                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+        } else {
+          tmem_st32(tK + lanes + (n & 1) * (kDim / 2) + 32 * half, h);
         }
       }
-      smem_to_async();
+      if (isv) {
+        smem_to_async();
+      } else {
+        tmem_wait_st();
+        tmem_fence_before();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
-    };
-    int sk = 0, sv = 0;
-    uint32_t ph = 0;
-    for (int n = -1; n < items; ++n) {
-      if (n + 1 < items) {
-        ok = mbar_wait(full(sk), ph);
-        if (n + 1 >= 2) ok = mbar_wait(k_free((n + 1) & 1), (((n + 1) >> 1) - 1) & 1) && ok;
-        if (!ok) break;
-        expand(sk, n + 1, 0);
-        if (++sk == C::kStages) { sk = 0; ph ^= 1u; }
-      }
-      if (n >= 0) {
-        if (n >= 2 && !mbar_wait(v_free(n & 1), ((n >> 1) - 1) & 1)) { ok = false; break; }
-        expand(sv, n, 1);
-        if (lane == 0) mbar_arrive(empty(sv));
-        if (++sv == C::kStages) sv = 0;
-      }
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   }
@@ -1373,17 +1391,20 @@ static EncodeFn encode_fn() {
   return fn;
 }
 
-// 2-D map over a cache [P * G * 128 rows][128 dims]: boxes of 128 rows x 128 bytes, 128-byte swizzle.
-static cudaError_t cache_map(CUtensorMap* map, const void* base, int64_t rows, bool bf16) {
+// 2-D map over a cache's rows [P * G * 128][128 dims]: boxes of 128 rows x 128 bytes
+// (bf16: half a row) in the 128-byte swizzle, or NVFP4 codes, 128 rows x 64 bytes in
+// the 64-byte swizzle.
+static cudaError_t cache_map(CUtensorMap* map, const void* base, int64_t rows, msa_dtype_t kv) {
+  const bool bf16 = kv == MSA_BF16, fp4 = kv == MSA_NVFP4;
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kDim) * (bf16 ? 2 : 1)};
-  const cuuint32_t box[2] = {bf16 ? 64u : 128u, static_cast<cuuint32_t>(kBlock)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(fp4 ? kDim / 2 : kDim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(bf16 ? 2 * kDim : fp4 ? kDim / 2 : kDim)};
+  const cuuint32_t box[2] = {bf16 || fp4 ? 64u : 128u, static_cast<cuuint32_t>(kBlock)};
   const cuuint32_t ones[2] = {1, 1};
   const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                         const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        fp4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1394,11 +1415,9 @@ static cudaError_t launch_tc(const PagedParams& p, int ctas, cudaStream_t stream
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
   cudaError_t err;
-  if (C::kFp8) {
-    const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
-    if ((err = cache_map(&tk, p.k, rows, false)) != cudaSuccess) return err;
-    if ((err = cache_map(&tv, p.v, rows, false)) != cudaSuccess) return err;
-  }
+  const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
+  if ((err = cache_map(&tk, p.k, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
+  if ((err = cache_map(&tv, p.v, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
   constexpr size_t smem = C::kTotal + 1024;
   err = cudaFuncSetAttribute(paged_gqa_tc_kernel<kKv, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
