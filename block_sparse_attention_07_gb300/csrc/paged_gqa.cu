@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   NVFP4: eight warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
 //   memory, V into swizzled shared memory (its rows are tokens, and as A it is
 //   needed by dims). Q is scaled into f16's range and P rounded to f16.
-// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2 and 3 bring the next row's
-// queries into shared memory, then 4 softmax warps per row group (a thread owns a
+// Roles: warp 0 copies, warps 1 and 2 issue the MMAs of S and of P V, warp 3 brings
+// the next row's queries into shared memory, then 4 softmax warps per row group (a thread owns a
 // token of S and a dim of O), then the expanding warps. The softmax warps agree on
 // a rescale with one barrier-with-vote per block; a row's reference is raised only
 // when a logit exceeds it by 2^8, so that after a row's first block they hardly
@@ -601,7 +601,7 @@ struct TcCfg {
   static constexpr uint32_t oRed = oAlpha + NR * 4;                      // [4][NR]
   static constexpr uint32_t oPos = oRed + 4 * NR * 4;                    // [NR] position of a row
   static constexpr uint32_t oBars = oPos + NR * 4;
-  static constexpr int kBars = 2 * kStages + kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 1;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
@@ -609,15 +609,20 @@ struct TcCfg {
   static_assert(kTotal - oInfo <= kSmall, "small area");
 };
 
-// Shared-memory matrix descriptors (leading and stride byte offsets in 16-byte
-// units, descriptor version 1). Swizzled 128 B: as the tensor maps write. Plain:
-// core matrices of 8 rows of 16 bytes.
-__device__ __forceinline__ uint64_t mat_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(swizzle) << 61);
-}
+// Shared-memory matrix descriptors: start address and leading and stride byte
+// offsets in 16-byte units, descriptor version 1, swizzle. Swizzled 128 B: as the
+// tensor maps write. Plain: core matrices of 8 rows of 16 bytes.
 constexpr uint32_t kSwz128 = 2, kSwzNone = 0;
+// The descriptor's upper half, and its lower half at `saddr`: within one operand
+// only the address changes, by plain additions to the lower half.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
+  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  // one lane's value for the whole warp, so that it is kept in a uniform register
+  return __shfl_sync(kEvery, (saddr >> 4) | ((lbo >> 4) << 16), 0);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
 
 // Instruction descriptor: fp32 accumulator, operand types, majorness (0 K, 1 MN), N / 8, M / 16.
 __host__ __device__ constexpr uint32_t mma_idesc(int a_type, int b_type, int N, int a_mn, int b_mn) {
@@ -753,7 +758,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   auto s_full = [&](int i) { return bars + 8u * (b0 + i); };                       // S of a block is there
   auto p_full = [&](int i) { return bars + 8u * (b0 + kTcS + i); };                // P is written
   auto p_free = [&](int i) { return bars + 8u * (b0 + kTcS + C::kPBufs + i); };    // P V is done
-  constexpr int b1 = b0 + kTcS + 2 * C::kPBufs;
+  auto s_free = [&](int i) { return bars + 8u * (b0 + kTcS + 2 * C::kPBufs + i); }; // S is in the softmax warps' registers
+  constexpr int b1 = b0 + 2 * kTcS + 2 * C::kPBufs;
   auto q_full = [&](int i) { return bars + 8u * (b1 + i); };
   auto q_free = [&](int i) { return bars + 8u * (b1 + 2 + i); };
   auto k_full = [&](int i) { return bars + 8u * (b1 + 4 + i); };                   // NVFP4: f16 tiles
@@ -769,13 +775,16 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       mbar_init(full(s), 1);
       mbar_init(empty(s), kFp8 ? 1 : C::kConv);
     }
-    for (int i = 0; i < kTcS; ++i) mbar_init(s_full(i), 2);          // the commit, and the issuing thread's own arrival
+    for (int i = 0; i < kTcS; ++i) {
+      mbar_init(s_full(i), 2);                                        // the commit, and the issuing thread's own arrival
+      mbar_init(s_free(i), 4 * C::kGroups);
+    }
     for (int i = 0; i < C::kPBufs; ++i) {
       mbar_init(p_full(i), 4 * C::kGroups);
       mbar_init(p_free(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full(i), 2);
+      mbar_init(q_full(i), 1);
       mbar_init(q_free(i), 1 + 4 * C::kGroups);                      // S is done with Q, softmax with its multipliers
       if (!kFp8) {
         mbar_init(k_full(i), C::kConv / 2);
@@ -784,7 +793,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         mbar_init(v_free(i), 1);
       }
     }
-    mbar_init(done_bar, 1);
+    mbar_init(done_bar, 2);
     fence_mbar_init();
     prefetch_tensormap(&tk);
     prefetch_tensormap(&tv);
@@ -865,94 +874,92 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     }
     __syncwarp();
-  } else if (items > 0 && warp == 1) {
+  } else if (items > 0 && warp <= 2) {
     // ------------------------------------------------------------- MMAs --
-    // The whole warp runs the loop and one elected lane issues: the descriptors then stay in uniform registers
-    // (68 cycles per MMA from a lane's branch against 40 here, which is the operand's 4 KB at 128 bytes a cycle).
-    {
-      const bool lead = elect_one();
-      constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0);
-      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
-      constexpr int q_passes = C::kStacked ? 1 : C::kQParts, p_passes = C::kStacked ? 1 : C::kPParts;
-      int s_stage = 0, v_stage = 0;
-      uint32_t s_ph = 0;
-      int seg_q = -1;                               // segment whose queries S uses
-      auto issue_s = [&](int n) -> bool {
-        if (kFp8 ? !warp_wait(full(s_stage), s_ph) : !warp_wait(k_full(n & 1), (n >> 1) & 1)) return false;
+    // S and P V are issued by a warp each, so that one's waits do not hold up the other. The whole warp runs the
+    // loop and one elected lane issues, with descriptors in uniform registers: 40 cycles per MMA, which is A's
+    // 4 KB at 128 bytes a cycle (10 from tensor memory), against 68 from a lane's branch.
+    const bool lead = elect_one();
+    if (warp == 1) {
+      constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0), hi = desc_hi(1024, kSwz128);
+      constexpr int q_passes = C::kStacked ? 1 : C::kQParts;
+      const uint32_t q0 = desc_lo(base + C::oQ, 16), k0 = desc_lo(base + C::oStage, 16);
+      int stage = 0, seg = -1;
+      uint32_t ph = 0;
+      for (int n = 0; n < items; ++n) {
+        ok = kFp8 ? warp_wait(full(stage), ph) : warp_wait(k_full(n & 1), (n >> 1) & 1);
+        if (n >= kTcS) ok = ok && warp_wait(s_free(n & 1), ((n >> 1) - 1) & 1);
+        if (!ok) break;
         const int fl = infos[n & (kInfos - 1)].flags;
         if (fl & 1) {
-          ++seg_q;
-          if (!warp_wait(q_full(seg_q & 1), (seg_q >> 1) & 1)) return false;
+          ++seg;
+          if (!warp_wait(q_full(seg & 1), (seg >> 1) & 1)) { ok = false; break; }
         }
         tmem_fence_after();
-        const uint32_t q = base + C::oQ + (seg_q & 1) * (C::kQParts * C::kQPart);
-        const uint32_t d = tmem + (n & 1) * C::kSCols;
-        if (!lead) {
-        } else if (kFp8) {
-          const uint32_t k = base + C::oStage + s_stage * C::kStage;
-#pragma unroll
-          for (int part = 0; part < q_passes; ++part)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss<true>(d, mat_desc(k + kk * 32, 16, 1024, kSwz128),
-                           mat_desc(q + part * C::kQPart + kk * 32, 16, 1024, kSwz128), id_s, part + kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(d, tK + (n & 1) * (kDim / 2) + 8 * kk,
-                   mat_desc(q + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024, kSwz128), id_s, kk > 0);
-          mma_commit(k_free(n & 1));
-        }
         if (lead) {
+          const uint32_t q = q0 + (seg & 1) * (C::kQParts * C::kQPart >> 4);
+          const uint32_t d = tmem + (n & 1) * C::kSCols;
+          if (kFp8) {
+            const uint32_t k = k0 + stage * (C::kStage >> 4);
+#pragma unroll
+            for (int part = 0; part < q_passes; ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss<true>(d, desc_of(k + kk * 2, hi), desc_of(q + (part * C::kQPart >> 4) + kk * 2, hi), id_s, part + kk > 0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(d, tK + (n & 1) * (kDim / 2) + 8 * kk, desc_of(q + (kk >> 2) * (NR * 128 >> 4) + (kk & 3) * 2, hi), id_s, kk > 0);
+            mma_commit(k_free(n & 1));
+          }
           mma_commit(s_full(n & 1));
           mbar_arrive(s_full(n & 1));
-          if (fl & 2) mma_commit(q_free(seg_q & 1));
+          if (fl & 2) mma_commit(q_free(seg & 1));
         }
         __syncwarp();
-        if (++s_stage == C::kStages) { s_stage = 0; s_ph ^= 1u; }
-        return true;
-      };
-      auto issue_pv = [&](int n) -> bool {
+        if (++stage == C::kStages) { stage = 0; ph ^= 1u; }
+      }
+    } else {
+      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
+      constexpr uint32_t hi_v = desc_hi(1024, kSwz128), hi_p = desc_hi(2048, kSwzNone);
+      constexpr int p_passes = C::kStacked ? 1 : C::kPParts;
+      const uint32_t p0 = desc_lo(base + C::oP, 128);
+      const uint32_t v0 = kFp8 ? desc_lo(base + C::oStage + kBlock * kDim, 16384) : desc_lo(base + C::oTiles, kHalfBox);
+      int stage = 0;
+      for (int n = 0; n < items; ++n) {
         const int pb = n % C::kPBufs;
-        if (!warp_wait(p_full(pb), (n / C::kPBufs) & 1)) return false;
-        if (!kFp8 && !warp_wait(v_full(n & 1), (n >> 1) & 1)) return false;
+        ok = (kFp8 || warp_wait(v_full(n & 1), (n >> 1) & 1)) && warp_wait(p_full(pb), (n / C::kPBufs) & 1);
+        if (!ok) break;
         const bool fresh = (infos[n & (kInfos - 1)].flags & 1) != 0;
         tmem_fence_after();
-        const uint32_t pt = base + C::oP + pb * (C::kPParts * C::kPPart);
-        if (!lead) {
-        } else if (kFp8) {
-          const uint32_t v = base + C::oStage + v_stage * C::kStage + kBlock * kDim;
+        if (lead) {
+          const uint32_t pt = p0 + pb * (C::kPParts * C::kPPart >> 4);
+          if (kFp8) {
+            const uint32_t v = v0 + stage * (C::kStage >> 4);
 #pragma unroll
-          for (int part = 0; part < p_passes; ++part)
+            for (int part = 0; part < p_passes; ++part)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss<true>(tO, mat_desc(v + kk * 4096, 16384, 1024, kSwz128),
-                           mat_desc(pt + part * C::kPPart + kk * 512, 128, 2048, kSwzNone), id_o, !(fresh && part + kk == 0));
-          mma_commit(empty(v_stage));
-        } else {
-          const uint32_t v = base + C::oTiles + (n & 1) * 2 * kHalfBox;
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss<true>(tO, desc_of(v + kk * 256, hi_v), desc_of(pt + (part * C::kPPart >> 4) + kk * 32, hi_p), id_o,
+                             !(fresh && part + kk == 0));
+            mma_commit(empty(stage));
+          } else {
+            const uint32_t v = v0 + (n & 1) * (2 * kHalfBox >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss<false>(tO, mat_desc(v + kk * 2048, kHalfBox, 1024, kSwz128),
-                          mat_desc(pt + kk * 256, 128, 2048, kSwzNone), id_o, !(fresh && kk == 0));
-          mma_commit(v_free(n & 1));
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ss<false>(tO, desc_of(v + kk * 128, hi_v), desc_of(pt + kk * 16, hi_p), id_o, !(fresh && kk == 0));
+            mma_commit(v_free(n & 1));
+          }
+          mma_commit(p_free(pb));
         }
-        if (lead) mma_commit(p_free(pb));
         __syncwarp();
-        if (++v_stage == C::kStages) v_stage = 0;
-        return true;
-      };
-      ok = issue_s(0);
-      if (ok && items > 1) ok = issue_s(1);
-      for (int n = 0; n < items && ok; ++n) {
-        ok = issue_pv(n);
-        if (ok && n + 2 < items) ok = issue_s(n + 2);
+        if (++stage == C::kStages) stage = 0;
       }
-      if (!ok && lead) set_flag(p.flags, MSA_FLAG_TIMEOUT);
-      if (lead) mma_commit(done_bar);               // every MMA has finished before tensor memory is freed
-      __syncwarp();
-      mbar_wait(done_bar, 0);
     }
+    if (!ok && lead) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    if (lead) mma_commit(done_bar);                 // every MMA has finished before tensor memory is freed
+    __syncwarp();
+    mbar_wait(done_bar, 0);
     __syncwarp();
   } else if (items > 0 && warp < C::kSoft0) {
     // ---------------------------------------------------------- queries --
@@ -962,17 +969,17 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       const int qb = seg & 1;
       if (seg >= 2 && !mbar_wait(q_free(qb), ((seg >> 1) - 1) & 1)) { ok = false; break; }
       uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
-      for (int rb = warp - 2; rb < NR; rb += 16) {
-        // eight rows at a time, all loads before the first use
-        uint2 v[8];
+      for (int rb = 0; rb < NR; rb += 16) {
+        // sixteen rows at a time, all loads before the first use
+        uint2 v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = rb + 2 * i;
+        for (int i = 0; i < 16; ++i) {
+          const int r = rb + i;
           v[i] = r < p.R ? *reinterpret_cast<const uint2*>(p.q + paged_head(p, w.b, w.g, r) * kDim + 4 * lane) : make_uint2(0u, 0u);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = rb + 2 * i;
+        for (int i = 0; i < 16; ++i) {
+          const int r = rb + i;
           const float x[4] = {bf16_bits_to_f32(v[i].x & 0xFFFF), bf16_bits_to_f32(v[i].x >> 16),
                               bf16_bits_to_f32(v[i].y & 0xFFFF), bf16_bits_to_f32(v[i].y >> 16)};
           // the largest magnitude: for values without sign, the order of the bits is the order of the values
@@ -1036,6 +1043,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         for (int r = 0; r < RG; ++r) x[r] += lo[r];
       }
       tmem_wait_ld();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free(sb));
       const bool edge = bi.lim0 < kBlock - 1;
       float top = -INFINITY;
 #pragma unroll
