@@ -559,14 +559,21 @@ constexpr int kInfos = 16;              // ring of block descriptions, longer th
 
 struct BlockInfo {
   int live, lim0;                       // cached tokens of the block; last token of position 0, both from its start
-  int b, g, flags, pad0, pad1, pad2;    // 1 first of a segment, 2 last, 4 starts its row, 8 ends its row
+  int b, g, seg;                        // row; the CTA's segment (its run of one row's blocks)
+  int idx, left;                        // blocks of the segment before and after this one, held to 2
+  int flags;                            // 4: the segment starts its row, 8: it ends it
 };
 
 template <int kKv, int NR>
 struct TcCfg {
   static constexpr bool kFp8 = kKv == MSA_FP8_E4M3;
-  static constexpr int kGroups = NR > 32 ? 2 : 1;
-  static constexpr int kRG = NR / kGroups;                     // rows per softmax group
+  // Two softmax groups. Few rows: a group takes every second block, with its own
+  // references, sums and O, joined at the segment's end (a block's chain of waits,
+  // exchange and stores is longer than its arithmetic). Many: half the rows of every block.
+  static constexpr bool kAlt = NR <= 32;
+  static constexpr int kGroups = 2;
+  static constexpr int kRG = kAlt ? NR : NR / 2;               // rows per softmax group
+  static constexpr int kSoftArrive = kAlt ? 4 : 8;             // softmax warps per block
   static constexpr int kConv = kFp8 ? 0 : 8;                   // expanding warps
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kWarpsAll = kConv0 + kConv;
@@ -574,10 +581,12 @@ struct TcCfg {
   static constexpr int kPBufs = NR > 64 ? 1 : 2;
   static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
   static constexpr uint32_t kPPart = NR * (kFp8 ? 128 : 256);
+  // One P buffer; it also stages 16 output rows per group, in the space of the group's own rows
+  static constexpr uint32_t kPBuf = kPParts * kPPart < 16 * kDim * 4 ? 16 * kDim * 4 : kPParts * kPPart;
   static constexpr uint32_t kStage = raw_bytes<kKv>();
   static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
-  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPParts * kPPart;
-  static constexpr uint32_t kSmall = 4096 + NR * 64;
+  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf;
+  static constexpr uint32_t kSmall = 2048 + NR * 64;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   // The parts of Q and P side by side as columns of one MMA (fewer, wider MMAs;
@@ -586,7 +595,8 @@ struct TcCfg {
   static constexpr bool kStacked = kFp8 && NR <= 32;
   static constexpr int kSCols = kStacked ? kQParts * NR : NR, kOCols = kStacked ? kPParts * NR : NR;
   static constexpr int kKCols = kFp8 ? 0 : 2 * (kDim / 2);     // NVFP4: K[2] in f16, two dims per column
-  static constexpr int kUsedCols = kTcS * kSCols + kOCols + kKCols;
+  static constexpr int kOBufs = kAlt ? 2 : 1;
+  static constexpr int kUsedCols = kTcS * kSCols + kOBufs * kOCols + kKCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
   // shared memory
@@ -594,18 +604,20 @@ struct TcCfg {
   static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
   static constexpr uint32_t oQ = oTiles + kTiles;
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
-  static constexpr uint32_t oInfo = oP + kPBufs * kPParts * kPPart;
+  static constexpr uint32_t oInfo = oP + kPBufs * kPBuf;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
-  static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [NR] kOff - reference
-  static constexpr uint32_t oAlpha = oRef + NR * 4;                      // [NR]
-  static constexpr uint32_t oRed = oAlpha + NR * 4;                      // [4][NR]
-  static constexpr uint32_t oPos = oRed + 4 * NR * 4;                    // [NR] position of a row
+  static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [2][NR] kOff - reference
+  static constexpr uint32_t oAlpha = oRef + 2 * NR * 4;                  // [2][NR]
+  static constexpr uint32_t oRed = oAlpha + 2 * NR * 4;                  // [2][4][NR]
+  static constexpr uint32_t oPos = oRed + 8 * NR * 4;                    // [NR] position of a row
   static constexpr uint32_t oBars = oPos + NR * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 3;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
-  static_assert(kPBufs * kPParts * kPPart >= kGroups * 16 * kDim * 4, "P's space holds the staged output rows");
+  // rows of staged output that fit a group's rows of one part of P
+  static constexpr int kStgRows = kAlt ? 16 : kRG / 4;
+  static_assert(kAlt || kStgRows * kPParts >= 16, "P's space holds the staged output rows");
   static_assert(kTotal - oInfo <= kSmall, "small area");
 };
 
@@ -749,7 +761,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   float* row_mul = reinterpret_cast<float*>(sm + C::oRow);
   float* row_ref = reinterpret_cast<float*>(sm + C::oRef);
   float* row_alpha = reinterpret_cast<float*>(sm + C::oAlpha);
-  float* red = reinterpret_cast<float*>(sm + C::oRed);
+  float* row_red = reinterpret_cast<float*>(sm + C::oRed);
   int* row_pos = reinterpret_cast<int*>(sm + C::oPos);
   const uint32_t bars = base + C::oBars;
   auto full = [&](int s) { return bars + 8u * s; };
@@ -766,6 +778,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   auto k_free = [&](int i) { return bars + 8u * (b1 + 6 + i); };
   auto v_full = [&](int i) { return bars + 8u * (b1 + 8 + i); };
   auto v_free = [&](int i) { return bars + 8u * (b1 + 10 + i); };
+  const uint32_t join_full = bars + 8u * (C::kBars - 3), join_free = bars + 8u * (C::kBars - 2);   // the groups' states
   const uint32_t done_bar = bars + 8u * (C::kBars - 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -777,15 +790,15 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     }
     for (int i = 0; i < kTcS; ++i) {
       mbar_init(s_full(i), 2);                                        // the commit, and the issuing thread's own arrival
-      mbar_init(s_free(i), 4 * C::kGroups);
+      mbar_init(s_free(i), C::kSoftArrive);
     }
     for (int i = 0; i < C::kPBufs; ++i) {
-      mbar_init(p_full(i), 4 * C::kGroups);
+      mbar_init(p_full(i), C::kSoftArrive);
       mbar_init(p_free(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), 1);
-      mbar_init(q_free(i), 1 + 4 * C::kGroups);                      // S is done with Q, softmax with its multipliers
+      mbar_init(q_free(i), 1 + C::kSoftArrive);                       // S is done with Q, softmax with its multipliers
       if (!kFp8) {
         mbar_init(k_full(i), C::kConv / 2);
         mbar_init(k_free(i), 1);
@@ -793,6 +806,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         mbar_init(v_free(i), 1);
       }
     }
+    mbar_init(join_full, 4);
+    mbar_init(join_free, 4);
     mbar_init(done_bar, 2);
     fence_mbar_init();
     prefetch_tensormap(&tk);
@@ -808,7 +823,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
-  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kOCols;
+  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kOBufs * C::kOCols;
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -833,7 +848,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       const uint64_t policy = l2_evict_first_policy();
       int s = 0;
       uint32_t ph = 0;
-      bool first = true, from_start = cur.blk == 0;
+      bool from_start = cur.blk == 0;
+      int seg = 0, idx = 0;
       for (int n = 0; n < items && ok; ++n) {
         const int pg = page[0];
 #pragma unroll
@@ -843,16 +859,23 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           far.next(p);
         }
         if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
-        const bool ends = cur.blk == cur.nb - 1;
         BlockInfo& bi = infos[n & (kInfos - 1)];
-        const int left = cur.L - cur.blk * kBlock;
-        bi.live = pg < 0 ? 0 : left < kBlock ? left : kBlock;
-        bi.lim0 = pg < 0 ? -kBlock : left - p.Q;
+        const int toks = cur.L - cur.blk * kBlock;
+        bi.live = pg < 0 ? 0 : toks < kBlock ? toks : kBlock;
+        bi.lim0 = pg < 0 ? -kBlock : toks - p.Q;
         bi.b = cur.b;
         bi.g = cur.g;
-        bi.flags = (first ? 1 : 0) | (ends || n + 1 == items ? 2 : 0) | (from_start ? 4 : 0) | (ends ? 8 : 0);
-        first = ends;
-        from_start = from_start || ends;             // only the CTA's first segment may start inside a row
+        const int row_left = cur.nb - 1 - cur.blk, left_here = row_left < items - 1 - n ? row_left : items - 1 - n;
+        bi.seg = seg;
+        bi.idx = idx < 2 ? idx : 2;
+        bi.left = left_here < 2 ? left_here : 2;
+        bi.flags = (from_start ? 4 : 0) | (row_left == left_here ? 8 : 0);
+        ++idx;
+        if (left_here == 0) {
+          ++seg;
+          idx = 0;
+          from_start = true;                         // only the CTA's first segment may start inside a row
+        }
         const int64_t slab = static_cast<int64_t>(pg < 0 ? 0 : pg) * p.G + cur.g;     // a bad page's place is taken by page 0
         const uint32_t dst = base + C::oStage + s * C::kStage;
         mbar_arrive_expect_tx(full(s), C::kStage);
@@ -884,17 +907,14 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0), hi = desc_hi(1024, kSwz128);
       constexpr int q_passes = C::kStacked ? 1 : C::kQParts;
       const uint32_t q0 = desc_lo(base + C::oQ, 16), k0 = desc_lo(base + C::oStage, 16);
-      int stage = 0, seg = -1;
+      int stage = 0;
       uint32_t ph = 0;
       for (int n = 0; n < items; ++n) {
         ok = kFp8 ? warp_wait(full(stage), ph) : warp_wait(k_full(n & 1), (n >> 1) & 1);
         if (n >= kTcS) ok = ok && warp_wait(s_free(n & 1), ((n >> 1) - 1) & 1);
         if (!ok) break;
-        const int fl = infos[n & (kInfos - 1)].flags;
-        if (fl & 1) {
-          ++seg;
-          if (!warp_wait(q_full(seg & 1), (seg >> 1) & 1)) { ok = false; break; }
-        }
+        const int seg = infos[n & (kInfos - 1)].seg, left = infos[n & (kInfos - 1)].left;
+        if (infos[n & (kInfos - 1)].idx == 0 && !warp_wait(q_full(seg & 1), (seg >> 1) & 1)) { ok = false; break; }
         tmem_fence_after();
         if (lead) {
           const uint32_t q = q0 + (seg & 1) * (C::kQParts * C::kQPart >> 4);
@@ -914,7 +934,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           }
           mma_commit(s_full(n & 1));
           mbar_arrive(s_full(n & 1));
-          if (fl & 2) mma_commit(q_free(seg & 1));
+          if (left == 0) mma_commit(q_free(seg & 1));
         }
         __syncwarp();
         if (++stage == C::kStages) { stage = 0; ph ^= 1u; }
@@ -930,24 +950,25 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         const int pb = n % C::kPBufs;
         ok = (kFp8 || warp_wait(v_full(n & 1), (n >> 1) & 1)) && warp_wait(p_full(pb), (n / C::kPBufs) & 1);
         if (!ok) break;
-        const bool fresh = (infos[n & (kInfos - 1)].flags & 1) != 0;
+        const bool fresh = infos[n & (kInfos - 1)].idx < C::kOBufs;
+        const uint32_t d = tO + (n & (C::kOBufs - 1)) * C::kOCols;
         tmem_fence_after();
         if (lead) {
-          const uint32_t pt = p0 + pb * (C::kPParts * C::kPPart >> 4);
+          const uint32_t pt = p0 + pb * (C::kPBuf >> 4);
           if (kFp8) {
             const uint32_t v = v0 + stage * (C::kStage >> 4);
 #pragma unroll
             for (int part = 0; part < p_passes; ++part)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_ss<true>(tO, desc_of(v + kk * 256, hi_v), desc_of(pt + (part * C::kPPart >> 4) + kk * 32, hi_p), id_o,
+                mma_ss<true>(d, desc_of(v + kk * 256, hi_v), desc_of(pt + (part * C::kPPart >> 4) + kk * 32, hi_p), id_o,
                              !(fresh && part + kk == 0));
             mma_commit(empty(stage));
           } else {
             const uint32_t v = v0 + (n & 1) * (2 * kHalfBox >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ss<false>(tO, desc_of(v + kk * 128, hi_v), desc_of(pt + kk * 16, hi_p), id_o, !(fresh && kk == 0));
+              mma_ss<false>(d, desc_of(v + kk * 128, hi_v), desc_of(pt + kk * 16, hi_p), id_o, !(fresh && kk == 0));
             mma_commit(v_free(n & 1));
           }
           mma_commit(p_free(pb));
@@ -1013,23 +1034,30 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     constexpr int RG = C::kRG;
     const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
     const int t = 32 * wl + lane;                   // token of S, dim of O
-    const int r0 = grp * RG;
+    const int r0 = C::kAlt ? 0 : grp * RG;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
+    const uint32_t tOg = tO + (C::kAlt ? grp * C::kOCols : 0) + lanes;
+    constexpr int kStep = C::kAlt ? 2 : 1;
+    float* ref = row_ref + (C::kAlt ? grp * NR : 0);
+    float* alphas = row_alpha + (C::kAlt ? grp * NR : 0);
+    float* red = row_red + (C::kAlt ? grp * 4 * NR : 0);
     float l[RG];
-    int stage = 0, seg = -1;
+    int stage = C::kAlt ? grp : 0, joins = 0;
     bool first = false;                             // no block of the segment has set the references yet
-    for (int n = 0; n < items; ++n) {
+    bool must_wait = false;                         // the other group still reads this one's last O
+    for (int n = C::kAlt ? grp : 0; n < items; n += kStep) {
       const int sb = n & 1, pb = n % C::kPBufs;
       ok = mbar_wait(s_full(sb), (n >> 1) & 1);
       if (n >= C::kPBufs) ok = mbar_wait(p_free(pb), ((n / C::kPBufs) - 1) & 1) && ok;
       const BlockInfo bi = infos[n & (kInfos - 1)];
-      if (bi.flags & 1) {
-        ++seg;
+      if (bi.idx < kStep) {
         first = true;
 #pragma unroll
         for (int r = 0; r < RG; ++r) l[r] = 0.f;
+        if (must_wait) ok = mbar_wait(join_free, (joins - 1) & 1) && ok;
+        must_wait = false;
       }
-      const float* mul = row_mul + (seg & 1) * NR + r0;
+      const float* mul = row_mul + (bi.seg & 1) * NR + r0;
       float x[RG];
       tmem_fence_after();
 #pragma unroll
@@ -1051,7 +1079,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
 #pragma unroll
       for (int r = 0; r < RG; r += 4) {
         const float4 m4 = *reinterpret_cast<const float4*>(mul + r);
-        const float4 f4 = *reinterpret_cast<const float4*>(row_ref + r0 + r);
+        const float4 f4 = *reinterpret_cast<const float4*>(ref + r0 + r);
         const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -1070,23 +1098,24 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           if (lane < RG) red[wl * NR + r0 + lane] = v[0];
           if (RG == 64) red[wl * NR + r0 + 32 + lane] = v[1];
         }
-        if (!first && n >= 1) ok = mbar_wait(p_free((n - 1) % C::kPBufs), ((n - 1) / C::kPBufs) & 1) && ok;   // O is complete
+        if (!first && C::kPBufs != kStep)            // O is complete
+          ok = mbar_wait(p_free((n - 1) % C::kPBufs), ((n - 1) / C::kPBufs) & 1) && ok;
         if (group_any(bar_id, !ok)) { ok = false; break; }
         if (t < RG) {
-          // x = s - reference + kOff, s itself in a first block; row_ref holds kOff - reference. A row that its
+          // x = s - reference + kOff, s itself in a first block; ref holds kOff - reference. A row that its
           // first block masks is masked by every later one: its reference stays -inf and its x with it
           const int r = r0 + t;
           const float v = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
           float alpha = 1.f, delta = 0.f;
           if (first) {
             delta = v == -INFINITY ? -INFINITY : C::kOff - v;
-            row_ref[r] = delta;
+            ref[r] = delta;
           } else if (v > C::kOff + kSlack) {
             delta = C::kOff - v;
             alpha = ex2_approx(delta);
-            row_ref[r] += delta;
+            ref[r] += delta;
           }
-          row_alpha[r] = alpha;
+          alphas[r] = alpha;
           red[r] = delta;                            // (no other thread reads this row's maxima)
         }
         group_any(bar_id, false);
@@ -1094,18 +1123,18 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
           x[r] += red[r0 + r];
-          l[r] *= row_alpha[r0 + r];
+          l[r] *= alphas[r0 + r];
         }
         if (!first) {
 #pragma unroll
           for (int i = 0; i < (C::kOCols / NR) * (RG / 16); ++i) {
             const int at = (i / (RG / 16)) * NR + r0 + 16 * (i % (RG / 16));
             float o[16];
-            tmem_ld16(tO + lanes + at, o);
+            tmem_ld16(tOg + at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= row_alpha[r0 + 16 * (i % (RG / 16)) + e];
-            tmem_st16(tO + lanes + at, o);
+            for (int e = 0; e < 16; ++e) o[e] *= alphas[r0 + 16 * (i % (RG / 16)) + e];
+            tmem_st16(tOg + at, o);
           }
           tmem_wait_st();
         }
@@ -1113,7 +1142,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         group_any(bar_id, false);                    // `red` may change again
       }
       // probabilities
-      const uint32_t pt = C::oP + pb * (C::kPParts * C::kPPart) + (t >> 3) * 128 + (t & 7) * 16;
+      const uint32_t pt = C::oP + pb * C::kPBuf + (t >> 3) * 128 + (t & 7) * 16;
 #pragma unroll
       for (int i = 0; i < RG / 16; ++i) {
         uint32_t h[8];
@@ -1151,54 +1180,99 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           *reinterpret_cast<uint4*>(d + 2048) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
-      if (kFp8 && grp == 0 && t >= bi.live) {
+      if (kFp8 && (C::kAlt || grp == 0) && t >= bi.live) {
         // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
         uint4* v = reinterpret_cast<uint4*>(sm + C::oStage + stage * C::kStage + kBlock * kDim + t * kDim);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
       }
-      if (++stage == C::kStages) stage = 0;
+      stage += kStep;
+      if (stage >= C::kStages) stage -= C::kStages;
       smem_to_async();
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(pb));
 
-      if (bi.flags & 2) {
-        // the segment's output: 16 rows at a time through shared memory (P's, which no MMA reads now), so that
-        // the stores are whole rows and the code is short
+      if (bi.left < kStep) {
+        // the group's last block of the segment
         warp_reduce_rows<RG, false>(l);
         if (lane < RG) red[wl * NR + r0 + lane] = l[0];
         if (RG == 64) red[wl * NR + r0 + 32 + lane] = l[1];
         ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1);
+        const bool two = C::kAlt && bi.idx + bi.left > 0;       // the other group has blocks of it too
+        if (two) ++joins;
+        if (two && bi.left == 0) ok = mbar_wait(join_full, (joins - 1) & 1) && ok;
         if (group_any(bar_id, !ok)) { ok = false; break; }
         tmem_fence_after();
+        if (two && bi.left == 1) {
+          // the state stays where it is (O in tensor memory, references and sums in shared memory); the group
+          // with the last block reads it
+          if (lane == 0) mbar_arrive(join_full);
+          must_wait = true;
+          continue;
+        }
+        // the segment's output: 16 rows at a time through shared memory (P's, which no MMA reads now), so that
+        // the stores are whole rows and the code is short
         const bool whole = (bi.flags & 12) == 12;
         float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
-        float* stg = reinterpret_cast<float*>(sm + C::oP + grp * (16 * kDim * 4));
-#pragma unroll 1
-        for (int i = 0; i < RG / 16 && r0 + 16 * i < p.R; ++i) {
-          float o[16];
-          tmem_ld16(tO + lanes + r0 + 16 * i, o);
+        auto stg = [&](int e) {
+          return reinterpret_cast<float*>(sm + C::oP + pb * C::kPBuf + (e / C::kStgRows) * C::kPPart +
+                                          (C::kAlt ? 0 : grp * RG * 128) + (e % C::kStgRows) * (kDim * 4));
+        };
+        const int other = grp ^ 1;
+        const float* red2 = row_red + other * 4 * NR;
+        const float* ref2 = row_ref + other * NR;
+        const uint32_t tO2 = tO + other * C::kOCols + lanes;
+        auto load_o = [&](uint32_t at, float (&o)[16]) {
+          tmem_ld16(at, o);
           if (C::kStacked) {
             float o1[16], o2[16];
-            tmem_ld16(tO + lanes + NR + r0 + 16 * i, o1);
-            tmem_ld16(tO + lanes + 2 * NR + r0 + 16 * i, o2);
+            tmem_ld16(at + NR, o1);
+            tmem_ld16(at + 2 * NR, o2);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] += o1[e] + o2[e];
           }
           tmem_wait_ld();
+        };
+        if (two && t < NR) {
+          // the groups' common maximum and sum; alphas: what each group's O is multiplied by
+          float l1 = red[t] + red[NR + t] + red[2 * NR + t] + red[3 * NR + t];
+          float l2 = red2[t] + red2[NR + t] + red2[2 * NR + t] + red2[3 * NR + t];
+          const float m1 = l1 > 0.f ? -ref[t] : -INFINITY, m2 = l2 > 0.f ? -ref2[t] : -INFINITY;
+          const float m = fmaxf(m1, m2);
+          const float f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m), f2 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - m);
+          alphas[t] = f1;
+          row_alpha[other * NR + t] = f2;
+          red[t] = f1 * l1 + f2 * l2;                // (no other thread reads this row's sums before the barrier)
+          red[NR + t] = red[2 * NR + t] = red[3 * NR + t] = 0.f;
+          ref[t] = -m;
+        }
+        if (two) group_any(bar_id, false);
+#pragma unroll 1
+        for (int i = 0; i < RG / 16 && r0 + 16 * i < p.R; ++i) {
+          float o[16];
+          load_o(tOg + r0 + 16 * i, o);
+          if (two) {
+            float o2[16];
+            load_o(tO2 + 16 * i, o2);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float f1 = alphas[16 * i + e], f2 = row_alpha[other * NR + 16 * i + e];
+              o[e] = (f1 == 0.f ? 0.f : f1 * o[e]) + (f2 == 0.f ? 0.f : f2 * o2[e]);
+            }
+          }
           if (i > 0) group_any(bar_id, false);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) stg[e * kDim + t] = o[e];
+          for (int e = 0; e < 16; ++e) stg(e)[t] = o[e];
           group_any(bar_id, false);
 #pragma unroll 1
           for (int e = wl; e < 16; e += 4) {
             const int r = r0 + 16 * i + e;
             if (r >= p.R) break;
             const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
-            const float M = L > 0.f ? -row_ref[r] : -INFINITY;      // L and O are in units of 2^M
-            const float4 v = *reinterpret_cast<const float4*>(stg + e * kDim + 4 * lane);
+            const float M = L > 0.f ? -ref[r] : -INFINITY;          // L and O are in units of 2^M
+            const float4 v = *reinterpret_cast<const float4*>(stg(e) + 4 * lane);
             if (whole) {
               const float inv = L > 0.f ? p.v_global / L : 0.f;
               const int j = row_pos[r];
@@ -1214,7 +1288,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_free(seg & 1));
+        if (lane == 0) {
+          mbar_arrive(q_free(bi.seg & 1));
+          if (two) mbar_arrive(join_free);
+        }
         group_any(bar_id, false);                     // `red` and the references may change again
       }
     }
