@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   after a power-of-two scaling of its row (4 significant bits each, a bf16
 //   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
 //   parts of its f16 value (3 significant bits each, rounded at 2^-10 relative).
-//   NVFP4: eight warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
+//   NVFP4: further warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
 //   memory, V into swizzled shared memory (its rows are tokens, and as A it is
 //   needed by dims). Q is scaled into f16's range and P rounded to f16.
 // Roles: warp 0 copies, warps 1 and 2 issue the MMAs of S and of P V, warp 3 brings
@@ -574,7 +574,8 @@ struct TcCfg {
   static constexpr int kGroups = 2;
   static constexpr int kRG = kAlt ? NR : NR / 2;               // rows per softmax group
   static constexpr int kSoftArrive = kAlt ? 4 : 8;             // softmax warps per block
-  static constexpr int kConv = kFp8 ? 0 : 8;                   // expanding warps
+  static constexpr int kVGroups = NR <= 16 ? 2 : 1;            // groups of 4 warps that expand V, taking turns
+  static constexpr int kConv = kFp8 ? 0 : 4 + 4 * kVGroups;    // expanding warps
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kWarpsAll = kConv0 + kConv;
   static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), kFp8 ? 1 : C::kConv);
+      mbar_init(empty(s), kFp8 ? 1 : 8);                              // NVFP4: the expanding warps of K and of V
     }
     for (int i = 0; i < kTcS; ++i) {
       mbar_init(s_full(i), 2);                                        // the commit, and the issuing thread's own arrival
@@ -800,9 +801,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       mbar_init(q_full(i), 1);
       mbar_init(q_free(i), 1 + C::kSoftArrive);                       // S is done with Q, softmax with its multipliers
       if (!kFp8) {
-        mbar_init(k_full(i), C::kConv / 2);
+        mbar_init(k_full(i), 4);
         mbar_init(k_free(i), 1);
-        mbar_init(v_full(i), C::kConv / 2);
+        mbar_init(v_full(i), 4);
         mbar_init(v_free(i), 1);
       }
     }
@@ -1298,44 +1299,48 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   } else if (items > 0 && C::kConv > 0) {
     // -------------------------------------------------- NVFP4 expansion --
-    // Four warps expand K into tensor memory, four expand V into shared memory; a
-    // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of
-    // eight rows in eight banks, and so does the V tile's for the stores.
-    const bool isv = warp >= C::kConv0 + 4;
-    const int row = 32 * (warp & 3) + lane;
+    // Four warps expand K into tensor memory, the others V into shared memory; a
+    // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of eight
+    // rows in eight banks, and so does the V tile's for the stores.
+    const int vg = ((warp - C::kConv0) >> 2) - 1;   // -1: K
+    const bool isv = vg >= 0;
+    const int row = 32 * (warp & 3) + lane, step = isv ? C::kVGroups : 1;
     constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    int s = 0;
+    const uint8_t* src = sm + C::oStage + (isv ? codes : 0) + row * (kDim / 2);
+    const uint8_t* ssrc = sm + C::oStage + 2 * codes + (isv ? scales : 0) + row * (kDim / 16);
+    const int swz = ((row >> 1) & 3) << 4, swz_v = (row & 7) << 4;
+    int s = isv ? vg : 0;
     uint32_t ph = 0;
-    for (int n = 0; n < items; ++n) {
+    for (int n = isv ? vg : 0; n < items; n += step) {
       ok = mbar_wait(full(s), ph);
       if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1) && ok;
       ok = __all_sync(kEvery, ok);
       if (!ok) break;
-      const uint8_t* st = sm + C::oStage + s * C::kStage + (isv ? codes : 0);
-      uint4 w[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        w[c] = *reinterpret_cast<const uint4*>(st + row * (kDim / 2) + ((c ^ ((row >> 1) & 3)) << 4));
-      uint2 sc = *reinterpret_cast<const uint2*>(sm + C::oStage + s * C::kStage + 2 * codes + (isv ? scales : 0) + row * (kDim / 16));
-      if (isv && row >= infos[n & (kInfos - 1)].live) {
-        // a row that was never written may hold NaN patterns, and 0 x NaN is NaN
-        sc = make_uint2(0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      // a row that was never written may hold NaN patterns, and 0 x NaN is NaN
+      const bool dead = isv && row >= infos[n & (kInfos - 1)].live;
       if (!isv) tmem_fence_after();
       uint8_t* tile = sm + C::oTiles + (n & 1) * 2 * kHalfBox + row * 128;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        uint4 w[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          w[q] = *reinterpret_cast<const uint4*>(src + s * C::kStage + ((32 * half + 16 * q) ^ swz));
+        uint32_t sc = *reinterpret_cast<const uint32_t*>(ssrc + s * C::kStage + 4 * half);
+        if (half == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty(s));
+        }
+        if (dead) {
+          sc = 0u;
+          w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
+        }
         uint32_t h[32];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int c = 2 * half + q;
-          const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>((half ? sc.y : sc.x) >> (16 * q)));
+          const uint32_t words[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc >> (16 * q)));
           const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
           const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
 #pragma unroll
@@ -1352,7 +1357,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         if (isv) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(tile + half * kHalfBox + ((c ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(tile + half * kHalfBox + ((c << 4) ^ swz_v)) =
                 make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
         } else {
           tmem_st32(tK + lanes + (n & 1) * (kDim / 2) + 32 * half, h);
@@ -1366,7 +1371,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
-      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      s += step;
+      if (s >= C::kStages) { s -= C::kStages; ph ^= 1u; }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   }
