@@ -564,6 +564,53 @@ struct BlockInfo {
   int flags;                            // 4: the segment starts its row, 8: it ends it
 };
 
+// The copy thread's view of the CTA's blocks, one after the other.
+struct BlockFeed {
+  static constexpr int kAhead = 4;      // page ids are fetched this many blocks ahead
+  int page[kAhead];
+  Walk far, cur;
+  int items, n, seg, idx;
+  bool from_start;
+  __device__ __forceinline__ BlockFeed(const PagedParams& p, const Walk& at, int count)
+      : far(at), cur(at), items(count), n(0), seg(0), idx(0), from_start(at.blk == 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      page[i] = i < items ? paged_page(p, far, true) : -1;
+      if (i < items) far.next(p);
+    }
+  }
+  // Describes the next block and returns its (page, KV head) slab.
+  __device__ __forceinline__ int64_t next(const PagedParams& p, BlockInfo& bi) {
+    const int pg = page[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i) page[i] = page[i + 1];
+    if (n + kAhead < items) {
+      page[kAhead - 1] = paged_page(p, far, true);
+      far.next(p);
+    }
+    const int toks = cur.L - cur.blk * kBlock;
+    bi.live = pg < 0 ? 0 : toks < kBlock ? toks : kBlock;
+    bi.lim0 = pg < 0 ? -kBlock : toks - p.Q;
+    bi.b = cur.b;
+    bi.g = cur.g;
+    const int row_left = cur.nb - 1 - cur.blk, left_here = row_left < items - 1 - n ? row_left : items - 1 - n;
+    bi.seg = seg;
+    bi.idx = idx < 2 ? idx : 2;
+    bi.left = left_here < 2 ? left_here : 2;
+    bi.flags = (from_start ? 4 : 0) | (row_left == left_here ? 8 : 0);
+    ++idx;
+    if (left_here == 0) {
+      ++seg;
+      idx = 0;
+      from_start = true;                             // only the CTA's first segment may start inside a row
+    }
+    const int64_t slab = static_cast<int64_t>(pg < 0 ? 0 : pg) * p.G + cur.g;     // a bad page's place is taken by page 0
+    ++n;
+    cur.next(p);
+    return slab;
+  }
+};
+
 template <int kKv, int NR>
 struct TcCfg {
   static constexpr bool kFp8 = kKv == MSA_FP8_E4M3;
@@ -838,46 +885,13 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   if (items > 0 && warp == 0) {
     // ----------------------------------------------------------- copies --
     if (lane == 0) {
-      constexpr int kAhead = 4;                     // page ids are fetched this many blocks ahead
-      int page[kAhead];
-      Walk far = rg.at, cur = rg.at;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        page[i] = i < items ? paged_page(p, far, true) : -1;
-        if (i < items) far.next(p);
-      }
+      BlockFeed feed(p, rg.at, items);
       const uint64_t policy = l2_evict_first_policy();
       int s = 0;
       uint32_t ph = 0;
-      bool from_start = cur.blk == 0;
-      int seg = 0, idx = 0;
-      for (int n = 0; n < items && ok; ++n) {
-        const int pg = page[0];
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) page[i] = page[i + 1];
-        if (n + kAhead < items) {
-          page[kAhead - 1] = paged_page(p, far, true);
-          far.next(p);
-        }
+      for (int n = 0; n < items; ++n) {
         if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
-        BlockInfo& bi = infos[n & (kInfos - 1)];
-        const int toks = cur.L - cur.blk * kBlock;
-        bi.live = pg < 0 ? 0 : toks < kBlock ? toks : kBlock;
-        bi.lim0 = pg < 0 ? -kBlock : toks - p.Q;
-        bi.b = cur.b;
-        bi.g = cur.g;
-        const int row_left = cur.nb - 1 - cur.blk, left_here = row_left < items - 1 - n ? row_left : items - 1 - n;
-        bi.seg = seg;
-        bi.idx = idx < 2 ? idx : 2;
-        bi.left = left_here < 2 ? left_here : 2;
-        bi.flags = (from_start ? 4 : 0) | (row_left == left_here ? 8 : 0);
-        ++idx;
-        if (left_here == 0) {
-          ++seg;
-          idx = 0;
-          from_start = true;                         // only the CTA's first segment may start inside a row
-        }
-        const int64_t slab = static_cast<int64_t>(pg < 0 ? 0 : pg) * p.G + cur.g;     // a bad page's place is taken by page 0
+        const int64_t slab = feed.next(p, infos[n & (kInfos - 1)]);
         const uint32_t dst = base + C::oStage + s * C::kStage;
         mbar_arrive_expect_tx(full(s), C::kStage);
         if (kFp8) {
@@ -891,7 +905,6 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           bulk_g2s(dst + 2 * codes + scales, p.vs + slab * scales, scales, full(s), policy);
         }
         if (++s == C::kStages) { s = 0; ph ^= 1u; }
-        cur.next(p);
       }
       // no copy may be in flight when the CTA ends, whatever the others did
       for (int k = 0; k < C::kStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
@@ -1385,6 +1398,319 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// bf16 K/V and more than 16 query rows per KV head (several positions): the rows
+// are the M = 128 of both products,
+//   S = Q K^T (N = 128 tokens, K = 128 dims), O += P V (N = 128 dims, K = 128 tokens),
+// with Q and P as A operands in tensor memory and K and V as the copies leave them.
+// A softmax thread owns a row: its 128 logits of a block are in its registers and
+// nothing is exchanged. Tensor memory: Q of this row and of the next (64 columns
+// each, two dims per column), S twice (128; P over its first 64), O (128). Roles:
+// copies, S, P V, an idle warp, four softmax warps.
+constexpr int kRwStages = 3, kRwWarps = 8;
+constexpr uint32_t kRwQ = 0, kRwS = 128, kRwO = 384, kRwCols = 512;
+constexpr uint32_t kRwInfo = kRwStages * 4 * kHalfBox, kRwBars = kRwInfo + kInfos * sizeof(BlockInfo);
+constexpr int kRwNumBars = 2 * kRwStages + 9;
+constexpr uint32_t kRwSlot = kRwBars + kRwNumBars * 8, kRwTotal = kRwSlot + 16;
+
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+                 "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+                 "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+               : "r"(a));
+}
+
+__global__ void __launch_bounds__(32 * kRwWarps, 1)
+    paged_gqa_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                          const __grid_constant__ PagedParams p) {
+  constexpr int kAllThreads = 32 * kRwWarps;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Range shared_range;
+  __shared__ int64_t warp_sums[kRwWarps];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + kRwInfo);
+  const uint32_t bars = base + kRwBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kRwStages + s); };
+  constexpr int b0 = 2 * kRwStages;
+  auto s_full = [&](int i) { return bars + 8u * (b0 + i); };
+  auto p_full = [&](int i) { return bars + 8u * (b0 + 2 + i); };
+  auto p_free = [&](int i) { return bars + 8u * (b0 + 4 + i); };       // P V is done: the S buffer is free
+  auto q_full = [&](int i) { return bars + 8u * (b0 + 6 + i); };
+  const uint32_t done_bar = bars + 8u * (b0 + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRwStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 2);
+      mbar_init(p_full(i), 4);
+      mbar_init(p_free(i), 1);
+      mbar_init(q_full(i), 4);
+    }
+    mbar_init(done_bar, 2);
+    fence_mbar_init();
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + kRwSlot), "r"(kRwCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kRwSlot);
+  griddep_wait();
+
+  const int cta = blockIdx.x;
+  Range rg;
+  find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
+  paged_empty_requests(p, kAllThreads);
+  if (threadIdx.x == 0) paged_describe_cut(p, rg, cta);
+  const int items = static_cast<int>(rg.x1 - rg.x0);
+  bool ok = true;
+
+  if (items > 0 && warp == 0) {
+    // ----------------------------------------------------------- copies --
+    if (lane == 0) {
+      BlockFeed feed(p, rg.at, items);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int n = 0; n < items; ++n) {
+        if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
+        const int64_t slab = feed.next(p, infos[n & (kInfos - 1)]);
+        const int y = static_cast<int>(slab * kBlock);
+        const uint32_t dst = base + s * 4 * kHalfBox;
+        mbar_arrive_expect_tx(full(s), 4 * kHalfBox);
+        tma_load_2d(dst, &tk, 0, y, full(s));
+        tma_load_2d(dst + kHalfBox, &tk, 64, y, full(s));
+        tma_load_2d(dst + 2 * kHalfBox, &tv, 0, y, full(s));
+        tma_load_2d(dst + 3 * kHalfBox, &tv, 64, y, full(s));
+        if (++s == kRwStages) { s = 0; ph ^= 1u; }
+      }
+      // no copy may be in flight when the CTA ends, whatever the others did
+      for (int k = 0; k < kRwStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
+      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (items > 0 && warp <= 2) {
+    // ------------------------------------------------------------- MMAs --
+    const bool lead = elect_one();
+    constexpr uint32_t hi = desc_hi(1024, kSwz128);
+    int stage = 0;
+    uint32_t ph = 0;
+    if (warp == 1) {
+      constexpr uint32_t id_s = mma_idesc(1, 1, 128, 0, 0);
+      const uint32_t k0 = desc_lo(base, 16);
+      for (int n = 0; n < items; ++n) {
+        ok = warp_wait(full(stage), ph);
+        if (n >= 2) ok = ok && warp_wait(p_free(n & 1), ((n >> 1) - 1) & 1);
+        if (!ok) break;
+        const int seg = infos[n & (kInfos - 1)].seg;
+        if (infos[n & (kInfos - 1)].idx == 0 && !warp_wait(q_full(seg & 1), (seg >> 1) & 1)) { ok = false; break; }
+        tmem_fence_after();
+        if (lead) {
+          const uint32_t k = k0 + stage * (4 * kHalfBox >> 4), d = tmem + kRwS + 128 * (n & 1), q = tmem + kRwQ + 64 * (seg & 1);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(d, q + 8 * kk, desc_of(k + (kk >> 2) * (kHalfBox >> 4) + (kk & 3) * 2, hi), id_s, kk > 0);
+          mma_commit(s_full(n & 1));
+          mbar_arrive(s_full(n & 1));
+        }
+        __syncwarp();
+        if (++stage == kRwStages) { stage = 0; ph ^= 1u; }
+      }
+    } else {
+      constexpr uint32_t id_o = mma_idesc(1, 1, 128, 0, 1);
+      const uint32_t v0 = desc_lo(base + 2 * kHalfBox, kHalfBox);
+      for (int n = 0; n < items; ++n) {
+        ok = warp_wait(p_full(n & 1), (n >> 1) & 1);
+        if (!ok) break;
+        const bool fresh = infos[n & (kInfos - 1)].idx == 0;
+        tmem_fence_after();
+        if (lead) {
+          const uint32_t v = v0 + stage * (4 * kHalfBox >> 4), pt = tmem + kRwS + 128 * (n & 1);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(tmem + kRwO, pt + 8 * kk, desc_of(v + kk * 128, hi), id_o, !(fresh && kk == 0));
+          mma_commit(empty(stage));
+          mma_commit(p_free(n & 1));
+        }
+        __syncwarp();
+        if (++stage == kRwStages) stage = 0;
+      }
+    }
+    if (!ok && lead) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    if (lead) mma_commit(done_bar);                 // every MMA has finished before tensor memory is freed
+    __syncwarp();
+    mbar_wait(done_bar, 0);
+    __syncwarp();
+  } else if (items > 0 && warp >= 4) {
+    // ---------------------------------------------------------- softmax --
+    const int r = 32 * (warp & 3) + lane;           // query row, tensor-memory lane; token of V's dead rows
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const bool live_warp = 32 * (warp & 3) < p.R, live_row = r < p.R;
+    const int j = live_row ? r / p.group : 0;
+    Walk w = rg.at;                                 // row of the queries loaded next
+    int64_t w_left = items;
+    auto load_q = [&](int buf) {
+      if (live_warp) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (live_row ? paged_head(p, w.b, w.g, r) : 0) * kDim);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 x = live_row ? src[8 * half + k] : make_uint4(0u, 0u, 0u, 0u);
+            v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+          }
+          tmem_st32(tmem + lanes + kRwQ + 64 * buf + 32 * half, v);
+        }
+        tmem_wait_st();
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(buf));
+      w_left -= w.nb - w.blk;
+      w.blk = w.nb - 1;
+      if (w_left > 0) w.next(p);
+    };
+    load_q(0);
+    float ref = -INFINITY, l = 0.f;
+    int stage = 0;
+    for (int n = 0; n < items; ++n) {
+      const int sb = n & 1;
+      ok = warp_wait(s_full(sb), (n >> 1) & 1);
+      if (!ok) break;
+      const BlockInfo bi = infos[n & (kInfos - 1)];
+      if (bi.idx == 0) {
+        ref = -INFINITY;
+        l = 0.f;
+        if (w_left > 0) load_q((bi.seg + 1) & 1);   // S of the row before this one is done with that buffer
+      }
+      tmem_fence_after();
+      if (live_warp) {
+        const uint32_t sbuf = tmem + lanes + kRwS + 128 * sb;
+        float x[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(sbuf + 32 * q, x + 32 * q);
+        tmem_wait_ld();
+        if (bi.lim0 < kBlock - 1) {
+          const int lim = bi.lim0 + j;
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k > lim) x[k] = -INFINITY;
+        }
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; ++k) top4[k & 3] = fmaxf(top4[k & 3], x[k]);
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.scale_log2;
+        const bool raise = top > ref + kSlack;
+        const float alpha = raise && ref != -INFINITY ? ex2_approx(ref - top) : 1.f;
+        if (__any_sync(kEvery, raise && ref != -INFINITY)) {
+          // O *= alpha once the block before has landed
+          ok = warp_wait(p_free((n - 1) & 1), ((n - 1) >> 1) & 1);
+          if (!ok) break;
+          tmem_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            float o[16];
+            tmem_ld16(tmem + lanes + kRwO + 16 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= alpha;
+            tmem_st16(tmem + lanes + kRwO + 16 * q, o);
+          }
+        }
+        if (raise) ref = top;
+        l *= alpha;
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float a = ex2_approx(fmaf(x[64 * q + 2 * k], p.scale_log2, neg));
+            const float b = ex2_approx(fmaf(x[64 * q + 2 * k + 1], p.scale_log2, neg));
+            l4[k & 3] += a + b;
+            pk[k] = pack_bf16x2(a, b);
+          }
+          tmem_st32(sbuf + 32 * q, pk);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      }
+      if (r >= bi.live) {
+        // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
+        uint8_t* v = sm + stage * 4 * kHalfBox + 2 * kHalfBox + r * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          *reinterpret_cast<uint4*>(v + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v + kHalfBox + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        smem_to_async();
+      }
+      if (++stage == kRwStages) stage = 0;
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(sb));
+      if (bi.left == 0) {
+        // the segment's output, a row per thread
+        ok = warp_wait(p_free(sb), (n >> 1) & 1);
+        if (!ok) break;
+        tmem_fence_after();
+        if (live_warp) {
+          const bool whole = (bi.flags & 12) == 12;
+          const float inv = l > 0.f ? 1.f / l : 0.f, M = l > 0.f ? ref : -INFINITY;
+          const int64_t head = live_row ? paged_head(p, bi.b, bi.g, r) : 0;
+          float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            float o[16];
+            tmem_ld16(tmem + lanes + kRwO + 16 * q, o);
+            tmem_wait_ld();
+            if (!live_row) continue;
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + head * kDim + 16 * q);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                dst[k] = l > 0.f ? make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                              pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                              pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                              pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + r * kDim + 16 * q);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[k] = l > 0.f ? make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3])
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          if (live_row && whole && p.lse != nullptr) p.lse[head] = l > 0.f ? (M + log2f(l)) * kLn2f : -INFINITY;
+          if (live_row && !whole) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = l; }
+        }
+        tmem_fence_before();
+      }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+  }
+
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kRwCols) : "memory");
+  }
+}
+
 // Joins the partials of a cut row, in CTA order. One CTA per (cut, group of
 // rows); with few rows the eight warps share a row's partials.
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
@@ -1517,6 +1843,18 @@ static cudaError_t launch_tc(const PagedParams& p, int ctas, cudaStream_t stream
   return launch_pdl(paged_gqa_tc_kernel<kKv, NR>, dim3(ctas), dim3(32 * C::kWarpsAll), smem, stream, tk, tv, p);
 }
 
+static cudaError_t launch_rows_tc(const PagedParams& p, int ctas, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  cudaError_t err;
+  const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
+  if ((err = cache_map(&tk, p.k, rows, MSA_BF16)) != cudaSuccess) return err;
+  if ((err = cache_map(&tv, p.v, rows, MSA_BF16)) != cudaSuccess) return err;
+  constexpr size_t smem = kRwTotal + 1024;
+  err = cudaFuncSetAttribute(paged_gqa_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  return launch_pdl(paged_gqa_rows_kernel, dim3(ctas), dim3(32 * kRwWarps), smem, stream, tk, tv, p);
+}
+
 cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRecord* rec) {
   PagedParams p;
   memset(&p, 0, sizeof(p));
@@ -1553,6 +1891,9 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   } else if (a.kv == MSA_NVFP4 && mt <= 2) {
     form = "tcgen05";
     err = mt == 1 ? launch_tc<MSA_NVFP4, 16>(p, ctas, stream) : launch_tc<MSA_NVFP4, 32>(p, ctas, stream);
+  } else if (a.kv == MSA_BF16 && mt > 1) {
+    form = "tcgen05";
+    err = launch_rows_tc(p, ctas, stream);
   } else {
     err = a.kv == MSA_BF16 ? launch_rows<MSA_BF16>(p, mt, ctas, stream) : launch_rows<MSA_NVFP4>(p, mt, ctas, stream);
   }
