@@ -31,9 +31,12 @@ constexpr float kLn2f = 0.693147180559945309f;
 constexpr float kSlack = 8.f;       // log2 units a maximum may exceed the reference by before a rescale
 constexpr int kMaxCtas = 320;       // partial slots in the workspace, two per CTA
 
-// A row cut by CTA boundaries: written by the CTA behind the first cut.
+// A row cut by CTA boundaries, written by the CTA behind the first cut: n
+// partials, CTA cta - 1's slot 1, then slot 0 of CTAs cta, cta + 1, ... The list
+// holds one entry per CTA (its own cut, n = 0 if it describes none), or, where
+// there are fewer rows than CTAs, one per row, so that the join is a small grid.
 struct CutRow {
-  int b, g, n, pad;                 // n partials: CTA c - 1's slot 1, then slot 0 of CTAs c, c + 1, ...
+  int b, g, n, cta;
 };
 
 struct PagedParams {
@@ -52,6 +55,7 @@ struct PagedParams {
   float k_global, v_global, scale_log2;
   int B, Q, H, G, NB, P;
   int group, R;                     // query heads per KV head; rows Q * group
+  int by_row;                       // the cuts are listed by row
 };
 
 // Cached tokens of request b (0 when the length is out of range).
@@ -174,6 +178,8 @@ __device__ void paged_empty_requests(const PagedParams& p, int nthreads) {
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (paged_len(p, b) > 0) continue;
     if (threadIdx.x == 0 && p.seq_lens[b] != 0) set_flag(p.flags, MSA_FLAG_BAD_SEQLEN);
+    if (p.by_row)
+      for (int g = threadIdx.x; g < p.G; g += nthreads) p.cuts[b * p.G + g] = CutRow{b, g, 0, 0};
     const int64_t row0 = static_cast<int64_t>(b) * p.Q * p.H;
     uint4* o = reinterpret_cast<uint4*>(p.out + row0 * kDim);
     for (int i = threadIdx.x; i < p.Q * p.H * kDim / 8; i += nthreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -182,16 +188,36 @@ __device__ void paged_empty_requests(const PagedParams& p, int nthreads) {
   }
 }
 
-// The cut this CTA describes for the join: its range starts inside a row whose
-// first CTA is the one before it.
-__device__ void paged_describe_cut(const PagedParams& p, const Range& r, int cta) {
-  CutRow c{0, 0, 0, 0};
-  if (r.x0 < r.x1 && r.at.blk > 0 && paged_cta_of(r.row0, r.W, r.ctas) == cta - 1) {
-    c.b = r.at.b;
-    c.g = r.at.g;
-    c.n = paged_cta_of(r.row0 + r.at.nb - 1, r.W, r.ctas) - (cta - 1) + 1;
+// The cuts this CTA describes for the join (one warp): its own, when its range
+// starts inside a row whose first CTA is the one before it; listed by row, every
+// row that starts in its range.
+__device__ void paged_describe_cuts(const PagedParams& p, const Range& r, int cta) {
+  const int lane = threadIdx.x & 31;
+  if (!p.by_row) {
+    CutRow c{0, 0, 0, cta};
+    if (r.x0 < r.x1 && r.at.blk > 0 && paged_cta_of(r.row0, r.W, r.ctas) == cta - 1) {
+      c.b = r.at.b;
+      c.g = r.at.g;
+      c.n = paged_cta_of(r.row0 + r.at.nb - 1, r.W, r.ctas) - (cta - 1) + 1;
+    }
+    if (lane == 0) p.cuts[cta] = c;
+    return;
   }
-  p.cuts[cta] = c;
+  if (r.x0 >= r.x1) return;
+  Walk w = r.at;
+  int64_t x = r.x0;
+  if (w.blk > 0) {                                   // a row begun elsewhere
+    x += w.nb - w.blk;
+    w.blk = w.nb - 1;
+    w.next(p);
+  }
+  while (x < r.x1) {
+    const int last = paged_cta_of(x + w.nb - 1, r.W, r.ctas);
+    if (lane == 0) p.cuts[w.b * p.G + w.g] = CutRow{w.b, w.g, last > cta ? last - cta + 1 : 0, cta + 1};
+    x += w.nb;
+    w.blk = w.nb - 1;
+    w.next(p);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -303,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
   Range rg;
   find_range<kThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kThreads);
-  if (threadIdx.x == 0) paged_describe_cut(p, rg, cta);
+  if (warp == kWarps - 1) paged_describe_cuts(p, rg, cta);
   if (rg.x0 >= rg.x1) return;
 
   uint32_t qf[8][4];
@@ -633,7 +659,8 @@ struct TcCfg {
   static constexpr uint32_t kPBuf = kPParts * kPPart < 16 * kDim * 4 ? 16 * kDim * 4 : kPParts * kPPart;
   static constexpr uint32_t kStage = raw_bytes<kKv>();
   static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
-  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf;
+  static constexpr int kQRaw = NR == 32 ? 32 : 16;             // query rows as they are in memory, before their parts
+  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf + kQRaw * 256;
   static constexpr uint32_t kSmall = 2048 + NR * 64;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -652,7 +679,8 @@ struct TcCfg {
   static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
   static constexpr uint32_t oQ = oTiles + kTiles;
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
-  static constexpr uint32_t oInfo = oP + kPBufs * kPBuf;
+  static constexpr uint32_t oRaw = oP + kPBufs * kPBuf;
+  static constexpr uint32_t oInfo = oRaw + kQRaw * 256;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
   static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [2][NR] kOff - reference
   static constexpr uint32_t oAlpha = oRef + 2 * NR * 4;                  // [2][NR]
@@ -878,7 +906,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   Range rg;
   find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kAllThreads);
-  if (threadIdx.x == 0) paged_describe_cut(p, rg, cta);
+  if (warp == C::kSoft0) paged_describe_cuts(p, rg, cta);
   const int items = static_cast<int>(rg.x1 - rg.x0);
   bool ok = true;
 
@@ -1004,37 +1032,52 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       const int qb = seg & 1;
       if (seg >= 2 && !mbar_wait(q_free(qb), ((seg >> 1) - 1) & 1)) { ok = false; break; }
       uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
-      for (int rb = 0; rb < NR; rb += 16) {
-        // sixteen rows at a time, all loads before the first use
-        uint2 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
+      // 16 lanes take a row, 8 dims each; the loads of up to 32 rows are in flight together. The loop over
+      // the rows is short code: it runs once per row, and instructions that are not cached cost more than it
+      const int l = lane & 15;
+#pragma unroll 1
+      for (int rb = 0; rb < NR; rb += C::kQRaw) {
+#pragma unroll 4
+        for (int i = lane >> 4; i < C::kQRaw; i += 2) {
           const int r = rb + i;
-          v[i] = r < p.R ? *reinterpret_cast<const uint2*>(p.q + paged_head(p, w.b, w.g, r) * kDim + 4 * lane) : make_uint2(0u, 0u);
+          if (r < p.R) {
+            const int j = row_pos[r];
+            const int64_t head = (static_cast<int64_t>(w.b) * p.Q + j) * p.H + w.g * p.group + (r - j * p.group);
+            cp_async16(base + C::oRaw + i * 256 + l * 16, p.q + head * kDim + 8 * l);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+#pragma unroll 1
+        for (int i = lane >> 4; i < C::kQRaw; i += 2) {
           const int r = rb + i;
-          const float x[4] = {bf16_bits_to_f32(v[i].x & 0xFFFF), bf16_bits_to_f32(v[i].x >> 16),
-                              bf16_bits_to_f32(v[i].y & 0xFFFF), bf16_bits_to_f32(v[i].y >> 16)};
-          // the largest magnitude: for values without sign, the order of the bits is the order of the values
-          const float amax = __uint_as_float(__reduce_max_sync(
-              kEvery, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
+          const uint4 v = r < p.R ? *reinterpret_cast<const uint4*>(sm + C::oRaw + i * 256 + l * 16) : make_uint4(0u, 0u, 0u, 0u);
+          const float x0[4] = {bf16_bits_to_f32(v.x & 0xFFFF), bf16_bits_to_f32(v.x >> 16), bf16_bits_to_f32(v.y & 0xFFFF),
+                               bf16_bits_to_f32(v.y >> 16)};
+          const float x1[4] = {bf16_bits_to_f32(v.z & 0xFFFF), bf16_bits_to_f32(v.z >> 16), bf16_bits_to_f32(v.w & 0xFFFF),
+                               bf16_bits_to_f32(v.w >> 16)};
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, o));
           // a power of two that brings it to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
           int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
           sh = sh < -126 ? -126 : sh;
           const float f = exp2_int(sh);
           if (kFp8) {
-            const uint2 parts = fp8_parts(x, f);
-            const uint32_t at = r * 128 + ((((lane >> 2) ^ r) & 7) << 4) + (lane & 3) * 4;
-            *reinterpret_cast<uint32_t*>(q + at) = parts.x;
-            *reinterpret_cast<uint32_t*>(q + C::kQPart + at) = parts.y;
+            const uint2 a = fp8_parts(x0, f), b = fp8_parts(x1, f);
+            const uint32_t at = r * 128 + ((((l >> 1) ^ r) & 7) << 4) + (l & 1) * 8;
+            *reinterpret_cast<uint2*>(q + at) = make_uint2(a.x, b.x);
+            *reinterpret_cast<uint2*>(q + C::kQPart + at) = make_uint2(a.y, b.y);
           } else {
-            const uint32_t at = (lane >> 4) * (NR * 128) + r * 128 + (((((lane & 15) >> 1) ^ r) & 7) << 4) + (lane & 1) * 8;
-            *reinterpret_cast<uint2*>(q + at) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
+            *reinterpret_cast<uint4*>(q + (l >> 3) * (NR * 128) + r * 128 + (((l ^ r) & 7) << 4)) =
+                make_uint4(pack_f16x2(x0[0] * f, x0[1] * f), pack_f16x2(x0[2] * f, x0[3] * f),
+                           pack_f16x2(x1[0] * f, x1[1] * f), pack_f16x2(x1[2] * f, x1[3] * f));
           }
-          if (lane == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+          if (l == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
         }
+        __syncwarp();
       }
       smem_to_async();
       __syncwarp();
@@ -1473,7 +1516,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
   Range rg;
   find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kAllThreads);
-  if (threadIdx.x == 0) paged_describe_cut(p, rg, cta);
+  if (warp == 3) paged_describe_cuts(p, rg, cta);
   const int items = static_cast<int>(rg.x1 - rg.x0);
   bool ok = true;
 
@@ -1719,9 +1762,11 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   griddep_launch_dependents();
   griddep_wait();
   const int chunks = (p.R + rows_per_cta - 1) / rows_per_cta;
-  const int cta = 1 + static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) % chunks;
-  const CutRow cut = p.cuts[cta];
+  const int entry = static_cast<int>(blockIdx.x) / chunks + (p.by_row ? 0 : 1);
+  const int chunk = static_cast<int>(blockIdx.x) % chunks;
+  const CutRow cut = p.cuts[entry];
   if (cut.n == 0) return;
+  const int cta = cut.cta;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wpr = kWarps / rows_per_cta;                           // warps per row
   const int row = chunk * rows_per_cta + warp / wpr, sub = warp % wpr;
@@ -1880,6 +1925,9 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   const int64_t most = static_cast<int64_t>(a.B) * a.G * a.NB;
   if (most < ctas) ctas = static_cast<int>(most);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.G;
+  p.by_row = rows < ctas - 1;
+  const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
   const int tiles = (p.R + 15) / 16;
   const int mt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
   cudaError_t err;
@@ -1901,7 +1949,7 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   if (ctas > 1) {
     const int rpc = p.R <= 16 ? 1 : 8;
     const int chunks = (p.R + rpc - 1) / rpc;
-    err = launch_pdl(paged_join_kernel, dim3((ctas - 1) * chunks), dim3(kThreads), 0, stream, p, rpc);
+    err = launch_pdl(paged_join_kernel, dim3(cuts * chunks), dim3(kThreads), 0, stream, p, rpc);
     if (err != cudaSuccess) return err;
   }
   rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"
