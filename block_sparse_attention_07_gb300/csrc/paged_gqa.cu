@@ -572,9 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   NVFP4: further warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
 //   memory, V into swizzled shared memory (its rows are tokens, and as A it is
 //   needed by dims). Q is scaled into f16's range and P rounded to f16.
-// Roles: warp 0 copies, warps 1 and 2 issue the MMAs of S and of P V, warp 3 brings
-// the next row's queries into shared memory, then 4 softmax warps per row group (a thread owns a
-// token of S and a dim of O), then the expanding warps. The softmax warps agree on
+// Roles: warp 0 copies, warps 1 and 2 issue the MMAs of S and of P V, warp 3 lists
+// the cut rows, then two groups of 4 softmax warps (a thread owns a token of S and
+// a dim of O; the group with a row's first block also brings the next row's
+// queries into shared memory), then the expanding warps. The softmax warps agree on
 // a rescale with one barrier-with-vote per block; a row's reference is raised only
 // when a logit exceeds it by 2^8, so that after a row's first block they hardly
 // ever have to. P's columns are written token by token (MN-major, unswizzled: a
@@ -659,8 +660,7 @@ struct TcCfg {
   static constexpr uint32_t kPBuf = kPParts * kPPart < 16 * kDim * 4 ? 16 * kDim * 4 : kPParts * kPPart;
   static constexpr uint32_t kStage = raw_bytes<kKv>();
   static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
-  static constexpr int kQRaw = NR == 32 ? 32 : 16;             // query rows as they are in memory, before their parts
-  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf + kQRaw * 256;
+  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf;
   static constexpr uint32_t kSmall = 2048 + NR * 64;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -679,8 +679,7 @@ struct TcCfg {
   static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
   static constexpr uint32_t oQ = oTiles + kTiles;
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
-  static constexpr uint32_t oRaw = oP + kPBufs * kPBuf;
-  static constexpr uint32_t oInfo = oRaw + kQRaw * 256;
+  static constexpr uint32_t oInfo = oP + kPBufs * kPBuf;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
   static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [2][NR] kOff - reference
   static constexpr uint32_t oAlpha = oRef + 2 * NR * 4;                  // [2][NR]
@@ -873,7 +872,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       mbar_init(p_free(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full(i), 1);
+      mbar_init(q_full(i), C::kSoftArrive);
       mbar_init(q_free(i), 1 + C::kSoftArrive);                       // S is done with Q, softmax with its multipliers
       if (!kFp8) {
         mbar_init(k_full(i), 4);
@@ -906,7 +905,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   Range rg;
   find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kAllThreads);
-  if (warp == C::kSoft0) paged_describe_cuts(p, rg, cta);
+  if (warp == 3) paged_describe_cuts(p, rg, cta);
   const int items = static_cast<int>(rg.x1 - rg.x0);
   bool ok = true;
 
@@ -1024,69 +1023,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     __syncwarp();
     mbar_wait(done_bar, 0);
     __syncwarp();
-  } else if (items > 0 && warp < C::kSoft0) {
-    // ---------------------------------------------------------- queries --
-    Walk w = rg.at;
-    int64_t left = items;
-    for (int seg = 0; left > 0; ++seg) {
-      const int qb = seg & 1;
-      if (seg >= 2 && !mbar_wait(q_free(qb), ((seg >> 1) - 1) & 1)) { ok = false; break; }
-      uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
-      // 16 lanes take a row, 8 dims each; the loads of up to 32 rows are in flight together. The loop over
-      // the rows is short code: it runs once per row, and instructions that are not cached cost more than it
-      const int l = lane & 15;
-#pragma unroll 1
-      for (int rb = 0; rb < NR; rb += C::kQRaw) {
-#pragma unroll 4
-        for (int i = lane >> 4; i < C::kQRaw; i += 2) {
-          const int r = rb + i;
-          if (r < p.R) {
-            const int j = row_pos[r];
-            const int64_t head = (static_cast<int64_t>(w.b) * p.Q + j) * p.H + w.g * p.group + (r - j * p.group);
-            cp_async16(base + C::oRaw + i * 256 + l * 16, p.q + head * kDim + 8 * l);
-          }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-#pragma unroll 1
-        for (int i = lane >> 4; i < C::kQRaw; i += 2) {
-          const int r = rb + i;
-          const uint4 v = r < p.R ? *reinterpret_cast<const uint4*>(sm + C::oRaw + i * 256 + l * 16) : make_uint4(0u, 0u, 0u, 0u);
-          const float x0[4] = {bf16_bits_to_f32(v.x & 0xFFFF), bf16_bits_to_f32(v.x >> 16), bf16_bits_to_f32(v.y & 0xFFFF),
-                               bf16_bits_to_f32(v.y >> 16)};
-          const float x1[4] = {bf16_bits_to_f32(v.z & 0xFFFF), bf16_bits_to_f32(v.z >> 16), bf16_bits_to_f32(v.w & 0xFFFF),
-                               bf16_bits_to_f32(v.w >> 16)};
-          float amax = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, o));
-          // a power of two that brings it to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
-          int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
-          sh = sh < -126 ? -126 : sh;
-          const float f = exp2_int(sh);
-          if (kFp8) {
-            const uint2 a = fp8_parts(x0, f), b = fp8_parts(x1, f);
-            const uint32_t at = r * 128 + ((((l >> 1) ^ r) & 7) << 4) + (l & 1) * 8;
-            *reinterpret_cast<uint2*>(q + at) = make_uint2(a.x, b.x);
-            *reinterpret_cast<uint2*>(q + C::kQPart + at) = make_uint2(a.y, b.y);
-          } else {
-            *reinterpret_cast<uint4*>(q + (l >> 3) * (NR * 128) + r * 128 + (((l ^ r) & 7) << 4)) =
-                make_uint4(pack_f16x2(x0[0] * f, x0[1] * f), pack_f16x2(x0[2] * f, x0[3] * f),
-                           pack_f16x2(x1[0] * f, x1[1] * f), pack_f16x2(x1[2] * f, x1[3] * f));
-          }
-          if (l == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
-        }
-        __syncwarp();
-      }
-      smem_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(qb));
-      left -= w.nb - w.blk;
-      w.blk = w.nb - 1;
-      if (left > 0) w.next(p);
-    }
-  } else if (items > 0 && warp < C::kConv0) {
+  } else if (items > 0 && warp >= C::kSoft0 && warp < C::kConv0) {
     // ---------------------------------------------------------- softmax --
     constexpr int RG = C::kRG;
     const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
@@ -1098,13 +1035,71 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     float* ref = row_ref + (C::kAlt ? grp * NR : 0);
     float* alphas = row_alpha + (C::kAlt ? grp * NR : 0);
     float* red = row_red + (C::kAlt ? grp * 4 * NR : 0);
+    // The queries of a segment, by the group with the first block of the segment before it (kAlt; else both
+    // groups): 16 lanes take a row, 8 dims each, all loads before the first use.
+    constexpr int kQPasses = NR / (8 * (C::kAlt ? 1 : 2));
+    Walk w = rg.at;
+    int w_seg = 0;
+    int64_t w_left = items;
+    auto put_q = [&](int seg) -> bool {
+      for (; w_seg < seg; ++w_seg) {
+        w_left -= w.nb - w.blk;
+        w.blk = w.nb - 1;
+        if (w_left <= 0) return true;               // there is no such segment
+        w.next(p);
+      }
+      const int qb = seg & 1, hl = lane & 15;
+      const int row = (C::kAlt ? wl : 4 * grp + wl) * 2 * kQPasses + (lane >> 4);
+      uint4 v[kQPasses];
+#pragma unroll
+      for (int i = 0; i < kQPasses; ++i) {
+        const int r = row + 2 * i, j = row_pos[r];
+        const int64_t head = (static_cast<int64_t>(w.b) * p.Q + j) * p.H + w.g * p.group + (r - j * p.group);
+        v[i] = r < p.R ? *reinterpret_cast<const uint4*>(p.q + head * kDim + 8 * hl) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (seg >= 2 && !warp_wait(q_free(qb), ((seg >> 1) - 1) & 1)) return false;
+      uint8_t* q = sm + C::oQ + qb * (C::kQParts * C::kQPart);
+#pragma unroll
+      for (int i = 0; i < kQPasses; ++i) {
+        const int r = row + 2 * i;
+        const float x0[4] = {bf16_bits_to_f32(v[i].x & 0xFFFF), bf16_bits_to_f32(v[i].x >> 16),
+                             bf16_bits_to_f32(v[i].y & 0xFFFF), bf16_bits_to_f32(v[i].y >> 16)};
+        const float x1[4] = {bf16_bits_to_f32(v[i].z & 0xFFFF), bf16_bits_to_f32(v[i].z >> 16),
+                             bf16_bits_to_f32(v[i].w & 0xFFFF), bf16_bits_to_f32(v[i].w >> 16)};
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, o));
+        // a power of two that brings it to [2^7, 2^8) (E4M3) or [2^14, 2^15) (f16)
+        int sh = fp16_shift_for(amax) - (kFp8 ? 7 : 0);
+        sh = sh < -126 ? -126 : sh;
+        const float f = exp2_int(sh);
+        if (kFp8) {
+          const uint2 a = fp8_parts(x0, f), b = fp8_parts(x1, f);
+          const uint32_t at = r * 128 + ((((hl >> 1) ^ r) & 7) << 4) + (hl & 1) * 8;
+          *reinterpret_cast<uint2*>(q + at) = make_uint2(a.x, b.x);
+          *reinterpret_cast<uint2*>(q + C::kQPart + at) = make_uint2(a.y, b.y);
+        } else {
+          *reinterpret_cast<uint4*>(q + (hl >> 3) * (NR * 128) + r * 128 + (((hl ^ r) & 7) << 4)) =
+              make_uint4(pack_f16x2(x0[0] * f, x0[1] * f), pack_f16x2(x0[2] * f, x0[3] * f),
+                         pack_f16x2(x1[0] * f, x1[1] * f), pack_f16x2(x1[2] * f, x1[3] * f));
+        }
+        if (hl == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+      }
+      smem_to_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(qb));
+      return true;
+    };
+    if (!C::kAlt || grp == 0) ok = put_q(0);
     float l[RG];
     int stage = C::kAlt ? grp : 0, joins = 0;
     bool first = false;                             // no block of the segment has set the references yet
     bool must_wait = false;                         // the other group still reads this one's last O
     for (int n = C::kAlt ? grp : 0; n < items; n += kStep) {
       const int sb = n & 1, pb = n % C::kPBufs;
-      ok = mbar_wait(s_full(sb), (n >> 1) & 1);
+      ok = mbar_wait(s_full(sb), (n >> 1) & 1) && ok;
       if (n >= C::kPBufs) ok = mbar_wait(p_free(pb), ((n / C::kPBufs) - 1) & 1) && ok;
       const BlockInfo bi = infos[n & (kInfos - 1)];
       if (bi.idx < kStep) {
@@ -1250,12 +1245,13 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(pb));
 
+      if (bi.idx == 0) ok = put_q(bi.seg + 1);
       if (bi.left < kStep) {
         // the group's last block of the segment
         warp_reduce_rows<RG, false>(l);
         if (lane < RG) red[wl * NR + r0 + lane] = l[0];
         if (RG == 64) red[wl * NR + r0 + 32 + lane] = l[1];
-        ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1);
+        ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1) && ok;
         const bool two = C::kAlt && bi.idx + bi.left > 0;       // the other group has blocks of it too
         if (two) ++joins;
         if (two && bi.left == 0) ok = mbar_wait(join_full, (joins - 1) & 1) && ok;
@@ -1353,7 +1349,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
-  } else if (items > 0 && C::kConv > 0) {
+  } else if (items > 0 && C::kConv > 0 && warp >= C::kConv0) {
     // -------------------------------------------------- NVFP4 expansion --
     // Four warps expand K into tensor memory, the others V into shared memory; a
     // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of eight
