@@ -661,7 +661,7 @@ struct TcCfg {
   static constexpr uint32_t kStage = raw_bytes<kKv>();
   static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
   static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf;
-  static constexpr uint32_t kSmall = 2048 + NR * 64;
+  static constexpr uint32_t kSmall = 2048 + NR * (kAlt ? 128 : 48);
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   // The parts of Q and P side by side as columns of one MMA (fewer, wider MMAs;
@@ -670,8 +670,8 @@ struct TcCfg {
   static constexpr bool kStacked = kFp8 && NR <= 32;
   static constexpr int kSCols = kStacked ? kQParts * NR : NR, kOCols = kStacked ? kPParts * NR : NR;
   static constexpr int kKCols = kFp8 ? 0 : 2 * (kDim / 2);     // NVFP4: K[2] in f16, two dims per column
-  static constexpr int kOBufs = kAlt ? 2 : 1;
-  static constexpr int kUsedCols = kTcS * kSCols + kOBufs * kOCols + kKCols;
+  static constexpr int kSets = kAlt ? 4 : 1;                   // states: of each group, for this segment and the one before
+  static constexpr int kUsedCols = kTcS * kSCols + kSets * kOCols + kKCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
   // shared memory
@@ -681,12 +681,12 @@ struct TcCfg {
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
   static constexpr uint32_t oInfo = oP + kPBufs * kPBuf;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
-  static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [2][NR] kOff - reference
-  static constexpr uint32_t oAlpha = oRef + 2 * NR * 4;                  // [2][NR]
-  static constexpr uint32_t oRed = oAlpha + 2 * NR * 4;                  // [2][4][NR]
-  static constexpr uint32_t oPos = oRed + 8 * NR * 4;                    // [NR] position of a row
+  static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [sets][NR] kOff - reference
+  static constexpr uint32_t oAlpha = oRef + kSets * NR * 4;              // [sets][NR]
+  static constexpr uint32_t oRed = oAlpha + kSets * NR * 4;              // [sets][4][NR]
+  static constexpr uint32_t oPos = oRed + kSets * 4 * NR * 4;            // [NR] position of a row
   static constexpr uint32_t oBars = oPos + NR * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 3;
+  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 5;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
@@ -853,7 +853,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   auto k_free = [&](int i) { return bars + 8u * (b1 + 6 + i); };
   auto v_full = [&](int i) { return bars + 8u * (b1 + 8 + i); };
   auto v_free = [&](int i) { return bars + 8u * (b1 + 10 + i); };
-  const uint32_t join_full = bars + 8u * (C::kBars - 3), join_free = bars + 8u * (C::kBars - 2);   // the groups' states
+  auto join_full = [&](int i) { return bars + 8u * (C::kBars - 5 + i); };           // a group's state of a segment
+  auto join_free = [&](int i) { return bars + 8u * (C::kBars - 3 + i); };
   const uint32_t done_bar = bars + 8u * (C::kBars - 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -881,8 +882,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         mbar_init(v_free(i), 1);
       }
     }
-    mbar_init(join_full, 4);
-    mbar_init(join_free, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(join_full(i), 4);
+      mbar_init(join_free(i), 4);
+    }
     mbar_init(done_bar, 2);
     fence_mbar_init();
     prefetch_tensormap(&tk);
@@ -898,7 +901,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
-  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kOBufs * C::kOCols;
+  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kSets * C::kOCols;
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -991,8 +994,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         const int pb = n % C::kPBufs;
         ok = (kFp8 || warp_wait(v_full(n & 1), (n >> 1) & 1)) && warp_wait(p_full(pb), (n / C::kPBufs) & 1);
         if (!ok) break;
-        const bool fresh = infos[n & (kInfos - 1)].idx < C::kOBufs;
-        const uint32_t d = tO + (n & (C::kOBufs - 1)) * C::kOCols;
+        const bool fresh = infos[n & (kInfos - 1)].idx < (C::kAlt ? 2 : 1);
+        const uint32_t d = tO + (C::kAlt ? (infos[n & (kInfos - 1)].seg & 1) * 2 + (n & 1) : 0) * C::kOCols;
         tmem_fence_after();
         if (lead) {
           const uint32_t pt = p0 + pb * (C::kPBuf >> 4);
@@ -1030,11 +1033,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     const int t = 32 * wl + lane;                   // token of S, dim of O
     const int r0 = C::kAlt ? 0 : grp * RG;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
-    const uint32_t tOg = tO + (C::kAlt ? grp * C::kOCols : 0) + lanes;
     constexpr int kStep = C::kAlt ? 2 : 1;
-    float* ref = row_ref + (C::kAlt ? grp * NR : 0);
-    float* alphas = row_alpha + (C::kAlt ? grp * NR : 0);
-    float* red = row_red + (C::kAlt ? grp * 4 * NR : 0);
     // The queries of a segment, by the group with the first block of the segment before it (kAlt; else both
     // groups): 16 lanes take a row, 8 dims each, all loads before the first use.
     constexpr int kQPasses = NR / (8 * (C::kAlt ? 1 : 2));
@@ -1094,9 +1093,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     };
     if (!C::kAlt || grp == 0) ok = put_q(0);
     float l[RG];
-    int stage = C::kAlt ? grp : 0, joins = 0;
+    int stage = C::kAlt ? grp : 0;
+    uint32_t joins = 0;                             // parity of the joins so far on either segment parity (bits 0, 1)
     bool first = false;                             // no block of the segment has set the references yet
-    bool must_wait = false;                         // the other group still reads this one's last O
+    uint32_t lent = 0;                              // bits 0, 1: the other group may still read this one's state
     for (int n = C::kAlt ? grp : 0; n < items; n += kStep) {
       const int sb = n & 1, pb = n % C::kPBufs;
       ok = mbar_wait(s_full(sb), (n >> 1) & 1) && ok;
@@ -1106,9 +1106,14 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         first = true;
 #pragma unroll
         for (int r = 0; r < RG; ++r) l[r] = 0.f;
-        if (must_wait) ok = mbar_wait(join_free, (joins - 1) & 1) && ok;
-        must_wait = false;
+        if (lent >> (bi.seg & 1) & 1) ok = mbar_wait(join_free(bi.seg & 1), ((joins >> (bi.seg & 1)) & 1) ^ 1) && ok;
+        lent &= ~(1u << (bi.seg & 1));
       }
+      const int set = C::kAlt ? (bi.seg & 1) * 2 + grp : 0;
+      const uint32_t tOg = tO + set * C::kOCols + lanes;
+      float* ref = row_ref + set * NR;
+      float* alphas = row_alpha + set * NR;
+      float* red = row_red + set * 4 * NR;
       const float* mul = row_mul + (bi.seg & 1) * NR + r0;
       float x[RG];
       tmem_fence_after();
@@ -1236,7 +1241,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
         uint4* v = reinterpret_cast<uint4*>(sm + C::oStage + stage * C::kStage + kBlock * kDim + t * kDim);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 8; ++k) v[k ^ (t & 7)] = make_uint4(0u, 0u, 0u, 0u);     // (eight rows, eight banks)
       }
       stage += kStep;
       if (stage >= C::kStages) stage -= C::kStages;
@@ -1253,15 +1258,16 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         if (RG == 64) red[wl * NR + r0 + 32 + lane] = l[1];
         ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1) && ok;
         const bool two = C::kAlt && bi.idx + bi.left > 0;       // the other group has blocks of it too
-        if (two) ++joins;
-        if (two && bi.left == 0) ok = mbar_wait(join_full, (joins - 1) & 1) && ok;
+        const int sp = bi.seg & 1;
+        if (two && bi.left == 0) ok = mbar_wait(join_full(sp), (joins >> sp) & 1) && ok;
+        if (two) joins ^= 1u << sp;
         if (group_any(bar_id, !ok)) { ok = false; break; }
         tmem_fence_after();
         if (two && bi.left == 1) {
           // the state stays where it is (O in tensor memory, references and sums in shared memory); the group
           // with the last block reads it
-          if (lane == 0) mbar_arrive(join_full);
-          must_wait = true;
+          if (lane == 0) mbar_arrive(join_full(sp));
+          lent |= 1u << sp;
           continue;
         }
         // the segment's output: 16 rows at a time through shared memory (P's, which no MMA reads now), so that
@@ -1272,9 +1278,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           return reinterpret_cast<float*>(sm + C::oP + pb * C::kPBuf + (e / C::kStgRows) * C::kPPart +
                                           (C::kAlt ? 0 : grp * RG * 128) + (e % C::kStgRows) * (kDim * 4));
         };
-        const int other = grp ^ 1;
+        const int other = set ^ 1;
         const float* red2 = row_red + other * 4 * NR;
         const float* ref2 = row_ref + other * NR;
+        float* alphas2 = row_alpha + other * NR;
         const uint32_t tO2 = tO + other * C::kOCols + lanes;
         auto load_o = [&](uint32_t at, float (&o)[16]) {
           tmem_ld16(at, o);
@@ -1296,7 +1303,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           const float m = fmaxf(m1, m2);
           const float f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m), f2 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - m);
           alphas[t] = f1;
-          row_alpha[other * NR + t] = f2;
+          alphas2[t] = f2;
           red[t] = f1 * l1 + f2 * l2;                // (no other thread reads this row's sums before the barrier)
           red[NR + t] = red[2 * NR + t] = red[3 * NR + t] = 0.f;
           ref[t] = -m;
@@ -1310,9 +1317,13 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
             float o2[16];
             load_o(tO2 + 16 * i, o2);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float f1 = alphas[16 * i + e], f2 = row_alpha[other * NR + 16 * i + e];
-              o[e] = (f1 == 0.f ? 0.f : f1 * o[e]) + (f2 == 0.f ? 0.f : f2 * o2[e]);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 f1 = *reinterpret_cast<const float4*>(alphas + 16 * i + e);
+              const float4 f2 = *reinterpret_cast<const float4*>(alphas2 + 16 * i + e);
+              o[e] = f1.x * o[e] + f2.x * o2[e];
+              o[e + 1] = f1.y * o[e + 1] + f2.y * o2[e + 1];
+              o[e + 2] = f1.z * o[e + 2] + f2.z * o2[e + 2];
+              o[e + 3] = f1.w * o[e + 3] + f2.w * o2[e + 3];
             }
           }
           if (i > 0) group_any(bar_id, false);
@@ -1343,7 +1354,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(q_free(bi.seg & 1));
-          if (two) mbar_arrive(join_free);
+          if (two) mbar_arrive(join_free(bi.seg & 1));
         }
         group_any(bar_id, false);                     // `red` and the references may change again
       }
@@ -1690,8 +1701,8 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
         uint8_t* v = sm + stage * 4 * kHalfBox + 2 * kHalfBox + r * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          *reinterpret_cast<uint4*>(v + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(v + kHalfBox + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v + 16 * (k ^ (r & 7))) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v + kHalfBox + 16 * (k ^ (r & 7))) = make_uint4(0u, 0u, 0u, 0u);
         }
         smem_to_async();
       }
