@@ -145,6 +145,26 @@ def test_captured_graph_serves_changing_lengths(kind):
         other.check()
 
 
+def test_one_workspace_for_calls_in_turn():
+    """Calls of other formats, rows and lengths take turns on one workspace, with anything written to it in between."""
+    cases = [Case([5000], "bf16", 1, 16, seed=20), Case([9000, 300], "fp8", 2, 8, 3, seed=21), Case([700] * 9, "nvfp4", 4, seed=22),
+             Case([20000], "fp8", 1, 16, 8, seed=23), Case([3000, 4000], "bf16", 1, 16, 8, seed=24), Case([30000], "nvfp4", 1, 4, seed=25)]
+    ws = torch.empty(max(c.ws.numel() for c in cases), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(3)
+    for turn in range(3):
+        for i in rng.permutation(len(cases)):
+            c = cases[i]
+            c.ws = ws
+            c.out.fill_(float("nan"))
+            for _ in range(1 + turn):
+                c.run()
+            c.check(which=range(1))
+            if turn == 1:
+                ws.random_(0, 256)
+            elif turn == 2:
+                ws.zero_()
+
+
 @pytest.mark.parametrize("kind", KV)
 def test_two_streams_at_once(kind):
     cases = [Case([3000, 10], kind, seed=13), Case([128, 4000], kind, Q=4, group=8, seed=14)]
