@@ -11,10 +11,11 @@
 // m = max(m1, m2), l = sum 2^(mi - m) li, o = sum 2^(mi - m) oi, and the result is
 // o / l, lse = ln 2 * (m + log2 l). Probabilities, sums and states are fp32.
 //
-// Work split. The items are the (request, KV head, block) triples in that
-// order, W in all; CTA c takes items [W c / C, W (c + 1) / C). It finds them
-// from seq_lens itself, so the host needs no lengths and a captured graph
-// serves changing ones. A (request, KV head) row inside one CTA is finished
+// Work split. The (request, KV head, block) triples in that order are the items;
+// a (request, KV head) row is as long as its blocks plus row_cost (what starting
+// and finishing a row costs, in blocks), W in all, and CTA c takes the items in
+// [W c / C, W (c + 1) / C). It finds them from seq_lens itself, so the host needs
+// no lengths and a captured graph serves changing ones. A (request, KV head) row inside one CTA is finished
 // there; a row cut by CTA boundaries leaves one partial per CTA, which
 // paged_join_kernel joins in CTA order.
 #include <cuda.h>
@@ -55,6 +56,7 @@ struct PagedParams {
   float k_global, v_global, scale_log2;
   int B, Q, H, G, NB, P;
   int group, R;                     // query heads per KV head; rows Q * group
+  int row_cost;
   int by_row;                       // the cuts are listed by row
 };
 
@@ -93,21 +95,27 @@ struct Walk {
 };
 
 struct Range {
-  int64_t x0, x1, W;
-  int ctas;                         // CTAs that take items: at most W, so that none is empty
-  Walk at;                          // place of x0
-  int64_t row0;                     // first item of x0's row
+  int64_t W;                        // length of all rows, row_cost included
+  int64_t row0;                     // where the row of `at` starts in it
+  int64_t n0, n1;                   // items before the CTA's first and behind its last
+  int ctas;                         // CTAs that share W: at most W
+  Walk at;                          // place of the first item
 };
 
-// The CTA's item range, found by all of its threads (kThreads of them): each
-// sums the blocks of a run of requests; the thread whose run holds x0 walks it.
+// The CTA's items, found by all of its threads (kThreads of them): each sums a
+// run of requests; the threads whose runs hold the ends of the CTA's range walk
+// them.
 template <int kThreads>
 __device__ void find_range(const PagedParams& p, int cta, int ctas, int64_t* warp_sums, Range* shared, Range& r) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = tid * per, b1 = b0 + per < p.B ? b0 + per : p.B;
+  // blocks, and from bit 48 on the requests that have any
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += paged_blocks(p, b);
+  for (int b = b0; b < b1; ++b) {
+    const int nb = paged_blocks(p, b);
+    mine += nb + (static_cast<int64_t>(nb > 0) << 48);
+  }
   int64_t in = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -123,28 +131,48 @@ __device__ void find_range(const PagedParams& p, int cta, int ctas, int64_t* war
     if (w < warp) before += s;
     total += s;
   }
-  const int64_t W = total * p.G;
+  auto blocks = [](int64_t v) { return v & ((1ll << 48) - 1); };
+  auto length = [&](int64_t v) { return (blocks(v) + (v >> 48) * p.row_cost) * p.G; };
+  const int64_t W = length(total);
   if (W < ctas) ctas = static_cast<int>(W);
   const int64_t x0 = cta < ctas ? W * cta / ctas : W, x1 = cta < ctas ? W * (cta + 1) / ctas : W;
-  if (tid == 0) { shared->x0 = x0; shared->x1 = x1; shared->W = W; shared->ctas = ctas; }
-  if (x0 < x1 && x0 >= before * p.G && x0 < (before + mine) * p.G) {
-    int64_t base = before * p.G;
+  if (tid == 0) {
+    shared->W = W;
+    shared->ctas = ctas;
+    shared->n0 = shared->n1 = blocks(total) * p.G;   // for an end at W
+  }
+  __syncthreads();
+  const int64_t lo = length(before), hi = length(before + mine);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int64_t x = which ? x1 : x0;
+    if (x < lo || x >= hi) continue;
+    int64_t base = lo, done = blocks(before) * p.G;
     for (int b = b0; b < b1; ++b) {
       const int nb = paged_blocks(p, b);
-      const int64_t n = static_cast<int64_t>(nb) * p.G;
-      if (x0 < base + n) {
-        const int64_t d = x0 - base;
+      if (nb == 0) continue;
+      const int span = nb + p.row_cost;
+      if (x < base + static_cast<int64_t>(span) * p.G) {
         Walk w;
         w.b = b;
         w.nb = nb;
         w.L = paged_len(p, b);
-        w.g = static_cast<int>(d / nb);
-        w.blk = static_cast<int>(d - static_cast<int64_t>(w.g) * nb);
-        shared->at = w;
-        shared->row0 = x0 - w.blk;
+        w.g = static_cast<int>((x - base) / span);
+        const int64_t row0 = base + static_cast<int64_t>(w.g) * span;
+        const int d = static_cast<int>(x - row0);
+        w.blk = d > p.row_cost ? d - p.row_cost : 0;  // a row's cost lies in front of its blocks
+        const int64_t n = done + static_cast<int64_t>(w.g) * nb + w.blk;
+        if (which) {
+          shared->n1 = n;
+        } else {
+          shared->n0 = n;
+          shared->at = w;
+          shared->row0 = row0;
+        }
         break;
       }
-      base += n;
+      base += static_cast<int64_t>(span) * p.G;
+      done += static_cast<int64_t>(nb) * p.G;
     }
   }
   __syncthreads();
@@ -193,28 +221,28 @@ __device__ void paged_empty_requests(const PagedParams& p, int nthreads) {
 // row that starts in its range.
 __device__ void paged_describe_cuts(const PagedParams& p, const Range& r, int cta) {
   const int lane = threadIdx.x & 31;
+  int64_t left = r.n1 - r.n0;
   if (!p.by_row) {
     CutRow c{0, 0, 0, cta};
-    if (r.x0 < r.x1 && r.at.blk > 0 && paged_cta_of(r.row0, r.W, r.ctas) == cta - 1) {
+    if (left > 0 && r.at.blk > 0 && paged_cta_of(r.row0 + p.row_cost, r.W, r.ctas) == cta - 1) {
       c.b = r.at.b;
       c.g = r.at.g;
-      c.n = paged_cta_of(r.row0 + r.at.nb - 1, r.W, r.ctas) - (cta - 1) + 1;
+      c.n = paged_cta_of(r.row0 + p.row_cost + r.at.nb - 1, r.W, r.ctas) - (cta - 1) + 1;
     }
     if (lane == 0) p.cuts[cta] = c;
     return;
   }
-  if (r.x0 >= r.x1) return;
+  if (left <= 0) return;
   Walk w = r.at;
-  int64_t x = r.x0;
-  if (w.blk > 0) {                                   // a row begun elsewhere
-    x += w.nb - w.blk;
-    w.blk = w.nb - 1;
-    w.next(p);
-  }
-  while (x < r.x1) {
-    const int last = paged_cta_of(x + w.nb - 1, r.W, r.ctas);
-    if (lane == 0) p.cuts[w.b * p.G + w.g] = CutRow{w.b, w.g, last > cta ? last - cta + 1 : 0, cta + 1};
-    x += w.nb;
+  int64_t row0 = r.row0;
+  for (;;) {
+    if (w.blk == 0) {
+      const int last = paged_cta_of(row0 + p.row_cost + w.nb - 1, r.W, r.ctas);
+      if (lane == 0) p.cuts[w.b * p.G + w.g] = CutRow{w.b, w.g, last > cta ? last - cta + 1 : 0, cta + 1};
+    }
+    left -= w.nb - w.blk;
+    if (left <= 0) return;
+    row0 += w.nb + p.row_cost;
     w.blk = w.nb - 1;
     w.next(p);
   }
@@ -330,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
   find_range<kThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kThreads);
   if (warp == kWarps - 1) paged_describe_cuts(p, rg, cta);
-  if (rg.x0 >= rg.x1) return;
+  const int64_t items = rg.n1 - rg.n0;
+  if (items <= 0) return;
 
   uint32_t qf[8][4];
   float o[16][4], m_r[2], l_r[2], mul[2];
@@ -518,13 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
   asm volatile("cp.async.commit_group;" ::: "memory");
   bool from_start = cur.blk == 0;
   begin(cur);
-  for (int64_t x = rg.x0; x < rg.x1; ++x) {
-    const uint32_t stage = stage0 + static_cast<uint32_t>((x - rg.x0) & 1) * raw_bytes<kKv>();
+  for (int64_t x = 0; x < items; ++x) {
+    const uint32_t stage = stage0 + static_cast<uint32_t>(x & 1) * raw_bytes<kKv>();
     int npage = -1;
     nxt.next(p);
-    if (x + 1 < rg.x1) {
+    if (x + 1 < items) {
       npage = paged_page(p, nxt, threadIdx.x == 0);
-      if (npage >= 0) load_block<kKv>(p, stage0 + static_cast<uint32_t>((x + 1 - rg.x0) & 1) * raw_bytes<kKv>(), npage, nxt.g);
+      if (npage >= 0) load_block<kKv>(p, stage0 + static_cast<uint32_t>((x + 1) & 1) * raw_bytes<kKv>(), npage, nxt.g);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -547,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
     }
     __syncthreads();                                               // the stage and the tile are free
     const bool row_ends = cur.blk == cur.nb - 1;
-    if (row_ends || x + 1 == rg.x1) flush(cur, from_start, row_ends);
-    if (x + 1 < rg.x1 && row_ends) {
+    if (row_ends || x + 1 == items) flush(cur, from_start, row_ends);
+    if (x + 1 < items && row_ends) {
       from_start = true;
       begin(nxt);
     }
@@ -909,7 +938,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kAllThreads);
   if (warp == 3) paged_describe_cuts(p, rg, cta);
-  const int items = static_cast<int>(rg.x1 - rg.x0);
+  const int items = static_cast<int>(rg.n1 - rg.n0);
   bool ok = true;
 
   if (items > 0 && warp == 0) {
@@ -1283,18 +1312,6 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         const float* ref2 = row_ref + other * NR;
         float* alphas2 = row_alpha + other * NR;
         const uint32_t tO2 = tO + other * C::kOCols + lanes;
-        auto load_o = [&](uint32_t at, float (&o)[16]) {
-          tmem_ld16(at, o);
-          if (C::kStacked) {
-            float o1[16], o2[16];
-            tmem_ld16(at + NR, o1);
-            tmem_ld16(at + 2 * NR, o2);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += o1[e] + o2[e];
-          }
-          tmem_wait_ld();
-        };
         if (two && t < NR) {
           // the groups' common maximum and sum; alphas: what each group's O is multiplied by
           float l1 = red[t] + red[NR + t] + red[2 * NR + t] + red[3 * NR + t];
@@ -1311,24 +1328,36 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         if (two) group_any(bar_id, false);
 #pragma unroll 1
         for (int i = 0; i < RG / 16 && r0 + 16 * i < p.R; ++i) {
-          float o[16];
-          load_o(tOg + r0 + 16 * i, o);
+          constexpr int kParts = C::kStacked ? 3 : 1;
+          float o[kParts][16], o2[kParts][16];
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            tmem_ld16(tOg + k * NR + r0 + 16 * i, o[k]);
+            if (two) tmem_ld16(tO2 + k * NR + 16 * i, o2[k]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+#pragma unroll
+            for (int k = 1; k < kParts; ++k) {
+              o[0][e] += o[k][e];
+              o2[0][e] += o2[k][e];
+            }
+          }
           if (two) {
-            float o2[16];
-            load_o(tO2 + 16 * i, o2);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               const float4 f1 = *reinterpret_cast<const float4*>(alphas + 16 * i + e);
               const float4 f2 = *reinterpret_cast<const float4*>(alphas2 + 16 * i + e);
-              o[e] = f1.x * o[e] + f2.x * o2[e];
-              o[e + 1] = f1.y * o[e + 1] + f2.y * o2[e + 1];
-              o[e + 2] = f1.z * o[e + 2] + f2.z * o2[e + 2];
-              o[e + 3] = f1.w * o[e + 3] + f2.w * o2[e + 3];
+              o[0][e] = f1.x * o[0][e] + f2.x * o2[0][e];
+              o[0][e + 1] = f1.y * o[0][e + 1] + f2.y * o2[0][e + 1];
+              o[0][e + 2] = f1.z * o[0][e + 2] + f2.z * o2[0][e + 2];
+              o[0][e + 3] = f1.w * o[0][e + 3] + f2.w * o2[0][e + 3];
             }
           }
           if (i > 0) group_any(bar_id, false);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) stg(e)[t] = o[e];
+          for (int e = 0; e < 16; ++e) stg(e)[t] = o[0][e];
           group_any(bar_id, false);
 #pragma unroll 1
           for (int e = wl; e < 16; e += 4) {
@@ -1524,7 +1553,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
   find_range<kAllThreads>(p, cta, gridDim.x, warp_sums, &shared_range, rg);
   paged_empty_requests(p, kAllThreads);
   if (warp == 3) paged_describe_cuts(p, rg, cta);
-  const int items = static_cast<int>(rg.x1 - rg.x0);
+  const int items = static_cast<int>(rg.n1 - rg.n0);
   bool ok = true;
 
   if (items > 0 && warp == 0) {
@@ -1763,6 +1792,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
 
 // Joins the partials of a cut row, in CTA order. One CTA per (cut, group of
 // rows); with few rows the eight warps share a row's partials.
+template <int kChunk>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
   __shared__ float sm_o[kWarps][kDim];
   __shared__ float sm_m[kWarps], sm_l[kWarps];
@@ -1781,29 +1811,34 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto part_of = [&](int i) { return i == 0 ? paged_part(p, cta - 1, 1) : paged_part(p, cta - 1 + i, 0); };
-  // 32 partials at a time: their maxima and sums by lane, then their rows
-  for (int base = sub; live && base < cut.n; base += 32 * wpr) {
-    const int mine = base + lane * wpr;
+  // kChunk partials at a time, all loads in flight together: their maxima and sums by lane, and their rows
+#pragma unroll 1
+  for (int base = sub; live && base < cut.n; base += kChunk * wpr) {
+    float4 x[kChunk];
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      if (base + i * wpr < cut.n) x[i] = *reinterpret_cast<const float4*>(part_of(base + i * wpr) + row * kDim + 4 * lane);
+    const int mine = base + (lane & (kChunk - 1)) * wpr;
     const float* part = part_of(mine < cut.n ? mine : 0);
     const float m = mine < cut.n ? part[p.R * kDim + row] : -INFINITY;
     const float l = mine < cut.n ? part[p.R * (kDim + 1) + row] : 0.f;
     float top = fmaxf(M, m);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kEvery, top, o));
+    for (int o = kChunk / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kEvery, top, o));
     if (top == -INFINITY) continue;                  // every partial so far is empty
     const float was = ex2_approx(M - top), f = ex2_approx(m - top);
     float ls = f * l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(kEvery, ls, o);
+    for (int o = kChunk / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(kEvery, ls, o);
     M = top;
     L = L * was + ls;
     acc.x *= was; acc.y *= was; acc.z *= was; acc.w *= was;
-    const int count = (cut.n - base + wpr - 1) / wpr < 32 ? (cut.n - base + wpr - 1) / wpr : 32;
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(part_of(base + i * wpr) + row * kDim + 4 * lane);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
       const float fi = __shfl_sync(kEvery, f, i);
-      acc.x += fi * x.x; acc.y += fi * x.y; acc.z += fi * x.z; acc.w += fi * x.w;
+      if (base + i * wpr < cut.n) {
+        acc.x += fi * x[i].x; acc.y += fi * x[i].y; acc.z += fi * x[i].z; acc.w += fi * x[i].w;
+      }
     }
   }
   if (wpr > 1) {
@@ -1937,6 +1972,9 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
   const int tiles = (p.R + 15) / 16;
   const int mt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+  // measured: what a row costs against a block, in its kernel's form
+  const bool tc = a.kv == MSA_FP8_E4M3 || (a.kv == MSA_NVFP4 && mt <= 2);
+  p.row_cost = tc ? 5 : mt > 1 ? 3 : 2;
   cudaError_t err;
   const char* form = "mma";
   if (a.kv == MSA_FP8_E4M3) {
@@ -1954,9 +1992,12 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   }
   if (err != cudaSuccess) return err;
   if (ctas > 1) {
-    const int rpc = p.R <= 16 ? 1 : 8;
+    // few rows: a CTA for each query row, whose warps share its many partials, 32 in flight each (165
+    // registers: one CTA per SM); else a warp for each, with mostly two or three partials
+    const bool few = static_cast<int64_t>(cuts) * p.R <= sms;
+    const int rpc = few ? 1 : 8;
     const int chunks = (p.R + rpc - 1) / rpc;
-    err = launch_pdl(paged_join_kernel, dim3(cuts * chunks), dim3(kThreads), 0, stream, p, rpc);
+    err = launch_pdl(few ? paged_join_kernel<32> : paged_join_kernel<4>, dim3(cuts * chunks), dim3(kThreads), 0, stream, p, rpc);
     if (err != cudaSuccess) return err;
   }
   rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"
