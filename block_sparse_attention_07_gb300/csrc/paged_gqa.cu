@@ -681,6 +681,12 @@ struct TcCfg {
   static constexpr int kConv = kFp8 ? 0 : 4 + 4 * kVGroups;    // expanding warps
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kWarpsAll = kConv0 + kConv;
+  // Registers per thread, moved between the warpgroups from what the launch gives each alike (65,536 over the
+  // threads, in eights): the sum over the warpgroups stays the launch's.
+  static constexpr int kRegs = 65536 / (32 * kWarpsAll) / 8 * 8;
+  static constexpr int kRegsCtl = 64, kRegsConv = kFp8 ? 0 : 56;
+  static constexpr int kRegsFit = (kRegs * (kWarpsAll / 4) - kRegsCtl - (kConv / 4) * kRegsConv) / kGroups / 8 * 8;
+  static constexpr int kRegsSoft = kRegsFit > 232 ? 232 : kRegsFit;
   static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
   static constexpr int kPBufs = NR > 64 ? 1 : 2;
   static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
@@ -792,6 +798,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -941,6 +952,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   const int items = static_cast<int>(rg.n1 - rg.n0);
   bool ok = true;
 
+  if (warp < C::kSoft0) {
+  regs_dec<C::kRegsCtl>();
   if (items > 0 && warp == 0) {
     // ----------------------------------------------------------- copies --
     if (lane == 0) {
@@ -1055,8 +1068,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     __syncwarp();
     mbar_wait(done_bar, 0);
     __syncwarp();
-  } else if (items > 0 && warp >= C::kSoft0 && warp < C::kConv0) {
+  }
+  } else if (warp < C::kConv0) {
     // ---------------------------------------------------------- softmax --
+    regs_inc<C::kRegsSoft>();
     constexpr int RG = C::kRG;
     const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
     const int t = 32 * wl + lane;                   // token of S, dim of O
@@ -1120,7 +1135,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (lane == 0) mbar_arrive(q_full(qb));
       return true;
     };
-    if (!C::kAlt || grp == 0) ok = put_q(0);
+    if (items > 0 && (!C::kAlt || grp == 0)) ok = put_q(0);
     float l[RG];
     int stage = C::kAlt ? grp : 0;
     uint32_t joins = 0;                             // parity of the joins so far on either segment parity (bits 0, 1)
@@ -1389,7 +1404,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
-  } else if (items > 0 && C::kConv > 0 && warp >= C::kConv0) {
+  } else if (C::kConv > 0) {
+    regs_dec<C::kConv ? C::kRegsConv : C::kRegsCtl>();
     // -------------------------------------------------- NVFP4 expansion --
     // Four warps expand K into tensor memory, the others V into shared memory; a
     // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of eight
@@ -1414,45 +1430,40 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (!isv) tmem_fence_after();
       uint8_t* tile = sm + C::oTiles + (n & 1) * 2 * kHalfBox + row * 128;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 w[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          w[q] = *reinterpret_cast<const uint4*>(src + s * C::kStage + ((32 * half + 16 * q) ^ swz));
-        uint32_t sc = *reinterpret_cast<const uint32_t*>(ssrc + s * C::kStage + 4 * half);
-        if (half == 1) {
+      for (int c = 0; c < 4; ++c) {
+        // 32 values, two scale groups
+        uint4 w = *reinterpret_cast<const uint4*>(src + s * C::kStage + ((16 * c) ^ swz));
+        uint32_t sc = *reinterpret_cast<const uint16_t*>(ssrc + s * C::kStage + 2 * c);
+        if (c == 3) {
           __syncwarp();
           if (lane == 0) mbar_arrive(empty(s));
         }
         if (dead) {
           sc = 0u;
-          w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
+          w = make_uint4(0u, 0u, 0u, 0u);
         }
-        uint32_t h[32];
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
+        const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
+        const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+        uint32_t h[16];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t words[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc >> (16 * q)));
-          const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
-          const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+        for (int k = 0; k < 4; ++k) {
+          uint32_t e[4];
+          e2m1x8_to_f16x2x4(words[k], e);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t e[4];
-            e2m1x8_to_f16x2x4(words[k], e);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&e[j]), s2[k >> 1]);
-              h[16 * q + 4 * k + j] = *reinterpret_cast<const uint32_t*>(&y);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&e[j]), s2[k >> 1]);
+            h[4 * k + j] = *reinterpret_cast<const uint32_t*>(&y);
           }
         }
         if (isv) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(tile + half * kHalfBox + ((c << 4) ^ swz_v)) =
-                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(tile + (c >> 1) * kHalfBox + (((4 * (c & 1) + k) << 4) ^ swz_v)) =
+                make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
         } else {
-          tmem_st32(tK + lanes + (n & 1) * (kDim / 2) + 32 * half, h);
+          tmem_st16(tK + lanes + (n & 1) * (kDim / 2) + 16 * c, reinterpret_cast<const float*>(h));
         }
       }
       if (isv) {
