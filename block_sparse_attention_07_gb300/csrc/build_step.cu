@@ -62,20 +62,28 @@ __device__ __forceinline__ StepReq step_req(const StepArgs& p, int b) {
   return r;
 }
 
-// Latency bound: lengths in, one scan, stores out. Shared memory: start[B + 1]
-// (places of the tokens, held to T) and first[B] (entry in the free list, or
-// -1 for a refused request).
+// What the CTAs keep of a request, in shared memory.
+struct StepSlot {
+  int ctx, off;                 // tokens cached; rotary offset
+  int last;                     // page of the last cached block, which new tokens may fill
+  int pages;                    // new pages before this request; negative (~pages): refused
+};
+
+// Latency bound: everything a request needs is loaded at once, before the scan;
+// after it come only stores. Shared memory: start[B + 1], the places of the
+// tokens (held to T), and a StepSlot per request.
 __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_constant__ StepArgs p) {
   extern __shared__ int32_t sm[];
   __shared__ StepScan warp_sums[kStepWarps];
   __shared__ int taken;
   griddep_launch_dependents();
   griddep_wait();
-  int32_t* start = sm;
-  int32_t* first = sm + p.B + 1;
+  StepSlot* slots = reinterpret_cast<StepSlot*>(sm);
+  int32_t* start = sm + 4 * p.B;
   const int tid = threadIdx.x;
   const bool lead = blockIdx.x == 0;
   if (tid == 0) taken = 0;
+  const int head = *p.free_head;
 
   // each thread sums a run of consecutive requests
   const int per = (p.B + kStepThreads - 1) / kStepThreads;
@@ -85,10 +93,15 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
     const StepReq r = step_req(p, b);
     mine.tokens += r.add;
     mine.pages += r.need;
+    StepSlot s;
+    s.ctx = r.ctx;
+    s.off = p.pos_offset ? p.pos_offset[b] : 0;
+    s.last = r.len_ok && r.ctx % kBlock != 0 ? p.block_table[static_cast<int64_t>(b) * p.NB + r.ctx / kBlock] : -1;
+    s.pages = 0;
+    slots[b] = s;
   }
   StepScan total;
   StepScan at = block_exclusive(mine, warp_sums, total);
-  const int head = *p.free_head;
   int got = 0;
   for (int b = b0; b < b1; ++b) {
     const StepReq r = step_req(p, b);
@@ -96,7 +109,9 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
     const bool placed = r.len_ok && end_tok <= p.T;
     const bool fits = r.need == 0 || (head >= 0 && end_page <= p.F);
     start[b] = static_cast<int32_t>(at.tokens < p.T ? at.tokens : p.T);
-    first[b] = placed && fits ? (r.need == 0 ? 0 : static_cast<int32_t>(head + at.pages)) : -1;
+    // (a count past the free list belongs to refused requests alone, but for those that need no page)
+    const int before = static_cast<int>(at.pages < INT32_MAX ? at.pages : INT32_MAX);
+    slots[b].pages = placed && fits ? before : ~before;
     if (placed && fits) got += r.need;
     if (lead) {
       if (!placed) set_flag(p.flags, MSA_FLAG_BAD_SEQLEN);
@@ -118,18 +133,22 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
     *p.free_head_out = head + taken;
   }
 
-  // new table entries: a warp per request
-  const int lane = tid & 31;
-  for (int b = blockIdx.x * kStepWarps + (tid >> 5); b < p.B; b += gridDim.x * kStepWarps) {
-    if (first[b] < 0) continue;
-    const StepReq r = step_req(p, b);
-    int32_t* row = p.block_table + static_cast<int64_t>(b) * p.NB + blocks_of(r.ctx);
-    for (int i = lane; i < r.need; i += 32) {
-      const int page = p.free_pages[first[b] + i];
-      const bool ok = page >= 0 && page < p.P;
-      if (!ok) set_flag(p.flags, MSA_FLAG_BAD_PAGE);
-      row[i] = ok ? page : -1;
+  // new table entries, a thread per page: the pages before `limit` may be taken
+  const int64_t left = head < 0 ? 0 : p.F - static_cast<int64_t>(head);
+  const int limit = static_cast<int>(total.pages < left ? total.pages : left);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kStepThreads + tid; i < limit;
+       i += static_cast<int64_t>(gridDim.x) * kStepThreads) {
+    // the last request whose first page is at or before i
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1, s = slots[mid].pages;
+      if ((s < 0 ? ~s : s) <= i) lo = mid; else hi = mid - 1;
     }
+    if (slots[lo].pages < 0) continue;
+    const int page = p.free_pages[head + i];
+    const bool ok = page >= 0 && page < p.P;
+    if (!ok) set_flag(p.flags, MSA_FLAG_BAD_PAGE);
+    p.block_table[static_cast<int64_t>(lo) * p.NB + blocks_of(slots[lo].ctx) + (i - slots[lo].pages)] = ok ? page : -1;
   }
 
   // tokens, four consecutive ones per thread
@@ -144,7 +163,7 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
       const int mid = (lo + hi) >> 1;
       if (start[mid + 1] <= i0) lo = mid + 1; else hi = mid;
     }
-    int b = lo, cur = -1, ctx = 0, off = 0;
+    int b = lo;
     int64_t slot[kTokPerThread];
     int32_t pos[kTokPerThread];
 #pragma unroll
@@ -154,16 +173,12 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
       pos[k] = 0;
       if (i >= placed_tokens) continue;
       while (start[b + 1] <= i) ++b;
-      if (b != cur) {
-        cur = b;
-        ctx = p.ctx_lens[b];
-        off = p.pos_offset ? p.pos_offset[b] : 0;
-      }
-      const int64_t tok = static_cast<int64_t>(ctx) + (i - start[b]);
-      pos[k] = static_cast<int32_t>(static_cast<uint32_t>(tok) + static_cast<uint32_t>(off));
-      if (first[b] < 0) continue;
-      const int64_t blk = tok / kBlock, old = blocks_of(ctx);
-      const int page = blk < old ? p.block_table[static_cast<int64_t>(b) * p.NB + blk] : p.free_pages[first[b] + (blk - old)];
+      const StepSlot s = slots[b];
+      const int64_t tok = static_cast<int64_t>(s.ctx) + (i - start[b]);
+      pos[k] = static_cast<int32_t>(static_cast<uint32_t>(tok) + static_cast<uint32_t>(s.off));
+      if (s.pages < 0) continue;
+      const int64_t blk = tok / kBlock, old = blocks_of(s.ctx);
+      const int page = blk < old ? s.last : p.free_pages[head + s.pages + (blk - old)];
       if (page < 0 || page >= p.P) {
         set_flag(p.flags, MSA_FLAG_BAD_PAGE);
         continue;
@@ -197,7 +212,12 @@ cudaError_t launch_build_step(const StepArgs& a, cudaStream_t stream, DispatchRe
   int64_t grid = (static_cast<int64_t>(a.T) + kTokPerPass - 1) / kTokPerPass;
   const int64_t cap = 4ll * device_sm_count();
   if (grid > cap) grid = cap;
-  const size_t smem = (2ull * a.B + 1) * sizeof(int32_t);
+  const size_t smem = (5ull * a.B + 1) * sizeof(int32_t);
+  if (smem > 40 * 1024) {
+    const cudaError_t set = cudaFuncSetAttribute(build_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem));
+    if (set != cudaSuccess) return set;
+  }
   const cudaError_t err = launch_pdl(build_step_kernel, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads), smem,
                                      stream, a);
   if (err != cudaSuccess) return err;

@@ -14,9 +14,9 @@
 // warp. A warp takes `passes` groups of four rows of one token.
 //
 // Phases: theta^(-2i/128) / 2 pi is held as a 64-bit fraction of a turn, so that
-// position times it, modulo one turn, is one integer product: its rounding,
-// 2^-65 of a turn times the position, stays below 2^-33 for any 32-bit position,
-// far under the fp32 rounding of the sine's argument.
+// position times it, modulo one turn, is one integer product. The fraction comes
+// from doubles, 2^-51 relative: a phase is off by at most 2^-22 of a turn at the
+// largest 32-bit position.
 #include <cmath>
 #include <cstring>
 
@@ -24,7 +24,7 @@
 
 namespace msa {
 
-constexpr int kMropeWarps = 8;
+constexpr int kMropeWarps = 4, kMropeCtas = 7;    // warps per CTA, CTAs per SM (72 registers)
 
 struct MropeParams {
   InsertParams ins;
@@ -132,17 +132,17 @@ __device__ __forceinline__ void store_idx16(const InsertParams& p, int64_t row, 
   if (l == 0) p.idx_scale[row] = s;
 }
 
-__global__ void __launch_bounds__(32 * kMropeWarps) qk_norm_mrope_insert_kernel(const __grid_constant__ MropeParams pp) {
+__global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_insert_kernel(const __grid_constant__ MropeParams pp) {
   griddep_launch_dependents();
   griddep_wait();
   const InsertParams& p = pp.ins;
   const int lane = threadIdx.x & 31, l = lane & 7;
+  const int nq = pp.H, nk = p.G, ni = pp.idx_q != nullptr ? pp.I : 0;
+  const int rows = nq + 2 * nk + 2 * ni;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * kMropeWarps + (threadIdx.x >> 5);
   const int64_t t = wid / pp.parts;
   const int part = static_cast<int>(wid - t * pp.parts);
   if (t >= p.T) return;
-  const int nq = pp.H, nk = p.G, ni = pp.idx_q != nullptr ? pp.I : 0;
-  const int rows = nq + 2 * nk + 2 * ni;
 
   // cos and sin of the lane's 8 pairs (8 l + i): each is computed by one of the
   // four lanes that use it
@@ -167,8 +167,65 @@ __global__ void __launch_bounds__(32 * kMropeWarps) qk_norm_mrope_insert_kernel(
   const bool held = slot >= 0 && slot < p.num_slots;
   if (slot >= p.num_slots && part == 0 && lane == 0) set_flag(p.flags, MSA_FLAG_BAD_SLOT);
 
-  for (int r0 = 4 * part; r0 < rows; r0 += 4 * pp.parts) {
-    const int r = r0 + (lane >> 3);
+  auto weights = [&](const float* wv, float (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(wv + (i < 2 ? 8 * l + 4 * i : 64 + 8 * l + 4 * (i - 2)));
+      w[4 * i] = f.x; w[4 * i + 1] = f.y; w[4 * i + 2] = f.z; w[4 * i + 3] = f.w;
+    }
+  };
+  // 1 / sqrt(mean of the row's squares + eps), by its 8 lanes
+  auto row_scale = [&](const float (&x)[16]) {
+    float s2[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s2[i & 1] = fmaf(x[i], x[i], s2[i & 1]);
+    float ss = s2[0] + s2[1];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return rsqrtf(fmaf(ss, 1.0f / kDim, pp.eps));
+  };
+
+  // Most rows are queries, four at a time: with their weights folded into the cosines and sines a pair is four
+  // products and two scalings. The next rows are on their way while these are computed.
+  const int q_passes = nq / 4;
+  int pass = part;
+  if (pass < q_passes) {
+    float wc[8], ws[8], vs[8], vc[8];
+    {
+      float w[16];
+      weights(pp.wq, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        wc[i] = w[i] * cs[i]; ws[i] = w[i] * sn[i];
+        vs[i] = w[8 + i] * sn[i]; vc[i] = w[8 + i] * cs[i];
+      }
+    }
+    const int64_t first = (t * nq + 4 * pass + (lane >> 3)) * kDim + 8 * l, hop = 4ll * pp.parts * kDim;
+    const uint16_t* src = pp.q + first;
+    uint16_t* dst = pp.q_out + first;
+    uint4 lo = *reinterpret_cast<const uint4*>(src), hi = *reinterpret_cast<const uint4*>(src + 64);
+    for (; pass < q_passes; pass += pp.parts, dst += hop) {
+      float x[16], y[16];
+      unpack8(lo, x);
+      unpack8(hi, x + 8);
+      if (pass + pp.parts < q_passes) {
+        src += hop;
+        lo = *reinterpret_cast<const uint4*>(src);
+        hi = *reinterpret_cast<const uint4*>(src + 64);
+      }
+      const float rinv = row_scale(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = (x[i] * wc[i] - x[8 + i] * vs[i]) * rinv;
+        y[8 + i] = (x[i] * ws[i] + x[8 + i] * vc[i]) * rinv;
+      }
+      *reinterpret_cast<uint4*>(dst) = pack8(y);
+      *reinterpret_cast<uint4*>(dst + 64) = pack8(y + 8);
+    }
+  }
+  // the rows behind them: any last queries, keys, values, index rows
+  for (; 4 * pass < rows; pass += pp.parts) {
+    const int r = 4 * pass + (lane >> 3);
     const bool live = r < rows;
     // kind 0 q, 1 k, 2 v, 3 index q, 4 index k
     int kind = 0, h = live ? r : 0;
@@ -184,25 +241,17 @@ __global__ void __launch_bounds__(32 * kMropeWarps) qk_norm_mrope_insert_kernel(
     float x[16];
     unpack8(*reinterpret_cast<const uint4*>(src + 8 * l), x);
     unpack8(*reinterpret_cast<const uint4*>(src + 64 + 8 * l), x + 8);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rinv = row_scale(x);
     if (kind != 2) {
-      const float rinv = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(ss, 1.0f / kDim, pp.eps)));
       float w[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(wv + (i < 2 ? 8 * l + 4 * i : 64 + 8 * l + 4 * (i - 2)));
-        w[4 * i] = f.x; w[4 * i + 1] = f.y; w[4 * i + 2] = f.z; w[4 * i + 3] = f.w;
-      }
+      weights(wv, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float a = x[i] * rinv * w[i], b = x[8 + i] * rinv * w[8 + i];
-        // rounded to bf16 here: what the outputs hold and the caches quantise
-        x[i] = bf16_bits_to_f32(static_cast<uint16_t>(pack_bf16x2(a * cs[i] - b * sn[i], 0.f) & 0xFFFF));
-        x[8 + i] = bf16_bits_to_f32(static_cast<uint16_t>(pack_bf16x2(a * sn[i] + b * cs[i], 0.f) & 0xFFFF));
+        // as above, and rounded to bf16 here: what the outputs hold and the caches quantise
+        const float a = (x[i] * (w[i] * cs[i]) - x[8 + i] * (w[8 + i] * sn[i])) * rinv;
+        const float b = (x[i] * (w[i] * sn[i]) + x[8 + i] * (w[8 + i] * cs[i])) * rinv;
+        x[i] = bf16_bits_to_f32(static_cast<uint16_t>(pack_bf16x2(a, 0.f) & 0xFFFF));
+        x[8 + i] = bf16_bits_to_f32(static_cast<uint16_t>(pack_bf16x2(b, 0.f) & 0xFFFF));
       }
     }
     if (live && (kind == 0 || kind == 3)) {
@@ -239,15 +288,21 @@ cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_ax
   pp.H = a.H;
   pp.I = a.I;
   constexpr double kTwoPi = 6.283185307179586476925286766559;
+  // theta^(-2i/128) as a product of two powers, i = 8 hi + lo: 16 powers instead of 64 on every call
+  double hi[8], lo[8];
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = pow(static_cast<double>(a.theta), -16.0 * i / kDim) / kTwoPi;
+    lo[i] = pow(static_cast<double>(a.theta), -2.0 * i / kDim);
+  }
   for (int i = 0; i < kDim / 2; ++i) {
-    pp.turn[i] = static_cast<uint64_t>(ldexp(pow(static_cast<double>(a.theta), -2.0 * i / kDim) / kTwoPi, 64));
+    pp.turn[i] = static_cast<uint64_t>(ldexp(hi[i >> 3] * lo[i & 7], 64));
     pp.axis[i] = axes.axis[i];
   }
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
   const int passes = (rows + 3) / 4;
   // one warp takes a whole token when there are tokens enough to fill the GPU's
   // warps; with fewer a token's rows are spread over up to `passes` warps
-  const int64_t want = 16ll * kMropeWarps / 4 * device_sm_count();
+  const int64_t want = 32ll * device_sm_count();
   int64_t parts = (want + a.ins.T - 1) / a.ins.T;
   if (parts > passes) parts = passes;
   pp.parts = static_cast<int>(parts);
