@@ -12,7 +12,7 @@
 
 namespace msa {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kTokPerThread = 4;
 constexpr int kTokPerPass = kStepThreads * kTokPerThread;
@@ -210,7 +210,9 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(const __grid_c
 
 cudaError_t launch_build_step(const StepArgs& a, cudaStream_t stream, DispatchRecord* rec) {
   int64_t grid = (static_cast<int64_t>(a.T) + kTokPerPass - 1) / kTokPerPass;
-  const int64_t cap = 4ll * device_sm_count();
+  // Short CTAs and many of them while the scan is short (prefill chunk of 524K tokens: 6.7 us; 256 threads 7.4,
+  // 4 CTAs per SM 10.0); with many requests every CTA scans them all, so fewer.
+  const int64_t cap = (a.B <= 512 ? 16ll : 4ll) * device_sm_count();
   if (grid > cap) grid = cap;
   const size_t smem = (5ull * a.B + 1) * sizeof(int32_t);
   if (smem > 40 * 1024) {
