@@ -677,14 +677,14 @@ struct TcCfg {
   static constexpr int kGroups = 2;
   static constexpr int kRG = kAlt ? NR : NR / 2;               // rows per softmax group
   static constexpr int kSoftArrive = kAlt ? 4 : 8;             // softmax warps per block
-  static constexpr int kVGroups = NR <= 16 ? 2 : 1;            // groups of 4 warps that expand V, taking turns
-  static constexpr int kConv = kFp8 ? 0 : 4 + 4 * kVGroups;    // expanding warps
+  static constexpr int kTurns = NR <= 16 ? 2 : 1;              // groups of 4 warps that expand K, and V, taking turns
+  static constexpr int kConv = kFp8 ? 0 : 8 * kTurns;          // expanding warps
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kWarpsAll = kConv0 + kConv;
   // Registers per thread, moved between the warpgroups from what the launch gives each alike (65,536 over the
   // threads, in eights): the sum over the warpgroups stays the launch's.
   static constexpr int kRegs = 65536 / (32 * kWarpsAll) / 8 * 8;
-  static constexpr int kRegsCtl = 64, kRegsConv = kFp8 ? 0 : 56;
+  static constexpr int kRegsCtl = kFp8 ? 64 : 56, kRegsConv = kFp8 ? 0 : 56;
   static constexpr int kRegsFit = (kRegs * (kWarpsAll / 4) - kRegsCtl - (kConv / 4) * kRegsConv) / kGroups / 8 * 8;
   static constexpr int kRegsSoft = kRegsFit > 232 ? 232 : kRegsFit;
   static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
@@ -1407,20 +1407,20 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   } else if (C::kConv > 0) {
     regs_dec<C::kConv ? C::kRegsConv : C::kRegsCtl>();
     // -------------------------------------------------- NVFP4 expansion --
-    // Four warps expand K into tensor memory, the others V into shared memory; a
+    // Four warps at a time expand K into tensor memory, four V into shared memory; a
     // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of eight
     // rows in eight banks, and so does the V tile's for the stores.
-    const int vg = ((warp - C::kConv0) >> 2) - 1;   // -1: K
-    const bool isv = vg >= 0;
-    const int row = 32 * (warp & 3) + lane, step = isv ? C::kVGroups : 1;
+    const int cg = (warp - C::kConv0) >> 2, turn = cg % C::kTurns;
+    const bool isv = cg >= C::kTurns;
+    const int row = 32 * (warp & 3) + lane;
     constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint8_t* src = sm + C::oStage + (isv ? codes : 0) + row * (kDim / 2);
     const uint8_t* ssrc = sm + C::oStage + 2 * codes + (isv ? scales : 0) + row * (kDim / 16);
     const int swz = ((row >> 1) & 3) << 4, swz_v = (row & 7) << 4;
-    int s = isv ? vg : 0;
+    int s = turn;
     uint32_t ph = 0;
-    for (int n = isv ? vg : 0; n < items; n += step) {
+    for (int n = turn; n < items; n += C::kTurns) {
       ok = mbar_wait(full(s), ph);
       if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1) && ok;
       ok = __all_sync(kEvery, ok);
@@ -1474,7 +1474,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
-      s += step;
+      s += C::kTurns;
       if (s >= C::kStages) { s -= C::kStages; ph ^= 1u; }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
