@@ -249,21 +249,19 @@ __device__ void paged_describe_cuts(const PagedParams& p, const Range& r, int ct
 }
 
 // ---------------------------------------------------------------------------
-// All formats, any number of rows, on warp-level mma. Eight warps: MT row tiles
-// of 16 x 8 / MT token slices. Blocks arrive by cp.async into two stages; FP8
-// and NVFP4 values are expanded (exactly) to f16 in shared memory.
+// bf16 K/V and up to 16 query rows, on warp-level mma. Eight warps take 16 tokens
+// of every block each, with their own running maxima; blocks arrive by cp.async
+// into two stages. What bounds it is the cache's bytes.
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kHalfBox = kBlock * 128;               // 128 rows of 64 16-bit values, swizzled
 
+// Bytes of a block's K and V of one head, scales included.
 template <int kKv>
 __host__ __device__ constexpr uint32_t raw_bytes() {
   return kKv == MSA_BF16 ? 4 * kHalfBox : kKv == MSA_FP8_E4M3 ? 2 * kBlock * kDim : 2 * (kBlock * kDim / 2 + kBlock * kDim / 16);
 }
-template <int kKv>
-__host__ __device__ constexpr uint32_t simple_smem() {
-  return 2 * raw_bytes<kKv>() + 4 * kHalfBox + kWarps * 16 * 2 * 4;
-}
+constexpr uint32_t kMmaSmem = 2 * 4 * kHalfBox + kWarps * 16 * kDim * 4 + kWarps * 16 * 2 * 4;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -275,80 +273,26 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int row, int c) {
   return tile + (c >> 3) * kHalfBox + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
-template <int kKv>
 __device__ __forceinline__ void load_block(const PagedParams& p, uint32_t stage, int page, int g) {
   const int64_t slab = static_cast<int64_t>(page) * p.G + g;
-  const int tid = threadIdx.x;
-  if (kKv == MSA_BF16) {
-    const uint8_t* k = p.k + slab * (kBlock * kDim * 2);
-    const uint8_t* v = p.v + slab * (kBlock * kDim * 2);
-    for (int i = tid; i < kBlock * 16; i += kThreads) {
-      cp_async16(tile_at(stage, i >> 4, i & 15), k + i * 16);
-      cp_async16(tile_at(stage + 2 * kHalfBox, i >> 4, i & 15), v + i * 16);
-    }
-  } else {
-    constexpr int row = kKv == MSA_FP8_E4M3 ? kDim : kDim / 2;
-    constexpr int n = kBlock * row / 16;
-    const uint8_t* k = p.k + slab * (kBlock * row);
-    const uint8_t* v = p.v + slab * (kBlock * row);
-    for (int i = tid; i < n; i += kThreads) {
-      cp_async16(stage + i * 16, k + i * 16);
-      cp_async16(stage + kBlock * row + i * 16, v + i * 16);
-    }
-    if (kKv == MSA_NVFP4) {
-      const int64_t at = slab * (kBlock * kDim / 16);
-      const uint32_t sc = stage + 2 * kBlock * row;
-      if (tid < 64) cp_async16(sc + tid * 16, p.ks + at + tid * 16);
-      else if (tid < 128) cp_async16(sc + tid * 16, p.vs + at + (tid - 64) * 16);
-    }
+  const uint8_t* k = p.k + slab * (kBlock * kDim * 2);
+  const uint8_t* v = p.v + slab * (kBlock * kDim * 2);
+  for (int i = threadIdx.x; i < kBlock * 16; i += kThreads) {
+    cp_async16(tile_at(stage, i >> 4, i & 15), k + i * 16);
+    cp_async16(tile_at(stage + 2 * kHalfBox, i >> 4, i & 15), v + i * 16);
   }
 }
 
-// Expands a raw stage into the f16 tile; V rows from `live` on become zero.
-template <int kKv>
-__device__ __forceinline__ void expand_block(uint8_t* sm, uint32_t raw, uint32_t base, uint32_t tile, int live) {
-  for (int i = threadIdx.x; i < 2 * kBlock * 16; i += kThreads) {
-    const int isv = i >= kBlock * 16, row = (i >> 4) & (kBlock - 1), c = i & 15;
-    uint32_t h[4];
-    if (kKv == MSA_FP8_E4M3) {
-      const uint2 w = *reinterpret_cast<const uint2*>(sm + (raw - base) + isv * kBlock * kDim + row * kDim + 8 * c);
-      h[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x & 0xFFFF));
-      h[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x >> 16));
-      h[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y & 0xFFFF));
-      h[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y >> 16));
-    } else {
-      constexpr int rowb = kDim / 2;
-      const uint8_t* st = sm + (raw - base);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(st + isv * kBlock * rowb + row * rowb + 4 * c);
-      const uint8_t s = st[2 * kBlock * rowb + isv * (kBlock * kDim / 16) + row * (kDim / 16) + (c >> 1)];
-      e2m1x8_to_f16x2x4(w, h);
-      const uint32_t s2 = e4m3x2_to_f16x2(static_cast<uint16_t>(s | (s << 8)));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<const __half2*>(&s2));
-        h[k] = *reinterpret_cast<const uint32_t*>(&y);
-      }
-    }
-    if (isv && row >= live) h[0] = h[1] = h[2] = h[3] = 0u;
-    *reinterpret_cast<uint4*>(sm + (tile_at(tile + isv * 2 * kHalfBox, row, c) - base)) = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-}
-
-template <int kKv, int MT>
 __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_constant__ PagedParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Range shared_range;
   __shared__ int64_t warp_sums[kWarps];
-  constexpr int kSlices = kWarps / MT, kSliceTok = kBlock / kSlices;
-  constexpr bool kF16 = kKv != MSA_BF16;
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
-  const uint32_t stage0 = base, extra = base + 2 * raw_bytes<kKv>();
-  float* merge = reinterpret_cast<float*>(sm + 2 * raw_bytes<kKv>());      // the f16 tile; row merges between blocks
-  float* merge_m = reinterpret_cast<float*>(sm + 2 * raw_bytes<kKv>() + 4 * kHalfBox);
+  float* merge = reinterpret_cast<float*>(sm + 2 * 4 * kHalfBox);          // the warps' states at a row's end
+  float* merge_m = merge + kWarps * 16 * kDim;
   float* merge_l = merge_m + kWarps * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mt = warp % MT, sl = warp / MT;
   const int gr = lane >> 2, c = lane & 3;
 
   griddep_launch_dependents();
@@ -362,42 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
   if (items <= 0) return;
 
   uint32_t qf[8][4];
-  float o[16][4], m_r[2], l_r[2], mul[2];
+  float o[16][4], m_r[2], l_r[2];
   int limit[2];                                   // last token each of the thread's two rows sees
 
   auto begin = [&](const Walk& w) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = 16 * mt + gr + 8 * r;
+      const int row = gr + 8 * r;
       const bool live = row < p.R;
       const uint16_t* qh = p.q + (live ? paged_head(p, w.b, w.g, row) : 0) * kDim;
       limit[r] = live ? w.L - p.Q + row / p.group : -1;
-      float amax = 0.f;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         qf[s][r] = live ? *reinterpret_cast<const uint32_t*>(qh + 16 * s + 2 * c) : 0u;
         qf[s][2 + r] = live ? *reinterpret_cast<const uint32_t*>(qh + 16 * s + 8 + 2 * c) : 0u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t wq = qf[s][2 * h + r];
-          amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(wq & 0xFFFF)), fabsf(bf16_bits_to_f32(wq >> 16))));
-        }
-      }
-      mul[r] = p.scale_log2;
-      if (kF16) {
-        // f16 operands: the row times an exact power of two that brings it into f16's range
-        amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(kEvery, amax, 2));
-        const int sh = fp16_shift_for(amax);
-        const float f = exp2_int(sh);
-        mul[r] = p.scale_log2 * p.k_global * exp2_int(-sh);
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t wq = qf[s][2 * h + r];
-            qf[s][2 * h + r] = pack_f16x2(bf16_bits_to_f32(wq & 0xFFFF) * f, bf16_bits_to_f32(wq >> 16) * f);
-          }
       }
       m_r[r] = -INFINITY;
       l_r[r] = 0.f;
@@ -406,11 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
     for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   };
 
-  // One block's tokens of this warp's slice, 16 at a time.
+  // One block's 16 tokens of this warp.
   auto compute = [&](const Walk& w, uint32_t tile) {
     const bool edge = (w.blk + 1) * kBlock - 1 > w.L - p.Q;      // some row's limit lies before the block's end
-#pragma unroll 1
-    for (int t16 = sl * kSliceTok; t16 < (sl + 1) * kSliceTok; t16 += 16) {
+    const int t16 = 16 * warp;
+    {
       float sc[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
@@ -420,13 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
         for (int nt = 0; nt < 2; ++nt) {
           uint32_t b[4];
           ldsm_x4(tile_at(tile, t16 + 8 * nt + (lane & 7), 4 * sp + (lane >> 3)), b[0], b[1], b[2], b[3]);
-          if (kF16) {
-            mma_f16(sc[nt], qf[2 * sp], b[0], b[1]);
-            mma_f16(sc[nt], qf[2 * sp + 1], b[2], b[3]);
-          } else {
-            mma_bf16(sc[nt], qf[2 * sp], b[0], b[1]);
-            mma_bf16(sc[nt], qf[2 * sp + 1], b[2], b[3]);
-          }
+          mma_bf16(sc[nt], qf[2 * sp], b[0], b[1]);
+          mma_bf16(sc[nt], qf[2 * sp + 1], b[2], b[3]);
         }
       }
       if (edge) {
@@ -442,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
       for (int r = 0; r < 2; ++r) {
         float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(kEvery, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kEvery, mx, 2)) * mul[r];
+        mx = fmaxf(mx, __shfl_xor_sync(kEvery, mx, 2)) * p.scale_log2;
         alpha[r] = 1.f;
         if (mx > m_r[r] + kSlack) {
           alpha[r] = ex2_approx(m_r[r] - mx);
@@ -466,35 +383,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float pv = ex2_approx(fmaf(sc[nt][2 * r + e], mul[r], neg));
+            const float pv = ex2_approx(fmaf(sc[nt][2 * r + e], p.scale_log2, neg));
             pr[nt][2 * r + e] = pv;
             l_r[r] += pv;
           }
       }
       uint32_t a[4];
-      if (kF16) {
-        a[0] = pack_f16x2(pr[0][0], pr[0][1]); a[1] = pack_f16x2(pr[0][2], pr[0][3]);
-        a[2] = pack_f16x2(pr[1][0], pr[1][1]); a[3] = pack_f16x2(pr[1][2], pr[1][3]);
-      } else {
-        a[0] = pack_bf16x2(pr[0][0], pr[0][1]); a[1] = pack_bf16x2(pr[0][2], pr[0][3]);
-        a[2] = pack_bf16x2(pr[1][0], pr[1][1]); a[3] = pack_bf16x2(pr[1][2], pr[1][3]);
-      }
+      a[0] = pack_bf16x2(pr[0][0], pr[0][1]); a[1] = pack_bf16x2(pr[0][2], pr[0][3]);
+      a[2] = pack_bf16x2(pr[1][0], pr[1][1]); a[3] = pack_bf16x2(pr[1][2], pr[1][3]);
 #pragma unroll
       for (int np = 0; np < 8; ++np) {
         uint32_t b0, b1, b2, b3;
         ldsm_x4_t(tile_at(tile + 2 * kHalfBox, t16 + 8 * ((lane >> 3) & 1) + (lane & 7), 2 * np + (lane >> 4)), b0, b1, b2, b3);
-        if (kF16) {
-          mma_f16(o[2 * np], a, b0, b1);
-          mma_f16(o[2 * np + 1], a, b2, b3);
-        } else {
-          mma_bf16(o[2 * np], a, b0, b1);
-          mma_bf16(o[2 * np + 1], a, b2, b3);
-        }
+        mma_bf16(o[2 * np], a, b0, b1);
+        mma_bf16(o[2 * np + 1], a, b2, b3);
       }
     }
   };
 
-  // Joins the token slices of the row tiles; the row's output, or a partial.
+  // Joins the warps' states: the row's output, or a partial.
   auto flush = [&](const Walk& w, bool from_start, bool to_end) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -511,16 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
     const bool whole = from_start && to_end;
     float* part = whole ? nullptr : paged_part(p, cta, from_start ? 1 : 0);
     for (int i = threadIdx.x; i < p.R * 32; i += kThreads) {
-      const int row = i >> 5, d = (i & 31) * 4, tm = row >> 4, tr = row & 15;
+      const int row = i >> 5, d = (i & 31) * 4;
       float M = -INFINITY;
 #pragma unroll
-      for (int s = 0; s < kSlices; ++s) M = fmaxf(M, merge_m[(s * MT + tm) * 16 + tr]);
+      for (int s = 0; s < kWarps; ++s) M = fmaxf(M, merge_m[16 * s + row]);
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       if (M != -INFINITY) {
 #pragma unroll
-        for (int s = 0; s < kSlices; ++s) {
-          const int at = (s * MT + tm) * 16 + tr;
+        for (int s = 0; s < kWarps; ++s) {
+          const int at = 16 * s + row;
           const float f = ex2_approx(merge_m[at] - M);
           const float4 x = *reinterpret_cast<const float4*>(merge + at * kDim + d);
           L += f * merge_l[at];
@@ -528,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
         }
       }
       if (whole) {
-        const float inv = L > 0.f ? p.v_global / L : 0.f;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
         const int64_t head = paged_head(p, w.b, w.g, row);
         *reinterpret_cast<uint2*>(p.out + head * kDim + d) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -543,38 +450,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 
   Walk cur = rg.at, nxt = rg.at;
   int page = paged_page(p, cur, threadIdx.x == 0);
-  if (page >= 0) load_block<kKv>(p, stage0, page, cur.g);
+  if (page >= 0) load_block(p, base, page, cur.g);
   asm volatile("cp.async.commit_group;" ::: "memory");
   bool from_start = cur.blk == 0;
   begin(cur);
   for (int64_t x = 0; x < items; ++x) {
-    const uint32_t stage = stage0 + static_cast<uint32_t>(x & 1) * raw_bytes<kKv>();
+    const uint32_t stage = base + static_cast<uint32_t>(x & 1) * 4 * kHalfBox;
     int npage = -1;
     nxt.next(p);
     if (x + 1 < items) {
       npage = paged_page(p, nxt, threadIdx.x == 0);
-      if (npage >= 0) load_block<kKv>(p, stage0 + static_cast<uint32_t>((x + 1) & 1) * raw_bytes<kKv>(), npage, nxt.g);
+      if (npage >= 0) load_block(p, base + static_cast<uint32_t>((x + 1) & 1) * 4 * kHalfBox, npage, nxt.g);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
     if (page >= 0) {
       const int live = cur.L - cur.blk * kBlock;                  // cached tokens of this block
-      uint32_t tile = stage;
-      if (kF16) {
-        expand_block<kKv>(sm, stage, base, extra, live);
-        tile = extra;
-        __syncthreads();
-      } else if (live < kBlock) {
+      if (live < kBlock) {
         // V rows never written may hold NaN patterns, and 0 x NaN is NaN
         for (int i = threadIdx.x; i < (kBlock - live) * 16; i += kThreads)
           *reinterpret_cast<uint4*>(sm + (tile_at(stage + 2 * kHalfBox, live + (i >> 4), i & 15) - base)) =
               make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
       }
-      compute(cur, tile);
+      compute(cur, stage);
     }
-    __syncthreads();                                               // the stage and the tile are free
+    __syncthreads();                                               // the stage is free
     const bool row_ends = cur.blk == cur.nb - 1;
     if (row_ends || x + 1 == items) flush(cur, from_start, row_ends);
     if (x + 1 < items && row_ends) {
@@ -666,6 +568,33 @@ struct BlockFeed {
     return slab;
   }
 };
+
+// Issues the copies of a block's K and V (codes and scales) into a stage.
+template <int kKv>
+__device__ __forceinline__ void copy_block(const PagedParams& p, const CUtensorMap* tk, const CUtensorMap* tv, int64_t slab,
+                                           uint32_t dst, uint32_t full, uint64_t policy) {
+  const int y = static_cast<int>(slab * kBlock);
+  mbar_arrive_expect_tx(full, raw_bytes<kKv>());
+  if (kKv == MSA_BF16) {
+    tma_load_2d(dst, tk, 0, y, full);
+    tma_load_2d(dst + kHalfBox, tk, 64, y, full);
+    tma_load_2d(dst + 2 * kHalfBox, tv, 0, y, full);
+    tma_load_2d(dst + 3 * kHalfBox, tv, 64, y, full);
+  } else if (kKv == MSA_FP8_E4M3) {
+    tma_load_2d(dst, tk, 0, y, full);
+    tma_load_2d(dst + kBlock * kDim, tv, 0, y, full);
+  } else {
+    constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
+    tma_load_2d(dst, tk, 0, y, full);
+    tma_load_2d(dst + codes, tv, 0, y, full);
+    bulk_g2s(dst + 2 * codes, p.ks + slab * scales, scales, full, policy);
+    bulk_g2s(dst + 2 * codes + scales, p.vs + slab * scales, scales, full, policy);
+  }
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t a, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 
 template <int kKv, int NR>
 struct TcCfg {
@@ -964,18 +893,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       for (int n = 0; n < items; ++n) {
         if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
         const int64_t slab = feed.next(p, infos[n & (kInfos - 1)]);
-        const uint32_t dst = base + C::oStage + s * C::kStage;
-        mbar_arrive_expect_tx(full(s), C::kStage);
-        if (kFp8) {
-          tma_load_2d(dst, &tk, 0, static_cast<int>(slab * kBlock), full(s));
-          tma_load_2d(dst + kBlock * kDim, &tv, 0, static_cast<int>(slab * kBlock), full(s));
-        } else {
-          constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
-          tma_load_2d(dst, &tk, 0, static_cast<int>(slab * kBlock), full(s));
-          tma_load_2d(dst + codes, &tv, 0, static_cast<int>(slab * kBlock), full(s));
-          bulk_g2s(dst + 2 * codes, p.ks + slab * scales, scales, full(s), policy);
-          bulk_g2s(dst + 2 * codes + scales, p.vs + slab * scales, scales, full(s), policy);
-        }
+        copy_block<kKv>(p, &tk, &tv, slab, base + C::oStage + s * C::kStage, full(s), policy);
         if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
       // no copy may be in flight when the CTA ends, whatever the others did
@@ -1489,19 +1407,32 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
 }
 
 // ---------------------------------------------------------------------------
-// bf16 K/V and more than 16 query rows per KV head (several positions): the rows
-// are the M = 128 of both products,
+// Many query rows per KV head (several positions; bf16 above 16, FP8 and NVFP4
+// above 32): the rows are the M = 128 of both products,
 //   S = Q K^T (N = 128 tokens, K = 128 dims), O += P V (N = 128 dims, K = 128 tokens),
-// with Q and P as A operands in tensor memory and K and V as the copies leave them.
-// A softmax thread owns a row: its 128 logits of a block are in its registers and
-// nothing is exchanged. Tensor memory: Q of this row and of the next (64 columns
+// with Q and P as A operands in tensor memory. A softmax thread owns a row: its
+// 128 logits of a block are in its registers and nothing is exchanged. bf16 K and
+// V are B operands as the copies leave them; FP8 and NVFP4 blocks are expanded
+// (exactly) by eight warps into f16 tiles, with Q scaled into f16's range by a
+// power of two per row. Tensor memory: Q of this row and of the next (64 columns
 // each, two dims per column), S twice (128; P over its first 64), O (128). Roles:
-// copies, S, P V, an idle warp, four softmax warps.
-constexpr int kRwStages = 3, kRwWarps = 8;
+// copies, S, P V, an idle warp, four softmax warps, the expanding warps.
+template <int kKv>
+struct RwCfg {
+  static constexpr bool kQuant = kKv != MSA_BF16;
+  static constexpr int kConv0 = 8, kWarpsAll = kQuant ? 16 : 8;
+  static constexpr uint32_t kStage = raw_bytes<kKv>();
+  static constexpr uint32_t kTiles = kQuant ? 8 * kHalfBox : 0;          // [2] of K, V in f16
+  static constexpr int kStages = kKv == MSA_NVFP4 ? 5 : 3;
+  static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
+  static constexpr uint32_t oInfo = oTiles + kTiles, oBars = oInfo + kInfos * sizeof(BlockInfo);
+  static constexpr int kBars = 2 * kStages + 9 + (kQuant ? 6 : 0);
+  static constexpr uint32_t oSlot = oBars + kBars * 8, kTotal = oSlot + 16;
+  static_assert(kTotal <= 230912, "shared memory");
+  // 512 threads have 128 registers each: 56 + 200 + 2 * 120 of the 4 * 128
+  static constexpr int kRegsCtl = 56, kRegsSoft = 208, kRegsConv = 120;
+};
 constexpr uint32_t kRwQ = 0, kRwS = 128, kRwO = 384, kRwCols = 512;
-constexpr uint32_t kRwInfo = kRwStages * 4 * kHalfBox, kRwBars = kRwInfo + kInfos * sizeof(BlockInfo);
-constexpr int kRwNumBars = 2 * kRwStages + 9;
-constexpr uint32_t kRwSlot = kRwBars + kRwNumBars * 8, kRwTotal = kRwSlot + 16;
 
 __device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -1513,35 +1444,46 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
                : "r"(a));
 }
 
-__global__ void __launch_bounds__(32 * kRwWarps, 1)
+template <int kKv>
+__global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
     paged_gqa_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                           const __grid_constant__ PagedParams p) {
-  constexpr int kAllThreads = 32 * kRwWarps;
+  using C = RwCfg<kKv>;
+  constexpr bool kQuant = C::kQuant;
+  constexpr int kAllThreads = 32 * C::kWarpsAll;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Range shared_range;
-  __shared__ int64_t warp_sums[kRwWarps];
+  __shared__ int64_t warp_sums[C::kWarpsAll];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
-  BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + kRwInfo);
-  const uint32_t bars = base + kRwBars;
+  BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + C::oInfo);
+  const uint32_t bars = base + C::oBars;
   auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (kRwStages + s); };
-  constexpr int b0 = 2 * kRwStages;
+  auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
+  constexpr int b0 = 2 * C::kStages;
   auto s_full = [&](int i) { return bars + 8u * (b0 + i); };
   auto p_full = [&](int i) { return bars + 8u * (b0 + 2 + i); };
-  auto p_free = [&](int i) { return bars + 8u * (b0 + 4 + i); };       // P V is done: the S buffer is free
+  auto p_free = [&](int i) { return bars + 8u * (b0 + 4 + i); };       // P V is done: the S buffer and V's tile are free
   auto q_full = [&](int i) { return bars + 8u * (b0 + 6 + i); };
   const uint32_t done_bar = bars + 8u * (b0 + 8);
+  auto k_full = [&](int i) { return bars + 8u * (b0 + 9 + i); };       // the f16 tiles
+  auto k_free = [&](int i) { return bars + 8u * (b0 + 11 + i); };
+  auto v_full = [&](int i) { return bars + 8u * (b0 + 13 + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRwStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), kQuant ? 8 : 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 2);
       mbar_init(p_full(i), 4);
       mbar_init(p_free(i), 1);
       mbar_init(q_full(i), 4);
+      if (kQuant) {
+        mbar_init(k_full(i), 4);
+        mbar_init(k_free(i), 1);
+        mbar_init(v_full(i), 4);
+      }
     }
     mbar_init(done_bar, 2);
     fence_mbar_init();
@@ -1549,14 +1491,14 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
     prefetch_tensormap(&tv);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + kRwSlot), "r"(kRwCols)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(kRwCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kRwSlot);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -1567,26 +1509,23 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
   const int items = static_cast<int>(rg.n1 - rg.n0);
   bool ok = true;
 
+  if (warp < 4) {
+  if (kQuant) regs_dec<C::kRegsCtl>();
   if (items > 0 && warp == 0) {
     // ----------------------------------------------------------- copies --
     if (lane == 0) {
       BlockFeed feed(p, rg.at, items);
+      const uint64_t policy = l2_evict_first_policy();
       int s = 0;
       uint32_t ph = 0;
       for (int n = 0; n < items; ++n) {
         if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
         const int64_t slab = feed.next(p, infos[n & (kInfos - 1)]);
-        const int y = static_cast<int>(slab * kBlock);
-        const uint32_t dst = base + s * 4 * kHalfBox;
-        mbar_arrive_expect_tx(full(s), 4 * kHalfBox);
-        tma_load_2d(dst, &tk, 0, y, full(s));
-        tma_load_2d(dst + kHalfBox, &tk, 64, y, full(s));
-        tma_load_2d(dst + 2 * kHalfBox, &tv, 0, y, full(s));
-        tma_load_2d(dst + 3 * kHalfBox, &tv, 64, y, full(s));
-        if (++s == kRwStages) { s = 0; ph ^= 1u; }
+        copy_block<kKv>(p, &tk, &tv, slab, base + s * C::kStage, full(s), policy);
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
       // no copy may be in flight when the CTA ends, whatever the others did
-      for (int k = 0; k < kRwStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
+      for (int k = 0; k < C::kStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
       if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     }
     __syncwarp();
@@ -1594,46 +1533,50 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
     // ------------------------------------------------------------- MMAs --
     const bool lead = elect_one();
     constexpr uint32_t hi = desc_hi(1024, kSwz128);
+    constexpr int type = kQuant ? 0 : 1;             // f16, bf16
     int stage = 0;
     uint32_t ph = 0;
     if (warp == 1) {
-      constexpr uint32_t id_s = mma_idesc(1, 1, 128, 0, 0);
-      const uint32_t k0 = desc_lo(base, 16);
+      constexpr uint32_t id_s = mma_idesc(type, type, 128, 0, 0);
+      const uint32_t k0 = desc_lo(base + (kQuant ? C::oTiles : 0), 16);
       for (int n = 0; n < items; ++n) {
-        ok = warp_wait(full(stage), ph);
+        ok = kQuant ? warp_wait(k_full(n & 1), (n >> 1) & 1) : warp_wait(full(stage), ph);
         if (n >= 2) ok = ok && warp_wait(p_free(n & 1), ((n >> 1) - 1) & 1);
         if (!ok) break;
         const int seg = infos[n & (kInfos - 1)].seg;
         if (infos[n & (kInfos - 1)].idx == 0 && !warp_wait(q_full(seg & 1), (seg >> 1) & 1)) { ok = false; break; }
         tmem_fence_after();
         if (lead) {
-          const uint32_t k = k0 + stage * (4 * kHalfBox >> 4), d = tmem + kRwS + 128 * (n & 1), q = tmem + kRwQ + 64 * (seg & 1);
+          const uint32_t k = k0 + (kQuant ? n & 1 : stage) * (4 * kHalfBox >> 4);
+          const uint32_t d = tmem + kRwS + 128 * (n & 1), q = tmem + kRwQ + 64 * (seg & 1);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ts(d, q + 8 * kk, desc_of(k + (kk >> 2) * (kHalfBox >> 4) + (kk & 3) * 2, hi), id_s, kk > 0);
+          if (kQuant) mma_commit(k_free(n & 1));
           mma_commit(s_full(n & 1));
           mbar_arrive(s_full(n & 1));
         }
         __syncwarp();
-        if (++stage == kRwStages) { stage = 0; ph ^= 1u; }
+        if (++stage == C::kStages) { stage = 0; ph ^= 1u; }
       }
     } else {
-      constexpr uint32_t id_o = mma_idesc(1, 1, 128, 0, 1);
-      const uint32_t v0 = desc_lo(base + 2 * kHalfBox, kHalfBox);
+      constexpr uint32_t id_o = mma_idesc(type, type, 128, 0, 1);
+      const uint32_t v0 = desc_lo(base + (kQuant ? C::oTiles : 0) + 2 * kHalfBox, kHalfBox);
       for (int n = 0; n < items; ++n) {
         ok = warp_wait(p_full(n & 1), (n >> 1) & 1);
+        if (kQuant) ok = ok && warp_wait(v_full(n & 1), (n >> 1) & 1);
         if (!ok) break;
         const bool fresh = infos[n & (kInfos - 1)].idx == 0;
         tmem_fence_after();
         if (lead) {
-          const uint32_t v = v0 + stage * (4 * kHalfBox >> 4), pt = tmem + kRwS + 128 * (n & 1);
+          const uint32_t v = v0 + (kQuant ? n & 1 : stage) * (4 * kHalfBox >> 4), pt = tmem + kRwS + 128 * (n & 1);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) mma_ts(tmem + kRwO, pt + 8 * kk, desc_of(v + kk * 128, hi), id_o, !(fresh && kk == 0));
-          mma_commit(empty(stage));
+          if (!kQuant) mma_commit(empty(stage));
           mma_commit(p_free(n & 1));
         }
         __syncwarp();
-        if (++stage == kRwStages) stage = 0;
+        if (++stage == C::kStages) stage = 0;
       }
     }
     if (!ok && lead) set_flag(p.flags, MSA_FLAG_TIMEOUT);
@@ -1641,26 +1584,44 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
     __syncwarp();
     mbar_wait(done_bar, 0);
     __syncwarp();
-  } else if (items > 0 && warp >= 4) {
+  }
+  } else if (warp < C::kConv0) {
     // ---------------------------------------------------------- softmax --
     const int r = 32 * (warp & 3) + lane;           // query row, tensor-memory lane; token of V's dead rows
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const bool live_warp = 32 * (warp & 3) < p.R, live_row = r < p.R;
     const int j = live_row ? r / p.group : 0;
+    if (kQuant) regs_inc<C::kRegsSoft>();
     Walk w = rg.at;                                 // row of the queries loaded next
     int64_t w_left = items;
+    float mul = 0.f, mul_next = 0.f;                // log2 units of a logit, of this row's and the next row's queries
     auto load_q = [&](int buf) {
       if (live_warp) {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (live_row ? paged_head(p, w.b, w.g, r) : 0) * kDim);
+        uint32_t v[64];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint4 x = live_row ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+          v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+        }
+        mul_next = p.scale_log2;
+        if (kQuant) {
+          // f16 operands: the row times a power of two that brings its largest value to [2^14, 2^15)
+          uint32_t big = 0u;                         // bf16 magnitudes order as their bits
+#pragma unroll
+          for (int k = 0; k < 64; ++k) big = __vmaxu2(big, v[k] & 0x7FFF7FFFu);
+          const int sh = fp16_shift_for(fmaxf(bf16_bits_to_f32(big & 0xFFFF), bf16_bits_to_f32(big >> 16)));
+          const float f = exp2_int(sh);
+          mul_next = p.scale_log2 * p.k_global * exp2_int(-sh);
+#pragma unroll
+          for (int k = 0; k < 64; ++k) v[k] = pack_f16x2(bf16_bits_to_f32(v[k] & 0xFFFF) * f, bf16_bits_to_f32(v[k] >> 16) * f);
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t v[32];
+          uint32_t h[32];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 x = live_row ? src[8 * half + k] : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
-          }
-          tmem_st32(tmem + lanes + kRwQ + 64 * buf + 32 * half, v);
+          for (int k = 0; k < 32; ++k) h[k] = v[32 * half + k];
+          tmem_st32(tmem + lanes + kRwQ + 64 * buf + 32 * half, h);
         }
         tmem_wait_st();
       }
@@ -1671,7 +1632,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
       w.blk = w.nb - 1;
       if (w_left > 0) w.next(p);
     };
-    load_q(0);
+    if (items > 0) load_q(0);
     float ref = -INFINITY, l = 0.f;
     int stage = 0;
     for (int n = 0; n < items; ++n) {
@@ -1682,6 +1643,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
       if (bi.idx == 0) {
         ref = -INFINITY;
         l = 0.f;
+        mul = mul_next;
         if (w_left > 0) load_q((bi.seg + 1) & 1);   // S of the row before this one is done with that buffer
       }
       tmem_fence_after();
@@ -1700,7 +1662,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < 128; ++k) top4[k & 3] = fmaxf(top4[k & 3], x[k]);
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.scale_log2;
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mul;
         const bool raise = top > ref + kSlack;
         const float alpha = raise && ref != -INFINITY ? ex2_approx(ref - top) : 1.f;
         if (__any_sync(kEvery, raise && ref != -INFINITY)) {
@@ -1727,16 +1689,16 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
           uint32_t pk[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float a = ex2_approx(fmaf(x[64 * q + 2 * k], p.scale_log2, neg));
-            const float b = ex2_approx(fmaf(x[64 * q + 2 * k + 1], p.scale_log2, neg));
+            const float a = ex2_approx(fmaf(x[64 * q + 2 * k], mul, neg));
+            const float b = ex2_approx(fmaf(x[64 * q + 2 * k + 1], mul, neg));
             l4[k & 3] += a + b;
-            pk[k] = pack_bf16x2(a, b);
+            pk[k] = kQuant ? pack_f16x2(a, b) : pack_bf16x2(a, b);
           }
           tmem_st32(sbuf + 32 * q, pk);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       }
-      if (r >= bi.live) {
+      if (!kQuant && r >= bi.live) {
         // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
         uint8_t* v = sm + stage * 4 * kHalfBox + 2 * kHalfBox + r * 128;
 #pragma unroll
@@ -1746,7 +1708,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
         }
         smem_to_async();
       }
-      if (++stage == kRwStages) stage = 0;
+      if (++stage == C::kStages) stage = 0;
       tmem_wait_st();
       tmem_fence_before();
       __syncwarp();
@@ -1758,7 +1720,7 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
         tmem_fence_after();
         if (live_warp) {
           const bool whole = (bi.flags & 12) == 12;
-          const float inv = l > 0.f ? 1.f / l : 0.f, M = l > 0.f ? ref : -INFINITY;
+          const float inv = l > 0.f ? p.v_global / l : 0.f, M = l > 0.f ? ref : -INFINITY;
           const int64_t head = live_row ? paged_head(p, bi.b, bi.g, r) : 0;
           float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
 #pragma unroll 1
@@ -1789,6 +1751,70 @@ __global__ void __launch_bounds__(32 * kRwWarps, 1)
         }
         tmem_fence_before();
       }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+  } else if (kQuant) {
+    // -------------------------------------------------------- expansion --
+    // Four warps K, four V; a thread takes a token's row. The copies' swizzle keeps the reads of eight rows in
+    // eight banks, the tiles' the stores.
+    regs_dec<C::kRegsConv>();
+    const bool isv = warp >= C::kConv0 + 4;
+    const int row = 32 * (warp & 3) + lane;
+    constexpr uint32_t rowb = kKv == MSA_FP8_E4M3 ? kDim : kDim / 2;
+    constexpr uint32_t scales = kBlock * kDim / 16;
+    const uint8_t* src = sm + (isv ? kBlock * rowb : 0) + row * rowb;
+    const uint8_t* ssrc = sm + 2 * kBlock * rowb + (isv ? scales : 0) + row * (kDim / 16);
+    const int swz = (kKv == MSA_FP8_E4M3 ? row & 7 : (row >> 1) & 3) << 4;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int n = 0; n < items; ++n) {
+      ok = mbar_wait(full(s), ph);
+      if (n >= 2) ok = mbar_wait(isv ? p_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1) && ok;
+      ok = __all_sync(kEvery, ok);
+      if (!ok) break;
+      // a row that was never written may hold NaN patterns, and 0 x NaN is NaN
+      const bool dead = isv && row >= infos[n & (kInfos - 1)].live;
+      const uint32_t tile = base + C::oTiles + (n & 1) * 4 * kHalfBox + (isv ? 2 * kHalfBox : 0);
+#pragma unroll
+      for (int c = 0; c < static_cast<int>(rowb / 16); ++c) {
+        uint4 w = *reinterpret_cast<const uint4*>(src + s * C::kStage + ((16 * c) ^ swz));
+        if (dead) w = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        if (kKv == MSA_FP8_E4M3) {
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[2 * k] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[k] & 0xFFFF));
+            h[2 * k + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[k] >> 16));
+          }
+          st_shared16(tile_at(tile, row, 2 * c), h);
+          st_shared16(tile_at(tile, row, 2 * c + 1), h + 4);
+        } else {
+          uint32_t sc = *reinterpret_cast<const uint16_t*>(ssrc + s * C::kStage + 2 * c);
+          if (dead) sc = 0u;
+          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
+          const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
+          const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            e2m1x8_to_f16x2x4(words[k], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[e]), s2[k >> 1]);
+              h[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            st_shared16(tile_at(tile, row, 4 * c + k), h);
+          }
+        }
+      }
+      smem_to_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(empty(s));
+        mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
+      }
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   }
@@ -1882,14 +1908,12 @@ size_t paged_gqa_workspace_bytes(int Q, int H, int G) {
   return kMaxCtas * sizeof(CutRow) + kMaxCtas * 2 * static_cast<size_t>(part_floats(Q * (H / G))) * sizeof(float);
 }
 
-template <int kKv>
-static cudaError_t launch_rows(const PagedParams& p, int mt, int ctas, cudaStream_t stream) {
-  constexpr size_t smem = simple_smem<kKv>() + 1024;
-  auto kern = mt == 1 ? paged_gqa_kernel<kKv, 1> : mt == 2 ? paged_gqa_kernel<kKv, 2>
-            : mt == 4 ? paged_gqa_kernel<kKv, 4> : paged_gqa_kernel<kKv, 8>;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+static cudaError_t launch_mma(const PagedParams& p, int ctas, cudaStream_t stream) {
+  constexpr size_t smem = kMmaSmem + 1024;
+  const cudaError_t err =
+      cudaFuncSetAttribute(paged_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
+  return launch_pdl(paged_gqa_kernel, dim3(ctas), dim3(kThreads), smem, stream, p);
 }
 
 // cuTensorMapEncodeTiled from the driver, looked up through the runtime (the
@@ -1941,16 +1965,17 @@ static cudaError_t launch_tc(const PagedParams& p, int ctas, cudaStream_t stream
   return launch_pdl(paged_gqa_tc_kernel<kKv, NR>, dim3(ctas), dim3(32 * C::kWarpsAll), smem, stream, tk, tv, p);
 }
 
-static cudaError_t launch_rows_tc(const PagedParams& p, int ctas, cudaStream_t stream) {
+template <int kKv>
+static cudaError_t launch_many(const PagedParams& p, int ctas, cudaStream_t stream) {
   CUtensorMap tk, tv;
   cudaError_t err;
   const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
-  if ((err = cache_map(&tk, p.k, rows, MSA_BF16)) != cudaSuccess) return err;
-  if ((err = cache_map(&tv, p.v, rows, MSA_BF16)) != cudaSuccess) return err;
-  constexpr size_t smem = kRwTotal + 1024;
-  err = cudaFuncSetAttribute(paged_gqa_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if ((err = cache_map(&tk, p.k, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
+  if ((err = cache_map(&tv, p.v, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
+  constexpr size_t smem = RwCfg<kKv>::kTotal + 1024;
+  err = cudaFuncSetAttribute(paged_gqa_rows_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  return launch_pdl(paged_gqa_rows_kernel, dim3(ctas), dim3(32 * kRwWarps), smem, stream, tk, tv, p);
+  return launch_pdl(paged_gqa_rows_kernel<kKv>, dim3(ctas), dim3(32 * RwCfg<kKv>::kWarpsAll), smem, stream, tk, tv, p);
 }
 
 cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRecord* rec) {
@@ -1981,26 +2006,19 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   const int64_t rows = static_cast<int64_t>(a.B) * a.G;
   p.by_row = rows < ctas - 1;
   const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
-  const int tiles = (p.R + 15) / 16;
-  const int mt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
-  // measured: what a row costs against a block, in its kernel's form
-  const bool tc = a.kv == MSA_FP8_E4M3 || (a.kv == MSA_NVFP4 && mt <= 2);
-  p.row_cost = tc ? 5 : mt > 1 ? 3 : 2;
+  // One form per number of query rows: up to 16 (bf16: warp mma, which the cache's bytes bound; FP8, NVFP4:
+  // tokens as M), up to 32 (FP8, NVFP4), more (rows as M).
+  const int rows_of = p.R <= 16 ? 16 : p.R <= 32 && a.kv != MSA_BF16 ? 32 : 128;
+  p.row_cost = rows_of == 128 ? 3 : a.kv == MSA_BF16 ? 2 : 5;         // measured
   cudaError_t err;
-  const char* form = "mma";
-  if (a.kv == MSA_FP8_E4M3) {
-    form = "tcgen05";
-    err = mt == 1 ? launch_tc<MSA_FP8_E4M3, 16>(p, ctas, stream) : mt == 2 ? launch_tc<MSA_FP8_E4M3, 32>(p, ctas, stream)
-        : mt == 4 ? launch_tc<MSA_FP8_E4M3, 64>(p, ctas, stream) : launch_tc<MSA_FP8_E4M3, 128>(p, ctas, stream);
-  } else if (a.kv == MSA_NVFP4 && mt <= 2) {
-    form = "tcgen05";
-    err = mt == 1 ? launch_tc<MSA_NVFP4, 16>(p, ctas, stream) : launch_tc<MSA_NVFP4, 32>(p, ctas, stream);
-  } else if (a.kv == MSA_BF16 && mt > 1) {
-    form = "tcgen05";
-    err = launch_rows_tc(p, ctas, stream);
-  } else {
-    err = a.kv == MSA_BF16 ? launch_rows<MSA_BF16>(p, mt, ctas, stream) : launch_rows<MSA_NVFP4>(p, mt, ctas, stream);
-  }
+  if (a.kv == MSA_BF16)
+    err = rows_of == 16 ? launch_mma(p, ctas, stream) : launch_many<MSA_BF16>(p, ctas, stream);
+  else if (a.kv == MSA_FP8_E4M3)
+    err = rows_of == 16 ? launch_tc<MSA_FP8_E4M3, 16>(p, ctas, stream)
+        : rows_of == 32 ? launch_tc<MSA_FP8_E4M3, 32>(p, ctas, stream) : launch_many<MSA_FP8_E4M3>(p, ctas, stream);
+  else
+    err = rows_of == 16 ? launch_tc<MSA_NVFP4, 16>(p, ctas, stream)
+        : rows_of == 32 ? launch_tc<MSA_NVFP4, 32>(p, ctas, stream) : launch_many<MSA_NVFP4>(p, ctas, stream);
   if (err != cudaSuccess) return err;
   if (ctas > 1) {
     // few rows: a CTA for each query row, whose warps share its many partials, 32 in flight each (165
@@ -2012,7 +2030,7 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
     if (err != cudaSuccess) return err;
   }
   rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"
-           : a.kv == MSA_FP8_E4M3 ? "fp8" : "nvfp4", form, p.R, 16 * mt, ctas);
+           : a.kv == MSA_FP8_E4M3 ? "fp8" : "nvfp4", a.kv == MSA_BF16 && rows_of == 16 ? "mma" : "tcgen05", p.R, rows_of, ctas);
   return cudaGetLastError();
 }
 
