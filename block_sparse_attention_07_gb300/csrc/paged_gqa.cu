@@ -599,13 +599,9 @@ __device__ __forceinline__ void st_shared16(uint32_t a, const uint32_t* v) {
 template <int kKv, int NR>
 struct TcCfg {
   static constexpr bool kFp8 = kKv == MSA_FP8_E4M3;
-  // Two softmax groups. Few rows: a group takes every second block, with its own
-  // references, sums and O, joined at the segment's end (a block's chain of waits,
-  // exchange and stores is longer than its arithmetic). Many: half the rows of every block.
-  static constexpr bool kAlt = NR <= 32;
+  // Two softmax groups of 4 warps take alternate blocks, each with its own references, sums and O, joined at the
+  // segment's end: a block's chain of waits, exchange and stores is longer than its arithmetic.
   static constexpr int kGroups = 2;
-  static constexpr int kRG = kAlt ? NR : NR / 2;               // rows per softmax group
-  static constexpr int kSoftArrive = kAlt ? 4 : 8;             // softmax warps per block
   static constexpr int kTurns = NR <= 16 ? 2 : 1;              // groups of 4 warps that expand K, and V, taking turns
   static constexpr int kConv = kFp8 ? 0 : 8 * kTurns;          // expanding warps
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
@@ -613,28 +609,25 @@ struct TcCfg {
   // Registers per thread, moved between the warpgroups from what the launch gives each alike (65,536 over the
   // threads, in eights): the sum over the warpgroups stays the launch's.
   static constexpr int kRegs = 65536 / (32 * kWarpsAll) / 8 * 8;
-  static constexpr int kRegsCtl = kFp8 ? 64 : 56, kRegsConv = kFp8 ? 0 : 56;
+  static constexpr int kRegsCtl = kFp8 ? 72 : NR <= 16 ? 56 : 64, kRegsConv = kFp8 ? 0 : NR <= 16 ? 56 : 64;
   static constexpr int kRegsFit = (kRegs * (kWarpsAll / 4) - kRegsCtl - (kConv / 4) * kRegsConv) / kGroups / 8 * 8;
   static constexpr int kRegsSoft = kRegsFit > 232 ? 232 : kRegsFit;
   static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
-  static constexpr int kPBufs = NR > 64 ? 1 : 2;
   static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
   static constexpr uint32_t kPPart = NR * (kFp8 ? 128 : 256);
-  // One P buffer; it also stages 16 output rows per group, in the space of the group's own rows
+  // One P buffer (there is one per group); it also stages 16 output rows
   static constexpr uint32_t kPBuf = kPParts * kPPart < 16 * kDim * 4 ? 16 * kDim * 4 : kPParts * kPPart;
   static constexpr uint32_t kStage = raw_bytes<kKv>();
   static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
-  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + kPBufs * kPBuf;
-  static constexpr uint32_t kSmall = 2048 + NR * (kAlt ? 128 : 48);
+  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + 2 * kPBuf;
+  static constexpr uint32_t kSmall = 2048 + NR * 128;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  // The parts of Q and P side by side as columns of one MMA (fewer, wider MMAs;
-  // the sums of the parts are taken where S and O are read), or one after the
-  // other into the same columns where tensor memory is too small for that.
-  static constexpr bool kStacked = kFp8 && NR <= 32;
-  static constexpr int kSCols = kStacked ? kQParts * NR : NR, kOCols = kStacked ? kPParts * NR : NR;
+  // The parts of Q and P lie side by side as columns of one MMA (few and wide ones; the sums of the parts are
+  // taken where S and O are read)
+  static constexpr int kSCols = kQParts * NR, kOCols = kPParts * NR;
   static constexpr int kKCols = kFp8 ? 0 : 2 * (kDim / 2);     // NVFP4: K[2] in f16, two dims per column
-  static constexpr int kSets = kAlt ? 4 : 1;                   // states: of each group, for this segment and the one before
+  static constexpr int kSets = 4;                              // states: of each group, for this segment and the one before
   static constexpr int kUsedCols = kTcS * kSCols + kSets * kOCols + kKCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
@@ -643,20 +636,17 @@ struct TcCfg {
   static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
   static constexpr uint32_t oQ = oTiles + kTiles;
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
-  static constexpr uint32_t oInfo = oP + kPBufs * kPBuf;
+  static constexpr uint32_t oInfo = oP + 2 * kPBuf;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
   static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [sets][NR] kOff - reference
   static constexpr uint32_t oAlpha = oRef + kSets * NR * 4;              // [sets][NR]
   static constexpr uint32_t oRed = oAlpha + kSets * NR * 4;              // [sets][4][NR]
   static constexpr uint32_t oPos = oRed + kSets * 4 * NR * 4;            // [NR] position of a row
   static constexpr uint32_t oBars = oPos + NR * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kTcS + 2 * kPBufs + 4 + (kFp8 ? 0 : 8) + 5;
+  static constexpr int kBars = 2 * kStages + 2 * kTcS + 4 + 4 + (kFp8 ? 0 : 8) + 5;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
-  // rows of staged output that fit a group's rows of one part of P
-  static constexpr int kStgRows = kAlt ? 16 : kRG / 4;
-  static_assert(kAlt || kStgRows * kPParts >= 16, "P's space holds the staged output rows");
   static_assert(kTotal - oInfo <= kSmall, "small area");
 };
 
@@ -763,9 +753,8 @@ __device__ __forceinline__ uint2 fp8_parts(const float (&x)[4], float f) {
   return make_uint2(a | (b << 16), la | (lb << 16));
 }
 
-// Reduces N values per lane over the warp, all of them at once: each step halves
-// the values a lane keeps. Lane i ends with value i mod N (N = 16, 32) in v[0],
-// and value 32 + i in v[1] for N = 64.
+// Reduces N (16 or 32) values per lane over the warp, all of them at once: each
+// step halves the values a lane keeps. Lane i ends with value i mod N in v[0].
 template <int N, bool kMax>
 __device__ __forceinline__ void warp_reduce_rows(float (&v)[N]) {
   auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
@@ -773,20 +762,15 @@ __device__ __forceinline__ void warp_reduce_rows(float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = op(v[i], __shfl_xor_sync(kEvery, v[i], 16));
   }
-  constexpr int kSets = N == 64 ? 2 : 1, kTop = N == 16 ? 8 : 16;
 #pragma unroll
-  for (int set = 0; set < kSets; ++set) {
+  for (int o = N == 16 ? 8 : 16; o > 0; o >>= 1) {
+    const bool up = (threadIdx.x & o) != 0;
 #pragma unroll
-    for (int o = kTop; o > 0; o >>= 1) {
-      const bool up = (threadIdx.x & o) != 0;
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float a = v[32 * set + i], b = v[32 * set + i + o];
-        v[32 * set + i] = op(up ? b : a, __shfl_xor_sync(kEvery, up ? a : b, o));
-      }
+    for (int i = 0; i < o; ++i) {
+      const float a = v[i], b = v[i + o];
+      v[i] = op(up ? b : a, __shfl_xor_sync(kEvery, up ? a : b, o));
     }
   }
-  if (N == 64) v[1] = v[32];
 }
 
 template <int kKv, int NR>
@@ -813,9 +797,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   constexpr int b0 = 2 * C::kStages;
   auto s_full = [&](int i) { return bars + 8u * (b0 + i); };                       // S of a block is there
   auto p_full = [&](int i) { return bars + 8u * (b0 + kTcS + i); };                // P is written
-  auto p_free = [&](int i) { return bars + 8u * (b0 + kTcS + C::kPBufs + i); };    // P V is done
-  auto s_free = [&](int i) { return bars + 8u * (b0 + kTcS + 2 * C::kPBufs + i); }; // S is in the softmax warps' registers
-  constexpr int b1 = b0 + 2 * kTcS + 2 * C::kPBufs;
+  auto p_free = [&](int i) { return bars + 8u * (b0 + kTcS + 2 + i); };    // P V is done
+  auto s_free = [&](int i) { return bars + 8u * (b0 + kTcS + 4 + i); }; // S is in the softmax warps' registers
+  constexpr int b1 = b0 + 2 * kTcS + 4;
   auto q_full = [&](int i) { return bars + 8u * (b1 + i); };
   auto q_free = [&](int i) { return bars + 8u * (b1 + 2 + i); };
   auto k_full = [&](int i) { return bars + 8u * (b1 + 4 + i); };                   // NVFP4: f16 tiles
@@ -835,15 +819,13 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     }
     for (int i = 0; i < kTcS; ++i) {
       mbar_init(s_full(i), 2);                                        // the commit, and the issuing thread's own arrival
-      mbar_init(s_free(i), C::kSoftArrive);
-    }
-    for (int i = 0; i < C::kPBufs; ++i) {
-      mbar_init(p_full(i), C::kSoftArrive);
-      mbar_init(p_free(i), 1);
+      mbar_init(s_free(i), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full(i), C::kSoftArrive);
-      mbar_init(q_free(i), 1 + C::kSoftArrive);                       // S is done with Q, softmax with its multipliers
+      mbar_init(p_full(i), 4);
+      mbar_init(p_free(i), 1);
+      mbar_init(q_full(i), 4);
+      mbar_init(q_free(i), 1 + 4);                       // S is done with Q, softmax with its multipliers
       if (!kFp8) {
         mbar_init(k_full(i), 4);
         mbar_init(k_free(i), 1);
@@ -909,7 +891,6 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     const bool lead = elect_one();
     if (warp == 1) {
       constexpr uint32_t id_s = mma_idesc(0, 0, C::kSCols, 0, 0), hi = desc_hi(1024, kSwz128);
-      constexpr int q_passes = C::kStacked ? 1 : C::kQParts;
       const uint32_t q0 = desc_lo(base + C::oQ, 16), k0 = desc_lo(base + C::oStage, 16);
       int stage = 0;
       uint32_t ph = 0;
@@ -926,10 +907,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           if (kFp8) {
             const uint32_t k = k0 + stage * (C::kStage >> 4);
 #pragma unroll
-            for (int part = 0; part < q_passes; ++part)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss<true>(d, desc_of(k + kk * 2, hi), desc_of(q + (part * C::kQPart >> 4) + kk * 2, hi), id_s, part + kk > 0);
+            for (int kk = 0; kk < 4; ++kk) mma_ss<true>(d, desc_of(k + kk * 2, hi), desc_of(q + kk * 2, hi), id_s, kk > 0);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -946,27 +924,23 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     } else {
       constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
       constexpr uint32_t hi_v = desc_hi(1024, kSwz128), hi_p = desc_hi(2048, kSwzNone);
-      constexpr int p_passes = C::kStacked ? 1 : C::kPParts;
       const uint32_t p0 = desc_lo(base + C::oP, 128);
       const uint32_t v0 = kFp8 ? desc_lo(base + C::oStage + kBlock * kDim, 16384) : desc_lo(base + C::oTiles, kHalfBox);
       int stage = 0;
       for (int n = 0; n < items; ++n) {
-        const int pb = n % C::kPBufs;
-        ok = (kFp8 || warp_wait(v_full(n & 1), (n >> 1) & 1)) && warp_wait(p_full(pb), (n / C::kPBufs) & 1);
+        const int pb = n & 1;
+        ok = (kFp8 || warp_wait(v_full(pb), (n >> 1) & 1)) && warp_wait(p_full(pb), (n >> 1) & 1);
         if (!ok) break;
-        const bool fresh = infos[n & (kInfos - 1)].idx < (C::kAlt ? 2 : 1);
-        const uint32_t d = tO + (C::kAlt ? (infos[n & (kInfos - 1)].seg & 1) * 2 + (n & 1) : 0) * C::kOCols;
+        const bool fresh = infos[n & (kInfos - 1)].idx < 2;
+        const uint32_t d = tO + ((infos[n & (kInfos - 1)].seg & 1) * 2 + (n & 1)) * C::kOCols;
         tmem_fence_after();
         if (lead) {
           const uint32_t pt = p0 + pb * (C::kPBuf >> 4);
           if (kFp8) {
             const uint32_t v = v0 + stage * (C::kStage >> 4);
 #pragma unroll
-            for (int part = 0; part < p_passes; ++part)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss<true>(d, desc_of(v + kk * 256, hi_v), desc_of(pt + (part * C::kPPart >> 4) + kk * 32, hi_p), id_o,
-                             !(fresh && part + kk == 0));
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss<true>(d, desc_of(v + kk * 256, hi_v), desc_of(pt + kk * 32, hi_p), id_o, !(fresh && kk == 0));
             mma_commit(empty(stage));
           } else {
             const uint32_t v = v0 + (n & 1) * (2 * kHalfBox >> 4);
@@ -990,15 +964,12 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   } else if (warp < C::kConv0) {
     // ---------------------------------------------------------- softmax --
     regs_inc<C::kRegsSoft>();
-    constexpr int RG = C::kRG;
     const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
     const int t = 32 * wl + lane;                   // token of S, dim of O
-    const int r0 = C::kAlt ? 0 : grp * RG;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
-    constexpr int kStep = C::kAlt ? 2 : 1;
-    // The queries of a segment, by the group with the first block of the segment before it (kAlt; else both
-    // groups): 16 lanes take a row, 8 dims each, all loads before the first use.
-    constexpr int kQPasses = NR / (8 * (C::kAlt ? 1 : 2));
+    // The queries of a segment, by the group with the first block of the segment before it: 16 lanes take a row,
+    // 8 dims each, all loads before the first use.
+    constexpr int kQPasses = NR / 8;
     Walk w = rg.at;
     int w_seg = 0;
     int64_t w_left = items;
@@ -1010,7 +981,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         w.next(p);
       }
       const int qb = seg & 1, hl = lane & 15;
-      const int row = (C::kAlt ? wl : 4 * grp + wl) * 2 * kQPasses + (lane >> 4);
+      const int row = wl * 2 * kQPasses + (lane >> 4);
       uint4 v[kQPasses];
 #pragma unroll
       for (int i = 0; i < kQPasses; ++i) {
@@ -1053,77 +1024,74 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (lane == 0) mbar_arrive(q_full(qb));
       return true;
     };
-    if (items > 0 && (!C::kAlt || grp == 0)) ok = put_q(0);
-    float l[RG];
-    int stage = C::kAlt ? grp : 0;
+    if (items > 0 && grp == 0) ok = put_q(0);
+    float l[NR];
+    int stage = grp;
     uint32_t joins = 0;                             // parity of the joins so far on either segment parity (bits 0, 1)
     bool first = false;                             // no block of the segment has set the references yet
     uint32_t lent = 0;                              // bits 0, 1: the other group may still read this one's state
-    for (int n = C::kAlt ? grp : 0; n < items; n += kStep) {
-      const int sb = n & 1, pb = n % C::kPBufs;
-      ok = mbar_wait(s_full(sb), (n >> 1) & 1) && ok;
-      if (n >= C::kPBufs) ok = mbar_wait(p_free(pb), ((n / C::kPBufs) - 1) & 1) && ok;
+    for (int n = grp; n < items; n += 2) {
+      // (n & 1, the buffer of S and P, is grp)
+      ok = mbar_wait(s_full(grp), (n >> 1) & 1) && ok;
+      if (n >= 2) ok = mbar_wait(p_free(grp), ((n >> 1) - 1) & 1) && ok;
       const BlockInfo bi = infos[n & (kInfos - 1)];
-      if (bi.idx < kStep) {
+      if (bi.idx < 2) {
         first = true;
 #pragma unroll
-        for (int r = 0; r < RG; ++r) l[r] = 0.f;
+        for (int r = 0; r < NR; ++r) l[r] = 0.f;
         if (lent >> (bi.seg & 1) & 1) ok = mbar_wait(join_free(bi.seg & 1), ((joins >> (bi.seg & 1)) & 1) ^ 1) && ok;
         lent &= ~(1u << (bi.seg & 1));
       }
-      const int set = C::kAlt ? (bi.seg & 1) * 2 + grp : 0;
+      const int set = (bi.seg & 1) * 2 + grp;
       const uint32_t tOg = tO + set * C::kOCols + lanes;
       float* ref = row_ref + set * NR;
       float* alphas = row_alpha + set * NR;
       float* red = row_red + set * 4 * NR;
-      const float* mul = row_mul + (bi.seg & 1) * NR + r0;
-      float x[RG];
+      const float* mul = row_mul + (bi.seg & 1) * NR ;
+      float x[NR];
       tmem_fence_after();
 #pragma unroll
-      for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * C::kSCols + r0 + 16 * i, x + 16 * i);
-      if (C::kStacked) {
-        float lo[RG];
+      for (int i = 0; i < NR / 16; ++i) tmem_ld16(tmem + lanes + grp * C::kSCols + 16 * i, x + 16 * i);
+      if (kFp8) {
+        float lo[NR];
 #pragma unroll
-        for (int i = 0; i < RG / 16; ++i) tmem_ld16(tmem + lanes + sb * C::kSCols + NR + r0 + 16 * i, lo + 16 * i);
+        for (int i = 0; i < NR / 16; ++i) tmem_ld16(tmem + lanes + grp * C::kSCols + NR + 16 * i, lo + 16 * i);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < RG; ++r) x[r] += lo[r];
+        for (int r = 0; r < NR; ++r) x[r] += lo[r];
       }
       tmem_wait_ld();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_free(sb));
+      if (lane == 0) mbar_arrive(s_free(grp));
       const bool edge = bi.lim0 < kBlock - 1;
       float top = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < RG; r += 4) {
+      for (int r = 0; r < NR; r += 4) {
         const float4 m4 = *reinterpret_cast<const float4*>(mul + r);
-        const float4 f4 = *reinterpret_cast<const float4*>(ref + r0 + r);
+        const float4 f4 = *reinterpret_cast<const float4*>(ref + r);
         const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[r + e] = first ? x[r + e] * mm[e] : fmaf(x[r + e], mm[e], ff[e]);
-          if (edge && t > bi.lim0 + row_pos[r0 + r + e]) x[r + e] = -INFINITY;
+          if (edge && t > bi.lim0 + row_pos[r + e]) x[r + e] = -INFINITY;
           top = fmaxf(top, x[r + e]);
         }
       }
       if (group_any(bar_id, first || !ok || top > C::kOff + kSlack)) {
         // the block's maxima over all tokens; rows that rise by more than the slack get a new reference
         {
-          float v[RG];
+          float v[NR];
 #pragma unroll
-          for (int r = 0; r < RG; ++r) v[r] = x[r];
-          warp_reduce_rows<RG, true>(v);
-          if (lane < RG) red[wl * NR + r0 + lane] = v[0];
-          if (RG == 64) red[wl * NR + r0 + 32 + lane] = v[1];
+          for (int r = 0; r < NR; ++r) v[r] = x[r];
+          warp_reduce_rows<NR, true>(v);
+          if (lane < NR) red[wl * NR + lane] = v[0];
         }
-        if (!first && C::kPBufs != kStep)            // O is complete
-          ok = mbar_wait(p_free((n - 1) % C::kPBufs), ((n - 1) / C::kPBufs) & 1) && ok;
         if (group_any(bar_id, !ok)) { ok = false; break; }
-        if (t < RG) {
+        if (t < NR) {
           // x = s - reference + kOff, s itself in a first block; ref holds kOff - reference. A row that its
           // first block masks is masked by every later one: its reference stays -inf and its x with it
-          const int r = r0 + t;
+          const int r = t;
           const float v = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
           float alpha = 1.f, delta = 0.f;
           if (first) {
@@ -1140,19 +1108,19 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         group_any(bar_id, false);
         tmem_fence_after();
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          x[r] += red[r0 + r];
-          l[r] *= alphas[r0 + r];
+        for (int r = 0; r < NR; ++r) {
+          x[r] += red[r];
+          l[r] *= alphas[r];
         }
         if (!first) {
 #pragma unroll
-          for (int i = 0; i < (C::kOCols / NR) * (RG / 16); ++i) {
-            const int at = (i / (RG / 16)) * NR + r0 + 16 * (i % (RG / 16));
+          for (int i = 0; i < C::kPParts * (NR / 16); ++i) {
+            const int at = 16 * i;
             float o[16];
             tmem_ld16(tOg + at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= alphas[r0 + 16 * (i % (RG / 16)) + e];
+            for (int e = 0; e < 16; ++e) o[e] *= alphas[16 * (i % (NR / 16)) + e];
             tmem_st16(tOg + at, o);
           }
           tmem_wait_st();
@@ -1161,9 +1129,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         group_any(bar_id, false);                    // `red` may change again
       }
       // probabilities
-      const uint32_t pt = C::oP + pb * C::kPBuf + (t >> 3) * 128 + (t & 7) * 16;
+      const uint32_t pt = C::oP + grp * C::kPBuf + (t >> 3) * 128 + (t & 7) * 16;
 #pragma unroll
-      for (int i = 0; i < RG / 16; ++i) {
+      for (int i = 0; i < NR / 16; ++i) {
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -1174,7 +1142,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         }
         if (kFp8) {
           // an E5M2 byte is the upper byte of an f16: three bytes of 3 significant bits, the last rounded
-          uint8_t* d = sm + pt + ((r0 >> 4) + i) * 2048;
+          uint8_t* d = sm + pt + (i) * 2048;
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             uint32_t w[4];
@@ -1194,32 +1162,31 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
             *reinterpret_cast<uint4*>(d + part * C::kPPart) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          uint8_t* d = sm + pt + ((r0 >> 3) + 2 * i) * 2048;
+          uint8_t* d = sm + pt + (2 * i) * 2048;
           *reinterpret_cast<uint4*>(d) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4*>(d + 2048) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
-      if (kFp8 && (C::kAlt || grp == 0) && t >= bi.live) {
+      if (kFp8 && t >= bi.live) {
         // a V row that was never written may hold NaN patterns, and 0 x NaN is NaN
         uint4* v = reinterpret_cast<uint4*>(sm + C::oStage + stage * C::kStage + kBlock * kDim + t * kDim);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k ^ (t & 7)] = make_uint4(0u, 0u, 0u, 0u);     // (eight rows, eight banks)
       }
-      stage += kStep;
+      stage += 2;
       if (stage >= C::kStages) stage -= C::kStages;
       smem_to_async();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(pb));
+      if (lane == 0) mbar_arrive(p_full(grp));
 
       if (bi.idx == 0) ok = put_q(bi.seg + 1);
-      if (bi.left < kStep) {
+      if (bi.left < 2) {
         // the group's last block of the segment
-        warp_reduce_rows<RG, false>(l);
-        if (lane < RG) red[wl * NR + r0 + lane] = l[0];
-        if (RG == 64) red[wl * NR + r0 + 32 + lane] = l[1];
-        ok = mbar_wait(p_free(pb), (n / C::kPBufs) & 1) && ok;
-        const bool two = C::kAlt && bi.idx + bi.left > 0;       // the other group has blocks of it too
+        warp_reduce_rows<NR, false>(l);
+        if (lane < NR) red[wl * NR + lane] = l[0];
+        ok = mbar_wait(p_free(grp), (n >> 1) & 1) && ok;
+        const bool two = bi.idx + bi.left > 0;       // the other group has blocks of it too
         const int sp = bi.seg & 1;
         if (two && bi.left == 0) ok = mbar_wait(join_full(sp), (joins >> sp) & 1) && ok;
         if (two) joins ^= 1u << sp;
@@ -1236,10 +1203,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         // the stores are whole rows and the code is short
         const bool whole = (bi.flags & 12) == 12;
         float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
-        auto stg = [&](int e) {
-          return reinterpret_cast<float*>(sm + C::oP + pb * C::kPBuf + (e / C::kStgRows) * C::kPPart +
-                                          (C::kAlt ? 0 : grp * RG * 128) + (e % C::kStgRows) * (kDim * 4));
-        };
+        float* stg = reinterpret_cast<float*>(sm + C::oP + grp * C::kPBuf);
         const int other = set ^ 1;
         const float* red2 = row_red + other * 4 * NR;
         const float* ref2 = row_ref + other * NR;
@@ -1260,12 +1224,12 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         }
         if (two) group_any(bar_id, false);
 #pragma unroll 1
-        for (int i = 0; i < RG / 16 && r0 + 16 * i < p.R; ++i) {
-          constexpr int kParts = C::kStacked ? 3 : 1;
+        for (int i = 0; i < NR / 16 && 16 * i < p.R; ++i) {
+          constexpr int kParts = C::kPParts;
           float o[kParts][16], o2[kParts][16];
 #pragma unroll
           for (int k = 0; k < kParts; ++k) {
-            tmem_ld16(tOg + k * NR + r0 + 16 * i, o[k]);
+            tmem_ld16(tOg + k * NR + 16 * i, o[k]);
             if (two) tmem_ld16(tO2 + k * NR + 16 * i, o2[k]);
           }
           tmem_wait_ld();
@@ -1290,15 +1254,15 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           }
           if (i > 0) group_any(bar_id, false);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) stg(e)[t] = o[0][e];
+          for (int e = 0; e < 16; ++e) stg[e * kDim + t] = o[0][e];
           group_any(bar_id, false);
 #pragma unroll 1
           for (int e = wl; e < 16; e += 4) {
-            const int r = r0 + 16 * i + e;
+            const int r = 16 * i + e;
             if (r >= p.R) break;
             const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
             const float M = L > 0.f ? -ref[r] : -INFINITY;          // L and O are in units of 2^M
-            const float4 v = *reinterpret_cast<const float4*>(stg(e) + 4 * lane);
+            const float4 v = *reinterpret_cast<const float4*>(stg + e * kDim + 4 * lane);
             if (whole) {
               const float inv = L > 0.f ? p.v_global / L : 0.f;
               const int j = row_pos[r];
