@@ -77,6 +77,7 @@ __device__ __forceinline__ int paged_cta_of(int64_t x, int64_t W, int C) {
 // A place in the item order.
 struct Walk {
   int b, g, blk, nb, L;
+  int end;                          // request behind the range's last: the unused places that follow may be many
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (++blk < nb) return;
     blk = 0;
@@ -85,7 +86,7 @@ struct Walk {
     skip(p, b + 1);
   }
   __device__ __forceinline__ void skip(const PagedParams& p, int from) {
-    for (b = from; b < p.B; ++b) {
+    for (b = from; b < end; ++b) {
       L = paged_len(p, b);
       nb = (L + kBlock - 1) / kBlock;
       if (nb > 0) return;
@@ -143,6 +144,7 @@ __device__ void find_range(const PagedParams& p, int cta, int ctas, int64_t* war
   }
   __syncthreads();
   const int64_t lo = length(before), hi = length(before + mine);
+  if (x1 == W && mine > 0 && hi == W) shared->at.end = b1;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int64_t x = which ? x1 : x0;
@@ -164,9 +166,14 @@ __device__ void find_range(const PagedParams& p, int cta, int ctas, int64_t* war
         const int64_t n = done + static_cast<int64_t>(w.g) * nb + w.blk;
         if (which) {
           shared->n1 = n;
+          shared->at.end = b + 1;
         } else {
           shared->n0 = n;
-          shared->at = w;
+          shared->at.b = w.b;
+          shared->at.g = w.g;
+          shared->at.blk = w.blk;
+          shared->at.nb = w.nb;
+          shared->at.L = w.L;
           shared->row0 = row0;
         }
         break;
@@ -1793,10 +1800,11 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
 
 // Joins the partials of a cut row, in CTA order. One CTA per (cut, group of
 // rows); with few rows the eight warps share a row's partials.
+constexpr int kJoinWarps = 16;
 template <int kChunk>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
-  __shared__ float sm_o[kWarps][kDim];
-  __shared__ float sm_m[kWarps], sm_l[kWarps];
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
+  __shared__ float sm_o[kJoinWarps][kDim];
+  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
   const int chunks = (p.R + rows_per_cta - 1) / rows_per_cta;
@@ -1806,7 +1814,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
   if (cut.n == 0) return;
   const int cta = cut.cta;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wpr = kWarps / rows_per_cta;                           // warps per row
+  const int wpr = kJoinWarps / rows_per_cta;                       // warps per row
   const int row = chunk * rows_per_cta + warp / wpr, sub = warp % wpr;
   const bool live = row < p.R;
   float M = -INFINITY, L = 0.f;
@@ -1985,12 +1993,12 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
         : rows_of == 32 ? launch_tc<MSA_NVFP4, 32>(p, ctas, stream) : launch_many<MSA_NVFP4>(p, ctas, stream);
   if (err != cudaSuccess) return err;
   if (ctas > 1) {
-    // few rows: a CTA for each query row, whose warps share its many partials, 32 in flight each (165
-    // registers: one CTA per SM); else a warp for each, with mostly two or three partials
+    // few rows: a CTA for each query row, whose warps share its many partials, 16 in flight each (1x128k: 16.0 us,
+    // 8 warps 16.9, 4 warps 20.6); else a warp for each, with mostly two or three partials
     const bool few = static_cast<int64_t>(cuts) * p.R <= sms;
-    const int rpc = few ? 1 : 8;
+    const int rpc = few ? 1 : kJoinWarps;
     const int chunks = (p.R + rpc - 1) / rpc;
-    err = launch_pdl(few ? paged_join_kernel<32> : paged_join_kernel<4>, dim3(cuts * chunks), dim3(kThreads), 0, stream, p, rpc);
+    err = launch_pdl(few ? paged_join_kernel<16> : paged_join_kernel<4>, dim3(cuts * chunks), dim3(32 * kJoinWarps), 0, stream, p, rpc);
     if (err != cudaSuccess) return err;
   }
   rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"

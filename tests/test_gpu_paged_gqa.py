@@ -224,3 +224,15 @@ def test_random_steps(seed):
     c = Case(lens, kind, G, group, Q, seed=seed)
     c.run()
     c.check(which=range(min(B, 6)))
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("Q", [1, 8])
+def test_few_requests_in_a_large_batch(kind, Q):
+    """Two live requests among 4,094 unused places, at the front, apart, and at the end."""
+    for at in ([0, 1], [5, 3000], [4094, 4095]):
+        lens = [0] * 4096
+        lens[at[0]], lens[at[1]] = 700, 300
+        c = Case(lens, kind, 1, 16, Q, seed=26)
+        c.run()
+        c.check(which=at + [2, 4000])
