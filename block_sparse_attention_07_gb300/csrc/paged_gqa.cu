@@ -1978,10 +1978,17 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   const int64_t rows = static_cast<int64_t>(a.B) * a.G;
   p.by_row = rows < ctas - 1;
   const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
-  // One form per number of query rows: up to 16 (bf16: warp mma, which the cache's bytes bound; FP8, NVFP4:
-  // tokens as M), up to 32 (FP8, NVFP4), more (rows as M).
-  const int rows_of = p.R <= 16 ? 16 : p.R <= 32 && a.kv != MSA_BF16 ? 32 : 128;
-  p.row_cost = rows_of == 128 ? 3 : a.kv == MSA_BF16 ? 2 : 5;         // measured
+  // One form per number of query rows R. FP8 and NVFP4: tokens as M for 16 and 32 rows, rows as M above (32x16k, FP8
+  // with 16 / 32 rows 91.7 / 97.7 us against 128.7 / 129.2, NVFP4 93.5 / 117.0 against 135.8 / 136.5; 64 rows on the
+  // 32-row form would read the cache twice). bf16: up to 16 rows, warp mma for what a small block table can hold
+  // (2x4k 12.2 us, rows as M 13.2; 8x8k 33.0, 33.8), rows as M for a table of at least 64 blocks per CTA (32x32k
+  // 315.5 us, warp mma 322.4; 64 requests of 8k-128k 1,284, 1,322).
+  const bool large = most >= 64ll * ctas;
+  const int rows_of = a.kv == MSA_BF16 ? (p.R <= 16 && !large ? 16 : 128) : p.R <= 16 ? 16 : p.R <= 32 ? 32 : 128;
+  // A row's start and end, in blocks of its form. 64 requests of up to 2,047 tokens, 4 KV heads, at 0 / 2 / 3 / 5 / 8:
+  // bf16 with 16 rows 54.7 / 39.2 / 36.6 / 37.3 / 39.9 us, 64 rows 56.0 / 43.6 / 41.8 / 41.7 / 42.8; FP8 16 rows
+  // 37.7 / 30.2 / 28.0 / 26.7 / 26.4, 64 rows 60.6 / 45.4 / 40.7 / 39.2 / 40.8; NVFP4 32 rows 58.7 / 43.3 / 38.7 / 37.4 / 37.5.
+  p.row_cost = a.kv == MSA_BF16 ? 3 : 5;
   cudaError_t err;
   if (a.kv == MSA_BF16)
     err = rows_of == 16 ? launch_mma(p, ctas, stream) : launch_many<MSA_BF16>(p, ctas, stream);

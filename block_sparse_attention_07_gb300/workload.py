@@ -292,6 +292,19 @@ class DeviceWorkload:
                             self.cache, None, self.flags, stream)
         self.attend(stream if stream is not None else torch.cuda.current_stream(self.device), selected)
 
+    def dense_step(self, stream=None):
+        """One decode step of a full-attention layer: insert this step's K/V, then
+        attend over every cached token (``out``, ``lse``; index cache and
+        ``selected`` untouched)."""
+        if getattr(self, "_dense_ws", None) is None:
+            size = msa.paged_gqa_workspace_size(self.dims, self.cache.dtype)
+            self._dense_ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        st = stream if stream is not None else torch.cuda.current_stream(self.device)
+        msa.kv_insert_quant(self.dims, self.new_k, self.new_v, None, self.idx_new_dtype, self.new_slots,
+                            self.cache, None, self.flags, st)
+        msa.paged_gqa_decode(self.dims, self.q, self.cache, self.block_table_d, self.seq_lens_d, self.out, self.lse,
+                             self._dense_ws, self.flags, st)
+
     def capture(self, fn) -> torch.cuda.CUDAGraph:
         """Captures ``fn(stream)`` (a step of this workload) into a CUDA graph;
         ``graph.replay()`` then reruns its kernels with the same buffers."""

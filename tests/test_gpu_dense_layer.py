@@ -5,9 +5,13 @@ import pytest
 import torch
 
 from block_sparse_attention_07_gb300 import msa, synth
+from block_sparse_attention_07_gb300.workload import DeviceWorkload
 from oracle import formats as F
 from oracle import mrope as Mr
+from oracle import msa as omsa
+from oracle import run as orun
 
+import parity
 from paged import FP4_G, FP8_S, KINDS, bf16, encode
 
 pytestmark = pytest.mark.gpu
@@ -153,3 +157,29 @@ def test_captured_steps_cross_a_block_border(kv):
         torch.cuda.synchronize()
         graph.replay()
         layer.check(one)
+
+
+@pytest.mark.parametrize("kv,Q", [("bf16", 1), ("fp8", 8), ("nvfp4", 2)])
+def test_workload_dense_step(kv, Q):
+    """A full-attention layer beside a sparse one: same requests, own caches; eager, then replayed."""
+    base = synth.WORKLOADS["nvfp4_256k" if kv == "nvfp4" else "b32_32k"]
+    w = synth.scaled(base, batch=3, ctx=700, kv_dtype=kv, q_len=Q)
+    src = parity.build(w)
+    layer = DeviceWorkload.layer_like(src, 2)
+    layer.dense_step()
+    torch.cuda.synchronize()
+    eager = layer.out.clone(), layer.lse.clone()
+    g = layer.capture(layer.dense_step)
+    layer.out.zero_()
+    layer.lse.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert layer.check_flags() == 0
+    assert torch.equal(layer.out, eager[0]) and torch.equal(layer.lse, eager[1])
+    scale = synth.kv_scale(w)
+    for bi, b in enumerate(layer.which):
+        L = int(layer.lens[bi])
+        req = synth.request(layer.w, b, L)
+        K, V = (orun.cached_kv_rows(req[n], kv, scale) for n in "kv")
+        out, lse = omsa.dense_gqa(orun.to_f32(req["q"]), K, V, L, w.softmax_scale)
+        parity.check_attention(eager[0][bi].float().cpu().numpy(), eager[1][bi].cpu().numpy(), out, lse, f"{kv} b={b}")

@@ -236,3 +236,21 @@ def test_few_requests_in_a_large_batch(kind, Q):
         c = Case(lens, kind, 1, 16, Q, seed=26)
         c.run()
         c.check(which=at + [2, 4000])
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("G,group,Q", [(4, 16, 1), (1, 8, 2), (3, 5, 1), (8, 1, 8), (2, 1, 1)])
+def test_wide_block_table(kind, G, group, Q):
+    """A table with room for a million tokens per request; short and empty requests in it."""
+    c = Case([1, 700, 0, 128, 2049, -3, 129], kind, G, group, Q, seed=27, cols_extra=8192)
+    c.run()
+    c.check(which=[0, 1, 2, 3, 4, 6], flags=msa.FLAG_BAD_SEQLEN)
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -100, 2.0 ** 20])
+def test_wide_block_table_query_magnitudes(kind, q_scale):
+    c = Case([300, 900], kind, 2, 8, 1, seed=28, q_scale=q_scale, scale=2.0 ** -20 if q_scale > 1 else None,
+             cols_extra=8192)
+    c.run()
+    c.check()
