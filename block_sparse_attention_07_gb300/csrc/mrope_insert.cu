@@ -11,7 +11,16 @@
 // A row belongs to 8 lanes; lane l holds dims 8l .. 8l+7 and 64 + 8l .. 64 + 8l+7
 // (two 16-byte loads), so both dims of its 8 pairs are in its registers: the
 // rotation needs no exchange and the norm three shuffles for four rows of a
-// warp. A warp takes `passes` groups of four rows of one token.
+// warp. A warp takes groups of four rows of one token; `parts` warps share a
+// token's.
+//
+// What bounds it is the rows' bytes, and what it takes to reach that rate is
+// bytes in flight: each warp has its next six groups of queries (1 KB each,
+// contiguous) on their way to its own part of shared memory by bulk copies,
+// and does the keys and values while the first of them arrive. 8,191 tokens,
+// 64 + 4 + 4 heads, FP8 cache: 51.5 us, 5.7 TB/s (85 % of a copy's rate); with
+// loads into registers, two groups ahead, 59.2 us. 64 tokens: 4.5 us, the
+// host's time per launch.
 //
 // Phases: theta^(-2i/128) / 2 pi is held as a 64-bit fraction of a turn, so that
 // position times it, modulo one turn, is one integer product. The fraction comes
@@ -25,6 +34,8 @@
 namespace msa {
 
 constexpr int kMropeWarps = 4, kMropeCtas = 7;    // warps per CTA, CTAs per SM (72 registers)
+constexpr int kRingSlots = 6;                     // passes of a warp's queries in flight
+constexpr uint32_t kPassBytes = 4 * kDim * 2;
 
 struct MropeParams {
   InsertParams ins;
@@ -55,6 +66,12 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* x) {
 }
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 // Eight values over a positive scale -> eight E4M3 codes.
@@ -133,6 +150,8 @@ __device__ __forceinline__ void store_idx16(const InsertParams& p, int64_t row, 
 }
 
 __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_insert_kernel(const __grid_constant__ MropeParams pp) {
+  __shared__ alignas(128) uint8_t ring_rows[kMropeWarps * kRingSlots * kPassBytes];
+  __shared__ uint64_t ring_bars[kMropeWarps * kRingSlots];
   griddep_launch_dependents();
   griddep_wait();
   const InsertParams& p = pp.ins;
@@ -143,6 +162,22 @@ __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_in
   const int64_t t = wid / pp.parts;
   const int part = static_cast<int>(wid - t * pp.parts);
   if (t >= p.T) return;
+
+  const int q_passes = nq / 4;
+  const uint32_t rows_at = smem_addr(ring_rows) + (threadIdx.x >> 5) * kRingSlots * kPassBytes;
+  const uint32_t bars_at = smem_addr(ring_bars) + (threadIdx.x >> 5) * kRingSlots * 8;
+  uint64_t policy = 0;
+  auto fetch = [&](int pass, int slot) {
+    mbar_arrive_expect_tx(bars_at + 8 * slot, kPassBytes);
+    bulk_g2s(rows_at + slot * kPassBytes, pp.q + (t * nq + 4 * pass) * kDim, kPassBytes, bars_at + 8 * slot, policy);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kRingSlots; ++i) mbar_init(bars_at + 8 * i, 1);
+    fence_mbar_init();
+    policy = l2_evict_first_policy();
+    for (int i = 0; i < kRingSlots && part + i * pp.parts < q_passes; ++i) fetch(part + i * pp.parts, i);
+  }
+  __syncwarp();
 
   // cos and sin of the lane's 8 pairs (8 l + i): each is computed by one of the
   // four lanes that use it
@@ -185,45 +220,9 @@ __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_in
     return rsqrtf(fmaf(ss, 1.0f / kDim, pp.eps));
   };
 
-  // Most rows are queries, four at a time: with their weights folded into the cosines and sines a pair is four
-  // products and two scalings. The next rows are on their way while these are computed.
-  const int q_passes = nq / 4;
+  // While the queries are on their way, the rows behind them: any last queries, keys, values, index rows
   int pass = part;
-  if (pass < q_passes) {
-    float wc[8], ws[8], vs[8], vc[8];
-    {
-      float w[16];
-      weights(pp.wq, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        wc[i] = w[i] * cs[i]; ws[i] = w[i] * sn[i];
-        vs[i] = w[8 + i] * sn[i]; vc[i] = w[8 + i] * cs[i];
-      }
-    }
-    const int64_t first = (t * nq + 4 * pass + (lane >> 3)) * kDim + 8 * l, hop = 4ll * pp.parts * kDim;
-    const uint16_t* src = pp.q + first;
-    uint16_t* dst = pp.q_out + first;
-    uint4 lo = *reinterpret_cast<const uint4*>(src), hi = *reinterpret_cast<const uint4*>(src + 64);
-    for (; pass < q_passes; pass += pp.parts, dst += hop) {
-      float x[16], y[16];
-      unpack8(lo, x);
-      unpack8(hi, x + 8);
-      if (pass + pp.parts < q_passes) {
-        src += hop;
-        lo = *reinterpret_cast<const uint4*>(src);
-        hi = *reinterpret_cast<const uint4*>(src + 64);
-      }
-      const float rinv = row_scale(x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = (x[i] * wc[i] - x[8 + i] * vs[i]) * rinv;
-        y[8 + i] = (x[i] * ws[i] + x[8 + i] * vc[i]) * rinv;
-      }
-      *reinterpret_cast<uint4*>(dst) = pack8(y);
-      *reinterpret_cast<uint4*>(dst + 64) = pack8(y + 8);
-    }
-  }
-  // the rows behind them: any last queries, keys, values, index rows
+  if (pass < q_passes) pass += (q_passes - pass + pp.parts - 1) / pp.parts * pp.parts;
   for (; 4 * pass < rows; pass += pp.parts) {
     const int r = 4 * pass + (lane >> 3);
     const bool live = r < rows;
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_in
       weights(wv, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // as above, and rounded to bf16 here: what the outputs hold and the caches quantise
+        // rounded to bf16 here: what the outputs hold and the caches quantise
         const float a = (x[i] * (w[i] * cs[i]) - x[8 + i] * (w[8 + i] * sn[i])) * rinv;
         const float b = (x[i] * (w[i] * sn[i]) + x[8 + i] * (w[8 + i] * cs[i])) * rinv;
         x[i] = bf16_bits_to_f32(static_cast<uint16_t>(pack_bf16x2(a, 0.f) & 0xFFFF));
@@ -269,6 +268,54 @@ __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_in
       const int64_t row = kind == 4 ? (page * ni + h) * kBlock + off : 0;
       store_idx16(p, row, x, l, kind == 4 && live && held);
     }
+  }
+
+  // Most rows are queries, four at a time: with their weights folded into the cosines and sines a pair is four
+  // products and two scalings.
+  if (part >= q_passes) return;
+  float wc[8], ws[8], vs[8], vc[8];
+  {
+    float w[16];
+    weights(pp.wq, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      wc[i] = w[i] * cs[i]; ws[i] = w[i] * sn[i];
+      vs[i] = w[8 + i] * sn[i]; vc[i] = w[8 + i] * cs[i];
+    }
+  }
+  uint16_t* dst = pp.q_out + (t * nq + 4 * part + (lane >> 3)) * kDim + 8 * l;
+  const int64_t hop = 4ll * pp.parts * kDim;
+  auto rotate = [&](const uint4& lo, const uint4& hi) {
+    float x[16], y[16];
+    unpack8(lo, x);
+    unpack8(hi, x + 8);
+    const float rinv = row_scale(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = (x[i] * wc[i] - x[8 + i] * vs[i]) * rinv;
+      y[8 + i] = (x[i] * ws[i] + x[8 + i] * vc[i]) * rinv;
+    }
+    *reinterpret_cast<uint4*>(dst) = pack8(y);
+    *reinterpret_cast<uint4*>(dst + 64) = pack8(y + 8);
+    dst += hop;
+  };
+  int buf = 0;
+  uint32_t phase = 0;
+  for (pass = part; pass < q_passes; pass += pp.parts) {
+    if (__all_sync(0xffffffffu, mbar_wait(bars_at + 8 * buf, phase)) == 0) {
+      // a copy that did not come in time; those behind it are waited for, so that none outlives the CTA
+      if (lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+      for (int i = 1; i < kRingSlots && pass + i * pp.parts < q_passes; ++i) {
+        if (++buf == kRingSlots) { buf = 0; phase ^= 1u; }
+        mbar_wait(bars_at + 8 * buf, phase);
+      }
+      return;
+    }
+    const uint32_t at = rows_at + buf * kPassBytes + (lane >> 3) * (kDim * 2) + 16 * l;
+    rotate(ld_shared16(at), ld_shared16(at + kDim));
+    __syncwarp();                                    // the buffer has been read
+    if (lane == 0 && pass + kRingSlots * pp.parts < q_passes) fetch(pass + kRingSlots * pp.parts, buf);
+    if (++buf == kRingSlots) { buf = 0; phase ^= 1u; }
   }
 }
 
@@ -300,10 +347,12 @@ cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_ax
   }
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
   const int passes = (rows + 3) / 4;
-  // one warp takes a whole token when there are tokens enough to fill the GPU's
-  // warps; with fewer a token's rows are spread over up to `passes` warps
-  const int64_t want = 32ll * device_sm_count();
-  int64_t parts = (want + a.ins.T - 1) / a.ins.T;
+  // Warps per token: one once there are 64 tokens per SM (16,000 tokens 92.9 us, two 95.3), two below (4,096
+  // tokens 28.6, one 31.0, three 31.2), more when there are few tokens (16 warps per SM: 1,024 tokens 11.5 us;
+  // 32 per SM 14.9, 8 per SM 13.7).
+  const int64_t sms = device_sm_count();
+  int64_t parts = a.ins.T >= 64 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
+  if (parts < 2 && a.ins.T < 64 * sms) parts = 2;
   if (parts > passes) parts = passes;
   pp.parts = static_cast<int>(parts);
   const int64_t grid = (a.ins.T * parts + kMropeWarps - 1) / kMropeWarps;
