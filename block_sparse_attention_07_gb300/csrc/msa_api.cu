@@ -2,6 +2,7 @@
 // the thread-local dispatch record, and the launches. Nothing here allocates
 // device memory and nothing synchronises except msa_read_device_flags.
 #include <cstring>
+#include <initializer_list>
 
 #include "msa_internal.h"
 
@@ -35,6 +36,11 @@ __global__ void bounded_wait_selftest_kernel(uint32_t* flags) {
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool aligned4(std::initializer_list<const void*> ps) {   // null counts as aligned
+  for (const void* p : ps)
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return false;
+  return true;
+}
 
 // Shape rules shared by every entry point.
 static msa_status_t check_dims(const msa_dims_t* d) {
@@ -417,7 +423,10 @@ msa_status_t msa_build_step(const msa_dims_t* dims, const int32_t* ctx_lens, con
       block_table == nullptr || seq_lens == nullptr || token_starts == nullptr || slot_mapping == nullptr ||
       positions == nullptr || free_head_out == nullptr || dev_flags == nullptr)
     return MSA_ERR_INVALID_ARG;
-  if (!aligned16(slot_mapping)) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(slot_mapping) ||
+      !aligned4({ctx_lens, new_lens, free_pages, free_head, pos_offset, block_table, seq_lens, token_starts, positions,
+                 free_head_out, dev_flags}))
+    return MSA_ERR_INVALID_ARG;
   if (seq_lens == ctx_lens || seq_lens == new_lens || free_head_out == free_head) return MSA_ERR_INVALID_ARG;
   StepArgs a{ctx_lens, new_lens, free_pages, free_head, pos_offset, block_table, seq_lens, token_starts,
              slot_mapping, positions, free_head_out, dev_flags, position_stride, dims->batch,
@@ -457,6 +466,8 @@ msa_status_t msa_qk_norm_mrope_insert(const msa_dims_t* dims, const void* q, con
   const void* ptrs16[] = {q, k, v, q_out, nr->q_weight, nr->k_weight};
   for (const void* ptr : ptrs16)
     if (!aligned16(ptr)) return MSA_ERR_INVALID_ARG;
+  if (!aligned4({positions, dev_flags}) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return MSA_ERR_INVALID_ARG;
   if (with_idx && (!aligned16(idx_q) || !aligned16(idx_k) || !aligned16(idx_q_out) || !aligned16(nr->idx_q_weight) ||
                    !aligned16(nr->idx_k_weight)))
     return MSA_ERR_INVALID_ARG;
@@ -499,11 +510,13 @@ msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const m
                                   void* workspace, size_t workspace_bytes, uint32_t* dev_flags, void* stream) {
   msa_status_t st = check_dense_dims(dims);
   if (st != MSA_OK) return st;
-  if (!(dims->softmax_scale > 0.f) || dims->softmax_scale > 3.0e38f) return MSA_ERR_INVALID_ARG;
+  if (!(dims->softmax_scale > 0.f) || dims->softmax_scale > 2.0e38f) return MSA_ERR_INVALID_ARG;   // times log2 e: finite
   if (q == nullptr || cache == nullptr || cache->k == nullptr || cache->v == nullptr || block_table == nullptr ||
       seq_lens == nullptr || out == nullptr || dev_flags == nullptr)
     return MSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(cache->k) || !aligned16(cache->v)) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(cache->k) || !aligned16(cache->v) ||
+      !aligned4({block_table, seq_lens, lse, dev_flags}))
+    return MSA_ERR_INVALID_ARG;
   PagedArgs a;
   memset(&a, 0, sizeof(a));
   a.kv = cache->dtype;

@@ -433,7 +433,8 @@ typedef struct {
  * Shapes: n_heads and n_kv_heads as in dims, any n_heads up to 16 n_kv_heads
  * that n_kv_heads divides, n_kv_heads up to 64; n_idx_heads rows in the index
  * branch. positions: int32, axes->num_axes rows of num_tokens, position_stride
- * elements apart. q_out may be q, idx_q_out may be idx_q.
+ * elements apart. q_out may be q, idx_q_out may be idx_q. No slot may occur
+ * twice among the tokens (negative ones aside).
  */
 msa_status_t msa_qk_norm_mrope_insert(const msa_dims_t* dims, const void* q, const void* k, const void* v,
                                       const void* idx_q, const void* idx_k, const int32_t* positions,

@@ -160,3 +160,17 @@ def test_oracle_mrope_with_equal_axes_is_the_one_axis_rotation():
     x, w, pos = rng.standard_normal((5, 2, 128)), rng.standard_normal(128), rng.integers(0, 9999, 5)
     got = mrope.norm_mrope(x, w, np.tile(pos, (3, 1)), mrope.sections_to_axis((16, 24, 24)), 1e-6, 1e4)
     assert np.array_equal(got, prologue.norm_rope(x, w, pos, 1e-6, 1e4))
+
+
+def test_pointers_off_their_type(m):
+    odd = ctypes.c_void_p(0x50002)
+    for name in ("table", "lens", "flags"):
+        assert _gqa(m, **{name: odd}) == m.ERR_INVALID_ARG, name
+    assert m.lib.msa_paged_gqa_decode(ctypes.byref(_dims(m)), FAKE, ctypes.byref(m._KVCache(m.BF16, FAKE, FAKE, None, None, 1.0, 1.0)),
+                                      FAKE, FAKE, FAKE, odd, FAKE, 1 << 40, FAKE, None) == m.ERR_INVALID_ARG
+    for name in ("ctx", "new", "free", "head", "off", "table", "seq", "starts", "pos", "out", "flags"):
+        assert _step(m, **{name: odd}) == m.ERR_INVALID_ARG, name
+    assert _gqa(m, _dims(m, softmax_scale=2.5e38)) == m.ERR_INVALID_ARG
+    for name in ("pos", "slots", "flags"):
+        assert _mrope(m, **{name: odd}) == m.ERR_INVALID_ARG, name
+    assert _mrope(m, slots=ctypes.c_void_p(0x50004)) == m.ERR_INVALID_ARG

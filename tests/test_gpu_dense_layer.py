@@ -183,3 +183,21 @@ def test_workload_dense_step(kv, Q):
         K, V = (orun.cached_kv_rows(req[n], kv, scale) for n in "kv")
         out, lse = omsa.dense_gqa(orun.to_f32(req["q"]), K, V, L, w.softmax_scale)
         parity.check_attention(eager[0][bi].float().cpu().numpy(), eager[1][bi].cpu().numpy(), out, lse, f"{kv} b={b}")
+
+
+def test_readme_example():
+    """The README's second block runs as written after its first; with one token per request the output is its V."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    blocks = re.findall(r"```python\n(.*?)```", open(path, encoding="utf-8").read(), flags=re.S)
+    env = {}
+    for block in blocks[:2]:
+        exec(compile(block, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    assert "paged_gqa_decode" in blocks[1]
+    slots = env["slot_map"].tolist()
+    assert slots == [int(env["free"][b]) * 128 for b in range(2)] and int(env["head_next"]) == 2
+    for b, slot in enumerate(slots):
+        v = env["cache"].v[slot // 128, :, slot % 128]
+        assert torch.equal(env["out"][b, 0].view(4, 16, 128), v[:, None].expand(4, 16, 128))

@@ -254,3 +254,21 @@ def test_wide_block_table_query_magnitudes(kind, q_scale):
              cols_extra=8192)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("Q", [1, 2, 8])
+def test_bad_pages_while_page_0_was_never_written(kind, Q):
+    """The kernels put page 0 in a bad page's place; what it holds must not matter."""
+    c = Case([900, 300, 128], kind, Q=Q, seed=29)
+    table = c.table.copy()
+    table[0, 2], table[1, 2] = c.P, -1
+    table[table == 0] = 2 ** 31 - 1
+    for t, fill in ((c.cache.k, 0xFF), (c.cache.v, 0xFF), (c.cache.k_scale, 0x7F), (c.cache.v_scale, 0x7F)):
+        if t is not None:
+            t[0].view(torch.uint8).fill_(fill)
+    c.table_d.copy_(torch.from_numpy(table))
+    c.run()
+    nb = [8, 3, 1]
+    live = {b: [i for i in range(nb[b]) if 0 < table[b, i] < c.P] for b in range(3)}
+    c.check(live_blocks=live, flags=msa.FLAG_BAD_PAGE)
