@@ -614,6 +614,10 @@ __device__ __forceinline__ void st_shared16(uint32_t a, const uint32_t* v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
+// A warp's V scales of a block: two groups of 16 dims x 128 tokens, as f16 pairs of two tokens in rows of 20 words
+// [group][(token / 2) % 4][token / 8], so that neither the stores nor the reads meet in a bank.
+constexpr uint32_t kVScaleRow = 20, kVScaleBuf = 8 * kVScaleRow * 4;
+
 template <int kKv, int NR>
 struct TcCfg {
   static constexpr bool kFp8 = kKv == MSA_FP8_E4M3;
@@ -636,8 +640,8 @@ struct TcCfg {
   // One P buffer (there is one per group); it also stages 16 output rows
   static constexpr uint32_t kPBuf = kPParts * kPPart < 16 * kDim * 4 ? 16 * kDim * 4 : kPParts * kPPart;
   static constexpr uint32_t kStage = raw_bytes<kKv>();
-  static constexpr uint32_t kTiles = kFp8 ? 0 : 4 * kHalfBox;  // V[2] in f16
-  static constexpr uint32_t kFixed = kTiles + 2 * kQParts * kQPart + 2 * kPBuf;
+  static constexpr uint32_t kVScales = kFp8 ? 0 : kTurns * 4 * kVScaleBuf;   // V's scales in f16, of a warp each
+  static constexpr uint32_t kFixed = kVScales + 2 * kQParts * kQPart + 2 * kPBuf;
   static constexpr uint32_t kSmall = 2048 + NR * 128;
   static constexpr int kFit = static_cast<int>((231424 - 1024 - kFixed - kSmall) / kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -645,16 +649,17 @@ struct TcCfg {
   // taken where S and O are read)
   static constexpr int kSCols = kQParts * NR, kOCols = kPParts * NR;
   static constexpr int kKCols = kFp8 ? 0 : 2 * (kDim / 2);     // NVFP4: K[2] in f16, two dims per column
+  static constexpr int kVCols = kFp8 ? 0 : 2 * (kBlock / 2);   // and V[2], two tokens per column
   static constexpr int kSets = 4;                              // states: of each group, for this segment and the one before
-  static constexpr int kUsedCols = kTcS * kSCols + kSets * kOCols + kKCols;
+  static constexpr int kUsedCols = kTcS * kSCols + kSets * kOCols + kKCols + kVCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
   // shared memory
   static constexpr uint32_t oStage = 0;
-  static constexpr uint32_t oTiles = (kStages * kStage + 1023) & ~1023u;
-  static constexpr uint32_t oQ = oTiles + kTiles;
+  static constexpr uint32_t oQ = (kStages * kStage + 1023) & ~1023u;
   static constexpr uint32_t oP = oQ + 2 * kQParts * kQPart;
-  static constexpr uint32_t oInfo = oP + 2 * kPBuf;
+  static constexpr uint32_t oVScales = oP + 2 * kPBuf;
+  static constexpr uint32_t oInfo = oVScales + kVScales;
   static constexpr uint32_t oRow = oInfo + kInfos * sizeof(BlockInfo);   // [2 q buffers][NR] multiplier
   static constexpr uint32_t oRef = oRow + 2 * NR * 4;                    // [sets][NR] kOff - reference
   static constexpr uint32_t oAlpha = oRef + kSets * NR * 4;              // [sets][NR]
@@ -666,6 +671,7 @@ struct TcCfg {
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
   static_assert(kTotal - oInfo <= kSmall, "small area");
+  static_assert(kUsedCols <= 512, "tensor memory");
 };
 
 // Shared-memory matrix descriptors: start address and leading and stride byte
@@ -691,14 +697,9 @@ __host__ __device__ constexpr uint32_t mma_idesc(int a_type, int b_type, int N, 
 }
 // kind::f16 operand types: 0 f16, 1 bf16. kind::f8f6f4: 0 E4M3, 1 E5M2.
 
-template <bool kFp8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  if (kFp8)
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
-  else
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
 }
 // A from tensor memory (kind::f16).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -722,6 +723,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const float* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                ::"r"(a), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
                  "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+               : "memory");
+}
+// 16 lanes x 16 columns: lane i of the warp holds lanes i / 4 (r[2k]) and 8 + i / 4 (r[2k + 1]) of column 4 k + i % 4.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
-  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kSets * C::kOCols;
+  const uint32_t tO = tmem + kTcS * C::kSCols, tK = tO + C::kSets * C::kOCols, tV = tK + C::kKCols;
   griddep_wait();
 
   const int cta = blockIdx.x;
@@ -925,7 +932,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           if (kFp8) {
             const uint32_t k = k0 + stage * (C::kStage >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_ss<true>(d, desc_of(k + kk * 2, hi), desc_of(q + kk * 2, hi), id_s, kk > 0);
+            for (int kk = 0; kk < 4; ++kk) mma_fp8(d, desc_of(k + kk * 2, hi), desc_of(q + kk * 2, hi), id_s, kk > 0);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -940,10 +947,10 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         if (++stage == C::kStages) { stage = 0; ph ^= 1u; }
       }
     } else {
-      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, 1, 1);
+      constexpr uint32_t id_o = mma_idesc(0, kFp8 ? 1 : 0, C::kOCols, kFp8 ? 1 : 0, 1);
       constexpr uint32_t hi_v = desc_hi(1024, kSwz128), hi_p = desc_hi(2048, kSwzNone);
       const uint32_t p0 = desc_lo(base + C::oP, 128);
-      const uint32_t v0 = kFp8 ? desc_lo(base + C::oStage + kBlock * kDim, 16384) : desc_lo(base + C::oTiles, kHalfBox);
+      const uint32_t v0 = desc_lo(base + C::oStage + kBlock * kDim, 16384);             // (FP8)
       int stage = 0;
       for (int n = 0; n < items; ++n) {
         const int pb = n & 1;
@@ -958,13 +965,12 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
             const uint32_t v = v0 + stage * (C::kStage >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ss<true>(d, desc_of(v + kk * 256, hi_v), desc_of(pt + kk * 32, hi_p), id_o, !(fresh && kk == 0));
+              mma_fp8(d, desc_of(v + kk * 256, hi_v), desc_of(pt + kk * 32, hi_p), id_o, !(fresh && kk == 0));
             mma_commit(empty(stage));
           } else {
-            const uint32_t v = v0 + (n & 1) * (2 * kHalfBox >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ss<false>(d, desc_of(v + kk * 128, hi_v), desc_of(pt + kk * 16, hi_p), id_o, !(fresh && kk == 0));
+              mma_ts(d, tV + (n & 1) * (kBlock / 2) + 8 * kk, desc_of(pt + kk * 16, hi_p), id_o, !(fresh && kk == 0));
             mma_commit(v_free(n & 1));
           }
           mma_commit(p_free(pb));
@@ -983,7 +989,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
     // ---------------------------------------------------------- softmax --
     regs_inc<C::kRegsSoft>();
     const int grp = (warp - C::kSoft0) >> 2, wl = warp & 3, bar_id = 1 + grp;
-    const int t = 32 * wl + lane;                   // token of S, dim of O
+    const int t = 32 * wl + lane;                   // token of S
+    const int o_dim = kFp8 ? t : 32 * wl + 4 * (lane & 7) + (lane >> 3);        // dim of O: V's order of the lanes
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
     // The queries of a segment, by the group with the first block of the segment before it: 16 lanes take a row,
     // 8 dims each, all loads before the first use.
@@ -1272,7 +1279,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           }
           if (i > 0) group_any(bar_id, false);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) stg[e * kDim + t] = o[0][e];
+          for (int e = 0; e < 16; ++e) stg[e * kDim + o_dim] = o[0][e];
           group_any(bar_id, false);
 #pragma unroll 1
           for (int e = wl; e < 16; e += 4) {
@@ -1307,17 +1314,16 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
   } else if (C::kConv > 0) {
     regs_dec<C::kConv ? C::kRegsConv : C::kRegsCtl>();
     // -------------------------------------------------- NVFP4 expansion --
-    // Four warps at a time expand K into tensor memory, four V into shared memory; a
-    // thread takes a token's row. The codes' 64-byte swizzle keeps the reads of eight
-    // rows in eight banks, and so does the V tile's for the stores.
-    const int cg = (warp - C::kConv0) >> 2, turn = cg % C::kTurns;
+    // Four warps at a time expand K into tensor memory, four V. Of K a thread takes a token's row. V has to lie
+    // with a dim per lane and two tokens per column: a warp takes 32 dims, transposed on the way from shared memory
+    // (16-bit transposition: four dims of two tokens per register), in the order of lanes 8 k + j = dim 4 j + k. The
+    // codes' 64-byte swizzle keeps the reads of eight rows in eight banks.
+    const int cg = (warp - C::kConv0) >> 2, turn = cg % C::kTurns, wq = warp & 3;
     const bool isv = cg >= C::kTurns;
-    const int row = 32 * (warp & 3) + lane;
     constexpr uint32_t codes = kBlock * kDim / 2, scales = kBlock * kDim / 16;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint8_t* src = sm + C::oStage + (isv ? codes : 0) + row * (kDim / 2);
-    const uint8_t* ssrc = sm + C::oStage + 2 * codes + (isv ? scales : 0) + row * (kDim / 16);
-    const int swz = ((row >> 1) & 3) << 4, swz_v = (row & 7) << 4;
+    const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+    const int swz = ((lane >> 1) & 3) << 4;
+    uint32_t* vs = reinterpret_cast<uint32_t*>(sm + C::oVScales + (turn * 4 + wq) * kVScaleBuf);
     int s = turn;
     uint32_t ph = 0;
     for (int n = turn; n < items; n += C::kTurns) {
@@ -1325,53 +1331,82 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
       if (n >= 2) ok = mbar_wait(isv ? v_free(n & 1) : k_free(n & 1), ((n >> 1) - 1) & 1) && ok;
       ok = __all_sync(kEvery, ok);
       if (!ok) break;
-      // a row that was never written may hold NaN patterns, and 0 x NaN is NaN
-      const bool dead = isv && row >= infos[n & (kInfos - 1)].live;
-      if (!isv) tmem_fence_after();
-      uint8_t* tile = sm + C::oTiles + (n & 1) * 2 * kHalfBox + row * 128;
+      tmem_fence_after();
+      const uint8_t* st = sm + C::oStage + s * C::kStage;
+      if (isv) {
+        // a row that was never written may hold NaN patterns, and 0 x NaN is NaN: its scales count as 0
+        const int live = infos[n & (kInfos - 1)].live;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // 32 values, two scale groups
-        uint4 w = *reinterpret_cast<const uint4*>(src + s * C::kStage + ((16 * c) ^ swz));
-        uint32_t sc = *reinterpret_cast<const uint16_t*>(ssrc + s * C::kStage + 2 * c);
-        if (c == 3) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty(s));
+        for (int q = 0; q < 4; ++q) {
+          const int t = 32 * q + lane;
+          uint32_t sc = *reinterpret_cast<const uint16_t*>(st + 2 * codes + scales + t * (kDim / 16) + 2 * wq);
+          if (t >= live) sc = 0u;
+          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc)), other = __shfl_xor_sync(kEvery, pair, 1);
+          vs[((lane & 1) * 4 + ((lane >> 1) & 3)) * kVScaleRow + 4 * q + (lane >> 3)] =
+              lane & 1 ? __byte_perm(other, pair, 0x7632) : __byte_perm(pair, other, 0x5410);
         }
-        if (dead) {
-          sc = 0u;
-          w = make_uint4(0u, 0u, 0u, 0u);
-        }
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-        const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
-        const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
-        const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
-        uint32_t h[16];
+        __syncwarp();
+        const uint32_t src = base + C::oStage + s * C::kStage + codes + lane * (kDim / 2) + ((16 * wq) ^ swz);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t e[4];
-          e2m1x8_to_f16x2x4(words[k], e);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&e[j]), s2[k >> 1]);
-            h[4 * k + j] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4], a[8], b[8];
+          ldsm_x4_t(src + q * 32 * (kDim / 2), w[0], w[1], w[2], w[3]);
+          const uint4 f4 = *reinterpret_cast<const uint4*>(vs + ((lane >> 4) * 4 + (lane & 3)) * kVScaleRow + 4 * q);
+          const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+          if (q == 3) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(s));
           }
-        }
-        if (isv) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(tile + (c >> 1) * kHalfBox + (((4 * (c & 1) + k) << 4) ^ swz_v)) =
-                make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-        } else {
+          for (int m = 0; m < 4; ++m) {
+            uint32_t e[4];
+            e2m1x8_to_f16x2x4(w[m], e);              // dims (0, 1), (2, 3) of one token, then of the next
+            const uint32_t y[4] = {__byte_perm(e[0], e[2], 0x5410), __byte_perm(e[0], e[2], 0x7632),
+                                   __byte_perm(e[1], e[3], 0x5410), __byte_perm(e[1], e[3], 0x7632)};
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), *reinterpret_cast<const __half2*>(&f[m]));
+              z[k] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            a[2 * m] = z[0]; a[2 * m + 1] = z[1];
+            b[2 * m] = z[2]; b[2 * m + 1] = z[3];
+          }
+          const uint32_t to = tV + lanes + (n & 1) * (kBlock / 2) + 16 * q;
+          tmem_st_16x16(to, a);
+          tmem_st_16x16(to + (16u << 16), b);
+        }
+      } else {
+        const int row = 32 * wq + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // 32 values, two scale groups
+          const uint4 w = *reinterpret_cast<const uint4*>(st + row * (kDim / 2) + ((16 * c) ^ swz));
+          const uint32_t sc = *reinterpret_cast<const uint16_t*>(st + 2 * codes + row * (kDim / 16) + 2 * c);
+          if (c == 3) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(s));
+          }
+          const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t pair = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
+          const __half2 s01 = *reinterpret_cast<const __half2*>(&pair);
+          const __half2 s2[2] = {__low2half2(s01), __high2half2(s01)};
+          uint32_t h[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t e[4];
+            e2m1x8_to_f16x2x4(words[k], e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&e[j]), s2[k >> 1]);
+              h[4 * k + j] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
           tmem_st16(tK + lanes + (n & 1) * (kDim / 2) + 16 * c, reinterpret_cast<const float*>(h));
         }
       }
-      if (isv) {
-        smem_to_async();
-      } else {
-        tmem_wait_st();
-        tmem_fence_before();
-      }
+      tmem_wait_st();
+      tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(isv ? v_full(n & 1) : k_full(n & 1));
       s += C::kTurns;
