@@ -507,15 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 // FP8 417 us, 16x256k NVFP4 1,730); here both products take the tokens (then the dims) as the 128 rows of A,
 //   S^T = K Q^T   (M = 128 tokens, N = NR query rows, K = 128 dims)
 //   O^T = V^T P^T (M = 128 dims,   N = NR query rows, K = 128 tokens)
-// so that K and V are A operands read from shared memory.
+// so that K and V are A operands.
 //   FP8: the stage is the operand: nothing is converted. Q and P are split into
 //   8-bit parts that are accumulated one after the other: Q = two E4M3 parts
 //   after a power-of-two scaling of its row (4 significant bits each, a bf16
 //   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
 //   parts of its f16 value (3 significant bits each, rounded at 2^-10 relative).
-//   NVFP4: further warps expand each block (e2m1 x e4m3, exact in f16): K into tensor
-//   memory, V into swizzled shared memory (its rows are tokens, and as A it is
-//   needed by dims). Q is scaled into f16's range and P rounded to f16.
+//   NVFP4: further warps expand each block (e2m1 x e4m3, exact in f16) into tensor
+//   memory, V transposed on the way (its rows are tokens, and as A it is needed by
+//   dims). Q is scaled into f16's range and P rounded to f16.
 // Roles: warp 0 copies, warps 1 and 2 issue the MMAs of S and of P V, warp 3 lists
 // the cut rows, then two groups of 4 softmax warps (a thread owns a token of S and
 // a dim of O; the group with a row's first block also brings the next row's
@@ -526,10 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 // thread's rows are 16-byte runs). Every wait on memory is bounded; a warp whose
 // wait ran out still votes, so its group leaves together.
 // Measured, one position, 4 KV heads of 16 query heads: FP8 32x32k 167 us (96 % of
-// a copy's rate: the bytes bound it); NVFP4 16x256k 620 us (58 %): shared memory
-// does, about 1,190 wavefronts of a block's 1,450 cycles, with 62 % of the issue
-// slots. K in tensor memory instead of shared memory: 852 -> 740 us; S and P V
-// issued by a warp each: 676; two softmax groups: 627; expanding warps in turns: 620.
+// a copy's rate: the bytes bound it). NVFP4 16x256k 595 us (61 %): the softmax
+// groups' chains of waits and exchanges take 480 us without the expansion, whose
+// warps take issue slots from them. Its steps: K in tensor memory instead of shared
+// memory 852 -> 740 us; S and P V issued by a warp each 676; two softmax groups 627;
+// expanding warps in turns 620; V in tensor memory 595. A second P buffer per group:
+// 632.
 constexpr int kTcS = 2;                 // S buffers in tensor memory
 constexpr int kInfos = 16;              // ring of block descriptions, longer than anything in flight
 
@@ -2030,7 +2032,7 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   p.by_row = rows < ctas - 1;
   const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
   // One form per number of query rows R. FP8 and NVFP4: tokens as M for 16 and 32 rows, rows as M above (32x16k, FP8
-  // with 16 / 32 rows 91.7 / 97.7 us against 128.7 / 129.2, NVFP4 93.5 / 117.0 against 135.8 / 136.5; 64 rows on the
+  // with 16 / 32 rows 91.7 / 97.7 us against 128.7 / 129.2, NVFP4 88.9 / 111.1 against 135.8 / 136.5; 64 rows on the
   // 32-row form would read the cache twice). bf16: up to 16 rows, warp mma for what a small block table can hold
   // (2x4k 12.2 us, rows as M 13.2; 8x8k 33.0, 33.8), rows as M for a table of at least 64 blocks per CTA (32x32k
   // 315.5 us, warp mma 322.4; 64 requests of 8k-128k 1,284, 1,322).
