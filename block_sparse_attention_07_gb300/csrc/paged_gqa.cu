@@ -1635,7 +1635,8 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
           for (int k = 0; k < 64; ++k) big = __vmaxu2(big, v[k] & 0x7FFF7FFFu);
           const int sh = fp16_shift_for(fmaxf(bf16_bits_to_f32(big & 0xFFFF), bf16_bits_to_f32(big >> 16)));
           const float f = exp2_int(sh);
-          mul_next = p.scale_log2 * p.k_global * exp2_int(-sh);
+          // not below 2^-126 (logits of less than 2^-80 either way): a masked -inf times 0 would be NaN
+          mul_next = fmaxf(p.scale_log2 * p.k_global * exp2_int(-sh), 0x1p-126f);
 #pragma unroll
           for (int k = 0; k < 64; ++k) v[k] = pack_f16x2(bf16_bits_to_f32(v[k] & 0xFFFF) * f, bf16_bits_to_f32(v[k] >> 16) * f);
         }

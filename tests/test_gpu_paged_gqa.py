@@ -272,3 +272,22 @@ def test_bad_pages_while_page_0_was_never_written(kind, Q):
     nb = [8, 3, 1]
     live = {b: [i for i in range(nb[b]) if 0 < table[b, i] < c.P] for b in range(3)}
     c.check(live_blocks=live, flags=msa.FLAG_BAD_PAGE)
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -100, 2.0 ** -20, 2.0 ** 20])
+def test_query_magnitudes_with_many_rows(kind, q_scale):
+    c = Case([200, 129], kind, G=2, Q=4, seed=30, q_scale=q_scale, scale=1.0 / (128 ** 0.5 * max(q_scale, 1.0)))
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("Q", [1, 2, 4])
+def test_logits_too_small_for_fp32(kind, Q):
+    """Queries of 2^-60 over keys of 1e-30: their factors' product underflows; the attention is the plain mean."""
+    c = Case([200, 129, 1], kind, G=2, Q=Q, seed=31, q_scale=2.0 ** -60)
+    was, c.cache.k_global = c.cache.k_global, 1e-30
+    c.K = [k * (1e-30 / was) for k in c.K]
+    c.run()
+    c.check()
