@@ -210,6 +210,10 @@ __device__ __forceinline__ float* paged_part(const PagedParams& p, int cta, int 
   return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * part_floats(p.R);
 }
 
+// Maximum of a state with sum l: -inf for an empty one; a finite one where NaN logits left no other, so that joins
+// take the state up and the NaN reaches the output.
+__device__ __forceinline__ float partial_max(float m, float l) { return l > 0.f ? m : l == 0.f ? -INFINITY : 0.f; }
+
 // Outputs of requests without tokens, and the flag of bad lengths.
 __device__ void paged_empty_requests(const PagedParams& p, int nthreads) {
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
       v += __shfl_xor_sync(kEvery, v, 1);
       v += __shfl_xor_sync(kEvery, v, 2);
       const int at = warp * 16 + gr + 8 * r;
-      if (c == 0) { merge_m[at] = m_r[r]; merge_l[at] = v; }
+      if (c == 0) { merge_m[at] = partial_max(m_r[r], v); merge_l[at] = v; }
 #pragma unroll
       for (int n = 0; n < 16; ++n)
         *reinterpret_cast<float2*>(merge + at * kDim + 8 * n + 2 * c) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
@@ -448,11 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
         }
       }
       if (whole) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = L != 0.f ? 1.f / L : 0.f;
         const int64_t head = paged_head(p, w.b, w.g, row);
         *reinterpret_cast<uint2*>(p.out + head * kDim + d) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (p.lse != nullptr && d == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
+        if (p.lse != nullptr && d == 0) p.lse[head] = L != 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(part + row * kDim + d) = acc;
         if (d == 0) { part[p.R * kDim + row] = M; part[p.R * (kDim + 1) + row] = L; }
@@ -1044,7 +1048,8 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
               make_uint4(pack_f16x2(x0[0] * f, x0[1] * f), pack_f16x2(x0[2] * f, x0[3] * f),
                          pack_f16x2(x1[0] * f, x1[1] * f), pack_f16x2(x1[2] * f, x1[3] * f));
         }
-        if (hl == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * exp2_int(-sh);
+        // (an infinite query would be a finite code: its row is NaN)
+        if (hl == 0) row_mul[qb * NR + r] = p.scale_log2 * p.k_global * (amax < INFINITY ? exp2_int(-sh) : NAN);
       }
       smem_to_async();
       __syncwarp();
@@ -1288,17 +1293,17 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
             const int r = 16 * i + e;
             if (r >= p.R) break;
             const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
-            const float M = L > 0.f ? -ref[r] : -INFINITY;          // L and O are in units of 2^M
+            const float M = partial_max(-ref[r], L);                // L and O are in units of 2^M
             const float4 v = *reinterpret_cast<const float4*>(stg + e * kDim + 4 * lane);
             if (whole) {
-              const float inv = L > 0.f ? p.v_global / L : 0.f;
+              const float inv = L != 0.f ? p.v_global / L : 0.f;
               const int j = row_pos[r];
               const int64_t head = (static_cast<int64_t>(bi.b) * p.Q + j) * p.H + bi.g * p.group + (r - j * p.group);
               *reinterpret_cast<uint2*>(p.out + head * kDim + 4 * lane) =
-                  L > 0.f ? make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
-              if (p.lse != nullptr && lane == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
+                  L != 0.f ? make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
+              if (p.lse != nullptr && lane == 0) p.lse[head] = L != 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
             } else {
-              *reinterpret_cast<float4*>(part + r * kDim + 4 * lane) = L > 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+              *reinterpret_cast<float4*>(part + r * kDim + 4 * lane) = L != 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
               if (lane == 0) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = L; }
             }
           }
@@ -1744,7 +1749,7 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
         tmem_fence_after();
         if (live_warp) {
           const bool whole = (bi.flags & 12) == 12;
-          const float inv = l > 0.f ? p.v_global / l : 0.f, M = l > 0.f ? ref : -INFINITY;
+          const float inv = l != 0.f ? p.v_global / l : 0.f, M = partial_max(ref, l);
           const int64_t head = live_row ? paged_head(p, bi.b, bi.g, r) : 0;
           float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
 #pragma unroll 1
@@ -1757,7 +1762,7 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
               uint4* dst = reinterpret_cast<uint4*>(p.out + head * kDim + 16 * q);
 #pragma unroll
               for (int k = 0; k < 2; ++k)
-                dst[k] = l > 0.f ? make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                dst[k] = l != 0.f ? make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
                                               pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
                                               pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
                                               pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv))
@@ -1766,11 +1771,11 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
               float4* dst = reinterpret_cast<float4*>(part + r * kDim + 16 * q);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                dst[k] = l > 0.f ? make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3])
+                dst[k] = l != 0.f ? make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3])
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
             }
           }
-          if (live_row && whole && p.lse != nullptr) p.lse[head] = l > 0.f ? (M + log2f(l)) * kLn2f : -INFINITY;
+          if (live_row && whole && p.lse != nullptr) p.lse[head] = l != 0.f ? (M + log2f(l)) * kLn2f : -INFINITY;
           if (live_row && !whole) { part[p.R * kDim + r] = M; part[p.R * (kDim + 1) + r] = l; }
         }
         tmem_fence_before();
@@ -1923,11 +1928,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
     }
   }
   if (!live) return;
-  const float inv = L > 0.f ? p.v_global / L : 0.f;
+  const float inv = L != 0.f ? p.v_global / L : 0.f;
   const int64_t head = paged_head(p, cut.b, cut.g, row);
   *reinterpret_cast<uint2*>(p.out + head * kDim + 4 * lane) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (p.lse != nullptr && lane == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
+  if (p.lse != nullptr && lane == 0) p.lse[head] = L != 0.f ? (M + log2f(L)) * kLn2f : -INFINITY;
 }
 
 size_t paged_gqa_workspace_bytes(int Q, int H, int G) {

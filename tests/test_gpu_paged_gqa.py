@@ -291,3 +291,39 @@ def test_logits_too_small_for_fp32(kind, Q):
     c.K = [k * (1e-30 / was) for k in c.K]
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("Q,wide", [(1, False), (1, True), (2, False), (4, False)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_no_numbers(kind, Q, wide, bad):
+    """A head whose query holds a NaN or an infinity: NaN there, the other heads bit for bit as without it."""
+    c = Case([3000, 128, 70], kind, G=2, Q=Q, seed=32, cols_extra=8192 if wide else 1)
+    c.run()
+    torch.cuda.synchronize()
+    out, lse = c.out.clone(), c.lse.clone()
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    for b, j, h, d in ((0, 0, 3, 0), (0, Q - 1, 17, 127), (1, 0, 31, 64), (2, Q - 1, 0, 5)):
+        c.q[b, j, h, d] = bad
+        hit[b, j, h] = True
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(c.out[hit]).all() and torch.isnan(c.lse[hit]).all()
+    assert torch.equal(c.out[~hit], out[~hit]) and torch.equal(c.lse[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("kind", KV)
+@pytest.mark.parametrize("Q,wide", [(1, False), (1, True), (2, False), (4, False)])
+def test_keys_that_are_no_numbers(kind, Q, wide):
+    """A NaN in a live key: NaN for the heads of that KV head, the others bit for bit as without it."""
+    c = Case([3000, 128], kind, G=2, Q=Q, seed=33, cols_extra=8192 if wide else 1)
+    c.run()
+    torch.cuda.synchronize()
+    out, lse = c.out.clone(), c.lse.clone()
+    store = (c.cache.k_scale if kind == "nvfp4" else c.cache.k).view(torch.uint8)
+    for b, t in ((0, 1500), (1, 0)):
+        store[int(c.table[b, t // 128]), 1, t % 128, 2:4] = 0x7F if kind != "bf16" else 0xFF
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(c.out[:, :, 16:]).all() and torch.isnan(c.lse[:, :, 16:]).all()
+    assert torch.equal(c.out[:, :, :16], out[:, :, :16]) and torch.equal(c.lse[:, :, :16], lse[:, :, :16])
