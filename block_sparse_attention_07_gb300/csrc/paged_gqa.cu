@@ -2059,12 +2059,15 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
         : rows_of == 32 ? launch_tc<MSA_NVFP4, 32>(p, ctas, stream) : launch_many<MSA_NVFP4>(p, ctas, stream);
   if (err != cudaSuccess) return err;
   if (ctas > 1) {
-    // few rows: a CTA for each query row, whose warps share its many partials, 16 in flight each (1x128k: 16.0 us,
-    // 8 warps 16.9, 4 warps 20.6); else a warp for each, with mostly two or three partials
-    const bool few = static_cast<int64_t>(cuts) * p.R <= sms;
-    const int rpc = few ? 1 : kJoinWarps;
+    // Query rows per CTA: as few as a grid of two CTAs per SM allows, so that their warps share a row's partials
+    // (1x128k, 152 partials of a row: 16.0 us, with 8 warps 16.9, with 4 20.6; 4x2k bf16 11.5 us, one warp per row
+    // 13.9; 2x4k with 4 positions 13.9 and 18.4, a grid of one CTA per SM 14.4).
+    int rpc = 1;
+    while (rpc < kJoinWarps && static_cast<int64_t>(cuts) * ((p.R + rpc - 1) / rpc) > 2 * sms) rpc *= 2;
+    const int wpr = kJoinWarps / rpc;
+    const bool deep = p.by_row && ctas / rows + 2 > 4 * wpr;       // more partials than the warps take at once by fours
     const int chunks = (p.R + rpc - 1) / rpc;
-    err = launch_pdl(few ? paged_join_kernel<16> : paged_join_kernel<4>, dim3(cuts * chunks), dim3(32 * kJoinWarps), 0, stream, p, rpc);
+    err = launch_pdl(deep ? paged_join_kernel<16> : paged_join_kernel<4>, dim3(cuts * chunks), dim3(32 * kJoinWarps), 0, stream, p, rpc);
     if (err != cudaSuccess) return err;
   }
   rec->set("paged_gqa %s %s rows=%d of %d grid=%d + join", a.kv == MSA_BF16 ? "bf16"
