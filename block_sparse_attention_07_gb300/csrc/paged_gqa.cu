@@ -266,7 +266,7 @@ __device__ void paged_describe_cuts(const PagedParams& p, const Range& r, int ct
 // mma. Eight warps take 16 tokens of every block each, with their own running
 // maxima; blocks arrive by cp.async into two stages. Nothing passes between warps
 // until the row ends, which is what small calls need: 2 requests of 4,096 tokens
-// 12.2 us (rows as M on tcgen05: 13.2), bound by the two launches and the chain of
+// 12.1 us (rows as M on tcgen05: 12.9), bound by the two launches and the chain of
 // latencies. Large ones are bound by the cache's bytes (32x32k: 322 us, 99 % of a
 // copy's rate), where the rows-as-M form's third stage gains 2 %.
 constexpr int kWarps = 8;
@@ -2040,8 +2040,8 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   // One form per number of query rows R. FP8 and NVFP4: tokens as M for 16 and 32 rows, rows as M above (32x16k, FP8
   // with 16 / 32 rows 91.7 / 97.7 us against 128.7 / 129.2, NVFP4 88.9 / 111.1 against 135.8 / 136.5; 64 rows on the
   // 32-row form would read the cache twice). bf16: up to 16 rows, warp mma for what a small block table can hold
-  // (2x4k 12.2 us, rows as M 13.2; 8x8k 33.0, 33.8), rows as M for a table of at least 64 blocks per CTA (32x32k
-  // 315.5 us, warp mma 322.4; 64 requests of 8k-128k 1,284, 1,322).
+  // (2x4k 12.1 us, rows as M 12.9; 8x8k 31.9, 32.1), rows as M for a table of at least 64 blocks per CTA (16x16k, 54
+  // of them, 90.5 and 90.2; 32x32k 321.7 and 315.8; 64 requests of 8k-128k 1,322 and 1,284).
   const bool large = most >= 64ll * ctas;
   const int rows_of = a.kv == MSA_BF16 ? (p.R <= 16 && !large ? 16 : 128) : p.R <= 16 ? 16 : p.R <= 32 ? 32 : 128;
   // A row's start and end, in blocks of its form. 64 requests of up to 2,047 tokens, 4 KV heads, at 0 / 2 / 3 / 5 / 8:
