@@ -342,7 +342,7 @@ cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_ax
     lo[i] = pow(static_cast<double>(a.theta), -2.0 * i / kDim);
   }
   for (int i = 0; i < kDim / 2; ++i) {
-    pp.turn[i] = static_cast<uint64_t>(ldexp(hi[i >> 3] * lo[i & 7], 64));
+    pp.turn[i] = static_cast<uint64_t>(hi[i >> 3] * lo[i & 7] * 0x1p64);
     pp.axis[i] = axes.axis[i];
   }
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
