@@ -676,6 +676,8 @@ struct TcCfg {
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(kStages >= 3, "at least three stages");
+  // a wait by parity needs every phase of a stage to be seen by the same warps
+  static_assert(kStages % kTurns == 0, "a stage's blocks belong to one turn");
   static_assert(kTotal - oInfo <= kSmall, "small area");
   static_assert(kUsedCols <= 512, "tensor memory");
 };
@@ -1443,8 +1445,11 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
 // copies, S, P V, the cut rows, four softmax warps, the expanding warps.
 // Measured, 8 positions of 16 query heads, 4 KV heads: bf16 32x64k 640 us (the
 // copy's rate: the bytes bound it; the warp mma form needs 1,712); FP8 32x32k 256
-// us, 1,073 TFLOP/s, and NVFP4 16x64k 258 us: a block's softmax of 128 x 128 by four
-// warps bounds these. One position: 32x32k 315 us, 102 % of a copy's rate.
+// us, 1,087 TFLOP/s, and NVFP4 16x64k 258 us. What bounds these is neither the
+// softmax (two threads per row, on eight warps: 276 and 277 us) nor the expansion
+// alone (twice the warps: 252 and 255): a block passes through expansion, S, softmax
+// and P V one after the other, two blocks at a time, and three f16 tile pairs do not
+// fit shared memory. One position: 32x32k 315 us, 102 % of a copy's rate.
 template <int kKv>
 struct RwCfg {
   static constexpr bool kQuant = kKv != MSA_BF16;
