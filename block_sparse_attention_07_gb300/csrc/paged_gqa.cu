@@ -32,6 +32,10 @@ constexpr uint32_t kEvery = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.693147180559945309f;
 constexpr float kSlack = 8.f;       // log2 units a maximum may exceed the reference by before a rescale
+// Quantised caches hold P as f16, times 2^kPLift: with the slack it fills f16's range up to 2^15, so that weights are
+// exact to 2^-11 relative down to 2^-21 of the reference and to 2^-32 of it below. Without the lift those below 2^-25
+// of the reference would leave the numerator while the sum (fp32) keeps them.
+constexpr float kPLift = 7.f;
 constexpr int kMaxCtas = 320;       // partial slots in the workspace, two per CTA
 
 // A row cut by CTA boundaries, written by the CTA behind the first cut: n
@@ -659,7 +663,7 @@ struct TcCfg {
   static constexpr int kSets = 4;                              // states: of each group, for this segment and the one before
   static constexpr int kUsedCols = kTcS * kSCols + kSets * kOCols + kKCols + kVCols;
   static constexpr uint32_t kCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
-  static constexpr float kOff = kFp8 ? 7.f : 0.f;              // P is held times 2^kOff
+  static constexpr float kOff = kPLift;                        // P, sums and O are held times 2^kOff
   // shared memory
   static constexpr uint32_t oStage = 0;
   static constexpr uint32_t oQ = (kStages * kStage + 1023) & ~1023u;
@@ -1462,7 +1466,8 @@ struct RwCfg {
   static constexpr int kBars = 2 * kStages + 9 + (kQuant ? 6 : 0);
   static constexpr uint32_t oSlot = oBars + kBars * 8, kTotal = oSlot + 16;
   static_assert(kTotal <= 230912, "shared memory");
-  // 512 threads have 128 registers each: 56 + 200 + 2 * 120 of the 4 * 128
+  static constexpr float kOff = kQuant ? kPLift : 0.f;                   // P, sums and O are held times 2^kOff (bf16 has fp32's range)
+  // 512 threads have 128 registers each: 56 + 208 + 2 * 120 of the 4 * 128
   static constexpr int kRegsCtl = 56, kRegsSoft = 208, kRegsConv = 120;
 };
 constexpr uint32_t kRwQ = 0, kRwS = 128, kRwO = 384, kRwCols = 512;
@@ -1716,7 +1721,7 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
         }
         if (raise) ref = top;
         l *= alpha;
-        const float neg = ref == -INFINITY ? 0.f : -ref;
+        const float neg = ref == -INFINITY ? 0.f : C::kOff - ref;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -1754,7 +1759,7 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
         tmem_fence_after();
         if (live_warp) {
           const bool whole = (bi.flags & 12) == 12;
-          const float inv = l != 0.f ? p.v_global / l : 0.f, M = partial_max(ref, l);
+          const float inv = l != 0.f ? p.v_global / l : 0.f, M = partial_max(ref - C::kOff, l);
           const int64_t head = live_row ? paged_head(p, bi.b, bi.g, r) : 0;
           float* part = whole ? nullptr : paged_part(p, cta, (bi.flags & 4) ? 1 : 0);
 #pragma unroll 1
