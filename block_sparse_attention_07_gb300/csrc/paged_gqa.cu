@@ -520,7 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   8-bit parts that are accumulated one after the other: Q = two E4M3 parts
 //   after a power-of-two scaling of its row (4 significant bits each, a bf16
 //   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
-//   parts of its f16 value (3 significant bits each, rounded at 2^-10 relative).
+//   parts of its f16 value (each the rest rounded to 3 significant bits, the rests
+//   scaled by 2^3 and 2^7 into E5M2's range: exact down to 2^-13 of f16's 1, off by
+//   at most f16's last step of 2^-24 below).
 //   NVFP4: further warps expand each block (e2m1 x e4m3, exact in f16) into tensor
 //   memory, V transposed on the way (its rows are tokens, and as A it is needed by
 //   dims). Q is scaled into f16's range and P rounded to f16.
@@ -645,6 +647,7 @@ struct TcCfg {
   static constexpr int kRegsFit = (kRegs * (kWarpsAll / 4) - kRegsCtl - (kConv / 4) * kRegsConv) / kGroups / 8 * 8;
   static constexpr int kRegsSoft = kRegsFit > 232 ? 232 : kRegsFit;
   static constexpr int kQParts = kFp8 ? 2 : 1, kPParts = kFp8 ? 3 : 1;
+  static constexpr float kPUp1 = 8.f, kPUp2 = 128.f;           // scales of P's second and third part
   static constexpr uint32_t kQPart = NR * (kFp8 ? 128 : 256);  // bytes of one part
   static constexpr uint32_t kPPart = NR * (kFp8 ? 128 : 256);
   // One P buffer (there is one per group); it also stages 16 output rows
@@ -1179,20 +1182,24 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           h[e] = pack_f16x2(a, b);
         }
         if (kFp8) {
-          // an E5M2 byte is the upper byte of an f16: three bytes of 3 significant bits, the last rounded
+          // An E5M2 byte is the upper byte of an f16. Each part is the rest rounded to 3 significant bits (sign and
+          // magnitude, so adding half a step rounds either sign), and what it leaves fits the next one scaled by
+          // 2^3 (at most half a step of 2^-2 relative), then by 2^4.
           uint8_t* d = sm + pt + (i) * 2048;
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             uint32_t w[4];
+            const __half2 up = __float2half2_rn(part == 0 ? C::kPUp1 : C::kPUp2 / C::kPUp1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (part == 2) { h[2 * e] += 0x00800080u; h[2 * e + 1] += 0x00800080u; }
-              w[e] = __byte_perm(h[2 * e], h[2 * e + 1], 0x7531);
+              const uint32_t r[2] = {h[2 * e] + 0x00800080u, h[2 * e + 1] + 0x00800080u};
+              w[e] = __byte_perm(r[0], r[1], 0x7531);
               if (part < 2) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                  const uint32_t hi = h[2 * e + k] & 0xFF00FF00u;
-                  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * e + k]), *reinterpret_cast<const __half2*>(&hi));
+                  const uint32_t hi = r[k] & 0xFF00FF00u;
+                  const __half2 rest = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h[2 * e + k]),
+                                                       *reinterpret_cast<const __half2*>(&hi)), up);
                   h[2 * e + k] = *reinterpret_cast<const uint32_t*>(&rest);
                 }
               }
@@ -1275,8 +1282,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
           for (int e = 0; e < 16; ++e) {
 #pragma unroll
             for (int k = 1; k < kParts; ++k) {
-              o[0][e] += o[k][e];
-              o2[0][e] += o2[k][e];
+              const float down = 1.f / (k == 1 ? C::kPUp1 : C::kPUp2);
+              o[0][e] = fmaf(o[k][e], down, o[0][e]);
+              o2[0][e] = fmaf(o2[k][e], down, o2[0][e]);
             }
           }
           if (two) {

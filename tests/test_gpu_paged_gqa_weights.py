@@ -4,7 +4,8 @@ All values of V here are at least 0, so that the sum of softmax_t |v_t| is the o
 to it, with u(t) half a step of a type (bf16 2^-8, f16 2^-11, fp32 2^-24) and n the tokens seen:
   * the output's rounding to bf16: 2^-8;
   * a weight's rounding: bf16 caches 2^-8. FP8 and NVFP4 caches: 2^-11 as an f16 that is held times 2^7, whose
-    subnormal half-step is 2^-25: under 2^-30 of the largest weight, absolute;
+    subnormal half-step is 2^-25: 2^-32 of the largest weight, absolute; the three 8-bit parts that FP8 caches split it
+    into add half a step of the last one, 2^-17 held times 2^7 * 2^7: 2^-31. Together under 2^-30 of the largest weight;
   * the exponential: 2^-21; the logits move a weight by twice their own error (numerator and denominator);
   * logits: 132 * 2^-24 * scale * max_t sum_d |q_d k_td|;
   * fp32 sums of n terms, two of them (numerator, denominator): 2 n * 2^-24."""
@@ -18,7 +19,7 @@ pytestmark = pytest.mark.gpu
 
 # cache type, query heads per KV head, positions, wide block table: one line per form of the kernel
 FORMS = [("bf16", 16, 1, False), ("bf16", 16, 1, True), ("bf16", 8, 4, False),
-         ("fp8", 16, 4, False),
+         ("fp8", 16, 1, False), ("fp8", 16, 2, False), ("fp8", 16, 4, False),
          ("nvfp4", 16, 1, False), ("nvfp4", 16, 2, False), ("nvfp4", 16, 4, False)]
 
 
