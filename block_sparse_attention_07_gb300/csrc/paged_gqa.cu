@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 //   FP8: the stage is the operand: nothing is converted. Q and P are split into
 //   8-bit parts that are accumulated one after the other: Q = two E4M3 parts
 //   after a power-of-two scaling of its row (4 significant bits each, a bf16
-//   query's 8; exact down to 2^-18 of the row's largest value), P = three E5M2
+//   query's 8; the second times 2^5, so that the split is exact to 2^-22 of the
+//   row's largest value), P = three E5M2
 //   parts of its f16 value (each the rest rounded to 3 significant bits, the rests
 //   scaled by 2^3 and 2^7 into E5M2's range: exact down to 2^-13 of f16's 1, off by
 //   at most f16's last step of 2^-24 below).
@@ -783,13 +784,15 @@ __device__ __forceinline__ bool group_any(int id, bool vote) {
   return r != 0;
 }
 
+constexpr float kQUp = 32.f;        // scale of Q's second part: half a step of a value below 2^8 is 2^3 at most
 __device__ __forceinline__ uint2 fp8_parts(const float (&x)[4], float f) {
   const float y0 = x[0] * f, y1 = x[1] * f, y2 = x[2] * f, y3 = x[3] * f;
   const uint32_t a = f32x2_to_e4m3x2(y0, y1), b = f32x2_to_e4m3x2(y2, y3);
   const uint32_t ha = e4m3x2_to_f16x2(static_cast<uint16_t>(a)), hb = e4m3x2_to_f16x2(static_cast<uint16_t>(b));
   const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
   const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-  const uint32_t la = f32x2_to_e4m3x2(y0 - fa.x, y1 - fa.y), lb = f32x2_to_e4m3x2(y2 - fb.x, y3 - fb.y);
+  const uint32_t la = f32x2_to_e4m3x2((y0 - fa.x) * kQUp, (y1 - fa.y) * kQUp);
+  const uint32_t lb = f32x2_to_e4m3x2((y2 - fb.x) * kQUp, (y3 - fb.y) * kQUp);
   return make_uint2(a | (b << 16), la | (lb << 16));
 }
 
@@ -1099,7 +1102,7 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
         for (int i = 0; i < NR / 16; ++i) tmem_ld16(tmem + lanes + grp * C::kSCols + NR + 16 * i, lo + 16 * i);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) x[r] += lo[r];
+        for (int r = 0; r < NR; ++r) x[r] = fmaf(lo[r], 1.f / kQUp, x[r]);
       }
       tmem_wait_ld();
       tmem_fence_before();

@@ -7,7 +7,8 @@ to it, with u(t) half a step of a type (bf16 2^-8, f16 2^-11, fp32 2^-24) and n 
     subnormal half-step is 2^-25: 2^-32 of the largest weight, absolute; the three 8-bit parts that FP8 caches split it
     into add half a step of the last one, 2^-17 held times 2^7 * 2^7: 2^-31. Together under 2^-30 of the largest weight;
   * the exponential: 2^-21; the logits move a weight by twice their own error (numerator and denominator);
-  * logits: 132 * 2^-24 * scale * max_t sum_d |q_d k_td|;
+  * logits: 132 * 2^-24 * scale * max_t sum_d |q_d k_td|, and, for queries held as two 8-bit parts, 2^-22 of the row's
+    largest value per dim (128 dims): 2^-22 * scale * max|q| * max_t sum_d |k_td|;
   * fp32 sums of n terms, two of them (numerator, denominator): 2 n * 2^-24."""
 import numpy as np
 import pytest
@@ -43,6 +44,8 @@ def logit_error(c, b, q):
     for g in range(G):
         a, K = np.abs(q[g * n:(g + 1) * n]), np.abs(c.K[b][:, g])
         ds[g * n:(g + 1) * n] = 132 * 2.0 ** -24 * c.scale * (a @ K.T).max(1)
+        if c.kind != "bf16":
+            ds[g * n:(g + 1) * n] += 2.0 ** -22 * c.scale * a.max(1) * K.sum(1).max()
     return ds[:, None]
 
 
@@ -105,3 +108,29 @@ def test_many_small_weights_beside_a_large_one(kind, group, Q, wide, nats, even)
     out, lse = results(c)
     for b in (0, 1, 2, 77, 150, 298, 299):
         check(c, 0, out[b], lse[b])
+
+
+@pytest.mark.parametrize("kind,group,Q,wide", FORMS)
+def test_queries_with_one_large_dim(kind, group, Q, wide):
+    """A query value 2^9 to 2^11 times the others', in a dim where the keys are 0: the others decide, with all the bits
+    they have (8; the last one set). One token, so that lse is the logit."""
+    c = Case([1, 300], kind, 2, group, Q, seed=44)
+    h = np.arange(c.q_val.shape[2])
+    q = np.empty(c.q_val.shape, dtype=np.float32)
+    q[...] = (1 + 2.0 ** -7 * (1 + 2 * (h % 8)))[:, None]
+    q[..., 0] = 2.0 ** (9 + h // 2 % 3)
+    c.q = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    c.q_val = c.q.double().cpu().numpy()
+    rng = np.random.default_rng(46)
+    for b, n in enumerate(c.lens):
+        k = rng.uniform(0.5, 1.0, (n, 2, D)).astype(np.float32)
+        k[..., 0] = 0.0
+        put(c, "k", b, k)
+        put(c, "v", b, rng.uniform(0.5, 1.0, (n, 2, D)).astype(np.float32))
+    c.run()
+    out, lse = results(c)
+    j = Q - 1                                              # (a request of one token has it at its last position)
+    ds = logit_error(c, 0, c.q_val[0, j])[:, 0]
+    want = np.concatenate([c.scale * c.q_val[0, j, g * group:(g + 1) * group] @ c.K[0][0, g] for g in range(2)])
+    assert (np.abs(lse[0, j] - want) <= ds + 2.0 ** -21 + 2.0 ** -22 * np.abs(want)).all()
+    check(c, 1, out[1], lse[1])
