@@ -71,6 +71,26 @@ def results(c):
     return c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
 
 
+@pytest.mark.parametrize("kind,group,Q,wide", FORMS)
+@pytest.mark.parametrize("lens", [[30000, 129], [2000, 5, 777, 4096]], ids=lambda v: "-".join(map(str, v)))
+def test_every_block_adds_its_own_values(kind, group, Q, wide, lens):
+    """Block i has large values in dims i mod 64 and 64 + (i / 64) mod 64 and small ones elsewhere: a block left out,
+    taken twice or taken from another place moves those dims by several per cent."""
+    c = Case(lens, kind, 2, group, Q, seed=40, cols_extra=8192 if wide else 1)
+    rng = np.random.default_rng(41)
+    for b, n in enumerate(lens):
+        v = rng.uniform(0.0, 0.05, (n, 2, D)).astype(np.float32)
+        for t0 in range(0, n, BS):
+            i = t0 // BS
+            v[t0:t0 + BS, :, i % 64] += 2.0 + 0.25 * (i % 5)
+            v[t0:t0 + BS, :, 64 + i // 64 % 64] += 1.0 + 0.25 * (i % 7)
+        put(c, "v", b, v)
+    c.run()
+    out, lse = results(c)
+    for b in range(len(lens)):
+        check(c, b, out[b], lse[b])
+
+
 def shared_pages(c, copies):
     """Makes c a batch of `copies` requests that all read request 0's pages (a shared prompt), with its queries."""
     from block_sparse_attention_07_gb300 import msa
