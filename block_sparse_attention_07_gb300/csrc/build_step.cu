@@ -15,6 +15,7 @@ namespace msa {
 constexpr int kStepThreads = 128;
 constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kTokPerThread = 4;
+constexpr int kStepMaxBatch = 4096;               // the entry point refuses larger ones
 constexpr int kTokPerPass = kStepThreads * kTokPerThread;
 
 struct StepScan {
@@ -216,8 +217,9 @@ cudaError_t launch_build_step(const StepArgs& a, cudaStream_t stream, DispatchRe
   if (grid > cap) grid = cap;
   const size_t smem = (5ull * a.B + 1) * sizeof(int32_t);
   if (smem > 40 * 1024) {
+    // the limit is one for all host threads, so every call sets it to the largest batch's
     const cudaError_t set = cudaFuncSetAttribute(build_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
+                                                 (5 * kStepMaxBatch + 1) * static_cast<int>(sizeof(int32_t)));
     if (set != cudaSuccess) return set;
   }
   const cudaError_t err = launch_pdl(build_step_kernel, dim3(static_cast<unsigned>(grid)), dim3(kStepThreads), smem,
