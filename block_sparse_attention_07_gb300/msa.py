@@ -287,14 +287,22 @@ def sparse_gqa_decode_noalloc(dims: Dims, q, cache: KVCache, block_table, seq_le
 
 
 def _want(what: str, name: str, t, dtype: str, shape, strided_rows=False):
-    """Refuses (ERR_INVALID_ARG) a tensor of another type, shape, layout or device than the call reads."""
+    """Refuses (ERR_INVALID_ARG) a tensor of another type, shape or layout than the call reads."""
     import torch
     ok = t.dtype == getattr(torch, dtype) and tuple(t.shape) == tuple(shape)
     ok = ok and (t.is_contiguous() or (strided_rows and t.stride(-1) == 1))
-    ok = ok and (t.device.type != "cuda" or t.device.index == torch.cuda.current_device())
     if not ok:
-        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be {dtype} {list(shape)}, contiguous, on the current "
-                                        f"device (got {t.dtype} {list(t.shape)} strides {t.stride()} on {t.device})")
+        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be {dtype} {list(shape)}, contiguous "
+                                        f"(got {t.dtype} {list(t.shape)} strides {t.stride()})")
+
+
+def _want_on_device(what: str, **tensors):
+    """Refuses (ERR_INVALID_ARG) tensors (None aside) that do not lie on the current GPU: their addresses go to its
+    kernels. After the other checks, which need no GPU."""
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+            raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be on the current CUDA device (got {t.device})")
 
 
 def _want_cache(what: str, dims: Dims, cache: KVCache):
@@ -325,6 +333,9 @@ def build_step(dims: Dims, ctx_lens, new_lens, free_pages, free_head, block_tabl
     _want(what, "positions", positions, "int32", (positions.shape[0], T), strided_rows=True)
     if pos_offset is not None:
         _want(what, "pos_offset", pos_offset, "int32", (B,))
+    _want_on_device(what, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, free_head=free_head,
+                    block_table=block_table, seq_lens=seq_lens, token_starts=token_starts, slot_mapping=slot_mapping,
+                    positions=positions, free_head_out=free_head_out, pos_offset=pos_offset)
     axes = int(positions.shape[0])
     pos_stride = int(positions.stride(0)) if axes > 1 else T
     args = (ctypes.byref(dims), _ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), int(free_pages.numel()),
@@ -363,6 +374,9 @@ def qk_norm_mrope_insert(dims: Dims, q, k, v, idx_q, idx_k, positions, slot_mapp
     _want(what, "positions", positions, "int32", (axes.num_axes, T), strided_rows=True)
     _want(what, "slot_mapping", slot_mapping, "int64", (T,))
     _want_cache(what, dims, cache)
+    _want_on_device(what, q=q, k=k, v=v, idx_q=idx_q, idx_k=idx_k, positions=positions, slot_mapping=slot_mapping,
+                    q_out=q_out, idx_q_out=idx_q_out, k_cache=cache.k, v_cache=cache.v, k_scale=cache.k_scale,
+                    v_scale=cache.v_scale)
     kc = cache.c()
     ic = idx_cache.c() if idx_cache is not None else None
     pos_stride = int(positions.stride(0)) if axes.num_axes > 1 else T
@@ -388,6 +402,8 @@ def paged_gqa_decode(dims: Dims, q, cache: KVCache, block_table, seq_lens, out, 
     _want(what, "block_table", block_table, "int32", (dims.batch, dims.max_blocks_per_seq))
     _want(what, "seq_lens", seq_lens, "int32", (dims.batch,))
     _want_cache(what, dims, cache)
+    _want_on_device(what, q=q, out=out, lse=lse, block_table=block_table, seq_lens=seq_lens, k_cache=cache.k,
+                    v_cache=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     kc = cache.c()
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (ctypes.byref(dims), _ptr(q), ctypes.byref(kc), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse),

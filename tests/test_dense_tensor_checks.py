@@ -1,0 +1,86 @@
+"""The full-attention layer's calls refuse tensors whose addresses their kernels must not get. CPU only: nothing launches."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def m():
+    from block_sparse_attention_07_gb300 import _build
+    _build.build()
+    from block_sparse_attention_07_gb300 import msa
+    return msa
+
+
+class Fake:
+    """A tensor as the checks see it, on a device of the test's choice."""
+
+    def __init__(self, t, device):
+        self.t, self.device = t, torch.device(device)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def z(*shape, dt=torch.int32):
+    return torch.zeros(shape, dtype=dt)
+
+
+def calls(m):
+    """name -> (function of the arguments, arguments): every tensor on the CPU."""
+    bf, u8 = torch.bfloat16, torch.uint8
+    d = m.make_dims(2, 1, max_blocks_per_seq=4, num_pages=8)
+    step = dict(ctx_lens=z(2), new_lens=z(2), free_pages=z(4), free_head=z(1), block_table=z(2, 4), seq_lens=z(2),
+                token_starts=z(3), slot_mapping=z(8, dt=torch.int64), positions=z(3, 8), free_head_out=z(1), flags=z(1),
+                pos_offset=z(2))
+    gqa = dict(q=z(2, 1, 64, 128, dt=bf), k=z(8, 4, 128, 64, dt=u8), v=z(8, 4, 128, 64, dt=u8), k_scale=z(8, 4, 128, 8, dt=u8),
+               v_scale=z(8, 4, 128, 8, dt=u8), block_table=z(2, 4), seq_lens=z(2), out=z(2, 1, 64, 128, dt=bf),
+               lse=z(2, 1, 64, dt=torch.float32), workspace=z(m.paged_gqa_workspace_size(d, m.NVFP4), dt=u8), flags=z(1))
+    rope = dict(q=z(3, 64, 128, dt=bf), k=z(3, 4, 128, dt=bf), v=z(3, 4, 128, dt=bf), idx_q=z(3, 4, 128, dt=bf),
+                idx_k=z(3, 4, 128, dt=bf), positions=z(3, 3), slot_mapping=z(3, dt=torch.int64), q_out=z(3, 64, 128, dt=bf),
+                idx_q_out=z(3, 4, 128, dt=bf), k_cache=z(8, 4, 128, 128, dt=u8), v_cache=z(8, 4, 128, 128, dt=u8),
+                idx_keys=z(8, 4, 128, 128, dt=u8), idx_scale=z(8, 4, 128, dt=torch.float32), flags=z(1))
+    weights = {n: z(128, dt=torch.float32) for n in ("wq", "wk", "wiq", "wik")}
+    rope.update(weights)
+
+    def run_gqa(k, v, k_scale, v_scale, **a):
+        m.paged_gqa_decode(d, cache=m.KVCache(m.NVFP4, k, v, k_scale, v_scale), **a)
+
+    def run_rope(k_cache, v_cache, idx_keys, idx_scale, wq, wk, wiq, wik, **a):
+        m.qk_norm_mrope_insert(d, nr=m.make_norm_rope(wq, wk, wiq, wik), axes=m.make_rope_axes((16, 24, 24)),
+                               cache=m.KVCache(m.FP8_E4M3, k_cache, v_cache),
+                               idx_cache=m.IndexCache(m.FP8_E4M3, idx_keys, idx_scale), **a)
+
+    return {"step": (lambda **a: m.build_step(d, **a), step), "gqa": (run_gqa, gqa), "rope": (run_rope, rope)}
+
+
+HELD = {"step": ("ctx_lens", "new_lens", "free_pages", "free_head", "block_table", "seq_lens", "token_starts", "slot_mapping",
+                 "positions", "free_head_out", "pos_offset"),
+        "gqa": ("q", "k", "v", "k_scale", "v_scale", "block_table", "seq_lens", "out", "lse"),
+        "rope": ("q", "k", "v", "idx_q", "idx_k", "positions", "slot_mapping", "q_out", "idx_q_out", "k_cache", "v_cache")}
+
+
+@pytest.mark.parametrize("call", sorted(HELD))
+@pytest.mark.parametrize("where", ["cpu", "cuda:1"])
+def test_tensors_off_the_current_gpu(m, monkeypatch, call, where):
+    """One tensor in host memory, or on another GPU than the current one, the others where they belong."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(m, "_stream", lambda stream: None)
+    run, args = calls(m)[call]
+    reached = []
+    monkeypatch.setattr(m, "_call", lambda *a: reached.append(a[3]))
+    run(**{n: Fake(t, "cuda:0") for n, t in args.items()})
+    assert len(reached) == 1                                       # all of them in place: the call is made
+    for name in HELD[call]:
+        with pytest.raises(m.MSAError) as e:
+            run(**{n: Fake(t, where if n == name else "cuda:0") for n, t in args.items()})
+        assert e.value.status == m.ERR_INVALID_ARG and "device" in str(e.value), name
+    assert len(reached) == 1
+
+
+@pytest.mark.parametrize("call", sorted(HELD))
+def test_host_tensors_reach_no_kernel(m, monkeypatch, call):
+    run, args = calls(m)[call]
+    monkeypatch.setattr(m, "_call", lambda *a: pytest.fail("the call was made"))
+    with pytest.raises(m.MSAError) as e:
+        run(**args)
+    assert e.value.status == m.ERR_INVALID_ARG
