@@ -225,7 +225,10 @@ def select_sparse_gqa_decode(dims: Dims, q, cache: KVCache, block_table, seq_len
 
 def make_norm_rope(q_weight, k_weight, idx_q_weight=None, idx_k_weight=None, eps=1e-6, rope_theta=10000.0):
     """msa_norm_rope_t from device fp32 [D] weight tensors (kept alive by the caller)."""
-    return NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(idx_q_weight), _ptr(idx_k_weight), eps, rope_theta)
+    nr = NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(idx_q_weight), _ptr(idx_k_weight), eps, rope_theta)
+    # what the addresses came from, for qk_norm_mrope_insert's checks
+    nr.tensors = dict(q_weight=q_weight, k_weight=k_weight, idx_q_weight=idx_q_weight, idx_k_weight=idx_k_weight)
+    return nr
 
 
 def qk_norm_rope_insert(dims: Dims, q, k, v, idx_q, idx_k, positions, slot_mapping, nr: NormRope, q_out,
@@ -296,6 +299,14 @@ def _want(what: str, name: str, t, dtype: str, shape, strided_rows=False):
                                         f"(got {t.dtype} {list(t.shape)} strides {t.stride()})")
 
 
+def _want_flags(what: str, flags):
+    """The device flags: 32 bits at least, in 32-bit words."""
+    import torch
+    if flags.dtype not in (torch.int32, torch.uint32) or flags.numel() < 1 or not flags.is_contiguous():
+        raise MSAError(ERR_INVALID_ARG, f"{what}: flags has to be int32 or uint32, one element at least, contiguous "
+                                        f"(got {flags.dtype} {list(flags.shape)} strides {flags.stride()})")
+
+
 def _want_on_device(what: str, **tensors):
     """Refuses (ERR_INVALID_ARG) tensors (None aside) that do not lie on the current GPU: their addresses go to its
     kernels. After the other checks, which need no GPU."""
@@ -318,6 +329,21 @@ def _want_cache(what: str, dims: Dims, cache: KVCache):
             _want(what, f"cache.{name}_scale", getattr(cache, name + "_scale"), "uint8", (P, G, BS, D // 16))
 
 
+def _want_idx_cache(what: str, dims: Dims, ic: IndexCache):
+    P, I, BS, D = dims.num_pages, dims.n_idx_heads, dims.block_size, dims.head_dim
+    if ic.dtype == FP8_E4M3:
+        wants = (("keys", "uint8", (P, I, BS, D)), ("scale", "float32", (P, I, BS)))
+    elif ic.dtype == NVFP4:
+        wants = (("keys", "uint8", (P, I, BS, D // 2)), ("block_scale", "uint8", (P, I, BS, D // 16)))
+    else:
+        raise MSAError(ERR_UNSUPPORTED, f"{what}: no index cache of dtype {ic.dtype}")
+    for name, kind, shape in wants:
+        if getattr(ic, name) is None:
+            raise MSAError(ERR_INVALID_ARG, f"{what}: an index cache of this type needs {name}")
+        _want(what, "idx_cache." + name, getattr(ic, name), kind, shape)
+    return {"idx_" + name: getattr(ic, name) for name, _, _ in wants}
+
+
 def build_step(dims: Dims, ctx_lens, new_lens, free_pages, free_head, block_table, seq_lens, token_starts,
                slot_mapping, positions, free_head_out, flags, pos_offset=None, stream=None, prepare=False):
     """msa_build_step: block tables, slot map and positions ([axes, tokens]) of a step from its
@@ -333,9 +359,11 @@ def build_step(dims: Dims, ctx_lens, new_lens, free_pages, free_head, block_tabl
     _want(what, "positions", positions, "int32", (positions.shape[0], T), strided_rows=True)
     if pos_offset is not None:
         _want(what, "pos_offset", pos_offset, "int32", (B,))
+    _want_flags(what, flags)
     _want_on_device(what, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, free_head=free_head,
                     block_table=block_table, seq_lens=seq_lens, token_starts=token_starts, slot_mapping=slot_mapping,
-                    positions=positions, free_head_out=free_head_out, pos_offset=pos_offset)
+                    positions=positions, free_head_out=free_head_out, pos_offset=pos_offset,
+                    flags=flags)
     axes = int(positions.shape[0])
     pos_stride = int(positions.stride(0)) if axes > 1 else T
     args = (ctypes.byref(dims), _ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), int(free_pages.numel()),
@@ -374,9 +402,16 @@ def qk_norm_mrope_insert(dims: Dims, q, k, v, idx_q, idx_k, positions, slot_mapp
     _want(what, "positions", positions, "int32", (axes.num_axes, T), strided_rows=True)
     _want(what, "slot_mapping", slot_mapping, "int64", (T,))
     _want_cache(what, dims, cache)
+    _want_flags(what, flags)
+    wts = {n: t for n, t in getattr(nr, "tensors", {}).items() if t is not None}     # (a hand-made struct has addresses only)
+    for name, t in wts.items():
+        _want(what, name, t, "float32", (D,))
+    ics = {}
+    if idx_q is not None and idx_cache is not None:
+        ics = _want_idx_cache(what, dims, idx_cache)
     _want_on_device(what, q=q, k=k, v=v, idx_q=idx_q, idx_k=idx_k, positions=positions, slot_mapping=slot_mapping,
                     q_out=q_out, idx_q_out=idx_q_out, k_cache=cache.k, v_cache=cache.v, k_scale=cache.k_scale,
-                    v_scale=cache.v_scale)
+                    v_scale=cache.v_scale, flags=flags, **wts, **ics)
     kc = cache.c()
     ic = idx_cache.c() if idx_cache is not None else None
     pos_stride = int(positions.stride(0)) if axes.num_axes > 1 else T
@@ -402,8 +437,11 @@ def paged_gqa_decode(dims: Dims, q, cache: KVCache, block_table, seq_lens, out, 
     _want(what, "block_table", block_table, "int32", (dims.batch, dims.max_blocks_per_seq))
     _want(what, "seq_lens", seq_lens, "int32", (dims.batch,))
     _want_cache(what, dims, cache)
+    _want_flags(what, flags)
+    if workspace is not None and not workspace.is_contiguous():
+        raise MSAError(ERR_INVALID_ARG, f"{what}: workspace has to be contiguous (got strides {workspace.stride()})")
     _want_on_device(what, q=q, out=out, lse=lse, block_table=block_table, seq_lens=seq_lens, k_cache=cache.k,
-                    v_cache=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
+                    v_cache=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, workspace=workspace, flags=flags)
     kc = cache.c()
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (ctypes.byref(dims), _ptr(q), ctypes.byref(kc), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse),

@@ -54,9 +54,10 @@ def calls(m):
 
 
 HELD = {"step": ("ctx_lens", "new_lens", "free_pages", "free_head", "block_table", "seq_lens", "token_starts", "slot_mapping",
-                 "positions", "free_head_out", "pos_offset"),
-        "gqa": ("q", "k", "v", "k_scale", "v_scale", "block_table", "seq_lens", "out", "lse"),
-        "rope": ("q", "k", "v", "idx_q", "idx_k", "positions", "slot_mapping", "q_out", "idx_q_out", "k_cache", "v_cache")}
+                 "positions", "free_head_out", "pos_offset", "flags"),
+        "gqa": ("q", "k", "v", "k_scale", "v_scale", "block_table", "seq_lens", "out", "lse", "workspace", "flags"),
+        "rope": ("q", "k", "v", "idx_q", "idx_k", "positions", "slot_mapping", "q_out", "idx_q_out", "k_cache", "v_cache",
+                 "idx_keys", "idx_scale", "wq", "wk", "wiq", "wik", "flags")}
 
 
 @pytest.mark.parametrize("call", sorted(HELD))
@@ -84,3 +85,48 @@ def test_host_tensors_reach_no_kernel(m, monkeypatch, call):
     with pytest.raises(m.MSAError) as e:
         run(**args)
     assert e.value.status == m.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("call,name,bad", [
+    ("step", "flags", z(1, dt=torch.int64)), ("step", "flags", z(0)), ("gqa", "flags", z(1, dt=torch.uint8)),
+    ("gqa", "flags", z(8)[::2]), ("rope", "flags", z(1, dt=torch.float32)),
+    ("gqa", "workspace", z(1 << 24, dt=torch.uint8)[::2]),
+    ("rope", "wq", z(128, dt=torch.bfloat16)), ("rope", "wk", z(64, dt=torch.float32)),
+    ("rope", "wiq", z(256, dt=torch.float32)[::2]), ("rope", "wik", z(1, 128, dt=torch.float32)),
+    ("rope", "idx_keys", z(8, 4, 128, 64, dt=torch.uint8)), ("rope", "idx_keys", z(4, 4, 128, 128, dt=torch.uint8)),
+    ("rope", "idx_scale", z(8, 4, 128, dt=torch.bfloat16)), ("rope", "idx_scale", z(8, 4, 64, dt=torch.float32)),
+    ("rope", "idx_scale", None)])
+def test_wrong_flags_workspaces_weights_and_index_caches(m, monkeypatch, call, name, bad):
+    """Everything on the GPU, one argument of another type, length or layout than the kernel takes it for."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(m, "_stream", lambda stream: None)
+    monkeypatch.setattr(m, "_call", lambda *a: pytest.fail("the call was made"))
+    run, args = calls(m)[call]
+    with pytest.raises(m.MSAError) as e:
+        run(**{n: None if (t := bad if n == name else a) is None else Fake(t, "cuda:0") for n, a in args.items()})
+    assert e.value.status == m.ERR_INVALID_ARG
+
+
+def test_nvfp4_index_cache(m, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(m, "_stream", lambda stream: None)
+    made = []
+    monkeypatch.setattr(m, "_call", lambda *a: made.append(a[3]))
+    _, args = calls(m)["rope"]
+    a = {n: Fake(t, "cuda:0") for n, t in args.items() if not n.startswith(("w", "idx_keys", "idx_scale", "k_cache", "v_cache"))}
+    f = lambda *s, dt=torch.uint8: Fake(z(*s, dt=dt), "cuda:0")
+    w = [f(128, dt=torch.float32) for _ in range(4)]
+    d = m.make_dims(2, 1, max_blocks_per_seq=4, num_pages=8)
+    for keys, scales, status in ((f(8, 4, 128, 64), f(8, 4, 128, 8), None), (f(8, 4, 128, 128), f(8, 4, 128, 8), m.ERR_INVALID_ARG),
+                                 (f(8, 4, 128, 64), f(8, 4, 128, 4), m.ERR_INVALID_ARG), (f(8, 4, 128, 64), None, m.ERR_INVALID_ARG)):
+        def go():
+            m.qk_norm_mrope_insert(d, nr=m.make_norm_rope(*w), axes=m.make_rope_axes((64,)), cache=m.KVCache(
+                m.FP8_E4M3, f(8, 4, 128, 128), f(8, 4, 128, 128)), idx_cache=m.IndexCache(m.NVFP4, keys, None, scales),
+                **dict(a, positions=f(1, 3, dt=torch.int32)))
+        if status is None:
+            go()
+        else:
+            with pytest.raises(m.MSAError) as e:
+                go()
+            assert e.value.status == status
+    assert made == ["msa_qk_norm_mrope_insert"]
