@@ -472,6 +472,8 @@ msa_status_t msa_qk_norm_mrope_insert(const msa_dims_t* dims, const void* q, con
                    !aligned16(nr->idx_k_weight)))
     return MSA_ERR_INVALID_ARG;
   if (with_idx && idx_cache != nullptr && idx_cache->dtype == MSA_F32) return MSA_ERR_UNSUPPORTED;
+  if (with_idx && idx_cache != nullptr && idx_cache->dtype == MSA_FP8_E4M3 && !aligned4({idx_cache->scale}))
+    return MSA_ERR_INVALID_ARG;
   PrologueArgs a;
   memset(&a, 0, sizeof(a));
   st = insert_targets(dims, with_idx, MSA_BF16, cache, idx_cache, dev_flags, a.ins);

@@ -1,4 +1,6 @@
 """The full-attention layer's calls refuse tensors whose addresses their kernels must not get. CPU only: nothing launches."""
+import ctypes
+
 import pytest
 import torch
 
@@ -130,3 +132,14 @@ def test_nvfp4_index_cache(m, monkeypatch):
                 go()
             assert e.value.status == status
     assert made == ["msa_qk_norm_mrope_insert"]
+
+
+def test_index_scales_off_their_type(m):
+    """fp32 scales of an FP8 index cache off a 4-byte boundary."""
+    at = ctypes.c_void_p(0x10000)
+    d = m.make_dims(2, 1, max_blocks_per_seq=4, num_pages=8)
+    nr, kv = m.NormRope(0x10000, 0x10000, 0x10000, 0x10000, 1e-6, 1e4), m._KVCache(m.BF16, at, at, None, None, 1.0, 1.0)
+    ic, axes = m._IndexCache(m.FP8_E4M3, at, ctypes.c_void_p(0x10002), None, 1.0), m.make_rope_axes((64,))
+    got = m.lib.msa_qk_norm_mrope_insert(ctypes.byref(d), at, at, at, at, at, at, 3, at, 3, ctypes.byref(nr), ctypes.byref(axes),
+                                         at, at, ctypes.byref(kv), ctypes.byref(ic), at, None)
+    assert got == m.ERR_INVALID_ARG
