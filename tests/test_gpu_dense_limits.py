@@ -1,4 +1,6 @@
 """The full-attention layer's calls at the edges of their ranges."""
+import importlib.util
+import os
 import threading
 
 import pytest
@@ -37,3 +39,39 @@ def test_step_metadata_from_several_host_threads():
     assert not failed
     for s in steps:
         s.check()
+
+
+def test_measured_calls_follow_the_current_stream(monkeypatch):
+    """A pass of perf/operators.py under another stream than the first one's, and captured on its stream, is ordered with
+    that stream's work."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "perf", "operators.py")
+    spec = importlib.util.spec_from_file_location("measured_operators", path)
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    case = ops._gqa("small", 3, 100, 900, kv="fp8")
+    s = ops.prepare(case, 1)
+    out, lse = (t.clone() for t in ops.run(s))
+    torch.cuda.synchronize()
+    q = s["q"].clone()
+
+    def late(fn):
+        s["q"].zero_()
+        s["out"].zero_()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)                  # the queries arrive some 10 ms later, on this stream
+        s["q"].copy_(q)
+        fn()
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        late(lambda: ops.run(s))
+    side.synchronize()
+    assert torch.equal(s["out"], out) and torch.equal(s["lse"], lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ops.run(s)
+    with torch.cuda.stream(side):
+        late(graph.replay)
+    side.synchronize()
+    assert torch.equal(s["out"], out) and torch.equal(s["lse"], lse) and int(s["flags"].item()) == 0
