@@ -362,7 +362,7 @@ def _plain_mrope(s):
 # ------------------------------------------------------------------------------------- the framework's --
 def _own_call(s):
     """The marshalled call a decode loop keeps for its buffers and issues every step, on the stream that is current
-    here, and the workspace it launches with."""
+    here; its outputs; the workspace it launches with."""
     from block_sparse_attention_07_gb300 import msa
     c = s["case"]
     kind = {"bf16": msa.BF16, "fp8": msa.FP8_E4M3, "nvfp4": msa.NVFP4}
@@ -373,12 +373,13 @@ def _own_call(s):
         cache = msa.KVCache(kind[c["kv"]], s["k"], s["v"], s["k_scale"], s["v_scale"], g, g)
         ws = torch.empty(msa.paged_gqa_workspace_size(d, cache.dtype), dtype=torch.uint8, device="cuda")
         return msa.paged_gqa_decode(d, s["q"], cache, s["block_table"], s["seq_lens"], s["out"], s["lse"], ws,
-                                    s["flags"], prepare=True), ws
+                                    s["flags"], prepare=True), (s["out"], s["lse"]), ws
     if c["op"] == "build_step":
         d = msa.make_dims(c["batch"], 1, max_blocks_per_seq=s["block_table"].shape[1], num_pages=s["pages"])
         return msa.build_step(d, s["ctx_lens"], s["new_lens"], s["free_pages"], s["free_head"], s["block_table"],
                               s["seq_lens"], s["token_starts"], s["slots"], s["positions"], s["free_head_out"],
-                              s["flags"], pos_offset=s["pos_offset"], prepare=True), None
+                              s["flags"], pos_offset=s["pos_offset"], prepare=True), (
+            s["block_table"], s["seq_lens"], s["token_starts"], s["slots"], s["positions"], s["free_head_out"]), None
     G = c["kv_heads"]
     d = msa.make_dims(1, 1, 16 * G, G, G, max_blocks_per_seq=s["pages"], num_pages=s["pages"])
     g = _global(c["kv"])
@@ -386,7 +387,8 @@ def _own_call(s):
     nr = msa.make_norm_rope(s["wq"], s["wk"], eps=EPS, rope_theta=THETA)
     return msa.qk_norm_mrope_insert(d, s["q"], s["k"], s["v"], None, None, s["positions"], s["slots"], nr,
                                     msa.make_rope_axes(SECTIONS), s["q_out"], None, cache, None, s["flags"],
-                                    prepare=True), None
+                                    prepare=True), (
+        s["q_out"], _cache_view(c, s["k_cache"]), _cache_view(c, s["v_cache"])), None
 
 
 def run(s):
@@ -400,12 +402,9 @@ def run(s):
         stream = torch._C._cuda_getCurrentRawStream(device)
         if stream not in calls:
             calls[stream] = _own_call(s)
-        calls[stream][0]()
-        if c["op"] == "paged_gqa":
-            return s["out"], s["lse"]
-        if c["op"] == "build_step":
-            return s["block_table"], s["seq_lens"], s["token_starts"], s["slots"], s["positions"], s["free_head_out"]
-        return s["q_out"], _cache_view(c, s["k_cache"]), _cache_view(c, s["v_cache"])
+        call, outputs, _ = calls[stream]
+        call()
+        return outputs
     if c["op"] == "paged_gqa":
         return _plain_gqa(s)
     if c["op"] == "build_step":
