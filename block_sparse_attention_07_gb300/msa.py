@@ -292,6 +292,8 @@ def sparse_gqa_decode_noalloc(dims: Dims, q, cache: KVCache, block_table, seq_le
 def _want(what: str, name: str, t, dtype: str, shape, strided_rows=False):
     """Refuses (ERR_INVALID_ARG) a tensor of another type, shape or layout than the call reads."""
     import torch
+    if t is None:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} is missing")
     ok = t.dtype == getattr(torch, dtype) and tuple(t.shape) == tuple(shape)
     ok = ok and (t.is_contiguous() or (strided_rows and t.stride(-1) == 1))
     if not ok:
@@ -302,6 +304,8 @@ def _want(what: str, name: str, t, dtype: str, shape, strided_rows=False):
 def _want_flags(what: str, flags):
     """The device flags: 32 bits at least, in 32-bit words."""
     import torch
+    if flags is None:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: flags is missing")
     if flags.dtype not in (torch.int32, torch.uint32) or flags.numel() < 1 or not flags.is_contiguous():
         raise MSAError(ERR_INVALID_ARG, f"{what}: flags has to be int32 or uint32, one element at least, contiguous "
                                         f"(got {flags.dtype} {list(flags.shape)} strides {flags.stride()})")

@@ -134,6 +134,16 @@ def test_nvfp4_index_cache(m, monkeypatch):
     assert made == ["msa_qk_norm_mrope_insert"]
 
 
+@pytest.mark.parametrize("call,names", [("step", ("seq_lens", "block_table", "flags")), ("gqa", ("out", "k", "flags")),
+                                        ("rope", ("k", "q_out", "flags"))])
+def test_missing_tensors(m, call, names):
+    run, args = calls(m)[call]
+    for name in names:
+        with pytest.raises(m.MSAError) as e:
+            run(**dict(args, **{name: None}))
+        assert e.value.status == m.ERR_INVALID_ARG, name
+
+
 def test_index_scales_off_their_type(m):
     """fp32 scales of an FP8 index cache off a 4-byte boundary."""
     at = ctypes.c_void_p(0x10000)
