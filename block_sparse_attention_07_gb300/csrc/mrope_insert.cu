@@ -18,9 +18,11 @@
 // bytes in flight: each warp has its next six groups of queries (1 KB each,
 // contiguous) on their way to its own part of shared memory by bulk copies,
 // and does the keys and values while the first of them arrive. 8,191 tokens,
-// 64 + 4 + 4 heads, FP8 cache: 51.5 us, 5.7 TB/s (85 % of a copy's rate); with
-// loads into registers, two groups ahead, 59.2 us. 64 tokens: 4.5 us, the
-// host's time per launch.
+// 64 + 4 + 4 heads, FP8 cache: 51.3 us, 5.7 TB/s (85 % of a copy's rate); with
+// loads into registers, two groups ahead, 59.2 us. 64 tokens: 4.3 us, the
+// host's time per launch. With fewer heads a warp has fewer groups than its part
+// holds, and what comes before the first of them (position, sines, slot, weights)
+// shows: 32 + 2 + 2 heads 34.6 us (63 % of a copy's rate), 16 + 1 + 1 29.9 (37 %).
 //
 // Phases: theta^(-2i/128) / 2 pi is held as a 64-bit fraction of a turn, so that
 // position times it, modulo one turn, is one integer product. The fraction comes
@@ -349,7 +351,7 @@ cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_ax
   const int passes = (rows + 3) / 4;
   // Warps per token: one once there are 64 tokens per SM (16,000 tokens 92.9 us, two 95.3), two below (4,096
   // tokens 28.6, one 31.0, three 31.2), more when there are few tokens (16 warps per SM: 1,024 tokens 11.5 us;
-  // 32 per SM 14.9, 8 per SM 13.7).
+  // 32 per SM 14.9, 8 per SM 13.7). All with 64 + 4 + 4 heads: the rule counts tokens, not rows.
   const int64_t sms = device_sm_count();
   int64_t parts = a.ins.T >= 64 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
   if (parts < 2 && a.ins.T < 64 * sms) parts = 2;

@@ -9,7 +9,11 @@
 // Mathematics. With logits s_t = scale * log2(e) * q . k_t, a range of tokens
 // gives (m, l, o) = (max s, sum 2^(s - m), sum 2^(s - m) v); two ranges join as
 // m = max(m1, m2), l = sum 2^(mi - m) li, o = sum 2^(mi - m) oi, and the result is
-// o / l, lse = ln 2 * (m + log2 l). Probabilities, sums and states are fp32.
+// o / l, lse = ln 2 * (m + log2 l). Logits, sums and states are fp32. The weights
+// of P V are rounded to the type its tensor-core product takes: bf16 for bf16
+// caches (2^-8, V being bf16 and both operands of one type; a second product for
+// the rest would double P V's share of the tensor pipe), f16 times 2^kPLift for
+// NVFP4 and FP8 (2^-11, plus at most 2^-30 of the row's largest weight).
 //
 // Work split. The (request, KV head, block) triples in that order are the items;
 // a (request, KV head) row is as long as its blocks plus row_cost (what starting
@@ -270,9 +274,10 @@ __device__ void paged_describe_cuts(const PagedParams& p, const Range& r, int ct
 // mma. Eight warps take 16 tokens of every block each, with their own running
 // maxima; blocks arrive by cp.async into two stages. Nothing passes between warps
 // until the row ends, which is what small calls need: 2 requests of 4,096 tokens
-// 12.1 us (rows as M on tcgen05: 12.9), bound by the two launches and the chain of
-// latencies. Large ones are bound by the cache's bytes (32x32k: 322 us, 99 % of a
-// copy's rate), where the rows-as-M form's third stage gains 2 %.
+// 11.6 us (over caches that L2 does not hold 13.2; rows as M on tcgen05: 14.6),
+// bound by the two launches and the chain of latencies. Large ones are bound by
+// the cache's bytes (32x32k: 322 us, 99 % of a copy's rate), where the rows-as-M
+// form's third stage gains 2 %.
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kHalfBox = kBlock * 128;               // 128 rows of 64 16-bit values, swizzled
@@ -542,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_gqa_kernel(const __grid_con
 // warps take issue slots from them. Its steps: K in tensor memory instead of shared
 // memory 852 -> 740 us; S and P V issued by a warp each 676; two softmax groups 627;
 // expanding warps in turns 620; V in tensor memory 595. A second P buffer per group:
-// 632.
+// 632. All quantised forms keep a few values on the stack (bytes stored / loaded:
+// FP8 136 / 188, NVFP4 4 / 4 with 16 rows and 130 / 168 with 32).
 constexpr int kTcS = 2;                 // S buffers in tensor memory
 constexpr int kInfos = 16;              // ring of block descriptions, longer than anything in flight
 
@@ -1458,9 +1464,9 @@ __global__ void __launch_bounds__(32 * TcCfg<kKv, NR>::kWarpsAll, 1)
 // power of two per row. Tensor memory: Q of this row and of the next (64 columns
 // each, two dims per column), S twice (128; P over its first 64), O (128). Roles:
 // copies, S, P V, the cut rows, four softmax warps, the expanding warps.
-// Measured, 8 positions of 16 query heads, 4 KV heads: bf16 32x64k 640 us (the
-// copy's rate: the bytes bound it; the warp mma form needs 1,712); FP8 32x32k 256
-// us, 1,087 TFLOP/s, and NVFP4 16x64k 258 us. What bounds these is neither the
+// Measured, 8 positions of 16 query heads, 4 KV heads: bf16 32x64k 630 us (the
+// copy's rate: the bytes bound it; the warp mma form needs 1,712); FP8 32x32k 253
+// us, 1,087 TFLOP/s, and NVFP4 16x64k 257 us. What bounds these is neither the
 // softmax (two threads per row, on eight warps: 276 and 277 us) nor the expansion
 // alone (twice the warps: 252 and 255): a block passes through expansion, S, softmax
 // and P V one after the other, two blocks at a time, and three f16 tile pairs do not
@@ -1878,8 +1884,8 @@ __global__ void __launch_bounds__(32 * RwCfg<kKv>::kWarpsAll, 1)
 }
 
 // Joins the partials of a cut row, in CTA order. One CTA per (cut, group of
-// rows); with few rows its warps share a row's partials. Bound by latencies: 6 us
-// for 127 cuts of 16 rows on cold caches, 8 us for 127 cuts of 128 rows (12 MB).
+// rows); with few rows its warps share a row's partials. Bound by latencies: 6.7 us
+// for 128 rows' cuts of 16 queries on cold caches, 10 us for 32 of 128 queries (12 MB).
 constexpr int kJoinWarps = 16;
 template <int kChunk>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedParams p, int rows_per_cta) {
@@ -2059,10 +2065,12 @@ cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRe
   p.by_row = rows < ctas - 1;
   const int cuts = p.by_row ? static_cast<int>(rows) : ctas - 1;
   // One form per number of query rows R. FP8 and NVFP4: tokens as M for 16 and 32 rows, rows as M above (32x16k, FP8
-  // with 16 / 32 rows 91.7 / 97.7 us against 128.7 / 129.2, NVFP4 88.9 / 111.1 against 135.8 / 136.5; 64 rows on the
-  // 32-row form would read the cache twice). bf16: up to 16 rows, warp mma for what a small block table can hold
-  // (2x4k 12.1 us, rows as M 12.9; 8x8k 31.9, 32.1), rows as M for a table of at least 64 blocks per CTA (16x16k, 54
-  // of them, 90.5 and 90.2; 32x32k 321.7 and 315.8; 64 requests of 8k-128k 1,322 and 1,284).
+  // with 16 / 32 rows 91.3 / 98.0 us against 128.7 / 129.2, NVFP4 89.2 / 109.7 against 135.8 / 136.5; 64 rows on the
+  // 32-row form would read the cache twice). bf16: up to 16 rows, warp mma for what a small block table can hold,
+  // rows as M for a table of at least 64 blocks per CTA (32x32k 321.7 and 315.8; 64 requests of 8k-128k 1,322 and
+  // 1,284). The host knows the table's width only, so short requests in a wide table take rows as M too; on cold caches
+  // 2x4k 14.6 us instead of 13.2, 4x2k 14.5 and 13.0, 64 requests of up to 2,047 tokens 36.8 and 36.0, 8x8k 32.4 and
+  // 31.6, 16x16k 90.0 and 89.7.
   const bool large = most >= 64ll * ctas;
   const int rows_of = a.kv == MSA_BF16 ? (p.R <= 16 && !large ? 16 : 128) : p.R <= 16 ? 16 : p.R <= 32 ? 32 : 128;
   // A row's start and end, in blocks of its form. 64 requests of up to 2,047 tokens, 4 KV heads, at 0 / 2 / 3 / 5 / 8:

@@ -183,8 +183,10 @@ class IndexCache:
 class Prepared:
     """A library call whose arguments were marshalled once; calling it launches again.
 
-    Holds the ctypes structures the arguments point to. Used on launch-bound
-    paths (the same call issued every decode step)."""
+    Holds the ctypes structures the arguments point to; the tensors are kept
+    alive by the caller. Launches on the stream that was given, or current,
+    when it was made. Used on launch-bound paths (the same call issued every
+    decode step)."""
     __slots__ = ("fn", "args", "keep", "what")
 
     def __init__(self, fn, args, keep, what):

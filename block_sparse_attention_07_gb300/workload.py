@@ -295,7 +295,9 @@ class DeviceWorkload:
     def dense_step(self, stream=None):
         """One decode step of a full-attention layer: insert this step's K/V, then
         attend over every cached token (``out``, ``lse``; index cache and
-        ``selected`` untouched)."""
+        ``selected`` untouched). The workload has one attention workspace, as
+        it has one ``out``: steps on several streams, captured ones too, must
+        not overlap."""
         if getattr(self, "_dense_ws", None) is None:
             size = msa.paged_gqa_workspace_size(self.dims, self.cache.dtype)
             self._dense_ws = torch.empty(size, dtype=torch.uint8, device=self.device)

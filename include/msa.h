@@ -67,7 +67,7 @@ typedef enum {
   MSA_ERR_INVALID_ARG = 1,   /* null pointer, bad size, misaligned pointer */
   MSA_ERR_UNSUPPORTED = 2,   /* valid request outside what the kernels implement */
   MSA_ERR_CUDA = 3,          /* the CUDA runtime reported an error at launch */
-  MSA_ERR_WORKSPACE = 4,     /* workspace null or smaller than msa_sparse_gqa_workspace_size */
+  MSA_ERR_WORKSPACE = 4,     /* workspace null, misaligned or smaller than the call's workspace_size function says */
   MSA_ERR_DEVICE_FLAG = 5    /* msa_read_device_flags found a kernel-reported problem */
 } msa_status_t;
 
@@ -463,6 +463,9 @@ size_t msa_paged_gqa_workspace_size(const msa_dims_t* dims, msa_dtype_t kv_dtype
  * head) whose blocks fall to several CTAs leaves partial results (running
  * maximum, sum, unnormalised output, fp32) in the workspace, and a second
  * launch joins them in their order: results do not depend on timing.
+ * Logits, maxima, sums and states are fp32. A weight is rounded on its way to
+ * the products with V: bf16 caches 2^-8 relative; FP8 and NVFP4 caches 2^-11
+ * relative plus at most 2^-30 of the position's largest weight.
  * Cache slots past the last token may hold any bytes, NaN patterns included. A
  * later draft token's K is masked from earlier positions, but its V has to be
  * finite: it enters their sums with weight 0.
