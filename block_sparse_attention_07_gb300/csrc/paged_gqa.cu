@@ -28,11 +28,10 @@
 
 #include <cstring>
 
-#include "msa_internal.h"
+#include "tcgen05.cuh"
 
 namespace msa {
 
-constexpr uint32_t kEvery = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.693147180559945309f;
 constexpr float kSlack = 8.f;       // log2 units a maximum may exceed the reference by before a rescale
@@ -695,100 +694,6 @@ struct TcCfg {
   static_assert(kTotal - oInfo <= kSmall, "small area");
   static_assert(kUsedCols <= 512, "tensor memory");
 };
-
-// Shared-memory matrix descriptors: start address and leading and stride byte
-// offsets in 16-byte units, descriptor version 1, swizzle. Swizzled 128 B: as the
-// tensor maps write. Plain: core matrices of 8 rows of 16 bytes.
-constexpr uint32_t kSwz128 = 2, kSwzNone = 0;
-// The descriptor's upper half, and its lower half at `saddr`: within one operand
-// only the address changes, by plain additions to the lower half.
-__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
-  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
-}
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-  // one lane's value for the whole warp, so that it is kept in a uniform register
-  return __shfl_sync(kEvery, (saddr >> 4) | ((lbo >> 4) << 16), 0);
-}
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
-
-// Instruction descriptor: fp32 accumulator, operand types, majorness (0 K, 1 MN), N / 8, M / 16.
-__host__ __device__ constexpr uint32_t mma_idesc(int a_type, int b_type, int N, int a_mn, int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) |
-         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-// kind::f16 operand types: 0 f16, 1 bf16. kind::f8f6f4: 0 E4M3, 1 E5M2.
-
-__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
-}
-// A from tensor memory (kind::f16).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t a, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-               : "r"(a));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t a, const float* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-               ::"r"(a), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
-                 "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
-               : "memory");
-}
-// 16 lanes x 16 columns: lane i of the warp holds lanes i / 4 (r[2k]) and 8 + i / 4 (r[2k + 1]) of column 4 k + i % 4.
-__device__ __forceinline__ void tmem_st_16x16(uint32_t a, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-               "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-               ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-                 "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-                 "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
-}
-
-// A wait of a whole warp, with one answer for all of its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(kEvery, mbar_wait(bar, parity)) != 0;
-}
-
-// Barrier of a softmax group (128 threads) that returns whether any thread voted yes.
-__device__ __forceinline__ bool group_any(int id, bool vote) {
-  uint32_t r;
-  asm volatile("{\n .reg .pred q, a;\n setp.ne.u32 q, %2, 0;\n barrier.cta.red.or.pred a, %1, 128, q;\n selp.u32 %0, 1, 0, a;\n}"
-               : "=r"(r) : "r"(id), "r"(vote ? 1u : 0u) : "memory");
-  return r != 0;
-}
 
 constexpr float kQUp = 32.f;        // scale of Q's second part: half a step of a value below 2^8 is 2^3 at most
 __device__ __forceinline__ uint2 fp8_parts(const float (&x)[4], float f) {
@@ -1972,22 +1877,6 @@ static cudaError_t launch_mma(const PagedParams& p, int ctas, cudaStream_t strea
       cudaFuncSetAttribute(paged_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   return launch_pdl(paged_gqa_kernel, dim3(ctas), dim3(kThreads), smem, stream, p);
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up through the runtime (the
-// library does not link libcuda).
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool got = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                         cudaSuccess && q == cudaDriverEntryPointSuccess;
-    return got ? reinterpret_cast<EncodeFn>(ptr) : nullptr;
-  }();
-  return fn;
 }
 
 // 2-D map over a cache's rows [P * G * 128][128 dims]: boxes of 128 rows x 128 bytes
