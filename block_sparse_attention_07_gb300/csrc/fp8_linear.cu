@@ -1,0 +1,306 @@
+// Projection of FP8 rows: both operands E4M3 with fp32 scales per block of 128.
+//
+// "MiniMax-M3.1-Flash Day-0 対応" (aisoku.org), section "最適化と数値": the fused
+// projection in front of norm, rotary embedding and insert; the pages give no
+// formula. With g the blocks of 128 along K,
+//   out[t, n] = sum_g sa[t, g] sw[n / 128, g] sum_{k in g} a[t, k] w[n, k].
+// The inner sum is one tcgen05 product of K = 128 into tensor memory, fresh for
+// every block; the outer one is kept in fp32 registers, which read the block's
+// sums back and add them times their scales. Blocks of K beyond its end and rows
+// beyond the operands' arrive as zeros.
+#include <cstdlib>
+#include <cstring>
+
+#include "tcgen05.cuh"
+
+namespace msa {
+
+constexpr int kTile = 128;                              // weight rows of a tile, and K of a block
+constexpr int kChunk = 16;                              // blocks of K whose scales are held in shared memory
+
+struct LinearParams {
+  const float* sa;              // [T, KB]
+  const float* sw;              // [ceil(N / 128), KB]
+  void* out;                    // [T] rows of N, out_stride apart
+  uint32_t* flags;
+  int64_t out_stride;
+  int T, N, KB;
+  int split;                    // CTAs of a cluster, which share a tile's K
+  int f32;
+};
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// 16 bytes of another CTA's shared memory.
+__device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_out(const LinearParams& p, int64_t t, int n, float v) {
+  if (p.f32) static_cast<float*>(p.out)[t * p.out_stride + n] = v;
+  else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// Weights as M. A CTA has 128 weight rows and up to NT tokens as the product's N,
+// so that few tokens waste nothing but columns; the CTAs of a cluster share the
+// tile's K and add their sums through distributed shared memory, in rank order.
+template <int NT>
+struct RowsCfg {
+  static constexpr int kAcc = NT <= 32 ? 4 : 2;                       // blocks' sums in tensor memory
+  static constexpr uint32_t kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;     // two CTAs per SM up to 64 tokens
+  static constexpr uint32_t kStage = (kTile + NT) * 128;
+  static constexpr int kRow = NT + 4;                                 // floats of a scale row: 16-byte steps, spread over banks
+  static constexpr uint32_t oTable = kStages * kStage;
+  static constexpr uint32_t oBars = oTable + 2 * kChunk * kRow * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc;
+  static constexpr uint32_t oSlot = oBars + kBars * 8;
+  static constexpr uint32_t kTotal = oSlot + 16;
+  static_assert(NT * kTile * 4 <= kStages * kStage, "the sums of a tile fit into the stages");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
+    fp8_linear_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta,
+                           const __grid_constant__ LinearParams p) {
+  using C = RowsCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  float* table = reinterpret_cast<float*>(sm + C::oTable);
+  float* sums = reinterpret_cast<float*>(sm);                         // [NT][128], over the stages when they are done
+  const uint32_t bars = base + C::oBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
+  auto acc_full = [&](int i) { return bars + 8u * (2 * C::kStages + i); };
+  auto acc_free = [&](int i) { return bars + 8u * (2 * C::kStages + C::kAcc + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < C::kAcc; ++i) {
+      mbar_init(acc_full(i), 1);
+      mbar_init(acc_free(i), 4);
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&tw);
+    prefetch_tensormap(&ta);
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::oSlot);
+  // Behind the allocation: a kernel that starts early could otherwise hold the columns that this CTA waits for, while
+  // it waits for this CTA's end.
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
+  const int tok0 = static_cast<int>(blockIdx.y) * NT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.KB) * rank / p.split);
+  const int n = static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / p.split) - kb0;
+  bool ok = true;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
+        const uint32_t at = base + s * C::kStage;
+        mbar_arrive_expect_tx(full(s), C::kStage);
+        tma_load_2d(at, &tw, (kb0 + i) * kTile, tile * kTile, full(s));
+        tma_load_2d(at + kTile * 128, &ta, (kb0 + i) * kTile, tok0, full(s));
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+      // no copy may be in flight when the CTA ends, whatever the others did
+      for (int k = 0; k < C::kStages; ++k) mbar_wait(full(k), ph ^ (k < s ? 0u : 1u));
+      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    constexpr uint32_t id = mma_idesc(0, 0, NT, 0, 0), hi = desc_hi(1024, kSwz128);
+    const uint32_t w0 = desc_lo(base, 16), a0 = desc_lo(base + kTile * 128, 16);
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n; ++i) {
+      const int b = i % C::kAcc;
+      ok = warp_wait(full(s), ph) && (i < C::kAcc || warp_wait(acc_free(b), (i / C::kAcc - 1) & 1));
+      if (!ok) break;
+      tmem_fence_after();
+      if (lead) {
+        const uint32_t w = w0 + s * (C::kStage >> 4), a = a0 + s * (C::kStage >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_fp8(tmem + b * NT, desc_of(w + kk * 2, hi), desc_of(a + kk * 2, hi), id, kk > 0);
+        mma_commit(empty(s));
+        mma_commit(acc_full(b));
+      }
+      __syncwarp();
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+  } else {
+    // Thread = weight row; its sums over the blocks for every token, times the two scales of the block.
+    constexpr int kPer = NT * kChunk / 128;
+    const float* sw = p.sw + static_cast<int64_t>(tile) * p.KB + kb0;
+    float next[kPer];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int e = threadIdx.x + 128 * j, t = e / kChunk, i = c * kChunk + e % kChunk;
+        next[j] = i < n && tok0 + t < p.T ? p.sa[static_cast<int64_t>(tok0 + t) * p.KB + kb0 + i] * sw[i] : 0.f;
+      }
+    };
+    auto keep = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int e = threadIdx.x + 128 * j;
+        table[((c & 1) * kChunk + e % kChunk) * C::kRow + e / kChunk] = next[j];
+      }
+    };
+    float acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+    fetch(0);
+    keep(0);
+    named_barrier(1, 128);
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
+    for (int i = 0; i < n; ++i) {
+      const int b = i % C::kAcc, c = i / kChunk, j = i % kChunk;
+      if (j == 0 && c > 0) {
+        keep(c);                            // the other half: every thread is behind the barrier of its last use
+        named_barrier(1, 128);
+      }
+      if (j == 0) fetch(c + 1);
+      ok = ok && warp_wait(acc_full(b), (i / C::kAcc) & 1);
+      tmem_fence_after();
+      const float4* scale = reinterpret_cast<const float4*>(table + ((c & 1) * kChunk + j) * C::kRow);
+      constexpr int kLd = NT < 32 ? 16 : 32;
+#pragma unroll
+      for (int t0 = 0; t0 < NT; t0 += kLd) {
+        float part[kLd];
+#pragma unroll
+        for (int u = 0; u < kLd; u += 16) tmem_ld16(mine + b * NT + t0 + u, part + u);
+        tmem_wait_ld();
+        if (t0 + kLd == NT) {
+          tmem_fence_before();
+          if (lane == 0) mbar_arrive(acc_free(b));
+        }
+#pragma unroll
+        for (int u = 0; u < kLd; u += 4) {
+          const float4 f = scale[(t0 + u) / 4];
+          acc[t0 + u] = fmaf(part[u], f.x, acc[t0 + u]);
+          acc[t0 + u + 1] = fmaf(part[u + 1], f.y, acc[t0 + u + 1]);
+          acc[t0 + u + 2] = fmaf(part[u + 2], f.z, acc[t0 + u + 2]);
+          acc[t0 + u + 3] = fmaf(part[u + 3], f.w, acc[t0 + u + 3]);
+        }
+      }
+    }
+    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    if (p.split == 1) {
+      const int row = tile * kTile + threadIdx.x;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (row < p.N && tok0 + t < p.T) store_out(p, tok0 + t, row, acc[t]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) sums[t * kTile + threadIdx.x] = acc[t];
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  }
+  if (p.split == 1) return;
+
+  cluster_sync_all();
+  const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
+  for (int i = rank * blockDim.x + threadIdx.x; i < tokens * (kTile / 4); i += p.split * blockDim.x) {
+    const int t = i >> 5, r = 4 * (i & 31);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < p.split; ++q) {
+      const float4 x = ld_cluster(base + (t * kTile + r) * 4, q);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (tile * kTile + r + u < p.N) store_out(p, tok0 + t, tile * kTile + r + u, e[u]);
+  }
+  cluster_sync_all();                       // no CTA ends while another reads its sums
+}
+
+// 2-D map over E4M3 rows [rows][K]: boxes of `box` rows x 128 bytes in the 128-byte swizzle, zeros outside.
+static cudaError_t rows_map(CUtensorMap* map, const void* base, int64_t rows, int K, int box) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  memset(map, 0, sizeof(*map));
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)};
+  const cuuint32_t ones[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int NT>
+static cudaError_t launch_rows(const LinearArgs& a, LinearParams p, cudaStream_t stream, DispatchRecord* rec) {
+  using C = RowsCfg<NT>;
+  CUtensorMap tw, ta;
+  cudaError_t err;
+  if ((err = rows_map(&tw, a.w, a.N, a.K, kTile)) != cudaSuccess) return err;
+  if ((err = rows_map(&ta, a.a, a.T, a.K, NT)) != cudaSuccess) return err;
+  constexpr size_t smem = C::kTotal + 1024;
+  err = cudaFuncSetAttribute(fp8_linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  const int tiles = (a.N + kTile - 1) / kTile, groups = (a.T + NT - 1) / NT;
+  int split = 1;
+  while (split < 8 && split * 2 <= p.KB && static_cast<int64_t>(tiles) * groups * split < device_sm_count()) split *= 2;
+  if (const char* force = getenv("MSA_LINEAR_SPLIT")) {
+    const int s = atoi(force);
+    if ((s == 1 || s == 2 || s == 4 || s == 8) && s <= p.KB) split = s;
+  }
+  p.split = split;
+  err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(tiles * split, groups), dim3(192), smem, stream, split, tw, ta, p);
+  if (err != cudaSuccess) return err;
+  rec->set("fp8_linear rows tokens=%d grid=%dx%d split=%d", NT, tiles * split, groups, split);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, DispatchRecord* rec) {
+  LinearParams p;
+  memset(&p, 0, sizeof(p));
+  p.sa = a.sa;
+  p.sw = a.sw;
+  p.out = a.out;
+  p.flags = a.flags;
+  p.out_stride = a.out_stride;
+  p.T = a.T; p.N = a.N; p.KB = (a.K + kTile - 1) / kTile;
+  p.f32 = a.out_f32;
+  if (a.T <= 16) return launch_rows<16>(a, p, stream, rec);
+  if (a.T <= 32) return launch_rows<32>(a, p, stream, rec);
+  if (a.T <= 64) return launch_rows<64>(a, p, stream, rec);
+  return launch_rows<128>(a, p, stream, rec);
+}
+
+}  // namespace msa

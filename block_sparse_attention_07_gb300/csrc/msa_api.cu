@@ -1,6 +1,7 @@
 // C ABI of libmsa.so (declared in include/msa.h): host-side validation,
 // the thread-local dispatch record, and the launches. Nothing here allocates
 // device memory and nothing synchronises except msa_read_device_flags.
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 
@@ -557,6 +558,164 @@ msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const m
   a.P = dims->num_pages;
   a.softmax_scale = dims->softmax_scale;
   return cuda_status(launch_paged_gqa(a, static_cast<cudaStream_t>(stream), &g_record));
+}
+
+msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x, int64_t x_stride,
+                                const void* residual, void* residual_out, msa_dtype_t residual_dtype,
+                                const float* weight, float eps, void* out, void* codes, float* scales, void* stream) {
+  if (num_tokens < 0 || width < 1) return MSA_ERR_INVALID_ARG;
+  if (width % 16 != 0 || width > 16384) return MSA_ERR_UNSUPPORTED;
+  if ((codes == nullptr) != (scales == nullptr) || (out == nullptr && codes == nullptr)) return MSA_ERR_INVALID_ARG;
+  if (residual == nullptr && residual_out != nullptr) return MSA_ERR_INVALID_ARG;
+  if (residual != nullptr && residual_dtype != MSA_BF16 && residual_dtype != MSA_F32) return MSA_ERR_UNSUPPORTED;
+  if (weight != nullptr && (!(eps >= 0.f) || eps > 1.f)) return MSA_ERR_INVALID_ARG;
+  if (num_tokens == 0) {
+    g_record.set("add_norm_quant empty");
+    return MSA_OK;
+  }
+  if (x == nullptr || x_stride < width || x_stride % 8 != 0) return MSA_ERR_INVALID_ARG;
+  for (const void* ptr : {x, residual, static_cast<const void*>(residual_out), static_cast<const void*>(weight),
+                          static_cast<const void*>(out), static_cast<const void*>(codes)})
+    if (!aligned16(ptr)) return MSA_ERR_INVALID_ARG;
+  if (!aligned4({scales})) return MSA_ERR_INVALID_ARG;
+  if (out == x && x_stride != width) return MSA_ERR_INVALID_ARG;
+  const NormArgs a{x, residual, residual_out, residual_dtype == MSA_F32, weight, out, codes, scales, x_stride,
+                   num_tokens, width, eps};
+  return cuda_status(launch_add_norm_quant(a, static_cast<cudaStream_t>(stream), &g_record));
+}
+
+msa_status_t msa_fp8_linear(int32_t num_tokens, int32_t out_features, int32_t in_features, const void* a,
+                            const float* a_scales, const void* w, const float* w_scales, void* out,
+                            msa_dtype_t out_dtype, int64_t out_stride, uint32_t* dev_flags, void* stream) {
+  constexpr int32_t kMost = 1 << 24;
+  if (num_tokens < 0 || out_features < 1 || in_features < 1) return MSA_ERR_INVALID_ARG;
+  if (out_dtype != MSA_BF16 && out_dtype != MSA_F32) return MSA_ERR_UNSUPPORTED;
+  if (in_features % 16 != 0 || num_tokens > kMost || out_features > kMost || in_features > kMost ||
+      static_cast<int64_t>(num_tokens) * in_features >= (1ll << 40) ||
+      static_cast<int64_t>(out_features) * in_features >= (1ll << 40))
+    return MSA_ERR_UNSUPPORTED;
+  if (dev_flags == nullptr) return MSA_ERR_INVALID_ARG;
+  if (num_tokens == 0) {
+    g_record.set("fp8_linear empty");
+    return MSA_OK;
+  }
+  if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr ||
+      out_stride < out_features)
+    return MSA_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || !aligned4({a_scales, w_scales, dev_flags}))
+    return MSA_ERR_INVALID_ARG;
+  const LinearArgs l{a, a_scales, w, w_scales, out, out_stride, dev_flags, num_tokens, out_features, in_features,
+                     out_dtype == MSA_F32};
+  return cuda_status(launch_fp8_linear(l, static_cast<cudaStream_t>(stream), &g_record));
+}
+
+msa_status_t msa_make_rope(msa_rope_t* rope, int32_t rotary_dim, double theta, msa_rope_layout_t layout,
+                           msa_rope_scaling_t scaling, double factor, double trained_len, double low_turns,
+                           double high_turns) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559, kMost = 1e300;
+  if (rope == nullptr || rotary_dim < 1 || !(theta > 1.0) || theta > kMost) return MSA_ERR_INVALID_ARG;
+  if (rotary_dim > kDim || rotary_dim % 16 != 0) return MSA_ERR_UNSUPPORTED;
+  if (layout != MSA_ROPE_HALF && layout != MSA_ROPE_INTERLEAVED) return MSA_ERR_INVALID_ARG;
+  if (scaling < MSA_ROPE_NONE || scaling > MSA_ROPE_BY_TURNS) return MSA_ERR_INVALID_ARG;
+  if (scaling != MSA_ROPE_NONE && (!(factor >= 1.0) || factor > kMost)) return MSA_ERR_INVALID_ARG;
+  if (scaling == MSA_ROPE_BY_PARTS || scaling == MSA_ROPE_BY_TURNS) {
+    if (!(trained_len > 0.0) || trained_len > kMost || !(low_turns > 0.0) || !(high_turns > low_turns) || high_turns > kMost)
+      return MSA_ERR_INVALID_ARG;
+  }
+  memset(rope, 0, sizeof(*rope));
+  rope->layout = layout;
+  rope->rotary_dim = rotary_dim;
+  rope->gain = scaling == MSA_ROPE_BY_PARTS ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.f;
+  auto clamp01 = [](double v) { return v < 0.0 ? 0.0 : v > 1.0 ? 1.0 : v; };
+  auto pair_of = [&](double turns) { return rotary_dim * log(trained_len / (kTwoPi * turns)) / (2.0 * log(theta)); };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MSA_ROPE_BY_PARTS) {
+    lo = fmax(0.0, floor(pair_of(high_turns)));
+    hi = fmin(rotary_dim - 1.0, ceil(pair_of(low_turns)));
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = pow(theta, -2.0 * i / rotary_dim);
+    double slow = 0.0;                                     // share of the stretched frequency
+    if (scaling == MSA_ROPE_LINEAR) slow = 1.0;
+    else if (scaling == MSA_ROPE_BY_PARTS) slow = clamp01((i - lo) / fmax(hi - lo, 0.001));
+    else if (scaling == MSA_ROPE_BY_TURNS) slow = 1.0 - clamp01((trained_len * f / kTwoPi - low_turns) / (high_turns - low_turns));
+    rope->freq[i] = f * (1.0 - slow) + (slow > 0.0 ? f / factor * slow : 0.0);
+  }
+  return MSA_OK;
+}
+
+msa_status_t msa_qkv_rope_insert(const msa_dims_t* dims, const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, const void* idx_q,
+                                 int64_t idx_q_stride, const void* idx_k, int64_t idx_k_stride,
+                                 const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                 const msa_norm_rope_t* nr, const msa_rope_t* rope, void* q_out, void* idx_q_out,
+                                 const msa_kv_cache_t* cache, const msa_index_cache_t* idx_cache,
+                                 uint32_t* dev_flags, void* stream) {
+  msa_status_t st = check_dense_dims(dims);
+  if (st != MSA_OK) return st;
+  if (num_tokens < 0 || rope == nullptr || cache == nullptr || dev_flags == nullptr) return MSA_ERR_INVALID_ARG;
+  const bool with_idx = idx_q != nullptr || idx_k != nullptr;
+  if (with_idx && (idx_q == nullptr || idx_k == nullptr || idx_q_out == nullptr || dims->n_idx_heads < 1 ||
+                   (nr != nullptr && (nr->idx_q_weight == nullptr || nr->idx_k_weight == nullptr))))
+    return MSA_ERR_INVALID_ARG;
+  if (with_idx && dims->n_idx_heads != dims->n_kv_heads) return MSA_ERR_UNSUPPORTED;
+  if (nr != nullptr && (!(nr->eps >= 0.f) || nr->eps > 1.f)) return MSA_ERR_INVALID_ARG;
+  if (rope->layout != MSA_ROPE_HALF && rope->layout != MSA_ROPE_INTERLEAVED) return MSA_ERR_INVALID_ARG;
+  if (rope->rotary_dim < 1 || !(fabsf(rope->gain) <= 3.0e38f)) return MSA_ERR_INVALID_ARG;
+  if (rope->rotary_dim > kDim || rope->rotary_dim % 16 != 0) return MSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < rope->rotary_dim / 2; ++i)
+    if (!(fabs(rope->freq[i]) <= 6.28318)) return MSA_ERR_INVALID_ARG;         // at most a turn per position
+  if (num_tokens == 0) {
+    g_record.set("qkv_rope_insert empty");
+    return MSA_OK;
+  }
+  const int64_t row_q = static_cast<int64_t>(dims->n_heads) * kDim, row_kv = static_cast<int64_t>(dims->n_kv_heads) * kDim;
+  if (q == nullptr || k == nullptr || v == nullptr || positions == nullptr || slot_mapping == nullptr ||
+      q_out == nullptr || (nr != nullptr && (nr->q_weight == nullptr || nr->k_weight == nullptr)))
+    return MSA_ERR_INVALID_ARG;
+  if (q_stride < row_q || k_stride < row_kv || v_stride < row_kv || q_stride % 8 != 0 || k_stride % 8 != 0 ||
+      v_stride % 8 != 0)
+    return MSA_ERR_INVALID_ARG;
+  if (with_idx && (idx_q_stride < row_kv || idx_k_stride < row_kv || idx_q_stride % 8 != 0 || idx_k_stride % 8 != 0))
+    return MSA_ERR_INVALID_ARG;
+  if (q_out == q && q_stride != row_q) return MSA_ERR_INVALID_ARG;
+  if (with_idx && idx_q_out == idx_q && idx_q_stride != row_kv) return MSA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k, v, static_cast<const void*>(q_out)})
+    if (!aligned16(ptr)) return MSA_ERR_INVALID_ARG;
+  if (with_idx && (!aligned16(idx_q) || !aligned16(idx_k) || !aligned16(idx_q_out))) return MSA_ERR_INVALID_ARG;
+  if (nr != nullptr && (!aligned16(nr->q_weight) || !aligned16(nr->k_weight) ||
+                        (with_idx && (!aligned16(nr->idx_q_weight) || !aligned16(nr->idx_k_weight)))))
+    return MSA_ERR_INVALID_ARG;
+  if (!aligned4({positions, dev_flags}) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return MSA_ERR_INVALID_ARG;
+  if (with_idx && idx_cache != nullptr && idx_cache->dtype == MSA_F32) return MSA_ERR_UNSUPPORTED;
+  if (with_idx && idx_cache != nullptr && idx_cache->dtype == MSA_FP8_E4M3 && !aligned4({idx_cache->scale}))
+    return MSA_ERR_INVALID_ARG;
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  st = insert_targets(dims, with_idx, MSA_BF16, cache, idx_cache, dev_flags, a.ins);
+  if (st != MSA_OK) return st;
+  a.ins.k_new = k;
+  a.ins.v_new = v;
+  a.ins.idx_new = with_idx ? idx_k : nullptr;
+  a.ins.slots = slot_mapping;
+  a.ins.T = num_tokens;
+  a.q = q;
+  a.idx_q = with_idx ? idx_q : nullptr;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.iq_stride = idx_q_stride; a.ik_stride = idx_k_stride;
+  a.q_out = q_out;
+  a.idx_q_out = with_idx ? idx_q_out : nullptr;
+  a.positions = positions;
+  if (nr != nullptr) {
+    a.wq = nr->q_weight; a.wk = nr->k_weight;
+    a.wiq = nr->idx_q_weight; a.wik = nr->idx_k_weight;
+    a.eps = nr->eps;
+  }
+  a.rope = rope;
+  a.H = dims->n_heads;
+  a.I = dims->n_idx_heads;
+  return cuda_status(launch_qkv_rope_insert(a, static_cast<cudaStream_t>(stream), &g_record));
 }
 
 msa_status_t msa_selftest_bounded_wait(uint32_t* dev_flags, void* stream) {

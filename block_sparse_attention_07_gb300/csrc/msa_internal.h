@@ -205,6 +205,55 @@ struct PagedArgs {
 size_t paged_gqa_workspace_bytes(int Q, int H, int G);
 cudaError_t launch_paged_gqa(const PagedArgs& a, cudaStream_t stream, DispatchRecord* rec);
 
+// Residual + RMS norm + FP8 rows (msa_add_norm_quant).
+struct NormArgs {
+  const void* x;                // bf16 rows, x_stride elements apart
+  const void* residual;         // bf16 or fp32 [T, W], or null
+  void* residual_out;
+  int residual_f32;
+  const float* weight;          // [W], or null: no norm
+  void* out;                    // bf16 [T, W] or null
+  void* codes;                  // E4M3 [T, W] or null, with scales fp32 [T, ceil(W / 128)]
+  float* scales;
+  int64_t x_stride;
+  int rows, width;
+  float eps;
+};
+cudaError_t launch_add_norm_quant(const NormArgs& a, cudaStream_t stream, DispatchRecord* rec);
+
+// Product of FP8 rows and FP8 weights with scales per block of 128 (msa_fp8_linear).
+struct LinearArgs {
+  const void* a;                // E4M3 [T, K]
+  const float* sa;              // [T, ceil(K / 128)]
+  const void* w;                // E4M3 [N, K]
+  const float* sw;              // [ceil(N / 128), ceil(K / 128)]
+  void* out;                    // bf16 or fp32 rows of N, out_stride elements apart
+  int64_t out_stride;
+  uint32_t* flags;
+  int T, N, K;
+  int out_f32;
+};
+cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, DispatchRecord* rec);
+
+// Rotary forms + norms + insert on packed rows (msa_qkv_rope_insert).
+struct RopeArgs {
+  InsertArgs ins;               // k_new, v_new, idx_new: rows of heads, their strides below
+  const void* q;
+  const void* idx_q;            // or null
+  int64_t q_stride, k_stride, v_stride, iq_stride, ik_stride;
+  void* q_out;
+  void* idx_q_out;
+  const int32_t* positions;
+  const float* wq;              // null: no norm
+  const float* wk;
+  const float* wiq;
+  const float* wik;
+  float eps;
+  const msa_rope_t* rope;
+  int H, I;
+};
+cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, DispatchRecord* rec);
+
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, DispatchRecord* rec);
 cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRecord* rec);
 

@@ -16,6 +16,8 @@ import os
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libmsa.so")
 
 F32, BF16, FP8_E4M3, NVFP4 = 0, 1, 2, 3
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_BY_PARTS, ROPE_BY_TURNS = 0, 1, 2, 3
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_DEVICE_FLAG = range(6)
 
@@ -27,7 +29,8 @@ EXPORTED = ("msa_abi_version", "msa_status_string", "msa_get_last_dispatch", "ms
             "msa_index_score", "msa_insert_index_score", "msa_select_blocks", "msa_sparse_gqa_workspace_size",
             "msa_sparse_gqa_decode", "msa_sparse_gqa_decode_noalloc", "msa_read_device_flags",
             "msa_qk_norm_rope_insert", "msa_select_sparse_gqa_decode", "msa_selftest_bounded_wait",
-            "msa_build_step", "msa_qk_norm_mrope_insert", "msa_paged_gqa_workspace_size", "msa_paged_gqa_decode")
+            "msa_build_step", "msa_qk_norm_mrope_insert", "msa_paged_gqa_workspace_size", "msa_paged_gqa_decode",
+            "msa_add_norm_quant", "msa_fp8_linear", "msa_make_rope", "msa_qkv_rope_insert")
 
 
 class Dims(ctypes.Structure):
@@ -58,6 +61,12 @@ class NormRope(ctypes.Structure):
 class RopeAxes(ctypes.Structure):
     """msa_rope_axes_t: the number of position axes and the axis of each of the 64 rotary pairs."""
     _fields_ = [("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
+
+
+class Rope(ctypes.Structure):
+    """msa_rope_t: pair layout, rotated dims, factor on cosine and sine, angles per position."""
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("gain", ctypes.c_float),
+                ("freq", ctypes.c_double * 64)]
 
 
 class MSAError(RuntimeError):
@@ -104,6 +113,13 @@ def _load():
     lib.msa_paged_gqa_workspace_size.argtypes = [ctypes.POINTER(Dims), ctypes.c_int]
     lib.msa_paged_gqa_decode.argtypes = [ctypes.POINTER(Dims), vp, ctypes.POINTER(_KVCache), vp, vp, vp, vp, vp, sz,
                                          vp, vp]
+    f32, f64, i64 = ctypes.c_float, ctypes.c_double, ctypes.c_int64
+    lib.msa_add_norm_quant.argtypes = [i32, i32, vp, i64, vp, vp, ctypes.c_int, vp, f32, vp, vp, vp, vp]
+    lib.msa_fp8_linear.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, ctypes.c_int, i64, vp, vp]
+    lib.msa_make_rope.argtypes = [ctypes.POINTER(Rope), i32, f64, ctypes.c_int, ctypes.c_int, f64, f64, f64, f64]
+    lib.msa_qkv_rope_insert.argtypes = [ctypes.POINTER(Dims), vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32,
+                                        ctypes.POINTER(NormRope), ctypes.POINTER(Rope), vp, vp,
+                                        ctypes.POINTER(_KVCache), ctypes.POINTER(_IndexCache), vp, vp]
     for name in EXPORTED:       # every other entry point returns msa_status_t
         if name not in ("msa_abi_version", "msa_status_string", "msa_sparse_gqa_workspace_size",
                         "msa_paged_gqa_workspace_size"):
@@ -453,6 +469,129 @@ def paged_gqa_decode(dims: Dims, q, cache: KVCache, block_table, seq_lens, out, 
     args = (ctypes.byref(dims), _ptr(q), ctypes.byref(kc), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse),
             _ptr(workspace), nbytes, _ptr(flags), _stream(stream))
     return _call(lib.msa_paged_gqa_decode, args, (dims, kc), what, prepare)
+
+
+def _want_rows(what: str, name: str, t, dtype: str, shape):
+    """Refuses a tensor whose rows are not contiguous; the rows themselves may lie apart, but not on one another."""
+    import torch
+    if t is None:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} is missing")
+    ok = t.dtype == getattr(torch, dtype) and tuple(t.shape) == tuple(shape)
+    if ok and t.numel() > 0:
+        row = 1
+        for n, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            ok = ok and (n == 1 or stride == row)
+            row *= n
+        ok = ok and (t.shape[0] == 1 or t.stride(0) >= row)
+    if not ok:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be {dtype} {list(shape)}, contiguous within a row "
+                                        f"(got {t.dtype} {list(t.shape)} strides {t.stride()})")
+
+
+def _row_stride(t):
+    """Elements between rows; a single row's tensor may say anything."""
+    return int(t.stride(0)) if t.shape[0] > 1 else math.prod(t.shape[1:])
+
+
+def add_norm_quant(x, weight, residual=None, residual_out=None, out=None, codes=None, scales=None, eps=1e-6,
+                   stream=None, prepare=False):
+    """msa_add_norm_quant: ``x`` bf16 [T, width] (rows may lie apart), ``residual`` / ``residual_out`` bf16 or fp32,
+    ``weight`` fp32 [width] or None (no norm); results in ``out`` (bf16) and / or ``codes`` with ``scales``."""
+    what = "msa_add_norm_quant"
+    if x is None or x.dim() != 2:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: x has to be bfloat16 [tokens, width]")
+    T, W = (int(n) for n in x.shape)
+    _want_rows(what, "x", x, "bfloat16", (T, W))
+    kind = BF16
+    if residual is not None:
+        import torch
+        kind = F32 if residual.dtype == torch.float32 else BF16
+        _want(what, "residual", residual, "float32" if kind == F32 else "bfloat16", (T, W))
+    if residual_out is not None:
+        _want(what, "residual_out", residual_out, "float32" if kind == F32 else "bfloat16", (T, W))
+    if weight is not None:
+        _want(what, "weight", weight, "float32", (W,))
+    if out is not None:
+        _want(what, "out", out, "bfloat16", (T, W))
+    if codes is not None:
+        _want(what, "codes", codes, "uint8", (T, W))
+    if scales is not None:
+        _want(what, "scales", scales, "float32", (T, (W + 127) // 128))
+    _want_on_device(what, x=x, residual=residual, residual_out=residual_out, weight=weight, out=out, codes=codes,
+                    scales=scales)
+    args = (T, W, _ptr(x), _row_stride(x), _ptr(residual), _ptr(residual_out), kind, _ptr(weight), eps, _ptr(out),
+            _ptr(codes), _ptr(scales), _stream(stream))
+    return _call(lib.msa_add_norm_quant, args, (), what, prepare)
+
+
+def fp8_linear(a, a_scales, w, w_scales, out, flags, stream=None, prepare=False):
+    """msa_fp8_linear: ``out`` [T, N] (bf16 or fp32, rows may lie apart) from codes ``a`` [T, K] and ``w`` [N, K] (uint8
+    E4M3) with their scales per 128 values and per 128 x 128 block."""
+    what = "msa_fp8_linear"
+    for name, t in (("a", a), ("w", w), ("out", out)):
+        if t is None or t.dim() != 2:
+            raise MSAError(ERR_INVALID_ARG, f"{what}: {name} has to be a matrix")
+    import torch
+    T, N, K = int(a.shape[0]), int(w.shape[0]), int(a.shape[1])
+    KB = (K + 127) // 128
+    f32 = out.dtype == torch.float32
+    for name, t, dtype, shape in (("a", a, "uint8", (T, K)), ("a_scales", a_scales, "float32", (T, KB)),
+                                  ("w", w, "uint8", (N, K)), ("w_scales", w_scales, "float32", ((N + 127) // 128, KB))):
+        _want(what, name, t, dtype, shape)
+    _want_rows(what, "out", out, "float32" if f32 else "bfloat16", (T, N))
+    _want_flags(what, flags)
+    _want_on_device(what, a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out, flags=flags)
+    args = (T, N, K, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(out), F32 if f32 else BF16,
+            _row_stride(out), _ptr(flags), _stream(stream))
+    return _call(lib.msa_fp8_linear, args, (), what, prepare)
+
+
+def make_rope(rotary_dim=128, theta=10000.0, layout=ROPE_HALF, scaling=ROPE_NONE, factor=1.0, trained_len=0,
+              low_turns=1.0, high_turns=32.0) -> Rope:
+    """msa_make_rope: a rotary embedding's layout, rotated dims and (scaled) frequencies."""
+    rope = Rope()
+    _check(lib.msa_make_rope(ctypes.byref(rope), rotary_dim, theta, layout, scaling, factor, trained_len, low_turns,
+                             high_turns), "msa_make_rope")
+    return rope
+
+
+def qkv_rope_insert(dims: Dims, q, k, v, idx_q, idx_k, positions, slot_mapping, nr: NormRope | None, rope: Rope, q_out,
+                    idx_q_out, cache: KVCache, idx_cache: IndexCache | None, flags, stream=None, prepare=False):
+    """msa_qkv_rope_insert: ``q`` [T, H, D], ``k``, ``v`` [T, G, D], ``idx_q``, ``idx_k`` [T, I, D] may be views of packed
+    rows (heads contiguous, tokens apart); ``positions`` [T]."""
+    what, D = "msa_qkv_rope_insert", dims.head_dim
+    if q is None or q.dim() != 3:
+        raise MSAError(ERR_INVALID_ARG, f"{what}: q has to be bfloat16 [tokens, heads, {D}]")
+    T = int(q.shape[0])
+    for name, t, h in (("q", q, dims.n_heads), ("k", k, dims.n_kv_heads), ("v", v, dims.n_kv_heads),
+                       ("idx_q", idx_q, dims.n_idx_heads), ("idx_k", idx_k, dims.n_idx_heads)):
+        if t is not None or not name.startswith("idx"):
+            _want_rows(what, name, t, "bfloat16", (T, h, D))
+    _want(what, "q_out", q_out, "bfloat16", (T, dims.n_heads, D))
+    if idx_q_out is not None:
+        _want(what, "idx_q_out", idx_q_out, "bfloat16", (T, dims.n_idx_heads, D))
+    _want(what, "positions", positions, "int32", (T,))
+    _want(what, "slot_mapping", slot_mapping, "int64", (T,))
+    _want_cache(what, dims, cache)
+    _want_flags(what, flags)
+    wts = {n: t for n, t in getattr(nr, "tensors", {}).items() if t is not None}     # (a hand-made struct has addresses only)
+    for name, t in wts.items():
+        _want(what, name, t, "float32", (D,))
+    ics = {}
+    if idx_q is not None and idx_cache is not None:
+        ics = _want_idx_cache(what, dims, idx_cache)
+    _want_on_device(what, q=q, k=k, v=v, idx_q=idx_q, idx_k=idx_k, positions=positions, slot_mapping=slot_mapping,
+                    q_out=q_out, idx_q_out=idx_q_out, k_cache=cache.k, v_cache=cache.v, k_scale=cache.k_scale,
+                    v_scale=cache.v_scale, flags=flags, **wts, **ics)
+    kc = cache.c()
+    ic = idx_cache.c() if idx_cache is not None else None
+    args = [ctypes.byref(dims)]
+    for t in (q, k, v, idx_q, idx_k):
+        args += [_ptr(t), 0 if t is None else _row_stride(t)]
+    args += [_ptr(positions), _ptr(slot_mapping), T, ctypes.byref(nr) if nr is not None else None, ctypes.byref(rope),
+             _ptr(q_out), _ptr(idx_q_out), ctypes.byref(kc), ctypes.byref(ic) if ic is not None else None, _ptr(flags),
+             _stream(stream)]
+    return _call(lib.msa_qkv_rope_insert, tuple(args), (dims, nr, rope, kc, ic), what, prepare)
 
 
 def selftest_bounded_wait(flags, stream=None):

@@ -483,6 +483,121 @@ msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const m
                                   void* workspace, size_t workspace_bytes, uint32_t* dev_flags, void* stream);
 
 /*
+ * The residual's addition, RMS norm and rounding to FP8 rows in front of a
+ * projection, in one pass ("MiniMax-M3.1-Flash Day-0 対応", section
+ * "最適化と数値": projection, norm, rotary embedding and insert in a row; the
+ * pages give no formulas). For each of num_tokens rows of `width` values, in fp32:
+ *   h = x + residual (h = x with residual = NULL); residual_out = h, rounded
+ *       once to residual_dtype;
+ *   y = h / sqrt(mean(h^2) + eps) * weight, from the unrounded h; y = h with
+ *       weight = NULL (which rounds an attention output for its projection);
+ *   out = bf16(y), and per 128 values (the last group may be shorter)
+ *   scales = max|y| / 448, codes = E4M3_RNE_satfinite(y / scale), both IEEE
+ *       divisions; a group of zeros has scale 0 and codes 0.
+ * Squares beyond fp32's range are no limit: such rows are scaled by a power of
+ * two. A group that holds a NaN or an infinity comes out as NaN where its scale
+ * is applied; a row that holds one is NaN there after the norm, and zero where
+ * its values are finite and the norm is infinite.
+ * x: bf16, rows x_stride elements apart. residual, residual_out: [T, width] of
+ * residual_dtype (MSA_BF16 or MSA_F32); residual_out may be NULL, or residual
+ * itself. weight: fp32 [width] or NULL. out: bf16 [T, width] or NULL; it may be x
+ * where x_stride = width. codes: [T, width] and scales: fp32 [T, ceil(width / 128)],
+ * both or neither; out or codes has to be there. width: a multiple of 16, at most
+ * 16384. x_stride: at least width, a multiple of 8. Pointers 16-byte aligned
+ * (scales: 4). No other overlap of outputs and inputs. num_tokens = 0 launches
+ * nothing.
+ */
+msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x, int64_t x_stride,
+                                const void* residual, void* residual_out, msa_dtype_t residual_dtype,
+                                const float* weight, float eps, void* out, void* codes, float* scales, void* stream);
+
+/*
+ * A projection of FP8 rows with FP8 weights, one fp32 scale per row and 128
+ * values and one per 128 x 128 block of the weight (the rows are
+ * msa_add_norm_quant's; same section of the pages). With g the groups of 128
+ * along K = in_features (the last may be shorter) and N = out_features,
+ *   out[t, n] = sum_g a_scales[t, g] w_scales[n / 128, g] sum_{k in g} a[t, k] w[n, k].
+ * The sum of a group is taken on the tensor cores in fp32, the sum over groups in
+ * fp32 registers in a fixed order: results do not depend on timing. They do
+ * depend, within fp32's rounding, on num_tokens, which sets how K is split.
+ * A code that is NaN makes every output that it enters NaN.
+ * a: E4M3 [T, K]; a_scales: fp32 [T, ceil(K / 128)]; w: E4M3 [N, K]; w_scales:
+ * fp32 [ceil(N / 128), ceil(K / 128)]; all contiguous. out: MSA_BF16 or MSA_F32
+ * rows of N, out_stride >= N elements apart; what lies between N and out_stride is
+ * left as it is. K: a multiple of 16. T, N and K up to 2^24, T * K and N * K below
+ * 2^40. a, w and out 16-byte aligned, scales 4-byte. out overlaps no input.
+ * num_tokens = 0 launches nothing. MSA_LINEAR_SPLIT=1, 2, 4 or 8 in the
+ * environment (read on every call) forces the number of CTAs that share a tile's
+ * K where few tokens are projected.
+ */
+msa_status_t msa_fp8_linear(int32_t num_tokens, int32_t out_features, int32_t in_features, const void* a,
+                            const float* a_scales, const void* w, const float* w_scales, void* out,
+                            msa_dtype_t out_dtype, int64_t out_stride, uint32_t* dev_flags, void* stream);
+
+typedef enum {
+  MSA_ROPE_HALF = 0,           /* pairs (i, i + rotary_dim / 2) */
+  MSA_ROPE_INTERLEAVED = 1     /* pairs (2i, 2i + 1) */
+} msa_rope_layout_t;
+
+typedef enum {
+  MSA_ROPE_NONE = 0,
+  MSA_ROPE_LINEAR = 1,
+  MSA_ROPE_BY_PARTS = 2,
+  MSA_ROPE_BY_TURNS = 3
+} msa_rope_scaling_t;
+
+/* A rotary embedding (host struct): pair i < rotary_dim / 2 turns by
+ * freq[i] radians per position, cosine and sine times gain; dims from rotary_dim
+ * on pass. msa_make_rope fills it; a caller may also set its own frequencies. */
+typedef struct {
+  int32_t layout;              /* msa_rope_layout_t */
+  int32_t rotary_dim;          /* 16 to 128, a multiple of 16 */
+  float gain;
+  double freq[64];
+} msa_rope_t;
+
+/*
+ * Fills *rope (host; nothing is launched). With R = rotary_dim and
+ * f_i = theta^(-2i/R), i < R/2:
+ *   MSA_ROPE_NONE: freq = f, gain 1; the other arguments are not used.
+ *   MSA_ROPE_LINEAR: freq = f / factor, gain 1 (positions divided by factor).
+ *   MSA_ROPE_BY_PARTS: freq = f (1 - r) + f / factor * r, with r = clamp((i - lo) /
+ *     max(hi - lo, 0.001), 0, 1), lo = max(0, floor(d(high_turns))), hi = min(R - 1,
+ *     ceil(d(low_turns))), d(u) = R ln(trained_len / (2 pi u)) / (2 ln theta): the
+ *     pair that turns u times over the trained length; gain 0.1 ln(factor) + 1.
+ *   MSA_ROPE_BY_TURNS: freq = f / factor * (1 - s) + f s, with s =
+ *     clamp((trained_len f / 2 pi - low_turns) / (high_turns - low_turns), 0, 1); gain 1.
+ * theta > 1; factor >= 1; trained_len > 0; 0 < low_turns < high_turns.
+ */
+msa_status_t msa_make_rope(msa_rope_t* rope, int32_t rotary_dim, double theta, msa_rope_layout_t layout,
+                           msa_rope_scaling_t scaling, double factor, double trained_len, double low_turns,
+                           double high_turns);
+
+/*
+ * msa_qk_norm_rope_insert for a checkpoint's own rotary form, on packed rows: the
+ * heads of a token lie together, the tokens at a stride, so that the rows of one
+ * packed projection (msa_fp8_linear) are read where they are. The rotation is
+ * *rope's, on one position per token; its phase is reduced exactly modulo one turn,
+ * whatever the position. With nr = NULL there is no norm. Otherwise norm, rounding
+ * to bf16, quantisation, outputs, the index branch and negative slots are those of
+ * msa_qk_norm_rope_insert, whose rope_theta is not used here; squares beyond fp32's
+ * range are no limit. Dims that pass are not touched by NaN or infinities in others
+ * without a norm.
+ * q: bf16 rows of [H, D], q_stride elements apart; k, v: [G, D]; idx_q, idx_k: [I, D]
+ * or both NULL. Strides are multiples of 8 and at least the row. q_out: bf16
+ * [T, H, D], idx_q_out: bf16 [T, I, D]; they may be q and idx_q where those are
+ * contiguous, and overlap no other input. Shapes as msa_qk_norm_mrope_insert. No slot
+ * may occur twice among the tokens (negative ones aside).
+ */
+msa_status_t msa_qkv_rope_insert(const msa_dims_t* dims, const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, const void* idx_q,
+                                 int64_t idx_q_stride, const void* idx_k, int64_t idx_k_stride,
+                                 const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                 const msa_norm_rope_t* nr, const msa_rope_t* rope, void* q_out, void* idx_q_out,
+                                 const msa_kv_cache_t* cache, const msa_index_cache_t* idx_cache,
+                                 uint32_t* dev_flags, void* stream);
+
+/*
  * Diagnostic of the bounded waits (the pages have no counterpart). Launches
  * one thread that waits on a shared-memory barrier which nothing completes,
  * through the same bounded wait the library's kernels use; when the wait gives
