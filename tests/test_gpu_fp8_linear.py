@@ -70,6 +70,28 @@ def test_every_split(monkeypatch, split, T, N, K):
     c.check()
 
 
+@pytest.mark.parametrize("split", [1, 2, 4])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 512), (129, 130, 1040), (256, 256, 2048), (257, 520, 4096), (600, 1300, 528)])
+def test_pairs(monkeypatch, split, T, N, K):
+    """Two CTAs per tile, its K on one to four pairs, whatever the number of tokens."""
+    monkeypatch.setenv("MSA_LINEAR_SPLIT", str(split))
+    monkeypatch.setenv("MSA_LINEAR_FORM", "pairs")
+    for dtype, pad in ((torch.bfloat16, 0), (torch.float32, 5)):
+        c = Case(T, N, K, dtype, seed=split, pad=pad)
+        c.run()
+        assert "pairs" in msa.last_dispatch() and msa.last_dispatch().endswith(f"split={split}")
+        c.check()
+
+
+@pytest.mark.parametrize("T", [130, 300])
+def test_rows_form_with_many_tokens(monkeypatch, T):
+    monkeypatch.setenv("MSA_LINEAR_FORM", "rows")
+    c = Case(T, 300, 1040, seed=T)
+    c.run()
+    assert "rows" in msa.last_dispatch()
+    c.check()
+
+
 @pytest.mark.parametrize("T", [1, 20, 64, 200])
 def test_long_k(T):
     """More blocks of K than one table of scales holds, on one CTA and shared."""
