@@ -28,7 +28,7 @@ struct LinearParams {
   int split;                    // CTAs (pairs) of a cluster, which share a tile's K
   int f32;
   int tiles_m, tiles_n, group;  // pairs: tiles of 256 tokens and of 256 weight rows, token tiles that are walked together
-  int wide;                     // rows of the output start on 32-byte boundaries
+  int wide, quads;              // rows of the output start on 32-byte boundaries, on those of four values
 };
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -43,9 +43,56 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
   return v;
 }
 
+// 32 columns of the warp's 32 lanes, a lane each.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+                 "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+                 "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+               : "r"(a));
+}
+// Waits for the loads so far; the values are tied to it, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait_ld32(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+               ::"memory");
+}
+// (d0, d1) += (a0, a1) * s
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float s) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%0, %1};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
+      : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(s));
+}
+
+// (d0, d1) += (a0, a1) * (s0, s1)
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float s0, float s1) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%0, %1};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
+      : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(s0), "f"(s1));
+}
+
 __device__ __forceinline__ void store_out(const LinearParams& p, int64_t t, int n, float v) {
   if (p.f32) static_cast<float*>(p.out)[t * p.out_stride + n] = v;
   else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(v);
+}
+
+// Four outputs of a row in a row; `quads`: they are aligned to their size.
+__device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, const float4& v) {
+  if (p.quads && n + 4 <= p.N) {
+    if (p.f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + t * p.out_stride + n) = v;
+    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + t * p.out_stride + n) =
+             make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    return;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (n + u < p.N) store_out(p, t, n + u, e[u]);
 }
 
 // ---------------------------------------------------------------------------
@@ -54,9 +101,12 @@ __device__ __forceinline__ void store_out(const LinearParams& p, int64_t t, int 
 // tile's K and add their sums through distributed shared memory, in rank order.
 template <int NT>
 struct RowsCfg {
-  static constexpr int kAcc = NT <= 32 ? 4 : 2;                       // blocks' sums in tensor memory
+  static constexpr int kPer = NT < 32 ? NT : 32;                      // a thread's tokens
+  static constexpr int kSumThreads = 128 * (NT / kPer), kThreads = kSumThreads + 64;
+  static constexpr int kCtas = NT <= 64 ? 2 : 1;                      // per SM
+  static constexpr int kAcc = NT <= 64 ? 4 : 2;                       // blocks' sums in tensor memory
   static constexpr uint32_t kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
-  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;     // two CTAs per SM up to 64 tokens
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
   static constexpr uint32_t kStage = (kTile + NT) * 128;
   static constexpr int kRow = NT + 4;                                 // floats of a scale row: 16-byte steps, spread over banks
   static constexpr uint32_t oTable = kStages * kStage;
@@ -65,10 +115,11 @@ struct RowsCfg {
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static_assert(NT * kTile * 4 <= kStages * kStage, "the sums of a tile fit into the stages");
+  static_assert(kCols * kCtas <= 512, "tensor memory");
 };
 
 template <int NT>
-__global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
     fp8_linear_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta,
                            const __grid_constant__ LinearParams p) {
   using C = RowsCfg<NT>;
@@ -82,6 +133,7 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
   auto acc_full = [&](int i) { return bars + 8u * (2 * C::kStages + i); };
   auto acc_free = [&](int i) { return bars + 8u * (2 * C::kStages + C::kAcc + i); };
+  constexpr int kCopyWarp = C::kSumThreads / 32, kMmaWarp = kCopyWarp + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -91,13 +143,13 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
     }
     for (int i = 0; i < C::kAcc; ++i) {
       mbar_init(acc_full(i), 1);
-      mbar_init(acc_free(i), 4);
+      mbar_init(acc_free(i), C::kSumThreads / 32);
     }
     fence_mbar_init();
     prefetch_tensormap(&tw);
     prefetch_tensormap(&ta);
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(C::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -117,7 +169,7 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
   const int n = static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / p.split) - kb0;
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == kCopyWarp) {
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
@@ -134,7 +186,7 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
       if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     constexpr uint32_t id = mma_idesc(0, 0, NT, 0, 0), hi = desc_hi(1024, kSwz128);
     const uint32_t w0 = desc_lo(base, 16), a0 = desc_lo(base + kTile * 128, 16);
     const bool lead = elect_one();
@@ -157,77 +209,75 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   } else {
-    // Thread = weight row; its sums over the blocks for every token, times the two scales of the block.
-    constexpr int kPer = NT * kChunk / 128;
+    // Thread = weight row and up to 32 tokens: their sums over the blocks, times the two scales of the block.
+    constexpr int kFetch = NT * kChunk / C::kSumThreads;
     const float* sw = p.sw + static_cast<int64_t>(tile) * p.KB + kb0;
-    float next[kPer];
+    float next[kFetch];
     auto fetch = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int e = threadIdx.x + 128 * j, t = e / kChunk, i = c * kChunk + e % kChunk;
+      for (int j = 0; j < kFetch; ++j) {
+        const int e = threadIdx.x + C::kSumThreads * j, t = e / kChunk, i = c * kChunk + e % kChunk;
         next[j] = i < n && tok0 + t < p.T ? p.sa[static_cast<int64_t>(tok0 + t) * p.KB + kb0 + i] * sw[i] : 0.f;
       }
     };
     auto keep = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int e = threadIdx.x + 128 * j;
+      for (int j = 0; j < kFetch; ++j) {
+        const int e = threadIdx.x + C::kSumThreads * j;
         table[((c & 1) * kChunk + e % kChunk) * C::kRow + e / kChunk] = next[j];
       }
     };
-    float acc[NT];
+    const int sub = warp & 3, tok = warp / 4 * C::kPer;
+    float acc[C::kPer];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+    for (int t = 0; t < C::kPer; ++t) acc[t] = 0.f;
     fetch(0);
     keep(0);
-    named_barrier(1, 128);
-    const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
+    named_barrier(1, C::kSumThreads);
+    const uint32_t mine = tmem + (static_cast<uint32_t>(sub) << 21) + tok;
     for (int i = 0; i < n; ++i) {
       const int b = i % C::kAcc, c = i / kChunk, j = i % kChunk;
       if (j == 0 && c > 0) {
         keep(c);                            // the other half: every thread is behind the barrier of its last use
-        named_barrier(1, 128);
+        named_barrier(1, C::kSumThreads);
       }
       if (j == 0) fetch(c + 1);
       ok = ok && warp_wait(acc_full(b), (i / C::kAcc) & 1);
       tmem_fence_after();
-      const float4* scale = reinterpret_cast<const float4*>(table + ((c & 1) * kChunk + j) * C::kRow);
-      constexpr int kLd = NT < 32 ? 16 : 32;
+      const float4* scale = reinterpret_cast<const float4*>(table + ((c & 1) * kChunk + j) * C::kRow + tok);
+      float x[32];
+      if (C::kPer == 32) {
+        tmem_ld32(mine + b * NT, x);
+      } else {
+        tmem_ld16(mine + b * NT, x);
 #pragma unroll
-      for (int t0 = 0; t0 < NT; t0 += kLd) {
-        float part[kLd];
+        for (int u = C::kPer; u < 32; ++u) x[u] = 0.f;
+      }
+      tmem_wait_ld32(x);
+      tmem_fence_before();
+      if (lane == 0) mbar_arrive(acc_free(b));
 #pragma unroll
-        for (int u = 0; u < kLd; u += 16) tmem_ld16(mine + b * NT + t0 + u, part + u);
-        tmem_wait_ld();
-        if (t0 + kLd == NT) {
-          tmem_fence_before();
-          if (lane == 0) mbar_arrive(acc_free(b));
-        }
-#pragma unroll
-        for (int u = 0; u < kLd; u += 4) {
-          const float4 f = scale[(t0 + u) / 4];
-          acc[t0 + u] = fmaf(part[u], f.x, acc[t0 + u]);
-          acc[t0 + u + 1] = fmaf(part[u + 1], f.y, acc[t0 + u + 1]);
-          acc[t0 + u + 2] = fmaf(part[u + 2], f.z, acc[t0 + u + 2]);
-          acc[t0 + u + 3] = fmaf(part[u + 3], f.w, acc[t0 + u + 3]);
-        }
+      for (int u = 0; u < C::kPer; u += 4) {
+        const float4 f = scale[u / 4];
+        fma2(acc[u], acc[u + 1], x[u], x[u + 1], f.x, f.y);
+        fma2(acc[u + 2], acc[u + 3], x[u + 2], x[u + 3], f.z, f.w);
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    const int row = sub * 32 + lane;
     if (p.split == 1) {
-      const int row = tile * kTile + threadIdx.x;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (row < p.N && tok0 + t < p.T) store_out(p, tok0 + t, row, acc[t]);
+      for (int t = 0; t < C::kPer; ++t)
+        if (tile * kTile + row < p.N && tok0 + tok + t < p.T) store_out(p, tok0 + tok + t, tile * kTile + row, acc[t]);
     } else {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) sums[t * kTile + threadIdx.x] = acc[t];
+      for (int t = 0; t < C::kPer; ++t) sums[(tok + t) * kTile + row] = acc[t];
     }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
@@ -242,10 +292,7 @@ __global__ void __launch_bounds__(192, NT <= 64 ? 2 : 1)
       const float4 x = ld_cluster(base + (t * kTile + r) * 4, q);
       v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
     }
-    const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (tile * kTile + r + u < p.N) store_out(p, tok0 + t, tile * kTile + r + u, e[u]);
+    store4(p, tok0 + t, tile * kTile + r, v);
   }
   cluster_sync_all();                       // no CTA ends while another reads its sums
 }
@@ -269,7 +316,8 @@ struct PairCfg {
   static constexpr int kThreads = 384;                                // 4 control warps, 8 that hold the sums
   static constexpr int kRegsCtl = 64, kRegsSum = 216;
   static_assert(128 * kRegsCtl + 256 * kRegsSum <= 384 * 168, "registers of the launch");
-  static_assert(kTok * kOut * 4 <= kStages * kStage, "the sums of a tile fit into the stages");
+  static constexpr uint32_t kSumRow = kOut * 4 + 16;                  // bytes of a token's sums, spread over banks
+  static_assert(kTok * kSumRow <= kStages * kStage, "the sums of a tile fit into the stages");
 };
 
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
@@ -304,31 +352,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                ::"r"(bar), "h"(mask) : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
-                 "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
-                 "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-               : "r"(a));
-}
-// Waits for the loads so far; the values are tied to it, so that nothing reads them earlier.
-__device__ __forceinline__ void tmem_wait_ld32(float* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
-                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
-                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
-               ::"memory");
-}
-// (d0, d1) += (a0, a1) * s
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float s) {
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%0, %1};\n"
-      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
-      : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(s));
-}
-
 // Sixteen outputs of a row in a row; `wide`: 32-byte stores are aligned.
 __device__ __forceinline__ void store16(const LinearParams& p, int64_t t, int n, const float* v, bool wide) {
   if (wide && n + 16 <= p.N) {
@@ -517,10 +540,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           for (int c = 0; c < 128; c += 16) store16(p, t, n0 + c, acc + c, p.wide);
         }
       } else {
-        // [column][token]: every column's 128 tokens in a row. The stages are done with: the last block's products are.
-        float* sums = reinterpret_cast<float*>(sm) + (col * 128) * 128 + sub * 32 + lane;
+        // The stages are done with: the last block's products are.
+        float4* sums = reinterpret_cast<float4*>(sm + (sub * 32 + lane) * C::kSumRow + col * 128 * 4);
 #pragma unroll
-        for (int c = 0; c < 128; ++c) sums[c * 128] = acc[c];
+        for (int c = 0; c < 128; c += 4) sums[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
@@ -539,17 +562,16 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     int tm, tn;
     pair_tile(p, first, tm, tn);
     const int64_t t0 = static_cast<int64_t>(tm) * 2 * C::kTok + half * C::kTok;
-    // a warp takes a column's 128 tokens: 4 per lane
-    for (int c = part * 8 + warp - 4; c < C::kOut; c += p.split * 8) {
+    // a warp takes half a token's row: 4 outputs per lane
+    for (int i = part * 8 + warp - 4; i < 2 * C::kTok; i += p.split * 8) {
+      const int r = i >> 1, c = (i & 1) * 128 + 4 * lane;
+      if (t0 + r >= p.T) break;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int q = 0; q < p.split; ++q) {
-        const float4 x = ld_cluster(base + (c * 128 + 4 * lane) * 4, 2 * q + static_cast<int>(half));
+        const float4 x = ld_cluster(base + r * C::kSumRow + c * 4, 2 * q + static_cast<int>(half));
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
-      const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (t0 + 4 * lane + u < p.T && tn * C::kOut + c < p.N) store_out(p, t0 + 4 * lane + u, tn * C::kOut + c, e[u]);
+      store4(p, t0 + r, tn * C::kOut + c, v);
     }
   }
   cluster_sync_all();                       // no CTA ends while another reads its sums
@@ -588,7 +610,7 @@ static cudaError_t launch_rows(const LinearArgs& a, LinearParams p, cudaStream_t
     if ((s == 1 || s == 2 || s == 4 || s == 8) && s <= p.KB) split = s;
   }
   p.split = split;
-  err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(tiles * split, groups), dim3(192), smem, stream, split, tw, ta, p);
+  err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(tiles * split, groups), dim3(C::kThreads), smem, stream, split, tw, ta, p);
   if (err != cudaSuccess) return err;
   rec->set("fp8_linear rows tokens=%d grid=%dx%d split=%d", NT, tiles * split, groups, split);
   return cudaGetLastError();
@@ -636,6 +658,7 @@ cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, Dispatch
   p.out_stride = a.out_stride;
   p.T = a.T; p.N = a.N; p.KB = (a.K + kTile - 1) / kTile;
   p.f32 = a.out_f32;
+  p.quads = a.out_stride % 4 == 0;                       // (out itself is 16-byte aligned)
   bool pairs = a.T > 128;
   if (const char* form = getenv("MSA_LINEAR_FORM")) pairs = strcmp(form, "pairs") == 0 ? true : strcmp(form, "rows") == 0 ? false : pairs;
   if (pairs) return launch_pairs(a, p, stream, rec);
