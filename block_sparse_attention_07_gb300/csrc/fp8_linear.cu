@@ -28,21 +28,26 @@ struct LinearParams {
   int split;                    // CTAs (pairs) of a cluster, which share a tile's K
   int f32;
   int tiles_m, tiles_n, group;  // pairs: tiles of 256 tokens and of 256 weight rows, token tiles that are walked together
-  int wide, quads;              // rows of the output start on 32-byte boundaries, on those of four values
+  int quads, boxed;             // rows of the output start on boundaries of four values, of 16 bytes
 };
 
+// Asks for a tile of a tensor map in L2. It reads nothing that a later write could make stale: L2 is where all SMs meet.
+__device__ __forceinline__ void prefetch_2d(const void* tmap, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// 16 bytes of another CTA's shared memory.
-__device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
   uint32_t at;
-  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
+  return at;
 }
-
+// Copies shared memory to another CTA's, completed on a barrier there.
+__device__ __forceinline__ void bulk_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
+}
 // 32 columns of the warp's 32 lanes, a lane each.
 __device__ __forceinline__ void tmem_ld32(uint32_t a, float* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -76,6 +81,25 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
       : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(s0), "f"(s1));
 }
 
+// 16 bytes of another CTA's shared memory.
+__device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
+  const uint32_t at = cluster_addr(saddr, rank);
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// Sum of the values at `saddr` in the first `split` CTAs, in this order, all of them on their way together.
+template <int kMost>
+__device__ __forceinline__ float4 sum_cluster(uint32_t saddr, int split) {
+  float4 x[kMost];
+#pragma unroll
+  for (int q = 0; q < kMost; ++q) x[q] = q < split ? ld_cluster(saddr, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v = x[0];
+#pragma unroll
+  for (int q = 1; q < kMost; ++q) { v.x += x[q].x; v.y += x[q].y; v.z += x[q].z; v.w += x[q].w; }
+  return v;
+}
+
 __device__ __forceinline__ void store_out(const LinearParams& p, int64_t t, int n, float v) {
   if (p.f32) static_cast<float*>(p.out)[t * p.out_stride + n] = v;
   else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(v);
@@ -104,7 +128,7 @@ struct RowsCfg {
   static constexpr int kPer = NT < 32 ? NT : 32;                      // a thread's tokens
   static constexpr int kSumThreads = 128 * (NT / kPer), kThreads = kSumThreads + 64;
   static constexpr int kCtas = NT <= 64 ? 2 : 1;                      // per SM
-  static constexpr int kAcc = NT <= 64 ? 4 : 2;                       // blocks' sums in tensor memory
+  static constexpr int kAcc = 4;                                      // blocks' sums in tensor memory
   static constexpr uint32_t kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
   static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
   static constexpr uint32_t kStage = (kTile + NT) * 128;
@@ -127,7 +151,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
   float* table = reinterpret_cast<float*>(sm + C::oTable);
-  float* sums = reinterpret_cast<float*>(sm);                         // [NT][128], over the stages when they are done
+  float* sums = reinterpret_cast<float*>(sm);                         // over the stages when they are done
   const uint32_t bars = base + C::oBars;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
@@ -161,12 +185,15 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   // Behind the allocation: a kernel that starts early could otherwise hold the columns that this CTA waits for, while
   // it waits for this CTA's end.
   griddep_launch_dependents();
-  griddep_wait();
-
   const int rank = static_cast<int>(blockIdx.x) % p.split, tile = static_cast<int>(blockIdx.x) / p.split;
   const int tok0 = static_cast<int>(blockIdx.y) * NT;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.KB) * rank / p.split);
   const int n = static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / p.split) - kb0;
+  // While the kernel before ends: the first weights on their way to L2.
+  if (threadIdx.x == 0)
+    for (int i = 0; i < C::kStages && i < n; ++i) prefetch_2d(&tw, (kb0 + i) * kTile, tile * kTile);
+  griddep_wait();
+
   bool ok = true;
 
   if (warp == kCopyWarp) {
@@ -266,9 +293,10 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     const int row = sub * 32 + lane;
     if (p.split == 1) {
+      const bool in = tile * kTile + row < p.N;
 #pragma unroll
       for (int t = 0; t < C::kPer; ++t)
-        if (tile * kTile + row < p.N && tok0 + tok + t < p.T) store_out(p, tok0 + tok + t, tile * kTile + row, acc[t]);
+        if (in && tok0 + tok + t < p.T) store_out(p, tok0 + tok + t, tile * kTile + row, acc[t]);
     } else {
 #pragma unroll
       for (int t = 0; t < C::kPer; ++t) sums[(tok + t) * kTile + row] = acc[t];
@@ -287,12 +315,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
   for (int i = rank * blockDim.x + threadIdx.x; i < tokens * (kTile / 4); i += p.split * blockDim.x) {
     const int t = i >> 5, r = 4 * (i & 31);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q = 0; q < p.split; ++q) {
-      const float4 x = ld_cluster(base + (t * kTile + r) * 4, q);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-    }
-    store4(p, tok0 + t, tile * kTile + r, v);
+    store4(p, tok0 + t, tile * kTile + r, sum_cluster<8>(base + (t * kTile + r) * 4, p.split));
   }
   cluster_sync_all();                       // no CTA ends while another reads its sums
 }
@@ -303,28 +326,31 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
 // rows in shared memory, so that a block of K costs a CTA 32 KB of copies for 512
 // cycles of tensor core. The first CTA's warp issues for both. Thread = token: one
 // product of scales per block of K serves its 128 outputs. With few tiles, `split`
-// pairs of a cluster share a tile's K and add their sums through distributed shared
-// memory, in rank order; otherwise a pair walks over the tiles.
+// pairs of a cluster share a tile's K, and each finishes every split-th 16 columns
+// from the sums that the others copy there; otherwise a pair walks over the tiles.
 struct PairCfg {
   static constexpr int kTok = 128, kOut = 256;                        // a CTA's tokens, a tile's weight rows
   static constexpr int kStages = 6, kAcc = 2;
   static constexpr uint32_t kStage = 2 * 128 * 128;
-  static constexpr uint32_t oBars = kStages * kStage;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc;
+  static constexpr uint32_t oOut = kStages * kStage, kOutBuf = 32 * 128;   // 128 bytes of 32 rows per warp on their way out
+  static constexpr uint32_t oBars = oOut + 8 * kOutBuf;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
   static constexpr int kThreads = 384;                                // 4 control warps, 8 that hold the sums
-  static constexpr int kRegsCtl = 64, kRegsSum = 216;
+  static constexpr int kRegsCtl = 40, kRegsSum = 232;
   static_assert(128 * kRegsCtl + 256 * kRegsSum <= 384 * 168, "registers of the launch");
-  static constexpr uint32_t kSumRow = kOut * 4 + 16;                  // bytes of a token's sums, spread over banks
-  static_assert(kTok * kSumRow <= kStages * kStage, "the sums of a tile fit into the stages");
+  // With a split, 16 columns are a unit of sums: 4 columns of 128 tokens in a row, four times.
+  static constexpr int kUnits = kOut / 16;
+  static constexpr uint32_t kUnit = 16 * kTok * 4;
 };
-
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-  return at;
+constexpr int pair_share(int part, int split) { return (PairCfg::kUnits - part + split - 1) / split; }   // units of a pair
+constexpr bool pair_sums_fit(int split) {             // those that leave a CTA, and those that come
+  const int most = pair_share(0, split);
+  return 2 * (split - 1) * most * PairCfg::kUnit <= PairCfg::kStages * PairCfg::kStage;
 }
+static_assert(pair_sums_fit(2) && pair_sums_fit(3) && pair_sums_fit(4), "the others' sums fit into the stages");
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -343,6 +369,17 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Shared memory to a tile of a tensor map, rows and columns outside it left out.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               ::"l"(tmap), "r"(x), "r"(y), "r"(src) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until the copies out that this thread has issued have read their shared memory.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ void mma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
                ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
@@ -352,27 +389,23 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                ::"r"(bar), "h"(mask) : "memory");
 }
-// Sixteen outputs of a row in a row; `wide`: 32-byte stores are aligned.
-__device__ __forceinline__ void store16(const LinearParams& p, int64_t t, int n, const float* v, bool wide) {
-  if (wide && n + 16 <= p.N) {
-    if (p.f32) {
-      float* d = static_cast<float*>(p.out) + t * p.out_stride + n;
+// Sixteen outputs of a row in a row.
+__device__ __forceinline__ void store16(const LinearParams& p, int64_t t, int n, const float* v) {
+  if (!p.boxed || n + 16 > p.N) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 8)
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + i), "f"(v[i]), "f"(v[i + 1]),
-                     "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]), "f"(v[i + 7]) : "memory");
-    } else {
-      uint32_t w[8];
+    for (int i = 0; i < 16; ++i)
+      if (n + i < p.N) store_out(p, t, n + i, v[i]);
+  } else if (p.f32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + t * p.out_stride + n);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<__nv_bfloat16*>(p.out) + t * p.out_stride + n),
-                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-    }
-    return;
+    for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + t * p.out_stride + n);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      d[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (n + i < p.N) store_out(p, t, n + i, v[i]);
 }
 
 // Tile number -> its 256 tokens and 256 weight rows: tokens fastest within groups of `group` token tiles, so that the
@@ -387,7 +420,7 @@ __device__ __forceinline__ void pair_tile(const LinearParams& p, int i, int& tm,
 
 __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta,
-                           const __grid_constant__ LinearParams p) {
+                           const __grid_constant__ CUtensorMap to, const __grid_constant__ LinearParams p) {
   using C = PairCfg;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -397,6 +430,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
   auto acc_full = [&](int i) { return bars + 8u * (2 * C::kStages + i); };
   auto acc_free = [&](int i) { return bars + 8u * (2 * C::kStages + C::kAcc + i); };   // (the pair's first CTA)
+  const uint32_t got_bar = bars + 8u * (2 * C::kStages + 2 * C::kAcc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), half = crank & 1u, lead_rank = crank & ~1u;
   const int part = static_cast<int>(crank >> 1);                      // pair of the cluster
@@ -410,6 +444,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       mbar_init(acc_full(i), 1);
       mbar_init(acc_free(i), 16);
     }
+    mbar_init(got_bar, 1);
     fence_mbar_init();
     prefetch_tensormap(&tw);
     prefetch_tensormap(&ta);
@@ -489,15 +524,17 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     }
   } else {
     regs_inc<C::kRegsSum>();
-    const int sub = warp & 3, col = (warp - 4) >> 2;                  // tensor-memory lanes, half of the columns
-    const uint32_t mine = tmem + (static_cast<uint32_t>(sub) << 21) + col * 128;
+    const int sub = warp & 3, g = (warp - 4) >> 2;                    // tensor-memory lanes, half of the columns
+    const uint32_t mine = tmem + (static_cast<uint32_t>(sub) << 21) + g * 128;
     const uint32_t free0 = cluster_addr(acc_free(0), lead_rank);
+    const uint32_t out_at = base + C::oOut + (warp - 4) * C::kOutBuf;
+    const int blocks = (p.N + 127) / 128;
     int n = 0;
     for (int i = first; i < tiles; i += clusters) {
       int tm, tn;
       pair_tile(p, i, tm, tn);
       const int64_t t = static_cast<int64_t>(tm) * 2 * C::kTok + half * C::kTok + sub * 32 + lane;
-      const int blocks = (p.N + 127) / 128, wb = tn * 2 + col < blocks ? tn * 2 + col : blocks - 1;
+      const int wb = tn * 2 + g < blocks ? tn * 2 + g : blocks - 1;   // (a half without weight rows: any scale)
       const float* sa = p.sa + (t < p.T ? t : 0) * p.KB;
       const float* sw = p.sw + static_cast<int64_t>(wb) * p.KB;
       float acc[128];
@@ -524,7 +561,8 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
             tmem_fence_before();
             if (lane == 0) mbar_arrive_relaxed(free0 + 8u * b);
             if (kb + 1 < kb1) {
-              ok = ok && warp_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1);
+              if (!mbar_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1)) ok = false;
+              __syncwarp();
               tmem_fence_after();
               tmem_ld32(mine + (b ^ 1) * C::kOut, x[0]);
             }
@@ -533,48 +571,101 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           for (int u = 0; u < 32; u += 2) fma2(acc[32 * c + u], acc[32 * c + u + 1], x[c & 1][u], x[c & 1][u + 1], f);
         }
       }
-      const int n0 = tn * C::kOut + col * 128;
-      if (p.split == 1) {
+      const int n0 = tn * C::kOut + g * 128;
+      if (p.split == 1 && p.boxed) {
+        // 128 bytes of every row at a time, swizzled as the tensor map has them
+        const int row0 = static_cast<int>(t) - lane;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          const int x0 = n0 + c, chunk = p.f32 ? 0 : (c & 32) / 8;
+          if (p.f32 || (c & 32) == 0) {
+            tma_store_read();
+            __syncwarp();
+          }
+          if (p.f32) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 4)
+              st_shared16(out_at + lane * 128 + (((u >> 2) ^ (lane & 7)) << 4), __float_as_uint(acc[c + u]),
+                          __float_as_uint(acc[c + u + 1]), __float_as_uint(acc[c + u + 2]), __float_as_uint(acc[c + u + 3]));
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; u += 8)
+              st_shared16(out_at + lane * 128 + (((chunk + (u >> 3)) ^ (lane & 7)) << 4), pack_bf16x2(acc[c + u], acc[c + u + 1]),
+                          pack_bf16x2(acc[c + u + 2], acc[c + u + 3]), pack_bf16x2(acc[c + u + 4], acc[c + u + 5]),
+                          pack_bf16x2(acc[c + u + 6], acc[c + u + 7]));
+          }
+          if (p.f32 || (c & 32) != 0) {
+            smem_to_async();
+            __syncwarp();
+            const int at = p.f32 ? x0 : x0 - 32;
+            if (lane == 0 && row0 < p.T && at < p.N) tma_store_2d(&to, at, row0, out_at);
+          }
+        }
+      } else if (p.split == 1) {
         if (t < p.T) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) store16(p, t, n0 + c, acc + c, p.wide);
+          for (int c = 0; c < 128; c += 16) store16(p, t, n0 + c, acc + c);
         }
       } else {
-        // The stages are done with: the last block's products are.
-        float4* sums = reinterpret_cast<float4*>(sm + (sub * 32 + lane) * C::kSumRow + col * 128 * 4);
+        // Unit u of 16 columns belongs to pair u mod split, as its number u / split: the others' sums of it go there, by
+        // one copy of shared memory per CTA.
+        const int most = pair_share(0, p.split), own = pair_share(part, p.split), row = sub * 32 + lane;
+        const uint32_t box = most * C::kUnit, got0 = (p.split - 1) * box;
+        auto unit = [&](int u) { return g * 8 + u; };
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) sums[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        for (int u = 0; u < 8; ++u) {
+          const int q = unit(u) % p.split, k = unit(u) / p.split;
+          if (q != part) {
+            float4* d = reinterpret_cast<float4*>(sm + (q < part ? q : q - 1) * box + k * C::kUnit) + row;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              d[c * C::kTok] = make_float4(acc[16 * u + 4 * c], acc[16 * u + 4 * c + 1], acc[16 * u + 4 * c + 2], acc[16 * u + 4 * c + 3]);
+          }
+        }
+        if (warp == 4 && lane == 0) mbar_arrive_expect_tx(got_bar, (p.split - 1) * own * C::kUnit);
+        smem_to_async();
+        tmem_fence_before();
+        cluster_sync_all();                 // every CTA's sums are written, and the stages behind them free
+        if (warp == 4 && lane < p.split && lane != part) {
+          const int slot = part < lane ? part : part - 1;
+          const uint32_t to = 2 * lane + half;
+          bulk_to_cluster(cluster_addr(base + got0 + slot * box, to), base + (lane < part ? lane : lane - 1) * box,
+                          pair_share(lane, p.split) * C::kUnit, cluster_addr(got_bar, to));
+        }
+        __syncwarp();
+        if (!warp_wait(got_bar, 0)) {
+          ok = false;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int q = unit(u) % p.split, k = unit(u) / p.split;
+            if (q == part) {
+              for (int j = 0; j + 1 < p.split; ++j) {
+                const float4* got = reinterpret_cast<const float4*>(sm + got0 + j * box + k * C::kUnit) + row;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const float4 v = got[c * C::kTok];
+                  acc[16 * u + 4 * c] += v.x; acc[16 * u + 4 * c + 1] += v.y;
+                  acc[16 * u + 4 * c + 2] += v.z; acc[16 * u + 4 * c + 3] += v.w;
+                }
+              }
+              if (t < p.T) store16(p, t, tn * C::kOut + 16 * unit(u), acc + 16 * u);
+            }
+          }
+        }
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
   }
   __syncwarp();
   tmem_fence_before();
-  __syncthreads();
-  cluster_sync_all();                       // the pair is done with both CTAs' columns, barriers and stages
+  if (warp >= 4) tma_store_read();          // (the thread that issued them)
+  if (p.split > 1 && warp < 4) cluster_sync_all();                   // (the other warps have been through it)
+  cluster_sync_all();                       // the cluster is done with all columns, barriers, stages and sums
   if (warp == 1) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
-  if (p.split == 1) return;
-
-  if (warp >= 4) {
-    int tm, tn;
-    pair_tile(p, first, tm, tn);
-    const int64_t t0 = static_cast<int64_t>(tm) * 2 * C::kTok + half * C::kTok;
-    // a warp takes half a token's row: 4 outputs per lane
-    for (int i = part * 8 + warp - 4; i < 2 * C::kTok; i += p.split * 8) {
-      const int r = i >> 1, c = (i & 1) * 128 + 4 * lane;
-      if (t0 + r >= p.T) break;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < p.split; ++q) {
-        const float4 x = ld_cluster(base + r * C::kSumRow + c * 4, 2 * q + static_cast<int>(half));
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-      }
-      store4(p, t0 + r, tn * C::kOut + c, v);
-    }
-  }
-  cluster_sync_all();                       // no CTA ends while another reads its sums
 }
 
 // 2-D map over E4M3 rows [rows][K]: boxes of `box` rows x 128 bytes in the 128-byte swizzle, zeros outside.
@@ -592,61 +683,169 @@ static cudaError_t rows_map(CUtensorMap* map, const void* base, int64_t rows, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NT>
-static cudaError_t launch_rows(const LinearArgs& a, LinearParams p, cudaStream_t stream, DispatchRecord* rec) {
-  using C = RowsCfg<NT>;
-  CUtensorMap tw, ta;
-  cudaError_t err;
-  if ((err = rows_map(&tw, a.w, a.N, a.K, kTile)) != cudaSuccess) return err;
-  if ((err = rows_map(&ta, a.a, a.T, a.K, NT)) != cudaSuccess) return err;
-  constexpr size_t smem = C::kTotal + 1024;
-  err = cudaFuncSetAttribute(fp8_linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (err != cudaSuccess) return err;
-  const int tiles = (a.N + kTile - 1) / kTile, groups = (a.T + NT - 1) / NT;
-  int split = 1;
-  while (split < 8 && split * 2 <= p.KB && static_cast<int64_t>(tiles) * groups * split < device_sm_count()) split *= 2;
-  if (const char* force = getenv("MSA_LINEAR_SPLIT")) {
-    const int s = atoi(force);
-    if ((s == 1 || s == 2 || s == 4 || s == 8) && s <= p.KB) split = s;
-  }
-  p.split = split;
-  err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(tiles * split, groups), dim3(C::kThreads), smem, stream, split, tw, ta, p);
-  if (err != cudaSuccess) return err;
-  rec->set("fp8_linear rows tokens=%d grid=%dx%d split=%d", NT, tiles * split, groups, split);
-  return cudaGetLastError();
+// 2-D map over the output [T] rows of N, `stride` bytes apart: boxes of 32 rows x 128 bytes in the 128-byte swizzle.
+static cudaError_t out_map(CUtensorMap* map, void* base, int64_t T, int64_t N, int64_t stride, bool f32) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t boxes[2] = {f32 ? 32u : 64u, 32};
+  const cuuint32_t ones[2] = {1, 1};
+  const CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                        boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-static cudaError_t launch_pairs(const LinearArgs& a, LinearParams p, cudaStream_t stream, DispatchRecord* rec) {
-  using C = PairCfg;
-  CUtensorMap tw, ta;
-  cudaError_t err;
-  if ((err = rows_map(&tw, a.w, a.N, a.K, 128)) != cudaSuccess) return err;
-  if ((err = rows_map(&ta, a.a, a.T, a.K, 128)) != cudaSuccess) return err;
-  constexpr size_t smem = C::kTotal + 1024;
-  err = cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (err != cudaSuccess) return err;
-  p.tiles_m = (a.T + 2 * C::kTok - 1) / (2 * C::kTok);
-  p.tiles_n = (a.N + C::kOut - 1) / C::kOut;
-  const int64_t rows = (32ll << 20) / (2 * C::kTok * static_cast<int64_t>(a.K));
-  p.group = rows < 1 ? 1 : rows > p.tiles_m ? p.tiles_m : static_cast<int>(rows);
-  p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && (a.out_stride * (a.out_f32 ? 4 : 2)) % 32 == 0;
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
-  const int pairs = device_sm_count() / 2;
-  int split = 1;
-  while (split < 4 && split * 2 <= p.KB && tiles * split * 2 <= pairs) split *= 2;
-  if (const char* force = getenv("MSA_LINEAR_SPLIT")) {
-    const int s = atoi(force);
-    if ((s == 1 || s == 2 || s == 4) && s <= p.KB) split = s;
+// Clusters of n CTAs of a kernel that the device runs at one time, asked once per device. (Fewer than its SMs would
+// hold: 36 clusters of four and 15 of eight CTAs that take an SM each, on 152 SMs.)
+template <typename Kernel>
+static int clusters_at_once(Kernel kernel, int (*cache)[9], int n, int threads, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (cache[dev][n] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int most = 0;
+    if (cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess || most < 1) {
+      cudaGetLastError();
+      most = 1;
+    }
+    cache[dev][n] = most;
   }
-  p.split = split;
-  const int64_t clusters = split > 1 ? tiles : tiles < pairs ? tiles : pairs;
-  err = launch_pdl_cluster(fp8_linear_pair_kernel, dim3(static_cast<unsigned>(clusters * 2 * split)), dim3(C::kThreads), smem, stream,
-                           2 * split, tw, ta, p);
-  if (err != cudaSuccess) return err;
-  rec->set("fp8_linear pairs tiles=%dx%d grid=%lld split=%d", p.tiles_m, p.tiles_n, static_cast<long long>(clusters * 2 * split), split);
-  return cudaGetLastError();
+  return cache[dev][n];
 }
+
+// What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
+// between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 6.5 TB/s. The constants are fits to calls over weights that L2
+// does not hold, within 10 % of nearly all: rows of 128, 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 25.8 / 17.5 / 24.0 us,
+// pairs on 1 / 2 / 3 30.0 / 21.5 / 19.3; 256 x 10,240 x 4,096 rows 28.8 / 33.8, pairs 18.1 / 30.2; 64 x 10,240 x 4,096
+// on 1 / 2 / 3 / 4 CTAs 17.0 / 13.1 / 12.2 / 18.5.
+struct FormCost {
+  float launch, block, sums;
+};
+static float form_us(const FormCost& c, const LinearArgs& a, int64_t clusters, int at_once, int split, bool restart) {
+  const int64_t waves = (clusters + at_once - 1) / at_once;
+  const int KB = (a.K + kTile - 1) / kTile;
+  const float us = static_cast<float>(waves) * (static_cast<float>((KB + split - 1) / split) * c.block + (split > 1 ? c.sums : 0.f));
+  const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 6.5e6f + (split > 1 ? c.sums : 0.f);
+  return c.launch + (us > bytes ? us : bytes) + 2.5f * static_cast<float>(restart ? waves - 1 : 0);
+}
+
+// The environment's number of CTAs, 0 if it says none that fits.
+static int forced_split(int most, int KB) {
+  const char* force = getenv("MSA_LINEAR_SPLIT");
+  const int s = force != nullptr ? atoi(force) : 0;
+  return s >= 1 && s <= most && s <= KB ? s : 0;
+}
+
+template <int NT>
+struct RowsForm {
+  using C = RowsCfg<NT>;
+  static constexpr size_t kSmem = C::kTotal + 1024;
+  static constexpr FormCost kCost = NT == 16 ? FormCost{3.7f, 0.275f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.31f, 1.2f}
+                                  : NT == 64 ? FormCost{3.7f, 0.40f, 2.2f} : FormCost{3.9f, 0.338f, 2.5f};
+  // The number of CTAs that share a tile's K, and what the call then costs.
+  static cudaError_t plan(const LinearArgs& a, int& split, float& us) {
+    static int cache[64][9];
+    const cudaError_t err =
+        cudaFuncSetAttribute(fp8_linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    const int64_t tiles = static_cast<int64_t>((a.N + kTile - 1) / kTile) * ((a.T + NT - 1) / NT);
+    const int KB = (a.K + kTile - 1) / kTile, forced = forced_split(8, KB);
+    split = 0;
+    for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
+      const float t = form_us(kCost, a, tiles, clusters_at_once(fp8_linear_rows_kernel<NT>, cache, s, C::kThreads, kSmem), s, true);
+      if (split == 0 || t <= us) {
+        split = s;
+        us = t;
+      }
+    }
+    return cudaSuccess;
+  }
+  static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
+    CUtensorMap tw, ta;
+    cudaError_t err;
+    if ((err = rows_map(&tw, a.w, a.N, a.K, kTile)) != cudaSuccess) return err;
+    if ((err = rows_map(&ta, a.a, a.T, a.K, NT)) != cudaSuccess) return err;
+    const int64_t tiles = (a.N + kTile - 1) / kTile, groups = (a.T + NT - 1) / NT;
+    if (groups > 65535) return cudaErrorInvalidValue;
+    p.split = split;
+    err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups)),
+                             dim3(C::kThreads), kSmem, stream, split, tw, ta, p);
+    if (err != cudaSuccess) return err;
+    rec->set("fp8_linear rows tokens=%d grid=%lldx%lld split=%d", NT, static_cast<long long>(tiles * split),
+             static_cast<long long>(groups), split);
+    return cudaGetLastError();
+  }
+};
+
+template <int NT>
+static cudaError_t launch_rows(const LinearArgs& a, const LinearParams& p, cudaStream_t stream, DispatchRecord* rec) {
+  int split;
+  float us;
+  const cudaError_t err = RowsForm<NT>::plan(a, split, us);
+  return err != cudaSuccess ? err : RowsForm<NT>::launch(a, p, split, stream, rec);
+}
+
+struct PairForm {
+  using C = PairCfg;
+  static constexpr size_t kSmem = C::kTotal + 1024;
+  static int64_t tiles(const LinearArgs& a) {
+    return static_cast<int64_t>((a.T + 2 * C::kTok - 1) / (2 * C::kTok)) * ((a.N + C::kOut - 1) / C::kOut);
+  }
+  static int at_once(int split) {
+    static int cache[64][9];
+    return clusters_at_once(fp8_linear_pair_kernel, cache, 2 * split, C::kThreads, kSmem);
+  }
+  static cudaError_t plan(const LinearArgs& a, int& split, float& us) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    const int KB = (a.K + kTile - 1) / kTile, forced = forced_split(4, KB);
+    split = 0;
+    for (int s = forced ? forced : 1; s <= (forced ? forced : 4) && s <= KB; ++s) {
+      // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
+      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 4.f : 6.f}, a, tiles(a), at_once(s), s, s > 1);
+      t += 1.1f * static_cast<float>((tiles(a) + at_once(s) - 1) / at_once(s));
+      if (split == 0 || t < us) {
+        split = s;
+        us = t;
+      }
+    }
+    return cudaSuccess;
+  }
+  static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
+    CUtensorMap tw, ta, to;
+    cudaError_t err;
+    if ((err = rows_map(&tw, a.w, a.N, a.K, 128)) != cudaSuccess) return err;
+    if ((err = rows_map(&ta, a.a, a.T, a.K, 128)) != cudaSuccess) return err;
+    const int64_t stride = a.out_stride * (a.out_f32 ? 4 : 2);
+    p.boxed = stride % 16 == 0 && stride < (1ll << 40);
+    memset(&to, 0, sizeof(to));
+    if (p.boxed && (err = out_map(&to, a.out, a.T, a.N, stride, a.out_f32)) != cudaSuccess) return err;
+    p.tiles_m = (a.T + 2 * C::kTok - 1) / (2 * C::kTok);
+    p.tiles_n = (a.N + C::kOut - 1) / C::kOut;
+    const int64_t rows = (32ll << 20) / (2 * C::kTok * static_cast<int64_t>(a.K));
+    p.group = rows < 1 ? 1 : rows > p.tiles_m ? p.tiles_m : static_cast<int>(rows);
+    if (tiles(a) > INT32_MAX / 16) return cudaErrorInvalidValue;
+    p.split = split;
+    const int64_t clusters = split > 1 || tiles(a) < at_once(1) ? tiles(a) : at_once(1);
+    err = launch_pdl_cluster(fp8_linear_pair_kernel, dim3(static_cast<unsigned>(clusters * 2 * split)), dim3(C::kThreads), kSmem,
+                             stream, 2 * split, tw, ta, to, p);
+    if (err != cudaSuccess) return err;
+    rec->set("fp8_linear pairs tiles=%dx%d grid=%lld split=%d", p.tiles_m, p.tiles_n, static_cast<long long>(clusters * 2 * split), split);
+    return cudaGetLastError();
+  }
+};
 
 cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, DispatchRecord* rec) {
   LinearParams p;
@@ -659,13 +858,23 @@ cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, Dispatch
   p.T = a.T; p.N = a.N; p.KB = (a.K + kTile - 1) / kTile;
   p.f32 = a.out_f32;
   p.quads = a.out_stride % 4 == 0;                       // (out itself is 16-byte aligned)
-  bool pairs = a.T > 128;
-  if (const char* form = getenv("MSA_LINEAR_FORM")) pairs = strcmp(form, "pairs") == 0 ? true : strcmp(form, "rows") == 0 ? false : pairs;
-  if (pairs) return launch_pairs(a, p, stream, rec);
-  if (a.T <= 16) return launch_rows<16>(a, p, stream, rec);
-  if (a.T <= 32) return launch_rows<32>(a, p, stream, rec);
-  if (a.T <= 64) return launch_rows<64>(a, p, stream, rec);
-  return launch_rows<128>(a, p, stream, rec);
+  // Up to 64 tokens weights as M: the tokens' columns are what fills up. Above, what costs less.
+  const char* form = getenv("MSA_LINEAR_FORM");
+  const bool pairs_only = form != nullptr && strcmp(form, "pairs") == 0, rows_only = form != nullptr && strcmp(form, "rows") == 0;
+  if (!pairs_only) {
+    if (a.T <= 16) return launch_rows<16>(a, p, stream, rec);
+    if (a.T <= 32) return launch_rows<32>(a, p, stream, rec);
+    if (a.T <= 64) return launch_rows<64>(a, p, stream, rec);
+  }
+  int rows_split = 0, pair_split = 0;
+  float rows_us = 0.f, pair_us = 0.f;
+  cudaError_t err;
+  // (more groups of 128 tokens than a grid has in y: pairs)
+  const bool rows_fit = (a.T + 127) / 128 <= 65535;
+  if (!pairs_only && rows_fit && (err = RowsForm<128>::plan(a, rows_split, rows_us)) != cudaSuccess) return err;
+  if ((pairs_only || !rows_only || !rows_fit) && (err = PairForm::plan(a, pair_split, pair_us)) != cudaSuccess) return err;
+  if (pair_split == 0 || (rows_split != 0 && rows_us <= pair_us)) return RowsForm<128>::launch(a, p, rows_split, stream, rec);
+  return PairForm::launch(a, p, pair_split, stream, rec);
 }
 
 }  // namespace msa

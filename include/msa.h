@@ -526,9 +526,10 @@ msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x
  * rows of N, out_stride >= N elements apart; what lies between N and out_stride is
  * left as it is. K: a multiple of 16. T, N and K up to 2^24, T * K and N * K below
  * 2^40. a, w and out 16-byte aligned, scales 4-byte. out overlaps no input.
- * num_tokens = 0 launches nothing. MSA_LINEAR_SPLIT=1, 2, 4 or 8 in the
- * environment (read on every call) forces the number of CTAs that share a tile's
- * K where few tokens are projected.
+ * num_tokens = 0 launches nothing. MSA_LINEAR_FORM=rows or pairs in the
+ * environment (read on every call) forces tiles with the weights or the tokens as
+ * the product's rows, MSA_LINEAR_SPLIT=1 to 8 (pairs: 4) the number of CTAs (pairs
+ * of them) that share a tile's K; other values have no effect.
  */
 msa_status_t msa_fp8_linear(int32_t num_tokens, int32_t out_features, int32_t in_features, const void* a,
                             const float* a_scales, const void* w, const float* w_scales, void* out,
