@@ -697,8 +697,9 @@ static cudaError_t out_map(CUtensorMap* map, void* base, int64_t T, int64_t N, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Clusters of n CTAs of a kernel that the device runs at one time, asked once per device. (Fewer than its SMs would
-// hold: 36 clusters of four and 15 of eight CTAs that take an SM each, on 152 SMs.)
+// Clusters of n CTAs of a kernel that the device runs at one time, asked once per device: fewer than its SMs would
+// hold, 36 clusters of four and 15 of eight CTAs on 152 SMs. (It counts one CTA per SM for these kernels; where two
+// fit, there is room for twice as many.)
 template <typename Kernel>
 static int clusters_at_once(Kernel kernel, int (*cache)[9], int n, int threads, size_t smem) {
   int dev = 0;
@@ -763,7 +764,8 @@ struct RowsForm {
     const int KB = (a.K + kTile - 1) / kTile, forced = forced_split(8, KB);
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
-      const float t = form_us(kCost, a, tiles, clusters_at_once(fp8_linear_rows_kernel<NT>, cache, s, C::kThreads, kSmem), s, true);
+      const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT>, cache, s, C::kThreads, kSmem);
+      const float t = form_us(kCost, a, tiles, at_once, s, true);
       if (split == 0 || t <= us) {
         split = s;
         us = t;

@@ -3,7 +3,7 @@
 Bounds. h is one fp32 addition (2^-24). The mean of squares is a sum of at most 64 additions deep (8 passes x 8 values
 in two chains, then ten exchange steps) of squares within 2^-24, so the root is off by at most 33 * 2^-24; root,
 division and three products add five: |y - exact| <= 48 * 2^-24 |y|. bf16 adds 2^-8 |y|. A scale is one division of the
-group's largest |y|: 50 * 2^-24. A code's value is y over the scale, within one division and half a step of E4M3: 2^-4
+group's largest |y|: 50 * 2^-24. A code's value is y over the scale, within a reciprocal, a product and half a step of E4M3: 2^-4
 relative, or 2^-10 where it is subnormal."""
 import numpy as np
 import pytest
@@ -72,7 +72,8 @@ class Case:
 
 @pytest.mark.parametrize("res", [None, "bf16", "f32"])
 @pytest.mark.parametrize("T,W", [(1, 16), (1, 4096), (2, 112), (3, 128), (5, 144), (7, 1040), (300, 272), (333, 5008), (320, 8192),
-                                 (2, 16384), (310, 16384), (9, 12304), (1, 8208)])
+                                 (2, 16384), (310, 16384), (9, 12304), (1, 8208), (2050, 4096), (700, 12304),
+                                 (600, 16384), (1900, 4432)])
 def test_sizes(T, W, res):
     Case(T, W, res, seed=T + W).run()
 
