@@ -18,7 +18,11 @@
 //
 // Bound by the rows' bytes: as many as possible are kept in flight, the queries of
 // a token (contiguous, whatever the token's stride) by bulk copies into a ring per
-// warp, with keys and values done while the first of them arrive.
+// warp, with keys and values done while the first of them arrive. 8,191 tokens, 64 +
+// 4 + 4 heads, FP8 cache: 52.9 us, 5.5 TB/s (82 % of a copy's rate); 16,000 tokens
+// 94.7 us (89 %); 64 tokens 4.3 us, the host's time per launch. With fewer heads what
+// comes before a warp's queries (position, sines, slot, keys) shows: 16 + 1 + 1 heads
+// 27.8 us for 8,191 tokens.
 //
 // Phases: freq / 2 pi modulo one is held as a 64-bit fraction of a turn, so that
 // position times it, modulo one turn, is one integer product: 2^-53 relative to
@@ -30,7 +34,7 @@
 
 namespace msa {
 
-constexpr int kRopeWarps = 2, kRopeCtas = 14;     // warps per CTA, CTAs per SM
+constexpr int kRopeWarps = 1, kRopeCtas = 28;     // warps per CTA, CTAs per SM: 8,191 tokens 52.9 us, 2 x 14 54.7, 4 x 7 55.1
 constexpr int kRopeSlots = 6;                     // groups of four queries in flight per warp
 constexpr uint32_t kRopeGroup = 4 * kDim * 2;     // their bytes
 
@@ -50,6 +54,7 @@ struct RopeParams {
   const float* wiq;
   const float* wik;
   float eps, gain;
+  float low;                   // mean squares below it are too small beside eps
   int H, I, R;
   int parts;                   // warps per token
   uint64_t turn[kDim / 2];     // freq / 2 pi, in units of 2^-64 of a turn
@@ -120,7 +125,7 @@ __device__ __forceinline__ void write_idx(const InsertParams& p, int64_t row, co
   if (l == 0) p.idx_scale[row] = s;
 }
 
-template <bool kPairs>        // interleaved pairs (2i, 2i + 1)
+template <bool kPairs, bool kNorm>        // interleaved pairs (2i, 2i + 1); norms
 __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_kernel(const __grid_constant__ RopeParams pp) {
   __shared__ alignas(128) uint8_t ring_rows[kRopeWarps * kRopeSlots * kRopeGroup];
   __shared__ alignas(16) uint8_t turn_rows[kRopeWarps * kRopeGroup];
@@ -191,21 +196,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
   if (slot >= p.num_slots && part == 0 && lane == 0) set_flag(p.flags, MSA_FLAG_BAD_SLOT);
 
   auto weights = [&](const float* wv, float (&w)[16]) {
-    if (wv == nullptr) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = 1.f;
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 f = *reinterpret_cast<const float4*>(wv + (i < 2 ? 8 * ca + 4 * i : 8 * cb + 4 * (i - 2)));
       w[4 * i] = f.x; w[4 * i + 1] = f.y; w[4 * i + 2] = f.z; w[4 * i + 3] = f.w;
     }
   };
-  const bool norm = pp.wq != nullptr;
-  // Divides the row (8 lanes) by sqrt(mean of its squares + eps); the whole warp calls it.
-  auto normalise = [&](float (&x)[16]) {
-    if (!norm) return;
+  // 1 / sqrt(mean of the row's squares + eps), by its 8 lanes; the whole warp calls it. Squares that leave fp32's range:
+  // the row is scaled by a power of two.
+  auto row_scale = [&](float (&x)[16]) {
     auto squares = [&]() {
       float s2[2] = {0.f, 0.f};
 #pragma unroll
@@ -216,17 +215,40 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
       return ss * (1.0f / kDim);
     };
     float ms = squares(), eps = pp.eps;
-    // squares that leave fp32's range: the same with values scaled by a power of two
-    const float f = !(ms <= 0x1p120f) ? 0x1p-80f : ms + eps < 0x1p-100f ? 0x1p80f : 1.f;
-    if (__any_sync(0xffffffffu, f != 1.f)) {
+    if (__any_sync(0xffffffffu, !(ms <= 0x1p120f) || ms < pp.low)) {
+      const float f = !(ms <= 0x1p120f) ? 0x1p-80f : ms < pp.low ? 0x1p80f : 1.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] *= f;
       eps = eps * f * f;
       ms = squares();
     }
-    const float rinv = rsqrtf(ms + eps);
+    return rsqrtf(ms + eps);
+  };
+  // The row turned: with a norm its weights are folded into cosines and sines (wa cos, wb sin, wa sin, wb cos), so that a
+  // pair is four products and two scalings; without one, dims that pass are kept from their neighbours' infinities.
+  auto turned = [&](const float (&x)[16], const float (&k)[4][8], float rinv, float (&y)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= rinv;
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[ea(i)], b = x[eb(i)];
+      if (kNorm) {
+        y[ea(i)] = (a * k[0][i] - b * k[1][i]) * rinv;
+        y[eb(i)] = (a * k[2][i] + b * k[3][i]) * rinv;
+      } else {
+        const bool on = kPairs && i >= 4 ? turn_b : turn_a;
+        y[ea(i)] = on ? a * cs[i] - b * sn[i] : a;
+        y[eb(i)] = on ? a * sn[i] + b * cs[i] : b;
+      }
+    }
+  };
+  auto folded = [&](const float* wv, float (&k)[4][8]) {
+    if (!kNorm) return;
+    float w[16];
+    weights(wv, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      k[0][i] = w[ea(i)] * cs[i]; k[1][i] = w[eb(i)] * sn[i];
+      k[2][i] = w[ea(i)] * sn[i]; k[3][i] = w[eb(i)] * cs[i];
+    }
   };
 
   // While the queries are on their way, the rows behind them: any last queries, keys, values, index rows
@@ -252,20 +274,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
       float x[16];
       unpack8(lo, x);
       unpack8(hi, x + 8);
-      normalise(x);
+      const float rinv = kNorm ? row_scale(x) : 1.f;
       if (kind != 2) {
-        float w[16];
-        weights(wv, w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= w[i];
-        float y[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool on = kPairs && i >= 4 ? turn_b : turn_a;
-          const float a = x[ea(i)], b = x[eb(i)];
-          y[ea(i)] = on ? a * cs[i] - b * sn[i] : a;
-          y[eb(i)] = on ? a * sn[i] + b * cs[i] : b;
-        }
+        float k[4][8], y[16];
+        folded(wv, k);
+        turned(x, k, rinv, y);
         // rounded to bf16 here: what the outputs hold and the caches quantise
         lo = pack8(y);
         hi = pack8(y + 8);
@@ -292,8 +305,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
 
   // Most rows are queries, four at a time
   if (part >= q_passes) return;
-  float w[16];
-  weights(pp.wq, w);
+  float k[4][8];
+  folded(pp.wq, k);
   uint16_t* dst = pp.q_out + (t * nq + 4 * part + (lane >> 3)) * kDim;
   const int64_t hop = 4ll * pp.parts * kDim;
   int buf = 0;
@@ -312,16 +325,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
     float x[16], y[16];
     unpack8(ld_shared16(at + 16 * ca), x);
     unpack8(ld_shared16(at + 16 * cb), x + 8);
-    normalise(x);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= w[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool on = kPairs && i >= 4 ? turn_b : turn_a;
-      const float a = x[ea(i)], b = x[eb(i)];
-      y[ea(i)] = on ? a * cs[i] - b * sn[i] : a;
-      y[eb(i)] = on ? a * sn[i] + b * cs[i] : b;
-    }
+    turned(x, k, kNorm ? row_scale(x) : 1.f, y);
     *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(y);
     *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8(y + 8);
     dst += hop;
@@ -348,6 +352,7 @@ cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, Dispa
   pp.wq = a.wq; pp.wk = a.wk; pp.wiq = a.wiq; pp.wik = a.wik;
   pp.eps = a.eps;
   pp.gain = a.rope->gain;
+  pp.low = a.eps < 0x1p-100f ? 0x1p-100f : 0.f;
   pp.H = a.H;
   pp.I = a.I;
   pp.R = a.rope->rotary_dim;
@@ -359,16 +364,18 @@ cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, Dispa
   }
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
   const int passes = (rows + 3) / 4;
-  // Warps per token: about 16 warps per SM for few tokens, two per token for some, one for many.
+  // Warps per token: about 16 warps per SM for few tokens (as the multi-axis kernel, which measured it), two per token
+  // for some, one from 32 tokens per SM on (8,191 tokens 55.3 us, two 57.1; 16,000 tokens the same).
   const int64_t sms = device_sm_count();
-  int64_t parts = a.ins.T >= 64 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
-  if (parts < 2 && a.ins.T < 64 * sms) parts = 2;
+  int64_t parts = a.ins.T >= 32 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
+  if (parts < 2 && a.ins.T < 32 * sms) parts = 2;
   if (parts > passes) parts = passes;
   pp.parts = static_cast<int>(parts);
   const int64_t grid = (a.ins.T * parts + kRopeWarps - 1) / kRopeWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const bool pairs = a.rope->layout == MSA_ROPE_INTERLEAVED;
-  const cudaError_t err = launch_pdl(pairs ? qkv_rope_insert_kernel<true> : qkv_rope_insert_kernel<false>,
+  const cudaError_t err = launch_pdl(pairs ? (a.wq ? qkv_rope_insert_kernel<true, true> : qkv_rope_insert_kernel<true, false>)
+                                           : (a.wq ? qkv_rope_insert_kernel<false, true> : qkv_rope_insert_kernel<false, false>),
                                      dim3(static_cast<unsigned>(grid)), dim3(32 * kRopeWarps), 0, stream, pp);
   if (err != cudaSuccess) return err;
   rec->set("qkv_rope_insert %s%s %s%s dims=%d grid=%lld block=%d warps_per_token=%d heads=%d+%d+%d",
