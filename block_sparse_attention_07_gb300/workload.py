@@ -307,6 +307,75 @@ class DeviceWorkload:
         msa.paged_gqa_decode(self.dims, self.q, self.cache, self.block_table_d, self.seq_lens_d, self.out, self.lse,
                              self._dense_ws, self.flags, st)
 
+    # ------------------------------------- from hidden states to hidden states --
+    def _layer_state(self, hidden):
+        """Synthetic FP8 weights of the layer's projections (from the workload's seed) and the buffers of ``hidden_step``."""
+        st = getattr(self, "_layer", None)
+        if st is None or st["hidden"] != hidden:
+            w, dev = self.w, self.device
+            T, H, G, I, D = len(self.which) * w.q_len, w.n_heads, w.n_kv_heads, w.n_idx_heads, w.head_dim
+            gen = torch.Generator(device=dev)
+            gen.manual_seed(w.seed)
+            heads = H + 2 * G + (2 * I if self.has_index else 0)
+            groups = lambda n: (n + 127) // 128
+
+            def weight(n, k):
+                codes = torch.empty((n, k), dtype=torch.float32, device=dev).normal_(0.0, 64.0, generator=gen)
+                scales = torch.empty((groups(n), groups(k)), dtype=torch.float32, device=dev)
+                scales.uniform_(0.5, 1.5, generator=gen).mul_(k ** -0.5 / 64.0)
+                return codes.clamp_(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8), scales
+
+            def rows(width):
+                return (torch.empty((T, width), dtype=torch.uint8, device=dev),
+                        torch.empty((T, groups(width)), dtype=torch.float32, device=dev))
+
+            pro = self._prologue_state()
+            packed = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
+            cut = [H, G, G] + ([I, I] if self.has_index else [])
+            st = self._layer = dict(
+                hidden=hidden, norm=1.0 + 0.1 * torch.randn(hidden, generator=gen, device=dev), w_in=weight(heads * D, hidden),
+                w_out=weight(hidden, H * D), x8=rows(hidden), o8=rows(H * D), packed=packed,
+                parts=list(packed.split(cut, 1)) + [None] * (5 - len(cut)), rope=msa.make_rope(D, synth.PROLOGUE_THETA),
+                positions=pro["positions"], nr=pro["nr"], q=pro["q_out"], q_idx=pro["idx_q_out"] if self.has_index else None)
+            if not self.has_index:
+                st["ws"] = torch.empty(msa.paged_gqa_workspace_size(self.dims, self.cache.dtype), dtype=torch.uint8, device=dev)
+        return st
+
+    def hidden_step(self, x, residual, y, stream=None, rope=None):
+        """One decode step of a layer's attention half, from hidden states to hidden states: the residual's addition and
+        norm of ``x`` (bf16 [T, hidden], T the step's tokens; ``residual``, bf16 or fp32, is updated in place), the packed
+        FP8 projection, norm + rotary embedding + insert on its rows, attention (block-sparse; over every cached token
+        for a layer without an index cache), and the output projection into ``y`` (bf16 or fp32 [T, hidden]), which the
+        next norm adds. ``rope`` (``msa.make_rope``) replaces the workload's own rotary embedding. As with the other
+        steps, one at a time: the buffers are the workload's."""
+        if self.has_index and self.w.idx_dtype == "f32":
+            raise ValueError("hidden_step takes an FP8 or NVFP4 index cache")
+        st = self._layer_state(int(x.shape[1]))
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        msa.add_norm_quant(x, st["norm"], residual=residual, residual_out=residual, codes=st["x8"][0], scales=st["x8"][1],
+                           eps=synth.PROLOGUE_EPS, stream=s)
+        packed = st["packed"]
+        msa.fp8_linear(*st["x8"], *st["w_in"], packed.view(packed.shape[0], -1), self.flags, stream=s)
+        q, k, v, iq, ik = st["parts"]
+        msa.qkv_rope_insert(self.dims, q, k, v, iq, ik, st["positions"], self.new_slots, st["nr"], rope or st["rope"], st["q"],
+                            st["q_idx"], self.cache, self.idx_cache, self.flags, stream=s)
+        q = st["q"].view(self.out.shape)
+        if self.has_index:
+            msa.index_score(self.dims, st["q_idx"], msa.BF16, self.idx_cache, self.block_table_d, self.seq_lens_d, self.scores,
+                            self.flags, s)
+            if self.fuses_selection:
+                msa.select_sparse_gqa_decode(self.dims, q, self.cache, self.block_table_d, self.seq_lens_d, self.scores,
+                                             self.selected, self.out, self.lse, self.workspace, self.flags, s)
+            else:
+                msa.select_blocks(self.dims, self.scores, self.seq_lens_d, self.selected, self.flags, s)
+                msa.sparse_gqa_decode(self.dims, q, self.cache, self.block_table_d, self.seq_lens_d, self.selected, self.out,
+                                      self.lse, self.workspace, self.flags, s)
+        else:
+            msa.paged_gqa_decode(self.dims, q, self.cache, self.block_table_d, self.seq_lens_d, self.out, self.lse, st["ws"],
+                                 self.flags, s)
+        msa.add_norm_quant(self.out.view(st["o8"][0].shape), None, codes=st["o8"][0], scales=st["o8"][1], stream=s)
+        msa.fp8_linear(*st["o8"], *st["w_out"], y, self.flags, stream=s)
+
     def capture(self, fn) -> torch.cuda.CUDAGraph:
         """Captures ``fn(stream)`` (a step of this workload) into a CUDA graph;
         ``graph.replay()`` then reruns its kernels with the same buffers."""
