@@ -123,14 +123,16 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
 // Weights as M. A CTA has 128 weight rows and up to NT tokens as the product's N,
 // so that few tokens waste nothing but columns; the CTAs of a cluster share the
 // tile's K and add their sums through distributed shared memory, in rank order.
-template <int NT>
+// Up to 64 tokens there are two sizes: two CTAs per SM, or one with as much memory for copies in flight. kDeep: the latter.
+template <int NT, bool kDeep>
 struct RowsCfg {
   static constexpr int kPer = NT < 32 ? NT : 32;                      // a thread's tokens
   static constexpr int kSumThreads = 128 * (NT / kPer), kThreads = kSumThreads + 64;
-  static constexpr int kCtas = NT <= 64 ? 2 : 1;                      // per SM
+  static constexpr int kCtas = kDeep ? 1 : 2;                         // per SM
   static constexpr int kAcc = 4;                                      // blocks' sums in tensor memory
   static constexpr uint32_t kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
-  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
+  static constexpr int kStages = NT == 128 ? 6 : kDeep ? (NT == 16 ? 11 : NT == 32 ? 10 : 8) : NT == 64 ? 4 : 5;
+  static_assert(NT <= 64 || kDeep, "128 tokens fill an SM");
   static constexpr uint32_t kStage = (kTile + NT) * 128;
   static constexpr int kRow = NT + 4;                                 // floats of a scale row: 16-byte steps, spread over banks
   static constexpr uint32_t oTable = kStages * kStage;
@@ -142,11 +144,11 @@ struct RowsCfg {
   static_assert(kCols * kCtas <= 512, "tensor memory");
 };
 
-template <int NT>
-__global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
+template <int NT, bool kDeep>
+__global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDeep>::kCtas)
     fp8_linear_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap ta,
                            const __grid_constant__ LinearParams p) {
-  using C = RowsCfg<NT>;
+  using C = RowsCfg<NT, kDeep>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -700,11 +702,13 @@ static cudaError_t out_map(CUtensorMap* map, void* base, int64_t T, int64_t N, i
 // Clusters of n CTAs of a kernel that the device runs at one time, asked once per device: fewer than its SMs would
 // hold, 36 clusters of four and 15 of eight CTAs on 152 SMs. (It counts one CTA per SM for these kernels; where two
 // fit, there is room for twice as many.)
+struct AtOnce {
+  int of[64][9];
+};
 template <typename Kernel>
-static int clusters_at_once(Kernel kernel, int (*cache)[9], int n, int threads, size_t smem) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (cache[dev][n] == 0) {
+static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int threads, size_t smem) {
+  if (dev < 0) return 1;
+  if (cache.of[dev][n] == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n);
     cfg.blockDim = dim3(threads);
@@ -716,20 +720,24 @@ static int clusters_at_once(Kernel kernel, int (*cache)[9], int n, int threads, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int most = 0;
-    if (cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess || most < 1) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess || most < 1) {
       cudaGetLastError();
       most = 1;
     }
-    cache[dev][n] = most;
+    cache.of[dev][n] = most;
   }
-  return cache[dev][n];
+  return cache.of[dev][n];
 }
 
 // What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
-// between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 6.5 TB/s. The constants are fits to calls over weights that L2
-// does not hold, within 10 % of nearly all: rows of 128, 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 25.8 / 17.5 / 24.0 us,
-// pairs on 1 / 2 / 3 30.0 / 21.5 / 19.3; 256 x 10,240 x 4,096 rows 28.8 / 33.8, pairs 18.1 / 30.2; 64 x 10,240 x 4,096
-// on 1 / 2 / 3 / 4 CTAs 17.0 / 13.1 / 12.2 / 18.5.
+// between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
+// fits to calls over weights that L2 does not hold, within 10 % of nearly all (us):
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 25.8 / 17.5 / 24.0; pairs on 1 / 2 / 3 30.0 / 21.5 / 19.3;
+//   256 x 10,240 x 4,096: rows 28.8 / 33.8, pairs 18.1 / 30.2; 512 x 4,096 x 8,192: rows 26.0 / 34.1, pairs 29.9 / 21.8;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, two per SM 17.1 / 13.1 / 12.2 / 18.5, one per SM 13.3 / 19.4 / 17.6;
+//   64 x 4,096 x 8,192 on 3 / 4 / 6 / 8, two per SM 13.8 / 12.6 / 12.3 / 11.6, one per SM 11.9 / 10.8 / 17.2 / 22.6;
+//   1 x 1,280 x 4,096 on 8 4.6 and 4.2; 64 x 28,672 x 4,096 on 1 22.9 and 28.5.
 struct FormCost {
   float launch, block, sums;
 };
@@ -737,41 +745,32 @@ static float form_us(const FormCost& c, const LinearArgs& a, int64_t clusters, i
   const int64_t waves = (clusters + at_once - 1) / at_once;
   const int KB = (a.K + kTile - 1) / kTile;
   const float us = static_cast<float>(waves) * (static_cast<float>((KB + split - 1) / split) * c.block + (split > 1 ? c.sums : 0.f));
-  const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 6.5e6f + (split > 1 ? c.sums : 0.f);
+  const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 7.0e6f + (split > 1 ? c.sums : 0.f);
   return c.launch + (us > bytes ? us : bytes) + 2.5f * static_cast<float>(restart ? waves - 1 : 0);
 }
 
-// The environment's number of CTAs, 0 if it says none that fits.
-static int forced_split(int most, int KB) {
-  const char* force = getenv("MSA_LINEAR_SPLIT");
-  const int s = force != nullptr ? atoi(force) : 0;
-  return s >= 1 && s <= most && s <= KB ? s : 0;
-}
-
-template <int NT>
+template <int NT, bool kDeep>
 struct RowsForm {
-  using C = RowsCfg<NT>;
+  using C = RowsCfg<NT, kDeep>;
   static constexpr size_t kSmem = C::kTotal + 1024;
-  static constexpr FormCost kCost = NT == 16 ? FormCost{3.7f, 0.275f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.31f, 1.2f}
-                                  : NT == 64 ? FormCost{3.7f, 0.40f, 2.2f} : FormCost{3.9f, 0.338f, 2.5f};
+  static constexpr FormCost kCost = NT == 128 ? FormCost{3.9f, 0.338f, 2.5f}
+                                  : kDeep ? (NT == 16 ? FormCost{3.7f, 0.225f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.27f, 1.0f} : FormCost{3.7f, 0.29f, 2.0f})
+                                          : (NT == 16 ? FormCost{3.7f, 0.275f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.31f, 1.2f} : FormCost{3.7f, 0.40f, 2.2f});
   // The number of CTAs that share a tile's K, and what the call then costs.
-  static cudaError_t plan(const LinearArgs& a, int& split, float& us) {
-    static int cache[64][9];
-    const cudaError_t err =
-        cudaFuncSetAttribute(fp8_linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (err != cudaSuccess) return err;
+  static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
+    static AtOnce cache;
     const int64_t tiles = static_cast<int64_t>((a.N + kTile - 1) / kTile) * ((a.T + NT - 1) / NT);
-    const int KB = (a.K + kTile - 1) / kTile, forced = forced_split(8, KB);
+    const int KB = (a.K + kTile - 1) / kTile;
+    forced = forced <= KB ? forced : 0;
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
-      const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT>, cache, s, C::kThreads, kSmem);
+      const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem);
       const float t = form_us(kCost, a, tiles, at_once, s, true);
       if (split == 0 || t <= us) {
         split = s;
         us = t;
       }
     }
-    return cudaSuccess;
   }
   static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta;
@@ -781,21 +780,24 @@ struct RowsForm {
     const int64_t tiles = (a.N + kTile - 1) / kTile, groups = (a.T + NT - 1) / NT;
     if (groups > 65535) return cudaErrorInvalidValue;
     p.split = split;
-    err = launch_pdl_cluster(fp8_linear_rows_kernel<NT>, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups)),
+    err = cudaFuncSetAttribute(fp8_linear_rows_kernel<NT, kDeep>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    err = launch_pdl_cluster(fp8_linear_rows_kernel<NT, kDeep>, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups)),
                              dim3(C::kThreads), kSmem, stream, split, tw, ta, p);
     if (err != cudaSuccess) return err;
-    rec->set("fp8_linear rows tokens=%d grid=%lldx%lld split=%d", NT, static_cast<long long>(tiles * split),
+    rec->set("fp8_linear rows tokens=%d%s grid=%lldx%lld split=%d", NT, kDeep && NT <= 64 ? " deep" : "", static_cast<long long>(tiles * split),
              static_cast<long long>(groups), split);
     return cudaGetLastError();
   }
 };
 
 template <int NT>
-static cudaError_t launch_rows(const LinearArgs& a, const LinearParams& p, cudaStream_t stream, DispatchRecord* rec) {
-  int split;
-  float us;
-  const cudaError_t err = RowsForm<NT>::plan(a, split, us);
-  return err != cudaSuccess ? err : RowsForm<NT>::launch(a, p, split, stream, rec);
+static cudaError_t launch_rows(const LinearArgs& a, const LinearParams& p, int dev, int forced, cudaStream_t stream, DispatchRecord* rec) {
+  int split[2];
+  float us[2];
+  RowsForm<NT, false>::plan(a, dev, forced, split[0], us[0]);
+  RowsForm<NT, true>::plan(a, dev, forced, split[1], us[1]);
+  return us[1] < us[0] ? RowsForm<NT, true>::launch(a, p, split[1], stream, rec) : RowsForm<NT, false>::launch(a, p, split[0], stream, rec);
 }
 
 struct PairForm {
@@ -804,28 +806,25 @@ struct PairForm {
   static int64_t tiles(const LinearArgs& a) {
     return static_cast<int64_t>((a.T + 2 * C::kTok - 1) / (2 * C::kTok)) * ((a.N + C::kOut - 1) / C::kOut);
   }
-  static int at_once(int split) {
-    static int cache[64][9];
-    return clusters_at_once(fp8_linear_pair_kernel, cache, 2 * split, C::kThreads, kSmem);
+  static int at_once(int dev, int split) {
+    static AtOnce cache;
+    return clusters_at_once(fp8_linear_pair_kernel, cache, dev, 2 * split, C::kThreads, kSmem);
   }
-  static cudaError_t plan(const LinearArgs& a, int& split, float& us) {
-    const cudaError_t err =
-        cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (err != cudaSuccess) return err;
-    const int KB = (a.K + kTile - 1) / kTile, forced = forced_split(4, KB);
+  static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
+    const int KB = (a.K + kTile - 1) / kTile;
+    forced = forced <= 4 && forced <= KB ? forced : 0;
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 4) && s <= KB; ++s) {
       // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
-      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 4.f : 6.f}, a, tiles(a), at_once(s), s, s > 1);
-      t += 1.1f * static_cast<float>((tiles(a) + at_once(s) - 1) / at_once(s));
+      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 4.f : 6.f}, a, tiles(a), at_once(dev, s), s, s > 1);
+      t += 1.1f * static_cast<float>((tiles(a) + at_once(dev, s) - 1) / at_once(dev, s));
       if (split == 0 || t < us) {
         split = s;
         us = t;
       }
     }
-    return cudaSuccess;
   }
-  static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
+  static cudaError_t launch(const LinearArgs& a, LinearParams p, int dev, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta, to;
     cudaError_t err;
     if ((err = rows_map(&tw, a.w, a.N, a.K, 128)) != cudaSuccess) return err;
@@ -840,7 +839,9 @@ struct PairForm {
     p.group = rows < 1 ? 1 : rows > p.tiles_m ? p.tiles_m : static_cast<int>(rows);
     if (tiles(a) > INT32_MAX / 16) return cudaErrorInvalidValue;
     p.split = split;
-    const int64_t clusters = split > 1 || tiles(a) < at_once(1) ? tiles(a) : at_once(1);
+    err = cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    const int64_t clusters = split > 1 || tiles(a) < at_once(dev, 1) ? tiles(a) : at_once(dev, 1);
     err = launch_pdl_cluster(fp8_linear_pair_kernel, dim3(static_cast<unsigned>(clusters * 2 * split)), dim3(C::kThreads), kSmem,
                              stream, 2 * split, tw, ta, to, p);
     if (err != cudaSuccess) return err;
@@ -860,23 +861,26 @@ cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, Dispatch
   p.T = a.T; p.N = a.N; p.KB = (a.K + kTile - 1) / kTile;
   p.f32 = a.out_f32;
   p.quads = a.out_stride % 4 == 0;                       // (out itself is 16-byte aligned)
-  // Up to 64 tokens weights as M: the tokens' columns are what fills up. Above, what costs less.
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
   const char* form = getenv("MSA_LINEAR_FORM");
   const bool pairs_only = form != nullptr && strcmp(form, "pairs") == 0, rows_only = form != nullptr && strcmp(form, "rows") == 0;
+  const char* force = getenv("MSA_LINEAR_SPLIT");
+  int forced = force != nullptr ? atoi(force) : 0;
+  if (forced < 0 || forced > 8) forced = 0;
+  // Up to 64 tokens weights as M: the tokens' columns are what fills up. Above, what costs less.
   if (!pairs_only) {
-    if (a.T <= 16) return launch_rows<16>(a, p, stream, rec);
-    if (a.T <= 32) return launch_rows<32>(a, p, stream, rec);
-    if (a.T <= 64) return launch_rows<64>(a, p, stream, rec);
+    if (a.T <= 16) return launch_rows<16>(a, p, dev, forced, stream, rec);
+    if (a.T <= 32) return launch_rows<32>(a, p, dev, forced, stream, rec);
+    if (a.T <= 64) return launch_rows<64>(a, p, dev, forced, stream, rec);
   }
   int rows_split = 0, pair_split = 0;
   float rows_us = 0.f, pair_us = 0.f;
-  cudaError_t err;
-  // (more groups of 128 tokens than a grid has in y: pairs)
-  const bool rows_fit = (a.T + 127) / 128 <= 65535;
-  if (!pairs_only && rows_fit && (err = RowsForm<128>::plan(a, rows_split, rows_us)) != cudaSuccess) return err;
-  if ((pairs_only || !rows_only || !rows_fit) && (err = PairForm::plan(a, pair_split, pair_us)) != cudaSuccess) return err;
-  if (pair_split == 0 || (rows_split != 0 && rows_us <= pair_us)) return RowsForm<128>::launch(a, p, rows_split, stream, rec);
-  return PairForm::launch(a, p, pair_split, stream, rec);
+  const bool rows_fit = (a.T + 127) / 128 <= 65535;                 // groups of tokens are a grid's y
+  if (!pairs_only && rows_fit) RowsForm<128, true>::plan(a, dev, forced, rows_split, rows_us);
+  if (!rows_only || !rows_fit) PairForm::plan(a, dev, forced, pair_split, pair_us);
+  if (pair_split == 0 || (rows_split != 0 && rows_us <= pair_us)) return RowsForm<128, true>::launch(a, p, rows_split, stream, rec);
+  return PairForm::launch(a, p, dev, pair_split, stream, rec);
 }
 
 }  // namespace msa
