@@ -519,7 +519,8 @@ msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x
  *   out[t, n] = sum_g a_scales[t, g] w_scales[n / 128, g] sum_{k in g} a[t, k] w[n, k].
  * The sum of a group is taken on the tensor cores in fp32, the sum over groups in
  * fp32 registers in a fixed order: results do not depend on timing. They do
- * depend, within fp32's rounding, on num_tokens, which sets how K is split.
+ * depend, within fp32's rounding, on num_tokens and on the GPU's size, which set
+ * how K is split.
  * A code that is NaN makes every output that it enters NaN.
  * a: E4M3 [T, K]; a_scales: fp32 [T, ceil(K / 128)]; w: E4M3 [N, K]; w_scales:
  * fp32 [ceil(N / 128), ceil(K / 128)]; all contiguous. out: MSA_BF16 or MSA_F32

@@ -60,7 +60,7 @@ def test_sizes(T, N, K, dtype):
     c.check()
 
 
-@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("split", [1, 2, 3, 5, 7, 8])
 @pytest.mark.parametrize("T,N,K", [(1, 200, 1040), (40, 300, 2176), (128, 128, 4096), (9, 130, 1152)])
 def test_every_split(monkeypatch, split, T, N, K):
     monkeypatch.setenv("MSA_LINEAR_SPLIT", str(split))
@@ -70,7 +70,17 @@ def test_every_split(monkeypatch, split, T, N, K):
     c.check()
 
 
-@pytest.mark.parametrize("split", [1, 2, 4])
+@pytest.mark.parametrize("T", [1, 20, 64])
+def test_both_sizes_of_the_rows_form(T):
+    """Few tiles take a whole SM each, many share one; over two CTAs per SM they follow one another."""
+    for N, K, deep in ((1280, 2048, True), (28672, 272, False), (60000, 144, False)):
+        c = Case(T, N, K, seed=T)
+        c.run()
+        assert (" deep" in msa.last_dispatch()) == deep, msa.last_dispatch()
+        c.check()
+
+
+@pytest.mark.parametrize("split", [1, 2, 3, 4])
 @pytest.mark.parametrize("T,N,K", [(1, 300, 512), (129, 130, 1040), (256, 256, 2048), (257, 520, 4096), (600, 1300, 528)])
 def test_pairs(monkeypatch, split, T, N, K):
     """Two CTAs per tile, its K on one to four pairs, whatever the number of tokens."""
@@ -141,9 +151,11 @@ def test_large_sampled():
     c.check(rows=torch.tensor([0, 1, 127, 128, 255, 256, 1023, 1900, 2046, 2047, 2048]))
 
 
-def test_output_past_4_gib():
-    """Offsets of the output, and of the weights' rows, past 32 bits."""
-    T, N, K = 300, 4_000_000, 16
+@pytest.mark.parametrize("form,T", [("rows", 300), ("pairs", 300), ("rows", 75)])
+def test_output_past_4_gib(monkeypatch, form, T):
+    """Offsets of the output past 32 bits."""
+    monkeypatch.setenv("MSA_LINEAR_FORM", form)
+    N, K = 1_200_000_000 // T // 4096 * 4096, 16
     rng = np.random.default_rng(12)
     a = _codes(rng, T, K).cuda()
     w = _codes(rng, 4096, K).cuda().repeat(-(-N // 4096), 1)[:N].contiguous()
@@ -151,7 +163,8 @@ def test_output_past_4_gib():
     out, flags = torch.empty((T, N), dtype=torch.float32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     msa.fp8_linear(a, sa, w, sw, out, flags)
     assert int(flags.item()) == 0
-    assert torch.equal(out[:, :4096], out[:, 4096 * 900:4096 * 901]) and torch.equal(out[:, 4096 * 975:4096 * 976], out[:, :4096])
+    for i in range(4096, N, 4096):                            # the weight repeats
+        assert torch.equal(out[:, :4096], out[:, i:i + 4096]), i
     want, size = L.linear(a.cpu().numpy(), sa.cpu().numpy(), w[:4096].cpu().numpy(), sw[:32].cpu().numpy())
     assert (np.abs(out[:, :4096].double().cpu().numpy() - want) <= 200 * 2.0 ** -23 * size).all()
 

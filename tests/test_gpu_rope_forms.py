@@ -278,3 +278,31 @@ def test_batch_size_does_not_change_results_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(want, c.q_out)
+
+
+def test_packed_rows_past_4_gib():
+    """260,000 tokens of 66 heads: offsets of the packed rows and the queries past 32 bits; the last tokens are those of a
+    short call."""
+    T = 260_000
+    P = -(-T // 128)
+    packed = torch.zeros((T, 66, 128), dtype=torch.bfloat16, device="cuda")
+    n = 300
+    packed[-n:] = torch.randn((n, 66, 128), device="cuda").bfloat16()
+    rope = msa.make_rope(64)
+    pos = torch.arange(T, device="cuda").int()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(p, pos, slots, P):
+        t = p.shape[0]
+        dims = msa.make_dims(1, 1, 16, 1, 1, max_blocks_per_seq=P, num_pages=P)
+        kc, vc = (torch.zeros((P, 1, 128, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q = torch.empty((t, 16, 128), dtype=torch.bfloat16, device="cuda")
+        msa.qkv_rope_insert(dims, p[:, 40:56], p[:, 64:65], p[:, 65:66], None, None, pos, slots, None, rope, q, None,
+                            msa.KVCache(msa.BF16, kc, vc), None, flags)
+        return q, kc.view(-1, 128), vc.view(-1, 128)
+
+    q, k, v = call(packed, pos, torch.arange(T, device="cuda"), P)
+    q1, k1, v1 = call(packed[-n:].clone(), pos[-n:].contiguous(), torch.arange(n, device="cuda"), 3)
+    assert int(flags.item()) == 0
+    assert torch.equal(q[-n:], q1) and torch.equal(k[T - n:T], k1[:n]) and torch.equal(v[T - n:T], v1[:n])
+    assert q1.any() and not q[:-n].any()
