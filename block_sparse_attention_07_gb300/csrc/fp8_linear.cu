@@ -120,28 +120,38 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
 }
 
 // ---------------------------------------------------------------------------
-// Weights as M. A CTA has 128 weight rows and up to NT tokens as the product's N,
-// so that few tokens waste nothing but columns; the CTAs of a cluster share the
-// tile's K and add their sums through distributed shared memory, in rank order.
+// One CTA per tile of 128 weight rows and up to NT tokens; the CTAs of a cluster
+// share the tile's K and add their sums through distributed shared memory, in rank
+// order. Up to 64 tokens the weights are the product's M, so that few tokens waste
+// nothing but columns: a thread has a weight row and up to 32 tokens, whose scales
+// it reads from shared memory. With 128 tokens those reads are as many bytes as the
+// copies and the products take together, so the tokens are M: a thread has a token,
+// 64 weight rows and one scale per block of K.
 // Up to 64 tokens there are two sizes: two CTAs per SM, or one with as much memory for copies in flight. kDeep: the latter.
 template <int NT, bool kDeep>
 struct RowsCfg {
-  static constexpr int kPer = NT < 32 ? NT : 32;                      // a thread's tokens
-  static constexpr int kSumThreads = 128 * (NT / kPer), kThreads = kSumThreads + 64;
+  static constexpr bool kTokM = NT == 128;
+  static constexpr int kWide = kTokM ? kTile : NT;                    // a block's columns in tensor memory
+  static constexpr int kPer = kTokM ? 64 : NT < 32 ? NT : 32;         // a thread's columns
+  static constexpr int kSumThreads = 128 * (kWide / kPer), kThreads = kSumThreads + 64;
+  static constexpr int kCopyWarp = kSumThreads / 32, kMmaWarp = kCopyWarp + 1;
   static constexpr int kCtas = kDeep ? 1 : 2;                         // per SM
-  static constexpr int kAcc = 4;                                      // blocks' sums in tensor memory
-  static constexpr uint32_t kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
+  // Blocks that are read back at one time, as far as registers go, and how many times as many are in tensor memory.
+  static constexpr int kTake = kTokM || (NT == 64 && !kDeep) ? 1 : 2, kSets = 4 / kTake;
+  static constexpr int kLoads = kTokM ? 2 : kTake;                    // the reads for it
+  static constexpr uint32_t kCols = kSets * kTake * kWide;
   static constexpr int kStages = NT == 128 ? 6 : kDeep ? (NT == 16 ? 11 : NT == 32 ? 10 : 8) : NT == 64 ? 4 : 5;
-  static_assert(NT <= 64 || kDeep, "128 tokens fill an SM");
-  static constexpr uint32_t kStage = (kTile + NT) * 128;
+  static_assert(kDeep || !kTokM, "128 tokens fill an SM");
+  static constexpr uint32_t kStage = (kTile + NT) * 128;              // tokens, then weights
   static constexpr int kRow = NT + 4;                                 // floats of a scale row: 16-byte steps, spread over banks
   static constexpr uint32_t oTable = kStages * kStage;
   static constexpr uint32_t oBars = oTable + 2 * kChunk * kRow * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc;
+  static constexpr int kBars = 2 * kStages + 2 * kSets;
   static constexpr uint32_t oSlot = oBars + kBars * 8;
   static constexpr uint32_t kTotal = oSlot + 16;
+  static_assert(kChunk % kTake == 0, "blocks that are read together have their scales in one half of the table");
   static_assert(NT * kTile * 4 <= kStages * kStage, "the sums of a tile fit into the stages");
-  static_assert(kCols * kCtas <= 512, "tensor memory");
+  static_assert(kCols >= 32 && kCols * kCtas <= 512, "tensor memory");
 };
 
 template <int NT, bool kDeep>
@@ -158,8 +168,9 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
   auto acc_full = [&](int i) { return bars + 8u * (2 * C::kStages + i); };
-  auto acc_free = [&](int i) { return bars + 8u * (2 * C::kStages + C::kAcc + i); };
-  constexpr int kCopyWarp = C::kSumThreads / 32, kMmaWarp = kCopyWarp + 1;
+  auto acc_free = [&](int i) { return bars + 8u * (2 * C::kStages + C::kSets + i); };
+  // Four weight rows of a token, in 16 bytes. With a token per lane they are spread over the banks.
+  auto place = [](int t, int quad) { return t * kTile + 4 * (C::kTokM ? quad ^ (t & 31) : quad); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -167,7 +178,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int i = 0; i < C::kAcc; ++i) {
+    for (int i = 0; i < C::kSets; ++i) {
       mbar_init(acc_full(i), 1);
       mbar_init(acc_free(i), C::kSumThreads / 32);
     }
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
     prefetch_tensormap(&tw);
     prefetch_tensormap(&ta);
   }
-  if (warp == kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::oSlot), "r"(C::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -198,7 +209,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
 
   bool ok = true;
 
-  if (warp == kCopyWarp) {
+  if (warp == C::kCopyWarp) {
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
@@ -206,8 +217,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
         if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
         const uint32_t at = base + s * C::kStage;
         mbar_arrive_expect_tx(full(s), C::kStage);
-        tma_load_2d(at, &tw, (kb0 + i) * kTile, tile * kTile, full(s));
-        tma_load_2d(at + kTile * 128, &ta, (kb0 + i) * kTile, tok0, full(s));
+        tma_load_2d(at + NT * 128, &tw, (kb0 + i) * kTile, tile * kTile, full(s));
+        tma_load_2d(at, &ta, (kb0 + i) * kTile, tok0, full(s));
         if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
       // no copy may be in flight when the CTA ends, whatever the others did
@@ -215,111 +226,132 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
       if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    constexpr uint32_t id = mma_idesc(0, 0, NT, 0, 0), hi = desc_hi(1024, kSwz128);
-    const uint32_t w0 = desc_lo(base, 16), a0 = desc_lo(base + kTile * 128, 16);
-    const bool lead = elect_one();
-    int s = 0;
-    uint32_t ph = 0;
-    for (int i = 0; i < n; ++i) {
-      const int b = i % C::kAcc;
-      ok = warp_wait(full(s), ph) && (i < C::kAcc || warp_wait(acc_free(b), (i / C::kAcc - 1) & 1));
-      if (!ok) break;
-      tmem_fence_after();
-      if (lead) {
-        const uint32_t w = w0 + s * (C::kStage >> 4), a = a0 + s * (C::kStage >> 4);
+  } else if (warp == C::kMmaWarp) {
+    constexpr uint32_t id = mma_idesc(0, 0, C::kWide, 0, 0), hi = desc_hi(1024, kSwz128);
+    const uint32_t m0 = desc_lo(base + (C::kTokM ? 0 : NT * 128), 16), n0 = desc_lo(base + (C::kTokM ? NT * 128 : 0), 16);
+    if (elect_one()) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < n; ++i) {
+        const int set = i / C::kTake, b = set % C::kSets, in = i % C::kTake;
+        if (in == 0 && set >= C::kSets && !mbar_wait(acc_free(b), (set / C::kSets - 1) & 1)) { ok = false; break; }
+        if (!mbar_wait(full(s), ph)) { ok = false; break; }
+        tmem_fence_after();
+        const uint32_t at = s * (C::kStage >> 4), d = tmem + (b * C::kTake + in) * C::kWide;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_fp8(tmem + b * NT, desc_of(w + kk * 2, hi), desc_of(a + kk * 2, hi), id, kk > 0);
+        for (int kk = 0; kk < 4; ++kk) mma_fp8(d, desc_of(m0 + at + kk * 2, hi), desc_of(n0 + at + kk * 2, hi), id, kk > 0);
         mma_commit(empty(s));
-        mma_commit(acc_full(b));
+        if (in == C::kTake - 1 || i == n - 1) mma_commit(acc_full(b));
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
-      __syncwarp();
-      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     }
-    if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
+    __syncwarp();
   } else {
-    // Thread = weight row and up to 32 tokens: their sums over the blocks, times the two scales of the block.
+    // A block's sums, times its two scales, onto the thread's own.
+    const int sub = warp & 3, part = warp >> 2;                       // tensor-memory lanes, part of the columns
     constexpr int kFetch = NT * kChunk / C::kSumThreads;
     const float* sw = p.sw + static_cast<int64_t>(tile) * p.KB + kb0;
-    float next[kFetch];
-    auto fetch = [&](int c) {
+    static_assert(C::kSumThreads % kChunk == 0, "a thread fetches scales of one block");
+    float next[kFetch], next_w;
+    auto fetch = [&](int c) {               // (multiplied when they are kept: a product here would wait for the loads)
+      const int i = c * kChunk + threadIdx.x % kChunk;
+      next_w = i < n ? sw[i] : 0.f;
 #pragma unroll
       for (int j = 0; j < kFetch; ++j) {
-        const int e = threadIdx.x + C::kSumThreads * j, t = e / kChunk, i = c * kChunk + e % kChunk;
-        next[j] = i < n && tok0 + t < p.T ? p.sa[static_cast<int64_t>(tok0 + t) * p.KB + kb0 + i] * sw[i] : 0.f;
+        const int t = (threadIdx.x + C::kSumThreads * j) / kChunk;
+        next[j] = i < n && tok0 + t < p.T ? p.sa[static_cast<int64_t>(tok0 + t) * p.KB + kb0 + i] : 0.f;
       }
     };
     auto keep = [&](int c) {
 #pragma unroll
       for (int j = 0; j < kFetch; ++j) {
         const int e = threadIdx.x + C::kSumThreads * j;
-        table[((c & 1) * kChunk + e % kChunk) * C::kRow + e / kChunk] = next[j];
+        table[((c & 1) * kChunk + e % kChunk) * C::kRow + e / kChunk] = next[j] * next_w;
       }
     };
-    const int sub = warp & 3, tok = warp / 4 * C::kPer;
     float acc[C::kPer];
 #pragma unroll
     for (int t = 0; t < C::kPer; ++t) acc[t] = 0.f;
     fetch(0);
     keep(0);
     named_barrier(1, C::kSumThreads);
-    const uint32_t mine = tmem + (static_cast<uint32_t>(sub) << 21) + tok;
-    for (int i = 0; i < n; ++i) {
-      const int b = i % C::kAcc, c = i / kChunk, j = i % kChunk;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(sub) << 21) + part * C::kPer;
+    for (int i = 0; i < n; i += C::kTake) {
+      const int set = i / C::kTake, b = set % C::kSets, c = i / kChunk, j = i % kChunk;
       if (j == 0 && c > 0) {
         keep(c);                            // the other half: every thread is behind the barrier of its last use
         named_barrier(1, C::kSumThreads);
       }
       if (j == 0) fetch(c + 1);
-      ok = ok && warp_wait(acc_full(b), (i / C::kAcc) & 1);
+      const float* scale = table + ((c & 1) * kChunk + j) * C::kRow + (C::kTokM ? sub * 32 + lane : part * C::kPer);
+      const float f = C::kTokM ? *scale : 0.f;
+      if (!mbar_wait(acc_full(b), (set / C::kSets) & 1)) ok = false;
+      __syncwarp();
       tmem_fence_after();
-      const float4* scale = reinterpret_cast<const float4*>(table + ((c & 1) * kChunk + j) * C::kRow + tok);
-      float x[32];
-      if (C::kPer == 32) {
-        tmem_ld32(mine + b * NT, x);
-      } else {
-        tmem_ld16(mine + b * NT, x);
+      float x[C::kLoads][32];
 #pragma unroll
-        for (int u = C::kPer; u < 32; ++u) x[u] = 0.f;
+      for (int q = 0; q < C::kLoads; ++q) {
+        const uint32_t at = mine + b * C::kTake * C::kWide + q * (C::kTokM ? 32 : C::kWide);
+        if (NT == 16) tmem_ld16(at, x[q]);
+        else tmem_ld32(at, x[q]);
+#pragma unroll
+        for (int u = NT == 16 ? 16 : 32; u < 32; ++u) x[q][u] = 0.f;
       }
-      tmem_wait_ld32(x);
+#pragma unroll
+      for (int q = 0; q < C::kLoads; ++q) tmem_wait_ld32(x[q]);
       tmem_fence_before();
       if (lane == 0) mbar_arrive(acc_free(b));
 #pragma unroll
-      for (int u = 0; u < C::kPer; u += 4) {
-        const float4 f = scale[u / 4];
-        fma2(acc[u], acc[u + 1], x[u], x[u + 1], f.x, f.y);
-        fma2(acc[u + 2], acc[u + 3], x[u + 2], x[u + 3], f.z, f.w);
+      for (int q = 0; q < C::kLoads; ++q) {
+        if constexpr (C::kTokM) {
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) fma2(acc[32 * q + u], acc[32 * q + u + 1], x[q][u], x[q][u + 1], f);
+        } else if (i + q < n) {             // (behind an odd number of blocks: an older one's columns, or nothing's)
+#pragma unroll
+          for (int u = 0; u < C::kPer; u += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(scale + q * C::kRow + u);
+            fma2(acc[u], acc[u + 1], x[q][u], x[q][u + 1], v.x, v.y);
+            fma2(acc[u + 2], acc[u + 3], x[q][u + 2], x[q][u + 3], v.z, v.w);
+          }
+        }
       }
     }
     if (!ok && lane == 0) set_flag(p.flags, MSA_FLAG_TIMEOUT);
     const int row = sub * 32 + lane;
-    if (p.split == 1) {
-      const bool in = tile * kTile + row < p.N;
+    if constexpr (C::kTokM) {
 #pragma unroll
-      for (int t = 0; t < C::kPer; ++t)
-        if (in && tok0 + tok + t < p.T) store_out(p, tok0 + tok + t, tile * kTile + row, acc[t]);
+      for (int u = 0; u < C::kPer; u += 4)
+        *reinterpret_cast<float4*>(sums + place(row, part * (C::kPer / 4) + u / 4)) = make_float4(acc[u], acc[u + 1], acc[u + 2], acc[u + 3]);
     } else {
+      const int tok = part * C::kPer;
+      if (p.split == 1) {
+        const bool in = tile * kTile + row < p.N;
 #pragma unroll
-      for (int t = 0; t < C::kPer; ++t) sums[(tok + t) * kTile + row] = acc[t];
+        for (int t = 0; t < C::kPer; ++t)
+          if (in && tok0 + tok + t < p.T) store_out(p, tok0 + tok + t, tile * kTile + row, acc[t]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < C::kPer; ++t) sums[(tok + t) * kTile + row] = acc[t];
+      }
     }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
-  if (p.split == 1) return;
+  if (!C::kTokM && p.split == 1) return;
 
-  cluster_sync_all();
+  if (p.split > 1) cluster_sync_all();
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
   for (int i = rank * blockDim.x + threadIdx.x; i < tokens * (kTile / 4); i += p.split * blockDim.x) {
-    const int t = i >> 5, r = 4 * (i & 31);
-    store4(p, tok0 + t, tile * kTile + r, sum_cluster<8>(base + (t * kTile + r) * 4, p.split));
+    const int t = i >> 5, quad = i & 31;
+    store4(p, tok0 + t, tile * kTile + 4 * quad, sum_cluster<8>(base + place(t, quad) * 4, p.split));
   }
-  cluster_sync_all();                       // no CTA ends while another reads its sums
+  if (p.split > 1) cluster_sync_all();      // no CTA ends while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -732,20 +764,22 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 
 // What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
 // between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
-// fits to calls over weights that L2 does not hold, within 10 % of nearly all (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 25.8 / 17.5 / 24.0; pairs on 1 / 2 / 3 30.0 / 21.5 / 19.3;
-//   256 x 10,240 x 4,096: rows 28.8 / 33.8, pairs 18.1 / 30.2; 512 x 4,096 x 8,192: rows 26.0 / 34.1, pairs 29.9 / 21.8;
-//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, two per SM 17.1 / 13.1 / 12.2 / 18.5, one per SM 13.3 / 19.4 / 17.6;
-//   64 x 4,096 x 8,192 on 3 / 4 / 6 / 8, two per SM 13.8 / 12.6 / 12.3 / 11.6, one per SM 11.9 / 10.8 / 17.2 / 22.6;
-//   1 x 1,280 x 4,096 on 8 4.6 and 4.2; 64 x 28,672 x 4,096 on 1 22.9 and 28.5.
+// fits to calls whose weights come from memory; what they choose was within 5 % of the fastest at all of 61 sizes of 16
+// to 1,024 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 20.6 / 14.3 / 20.8; pairs on 1 / 2 / 3 30.0 / 21.5 / 19.4;
+//   256 x 10,240 x 4,096: rows 27.0 / 30.7, pairs 18.1 / 30.2; 512 x 4,096 x 8,192: rows 20.7 / 27.5, pairs 29.9 / 21.9;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.7, two per SM 17.1 / 12.8 / 12.2 / 18.9;
+//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 12.2 / 10.5 / 10.6, two per SM on 6 / 8 11.8 / 11.4;
+//   1 x 1,280 x 4,096 on 8 4.2 and 4.6; 64 x 28,672 x 4,096 on 1 27.0 and 22.4.
 struct FormCost {
   float launch, block, sums;
 };
 static float form_us(const FormCost& c, const LinearArgs& a, int64_t clusters, int at_once, int split, bool restart) {
   const int64_t waves = (clusters + at_once - 1) / at_once;
   const int KB = (a.K + kTile - 1) / kTile;
-  const float us = static_cast<float>(waves) * (static_cast<float>((KB + split - 1) / split) * c.block + (split > 1 ? c.sums : 0.f));
-  const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 7.0e6f + (split > 1 ? c.sums : 0.f);
+  const float sums = split > 1 ? c.sums * static_cast<float>(split) : 0.f;
+  const float us = static_cast<float>(waves) * (static_cast<float>((KB + split - 1) / split) * c.block + sums);
+  const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 7.0e6f + sums;
   return c.launch + (us > bytes ? us : bytes) + 2.5f * static_cast<float>(restart ? waves - 1 : 0);
 }
 
@@ -753,9 +787,9 @@ template <int NT, bool kDeep>
 struct RowsForm {
   using C = RowsCfg<NT, kDeep>;
   static constexpr size_t kSmem = C::kTotal + 1024;
-  static constexpr FormCost kCost = NT == 128 ? FormCost{3.9f, 0.338f, 2.5f}
-                                  : kDeep ? (NT == 16 ? FormCost{3.7f, 0.225f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.27f, 1.0f} : FormCost{3.7f, 0.29f, 2.0f})
-                                          : (NT == 16 ? FormCost{3.7f, 0.275f, 0.7f} : NT == 32 ? FormCost{3.7f, 0.31f, 1.2f} : FormCost{3.7f, 0.40f, 2.2f});
+  static constexpr FormCost kCost = NT == 128 ? FormCost{6.0f, 0.24f, 0.2f}
+                                  : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{4.2f, 0.2f, 0.2f})
+                                          : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.31f, 0.2f} : FormCost{4.5f, 0.35f, 0.8f});
   // The number of CTAs that share a tile's K, and what the call then costs.
   static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
     static AtOnce cache;
@@ -816,7 +850,7 @@ struct PairForm {
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 4) && s <= KB; ++s) {
       // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
-      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 4.f : 6.f}, a, tiles(a), at_once(dev, s), s, s > 1);
+      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 2.f : 6.f / static_cast<float>(s)}, a, tiles(a), at_once(dev, s), s, s > 1);
       t += 1.1f * static_cast<float>((tiles(a) + at_once(dev, s) - 1) / at_once(dev, s));
       if (split == 0 || t < us) {
         split = s;
