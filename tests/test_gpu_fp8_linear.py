@@ -93,6 +93,23 @@ def test_pairs(monkeypatch, split, T, N, K):
         c.check()
 
 
+@pytest.mark.parametrize("form,T,split", [("rows", 9, 2), ("rows", 150, 3), ("pairs", 300, 1), ("pairs", 300, 2), ("pairs", 300, 3)])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_scales_off_16_bytes(monkeypatch, off, form, T, split):
+    """Scales need boundaries of four bytes alone, also where a row of them is a multiple of 16 bytes."""
+    monkeypatch.setenv("MSA_LINEAR_FORM", form)
+    monkeypatch.setenv("MSA_LINEAR_SPLIT", str(split))
+    c = Case(T, 300, 1024, seed=off)
+    for name in ("sa", "sw"):
+        x = getattr(c, name)
+        room = torch.full((x.numel() + 8,), float("nan"), device="cuda")
+        room[off:off + x.numel()] = x.flatten()
+        setattr(c, name, room[off:off + x.numel()].view(x.shape))
+    c.run()
+    assert msa.last_dispatch().split()[1] == form and msa.last_dispatch().endswith(f"split={split}")
+    c.check()
+
+
 @pytest.mark.parametrize("T", [130, 300])
 def test_rows_form_with_many_tokens(monkeypatch, T):
     monkeypatch.setenv("MSA_LINEAR_FORM", "rows")
