@@ -8,6 +8,14 @@
 // every block; the outer one is kept in fp32 registers, which read the block's
 // sums back and add them times their scales. Blocks of K beyond its end and rows
 // beyond the operands' arrive as zeros.
+//
+// What bounds it: the weights' bytes where there are many and few tokens (64 x
+// 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
+// way between CTAs where there are few (1 x 1,280 x 4,096: 4.2 us, an empty launch
+// 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
+// 14.4 us); for prompts the products with the sums' way back beside them (8,191 x
+// 10,240 x 4,096: 237 us, 2.9 PFLOP/s; 265 in a run of a second, where the board's
+// power limit takes the clock to 1.75 GHz).
 #include <cstdlib>
 #include <cstring>
 
@@ -126,7 +134,8 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
 // nothing but columns: a thread has a weight row and up to 32 tokens, whose scales
 // it reads from shared memory. With 128 tokens those reads are as many bytes as the
 // copies and the products take together, so the tokens are M: a thread has a token,
-// 64 weight rows and one scale per block of K.
+// 64 weight rows and one scale per block of K (256 x 4,096 x 8,192: 17.6 -> 14.4 us;
+// 64 tokens as M, half of the product's rows unused: 64 x 100,003 x 4,096 72.4 -> 76.3).
 // Up to 64 tokens there are two sizes: two CTAs per SM, or one with as much memory for copies in flight. kDeep: the latter.
 template <int NT, bool kDeep>
 struct RowsCfg {
@@ -136,7 +145,8 @@ struct RowsCfg {
   static constexpr int kSumThreads = 128 * (kWide / kPer), kThreads = kSumThreads + 64;
   static constexpr int kCopyWarp = kSumThreads / 32, kMmaWarp = kCopyWarp + 1;
   static constexpr int kCtas = kDeep ? 1 : 2;                         // per SM
-  // Blocks that are read back at one time, as far as registers go, and how many times as many are in tensor memory.
+  // Blocks that are read back at one time, as far as registers go (64 x 4,096 x 8,192 by twos: 11.8 -> 11.1 us), and how
+  // many times as many are in tensor memory.
   static constexpr int kTake = kTokM || (NT == 64 && !kDeep) ? 1 : 2, kSets = 4 / kTake;
   static constexpr int kLoads = kTokM ? 2 : kTake;                    // the reads for it
   static constexpr uint32_t kCols = kSets * kTake * kWide;
@@ -362,6 +372,8 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
 // product of scales per block of K serves its 128 outputs. With few tiles, `split`
 // pairs of a cluster share a tile's K, and each finishes every split-th 16 columns
 // from the sums that the others copy there; otherwise a pair walks over the tiles.
+// A block takes some 830 cycles; without reading its sums back 710, as far as the
+// power limit lets the products go (8,191 x 10,240 x 4,096: 237 and 204 us).
 struct PairCfg {
   static constexpr int kTok = 128, kOut = 256;                        // a CTA's tokens, a tile's weight rows
   static constexpr int kStages = 6, kAcc = 2;

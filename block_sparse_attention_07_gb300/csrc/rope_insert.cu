@@ -22,7 +22,7 @@
 // 4 + 4 heads, FP8 cache: 52.9 us, 5.5 TB/s (82 % of a copy's rate); 16,000 tokens
 // 94.7 us (89 %); 64 tokens 4.3 us, the host's time per launch. With fewer heads what
 // comes before a warp's queries (position, sines, slot, keys) shows: 16 + 1 + 1 heads
-// 27.8 us for 8,191 tokens.
+// 21.2 us for 8,191 tokens (51 % of a copy's rate).
 //
 // Phases: freq / 2 pi modulo one is held as a 64-bit fraction of a turn, so that
 // position times it, modulo one turn, is one integer product: 2^-53 relative to
@@ -365,7 +365,7 @@ cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, Dispa
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
   const int passes = (rows + 3) / 4;
   // Warps per token: about 16 warps per SM for few tokens (as the multi-axis kernel, which measured it), two per token
-  // for some, one from 32 tokens per SM on (8,191 tokens 55.3 us, two 57.1; 16,000 tokens the same).
+  // for some, one from 32 tokens per SM on (8,191 tokens: two 3 % slower; 16,000 tokens the same).
   const int64_t sms = device_sm_count();
   int64_t parts = a.ins.T >= 32 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
   if (parts < 2 && a.ins.T < 32 * sms) parts = 2;

@@ -528,9 +528,9 @@ msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x
  * left as it is. K: a multiple of 16. T, N and K up to 2^24, T * K and N * K below
  * 2^40. a, w and out 16-byte aligned, scales 4-byte. out overlaps no input.
  * num_tokens = 0 launches nothing. MSA_LINEAR_FORM=rows or pairs in the
- * environment (read on every call) forces tiles with the weights or the tokens as
- * the product's rows, MSA_LINEAR_SPLIT=1 to 8 (pairs: 4) the number of CTAs (pairs
- * of them) that share a tile's K; other values have no effect.
+ * environment (read on every call) forces tiles of one CTA or of a pair of CTAs,
+ * MSA_LINEAR_SPLIT=1 to 8 (pairs: 4) the number of CTAs (pairs of them) that share
+ * a tile's K; other values have no effect.
  */
 msa_status_t msa_fp8_linear(int32_t num_tokens, int32_t out_features, int32_t in_features, const void* a,
                             const float* a_scales, const void* w, const float* w_scales, void* out,
