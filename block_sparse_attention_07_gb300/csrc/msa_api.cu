@@ -565,14 +565,14 @@ msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x
                                 const float* weight, float eps, void* out, void* codes, float* scales, void* stream) {
   if (num_tokens < 0 || width < 1) return MSA_ERR_INVALID_ARG;
   if (width % 16 != 0 || width > 16384) return MSA_ERR_UNSUPPORTED;
-  if ((codes == nullptr) != (scales == nullptr) || (out == nullptr && codes == nullptr)) return MSA_ERR_INVALID_ARG;
-  if (residual == nullptr && residual_out != nullptr) return MSA_ERR_INVALID_ARG;
   if (residual != nullptr && residual_dtype != MSA_BF16 && residual_dtype != MSA_F32) return MSA_ERR_UNSUPPORTED;
   if (weight != nullptr && (!(eps >= 0.f) || eps > 1.f)) return MSA_ERR_INVALID_ARG;
   if (num_tokens == 0) {
-    g_record.set("add_norm_quant empty");
+    g_record.set("add_norm_quant empty");              // (tensors without tokens have no addresses)
     return MSA_OK;
   }
+  if ((codes == nullptr) != (scales == nullptr) || (out == nullptr && codes == nullptr)) return MSA_ERR_INVALID_ARG;
+  if (residual == nullptr && residual_out != nullptr) return MSA_ERR_INVALID_ARG;
   if (x == nullptr || x_stride < width || x_stride % 8 != 0) return MSA_ERR_INVALID_ARG;
   for (const void* ptr : {x, residual, static_cast<const void*>(residual_out), static_cast<const void*>(weight),
                           static_cast<const void*>(out), static_cast<const void*>(codes)})

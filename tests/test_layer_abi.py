@@ -231,3 +231,28 @@ def test_strides_that_the_kernels_get(m, monkeypatch):
     assert got[-1][3] == 500
     m.fp8_linear(z(4, 16, dt=torch.uint8), z(4, 1), z(100, 16, dt=torch.uint8), z(1, 1), wide[:, 3:103], z(1, dt=torch.int32))
     assert got[-1][9] == 500
+
+
+def test_calls_without_tokens(m, monkeypatch):
+    """Tensors without tokens have no addresses; the calls take them and launch nothing."""
+    monkeypatch.setattr(m, "_stream", lambda stream: None)
+    monkeypatch.setattr(m, "_want_on_device", lambda *a, **k: None)
+    bf, u8 = torch.bfloat16, torch.uint8
+    x, r, codes, scales = z(0, 256, dt=bf), z(0, 256, dt=bf), z(0, 256, dt=u8), z(0, 2)
+    for outs in (dict(codes=codes, scales=scales), dict(out=x), dict(out=x, codes=codes, scales=scales)):
+        for res in (dict(), dict(residual=r), dict(residual=r, residual_out=r), dict(residual=r.float(), residual_out=r.float())):
+            m.add_norm_quant(x, z(256), **res, **outs)
+            assert m.last_dispatch() == "add_norm_quant empty"
+    flags = z(1, dt=torch.int32)
+    m.fp8_linear(codes, scales, z(128, 256, dt=u8), z(1, 2), z(0, 128), flags)
+    assert m.last_dispatch() == "fp8_linear empty"
+    d = m.make_dims(2, 1, max_blocks_per_seq=4, num_pages=8)
+    heads = z(0, 80, 128, dt=bf)
+    cache = m.KVCache(m.FP8_E4M3, z(8, 4, 128, 128, dt=u8), z(8, 4, 128, 128, dt=u8))
+    index = m.IndexCache(m.FP8_E4M3, z(8, 4, 128, 128, dt=u8), z(8, 4, 128))
+    for idx in (False, True):
+        w = (z(128),) * 4
+        m.qkv_rope_insert(d, heads[:, :64], heads[:, 64:68], heads[:, 68:72], heads[:, 72:76] if idx else None,
+                          heads[:, 76:] if idx else None, z(0, dt=torch.int32), z(0, dt=torch.int64), m.make_norm_rope(*w),
+                          m.make_rope(), z(0, 64, 128, dt=bf), z(0, 4, 128, dt=bf) if idx else None, cache, index if idx else None, flags)
+        assert m.last_dispatch() == "qkv_rope_insert empty"
