@@ -247,6 +247,8 @@ __global__ void __launch_bounds__(kMost, 1024 / kMost) add_norm_quant_ring_kerne
 #pragma unroll
   for (int v = 0; v < kVpt; ++v) {
     const int c = v * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[v][i] = 0.f;         // behind the row: its lanes take part in the last group's maximum
     if (p.weight != nullptr && c < chunks) weights8(p, c, w[v]);
   }
   int slot = 0, turn = 0;
