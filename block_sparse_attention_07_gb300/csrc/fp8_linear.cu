@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
       if (j == 0) fetch(c + 1);
       const float* scale = table + ((c & 1) * kChunk + j) * C::kRow + (C::kTokM ? sub * 32 + lane : part * C::kPer);
       const float f = C::kTokM ? *scale : 0.f;
-      if (!mbar_wait(acc_full(b), (set / C::kSets) & 1)) ok = false;
+      if (ok && !mbar_wait(acc_full(b), (set / C::kSets) & 1)) ok = false;
       __syncwarp();
       tmem_fence_after();
       float x[C::kLoads][32];
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
             tmem_fence_before();
             if (lane == 0) mbar_arrive_relaxed(free0 + 8u * b);
             if (kb + 1 < kb1) {
-              if (!mbar_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1)) ok = false;
+              if (ok && !mbar_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1)) ok = false;
               __syncwarp();
               tmem_fence_after();
               tmem_ld32(mine + (b ^ 1) * C::kOut, x[0]);
