@@ -208,9 +208,11 @@ def test_repeats_streams_and_graph(T):
     assert torch.equal(first, c.out) and int(c.flags.item()) == 0
 
 
-def test_two_calls_at_once():
+@pytest.mark.parametrize("sizes", [((64, 2560, 2048), (64, 2560, 2048)), ((600, 2560, 2048), (9, 2560, 4096)),
+                                   ((600, 2560, 2048), (700, 1280, 4096)), ((100, 4096, 4096), (64, 20480, 512))])
+def test_two_calls_at_once(sizes):
     """Calls on two streams share nothing."""
-    cs = [Case(64, 2560, 2048, seed=s) for s in (14, 15)]
+    cs = [Case(*n, seed=14 + i) for i, n in enumerate(sizes)]
     for c in cs:
         c.run()
     want = [c.out.clone() for c in cs]

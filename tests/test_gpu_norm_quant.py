@@ -107,6 +107,37 @@ def test_in_place():
     check(h, y, out=x, res_out=c.res)
 
 
+@pytest.mark.parametrize("T,W", [(2100, 4096), (1900, 4432), (6, 16384)])
+def test_in_place_with_rows_ahead(T, W):
+    """The same where rows are copied ahead of their turn, both streams in place; twice, the same bits."""
+    c = Case(T, W, "bf16", seed=8)
+    h, y = L.add_norm(f64(c.x), f64(c.res), f64(c.w), 1e-6)
+    got = []
+    for _ in range(2):
+        x, r = c.x.clone(), c.res.clone()
+        msa.add_norm_quant(x, c.w, residual=r, residual_out=r, out=x)
+        torch.cuda.synchronize()
+        assert ("ring" in msa.last_dispatch()) == (T > 100)
+        got.append((x, r))
+    check(h, y, out=got[0][0], res_out=got[0][1])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing."""
+    cs = [Case(T, 4096, "bf16", seed=T) for T in (2100, 64)]
+    outs = [{n: t[:c.T] for n, t in c.full.items()} for c in cs]
+    want = [{n: t.clone() for n, t in c.run().items()} for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for c, o, s in zip(cs, outs, streams):
+            msa.add_norm_quant(c.x, c.w, residual=c.res, stream=s, **o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(w[n], o[n]) for w, o in zip(want, outs) for n in w)
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-6, 1.0])
 @pytest.mark.parametrize("power", [-120, -70, -30, 30, 66, 120])
 def test_magnitudes(power, eps):

@@ -178,6 +178,36 @@ def test_padded_rows_contiguous_rows_and_in_place():
     assert torch.equal(first, c.q)
 
 
+@pytest.mark.parametrize("T,G,H", [(6000, 4, 64), (6000, 3, 15), (400, 2, 28), (5, 1, 6)])
+def test_in_place_by_warps_per_token(T, G, H):
+    """Queries turned where they lie, with rows on their way ahead of their turn: the bits of another place's."""
+    c = Case(T, G, H, seed=17, kv="fp8", R=64)
+    c.run()
+    first = c.q_out.clone()
+    for _ in range(2):
+        c.q_out = c.q = c.packed[:, :H * D].unflatten(1, (H, D)).contiguous()
+        c.run()
+        assert torch.equal(first, c.q_out)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing."""
+    cs = [Case(T, seed=T, kv="nvfp4", idx="nvfp4") for T in (900, 40)]
+    for c in cs:
+        c.run()
+    outs = lambda c: (c.q_out, c.iq_out, c.cache.k, c.cache.v, c.cache.k_scale, c.cache.v_scale, c.ic.keys, c.ic.block_scale)
+    want = [[t.clone() for t in outs(c)] for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for c, s in zip(cs, streams):
+            msa.qkv_rope_insert(c.dims, c.q, c.k, c.v, c.iq, c.ik, c.pos_d, c.slots_d, c.nr, c.rope, c.q_out, c.iq_out,
+                                c.cache, c.ic, c.flags, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for c, w in zip(cs, want) for a, b in zip(w, outs(c)))
+
+
 @pytest.mark.parametrize("kv", ["fp8", "nvfp4"])
 @pytest.mark.parametrize("idx", [None, "fp8", "nvfp4"])
 @pytest.mark.parametrize("T,G,R,inter", [(70, 4, 128, False), (9, 1, 64, True), (40, 3, 48, False), (300, 2, 80, False)])
