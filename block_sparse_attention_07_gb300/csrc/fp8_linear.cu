@@ -11,9 +11,9 @@
 //
 // What bounds it: the weights' bytes where there are many and few tokens (64 x
 // 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
-// way between CTAs where there are few (1 x 1,280 x 4,096: 4.2 us, an empty launch
+// way between CTAs where there are few (1 x 1,280 x 4,096: 3.9 us, an empty launch
 // 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
-// 14.4 us); for prompts the products with the sums' way back beside them (8,191 x
+// 14.2 us); for prompts the products with the sums' way back beside them (8,191 x
 // 10,240 x 4,096: 237 us, 2.9 PFLOP/s; 265 in a run of a second, where the board's
 // power limit takes the clock to 1.75 GHz).
 #include <cstdlib>
@@ -45,6 +45,10 @@ __device__ __forceinline__ void prefetch_2d(const void* tmap, int x, int y) {
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The same without order among memory accesses: it does not wait for the stores in front of it.
+__device__ __forceinline__ void cluster_meet_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
   uint32_t at;
@@ -358,10 +362,12 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
   if (p.split > 1) cluster_sync_all();
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
   for (int i = rank * blockDim.x + threadIdx.x; i < tokens * (kTile / 4); i += p.split * blockDim.x) {
-    const int t = i >> 5, quad = i & 31;
-    store4(p, tok0 + t, tile * kTile + 4 * quad, sum_cluster<8>(base + place(t, quad) * 4, p.split));
+    const int t = i >> 5, quad = i & 31, r = tile * kTile + 4 * quad;
+    if (r < p.N) store4(p, tok0 + t, r, sum_cluster<8>(base + place(t, quad) * 4, p.split));
   }
-  if (p.split > 1) cluster_sync_all();      // no CTA ends while another reads its sums
+  // No CTA ends while another reads its sums: every read above has come back before the store that its thread made of it,
+  // so that no order among memory accesses is asked for (1 x 1,280 x 4,096: 4.2 -> 3.9 us, 16 4.6 -> 4.1).
+  if (p.split > 1) cluster_meet_relaxed();
 }
 
 // ---------------------------------------------------------------------------
@@ -778,11 +784,11 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 // between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
 // fits to calls whose weights come from memory; what they choose was within 5 % of the fastest at all of 61 sizes of 16
 // to 1,024 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 20.6 / 14.3 / 20.8; pairs on 1 / 2 / 3 30.0 / 21.5 / 19.4;
-//   256 x 10,240 x 4,096: rows 27.0 / 30.7, pairs 18.1 / 30.2; 512 x 4,096 x 8,192: rows 20.7 / 27.5, pairs 29.9 / 21.9;
-//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.7, two per SM 17.1 / 12.8 / 12.2 / 18.9;
-//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 12.2 / 10.5 / 10.6, two per SM on 6 / 8 11.8 / 11.4;
-//   1 x 1,280 x 4,096 on 8 4.2 and 4.6; 64 x 28,672 x 4,096 on 1 27.0 and 22.4.
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 20.8 / 14.2 / 20.2; pairs on 1 / 2 / 3 30.1 / 21.8 / 19.6;
+//   256 x 10,240 x 4,096: rows 28.1 / 30.2, pairs 18.3 / 32.3; 512 x 4,096 x 8,192: rows 21.6 / 27.2, pairs 30.0 / 22.2;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.7 / 18.3 / 16.2 / 20.2, two 16.9 / 12.5 / 11.8 / 17.5;
+//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 11.8 / 10.1 / 10.1, two per SM on 6 / 8 11.3 / 11.0;
+//   16 x 1,280 x 4,096 on 8 4.2 and 4.8; 64 x 28,672 x 4,096 on 1 27.0 and 22.5.
 struct FormCost {
   float launch, block, sums;
 };
@@ -801,7 +807,7 @@ struct RowsForm {
   static constexpr size_t kSmem = C::kTotal + 1024;
   static constexpr FormCost kCost = NT == 128 ? FormCost{6.0f, 0.24f, 0.2f}
                                   : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{4.2f, 0.2f, 0.2f})
-                                          : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.31f, 0.2f} : FormCost{4.5f, 0.35f, 0.8f});
+                                          : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.45f, 0.2f} : FormCost{4.5f, 0.35f, 0.8f});
   // The number of CTAs that share a tile's K, and what the call then costs.
   static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
     static AtOnce cache;
@@ -811,7 +817,7 @@ struct RowsForm {
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
       const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem);
-      const float t = form_us(kCost, a, tiles, at_once, s, true);
+      const float t = form_us(kCost, a, tiles, at_once, s, true) - (s > 1 ? 0.5f : 0.f);
       if (split == 0 || t <= us) {
         split = s;
         us = t;
