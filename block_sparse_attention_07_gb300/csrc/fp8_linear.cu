@@ -37,6 +37,7 @@ struct LinearParams {
   int f32;
   int tiles_m, tiles_n, group;  // pairs: tiles of 256 tokens and of 256 weight rows, token tiles that are walked together
   int quads, boxed;             // rows of the output start on boundaries of four values, of 16 bytes
+  int whole;                    // boxed: the columns in front of a row's last, unfinished 16 bytes
 };
 
 // Asks for a tile of a tensor map in L2. It reads nothing that a later write could make stale: L2 is where all SMs meet.
@@ -460,6 +461,26 @@ __device__ __forceinline__ void store16(const LinearParams& p, int64_t t, int n,
   }
 }
 
+// The columns from p.whole on, of a row that lies at `row_at` of shared memory in 16-byte places swizzled by `swz`, from
+// column x0 on.
+__device__ __forceinline__ void store_rest(const LinearParams& p, int64_t t, uint32_t row_at, uint32_t swz, int x0) {
+  uint32_t w[4];
+  const uint32_t at = row_at + ((static_cast<uint32_t>((p.whole - x0) / (p.f32 ? 4 : 8)) ^ swz) << 4);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  const int left = p.N - p.whole;
+  if (p.f32) {
+    uint32_t* d = static_cast<uint32_t*>(p.out) + t * p.out_stride + p.whole;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < left) d[i] = w[i];
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(p.out) + t * p.out_stride + p.whole;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) d[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
 // Tile number -> its 256 tokens and 256 weight rows: tokens fastest within groups of `group` token tiles, so that the
 // rows that pairs read at one time stay in L2.
 __device__ __forceinline__ void pair_tile(const LinearParams& p, int i, int& tm, int& tn) {
@@ -649,8 +670,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           if (p.f32 || (c & 32) != 0) {
             smem_to_async();
             __syncwarp();
-            const int at = p.f32 ? x0 : x0 - 32;
-            if (lane == 0 && row0 < p.T && at < p.N) tma_store_2d(&to, at, row0, out_at);
+            const int at = p.f32 ? x0 : x0 - 32, cols = p.f32 ? 32 : 64;
+            if (lane == 0 && row0 < p.T && at < p.whole) tma_store_2d(&to, at, row0, out_at);
+            // Tensor copies write 16 bytes at least: what is left of the row, by its thread.
+            if (p.whole < p.N && p.whole >= at && p.whole < at + cols && t < p.T) store_rest(p, t, out_at + lane * 128, lane & 7, at);
           }
         }
       } else if (p.split == 1) {
@@ -735,7 +758,7 @@ static cudaError_t rows_map(CUtensorMap* map, const void* base, int64_t rows, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// 2-D map over the output [T] rows of N, `stride` bytes apart: boxes of 32 rows x 128 bytes in the 128-byte swizzle.
+// 2-D map over the output [T] rows of N (whole 16 bytes), `stride` bytes apart: boxes of 32 rows x 128 bytes in the 128-byte swizzle.
 static cudaError_t out_map(CUtensorMap* map, void* base, int64_t T, int64_t N, int64_t stride, bool f32) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
@@ -882,9 +905,10 @@ struct PairForm {
     if ((err = rows_map(&tw, a.w, a.N, a.K, 128)) != cudaSuccess) return err;
     if ((err = rows_map(&ta, a.a, a.T, a.K, 128)) != cudaSuccess) return err;
     const int64_t stride = a.out_stride * (a.out_f32 ? 4 : 2);
-    p.boxed = stride % 16 == 0 && stride < (1ll << 40);
+    p.whole = a.N / (a.out_f32 ? 4 : 8) * (a.out_f32 ? 4 : 8);
+    p.boxed = stride % 16 == 0 && stride < (1ll << 40) && p.whole > 0;
     memset(&to, 0, sizeof(to));
-    if (p.boxed && (err = out_map(&to, a.out, a.T, a.N, stride, a.out_f32)) != cudaSuccess) return err;
+    if (p.boxed && (err = out_map(&to, a.out, a.T, p.whole, stride, a.out_f32)) != cudaSuccess) return err;
     p.tiles_m = (a.T + 2 * C::kTok - 1) / (2 * C::kTok);
     p.tiles_n = (a.N + C::kOut - 1) / C::kOut;
     const int64_t rows = (32ll << 20) / (2 * C::kTok * static_cast<int64_t>(a.K));

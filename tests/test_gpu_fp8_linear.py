@@ -93,6 +93,21 @@ def test_pairs(monkeypatch, split, T, N, K):
         c.check()
 
 
+@pytest.mark.parametrize("form,T", [("rows", 9), ("rows", 40), ("rows", 60), ("rows", 150), ("pairs", 300)])
+@pytest.mark.parametrize("N", [1, 3, 4, 7, 8, 17, 127, 129, 130, 131, 255, 258, 300, 517])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_lies_behind_a_row(monkeypatch, dtype, N, form, T):
+    """Rows that end anywhere in their last 16 bytes, at a stride of whole ones and at the next odd one."""
+    monkeypatch.setenv("MSA_LINEAR_FORM", form)
+    for pad in (-N % 8, -N % 8 + 8, 1):
+        for split in (1, 2):
+            monkeypatch.setenv("MSA_LINEAR_SPLIT", str(split))
+            c = Case(T, N, 256, dtype, seed=N, pad=pad)
+            c.run()
+            assert msa.last_dispatch().split()[1] == form and msa.last_dispatch().endswith(f"split={split}")
+            c.check()
+
+
 @pytest.mark.parametrize("form,T,split", [("rows", 9, 2), ("rows", 150, 3), ("pairs", 300, 1), ("pairs", 300, 2), ("pairs", 300, 3)])
 @pytest.mark.parametrize("off", [1, 2, 3])
 def test_scales_off_16_bytes(monkeypatch, off, form, T, split):
