@@ -11,9 +11,9 @@
 //
 // What bounds it: the weights' bytes where there are many and few tokens (64 x
 // 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
-// way between CTAs where there are few (1 x 1,280 x 4,096: 3.9 us, an empty launch
+// way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us, an empty launch
 // 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
-// 14.2 us); for prompts the products with the sums' way back beside them (8,191 x
+// 13.7 us); for prompts the products with the sums' way back beside them (8,191 x
 // 10,240 x 4,096: 237 us, 2.9 PFLOP/s; 265 in a run of a second, where the board's
 // power limit takes the clock to 1.75 GHz).
 #include <cstdlib>
@@ -139,7 +139,7 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
 // nothing but columns: a thread has a weight row and up to 32 tokens, whose scales
 // it reads from shared memory. With 128 tokens those reads are as many bytes as the
 // copies and the products take together, so the tokens are M: a thread has a token,
-// 64 weight rows and one scale per block of K (256 x 4,096 x 8,192: 17.6 -> 14.4 us;
+// 64 weight rows and one scale per block of K (256 x 4,096 x 8,192 then: 17.6 -> 14.4 us;
 // 64 tokens as M, half of the product's rows unused: 64 x 100,003 x 4,096 72.4 -> 76.3).
 // Up to 64 tokens there are two sizes: two CTAs per SM, or one with as much memory for copies in flight. kDeep: the latter.
 template <int NT, bool kDeep>
@@ -353,16 +353,20 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
   }
   __syncwarp();
   tmem_fence_before();
-  __syncthreads();
+  // (Without a barrier of the CTA in front of the cluster's: 64 x 4,096 x 8,192 10.1 -> 9.7 us.)
+  if (p.split > 1) cluster_sync_all();      // every CTA's sums are written, and tensor memory has been read
+  else __syncthreads();
   if (warp == C::kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
   if (!C::kTokM && p.split == 1) return;
 
-  if (p.split > 1) cluster_sync_all();
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
-  for (int i = rank * blockDim.x + threadIdx.x; i < tokens * (kTile / 4); i += p.split * blockDim.x) {
+  // With many outputs without the warp that has just given tensor memory back (256 x 4,096 x 8,192: 13.8 -> 13.7 us); with
+  // few the others would take a turn more (16 x 4,096 x 8,192: 8.2 -> 8.5).
+  constexpr int kStore = NT >= 64 ? C::kThreads - 32 : C::kThreads;
+  for (int i = rank * kStore + threadIdx.x; threadIdx.x < kStore && i < tokens * (kTile / 4); i += p.split * kStore) {
     const int t = i >> 5, quad = i & 31, r = tile * kTile + 4 * quad;
     if (r < p.N) store4(p, tok0 + t, r, sum_cluster<8>(base + place(t, quad) * 4, p.split));
   }
@@ -807,11 +811,11 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 // between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
 // fits to calls whose weights come from memory; what they choose was within 5 % of the fastest at all of 61 sizes of 16
 // to 1,024 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 20.8 / 14.2 / 20.2; pairs on 1 / 2 / 3 30.1 / 21.8 / 19.6;
-//   256 x 10,240 x 4,096: rows 28.1 / 30.2, pairs 18.3 / 32.3; 512 x 4,096 x 8,192: rows 21.6 / 27.2, pairs 30.0 / 22.2;
-//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.7 / 18.3 / 16.2 / 20.2, two 16.9 / 12.5 / 11.8 / 17.5;
-//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 11.8 / 10.1 / 10.1, two per SM on 6 / 8 11.3 / 11.0;
-//   16 x 1,280 x 4,096 on 8 4.2 and 4.8; 64 x 28,672 x 4,096 on 1 27.0 and 22.5.
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 21.2 / 13.7 / 19.3; pairs on 1 / 2 / 3 30.0 / 21.9 / 20.3;
+//   256 x 10,240 x 4,096: rows 28.5 / 28.7, pairs 19.1 / 32.8; 512 x 4,096 x 8,192: rows 22.1 / 26.3, pairs 30.0 / 22.7;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.9 / 17.3 / 15.4 / 18.7, two 16.9 / 12.4 / 11.4 / 16.3;
+//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 11.2 / 9.7 / 9.6, two per SM on 6 / 8 11.1 / 10.7;
+//   16 x 1,280 x 4,096 on 8 4.0 and 4.4; 64 x 28,672 x 4,096 on 1 27.0 and 22.5.
 struct FormCost {
   float launch, block, sums;
 };
@@ -829,8 +833,8 @@ struct RowsForm {
   using C = RowsCfg<NT, kDeep>;
   static constexpr size_t kSmem = C::kTotal + 1024;
   static constexpr FormCost kCost = NT == 128 ? FormCost{6.0f, 0.24f, 0.2f}
-                                  : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{4.2f, 0.2f, 0.2f})
-                                          : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.45f, 0.2f} : FormCost{4.5f, 0.35f, 0.8f});
+                                  : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{5.2f, 0.2f, 0.2f})
+                                          : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.45f, 0.2f} : FormCost{5.7f, 0.45f, 0.19f});
   // The number of CTAs that share a tile's K, and what the call then costs.
   static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
     static AtOnce cache;
@@ -840,7 +844,7 @@ struct RowsForm {
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
       const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem);
-      const float t = form_us(kCost, a, tiles, at_once, s, true) - (s > 1 ? 0.5f : 0.f);
+      const float t = form_us(kCost, a, tiles, at_once, s, true) - (s > 1 ? 0.9f : 0.f);
       if (split == 0 || t <= us) {
         split = s;
         us = t;
