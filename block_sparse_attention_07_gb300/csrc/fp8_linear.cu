@@ -13,7 +13,7 @@
 // 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
 // way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us, an empty launch
 // 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
-// 13.7 us); for prompts the products with the sums' way back beside them (8,191 x
+// 13.1 us); for prompts the products with the sums' way back beside them (8,191 x
 // 10,240 x 4,096: 237 us, 2.9 PFLOP/s; 265 in a run of a second, where the board's
 // power limit takes the clock to 1.75 GHz).
 #include <cstdlib>
@@ -94,6 +94,11 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
       : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(s0), "f"(s1));
 }
 
+__device__ __forceinline__ float4 ld_shared4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
 // 16 bytes of another CTA's shared memory.
 __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
   const uint32_t at = cluster_addr(saddr, rank);
@@ -101,18 +106,6 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, int rank) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
   return v;
 }
-// Sum of the values at `saddr` in the first `split` CTAs, in this order, all of them on their way together.
-template <int kMost>
-__device__ __forceinline__ float4 sum_cluster(uint32_t saddr, int split) {
-  float4 x[kMost];
-#pragma unroll
-  for (int q = 0; q < kMost; ++q) x[q] = q < split ? ld_cluster(saddr, q) : make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 v = x[0];
-#pragma unroll
-  for (int q = 1; q < kMost; ++q) { v.x += x[q].x; v.y += x[q].y; v.z += x[q].z; v.w += x[q].w; }
-  return v;
-}
-
 __device__ __forceinline__ void store_out(const LinearParams& p, int64_t t, int n, float v) {
   if (p.f32) static_cast<float*>(p.out)[t * p.out_stride + n] = v;
   else static_cast<__nv_bfloat16*>(p.out)[t * p.out_stride + n] = __float2bfloat16_rn(v);
@@ -130,6 +123,38 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
 #pragma unroll
   for (int u = 0; u < 4; ++u)
     if (n + u < p.N) store_out(p, t, n + u, e[u]);
+}
+
+// A CTA's share of a tile's outputs, from the sums of the first `split` <= kMost CTAs of its cluster, added in rank order.
+// Thread `me` of `threads` takes four outputs of a row, kAhead times at one time: with all the sums on their way together
+// a tile of 128 tokens by itself is 2.5 us shorter (128 x 10,240 x 4,096: 15.6 -> 13.0), with two CTAs 0.5 (256 x 4,096 x
+// 8,192: 13.7 -> 13.2); more CTAs have enough on their way with one (64 x 4,096 x 8,192 on four: 9.6 and 9.7).
+template <int kMost, int kAhead, typename Place>
+__device__ __forceinline__ void join_sums(const LinearParams& p, uint32_t base, Place place, int tokens, int tok0, int row0, int rank,
+                                          int me, int threads) {
+  const int hop = p.split * threads, all = tokens * (kTile / 4);
+  for (int i0 = rank * threads + me; i0 < all; i0 += kAhead * hop) {
+    if (kAhead == 1 && row0 + 4 * (i0 & 31) >= p.N) continue;
+    float4 x[kAhead][kMost];
+    auto live = [&](int b) { return kAhead == 1 || (i0 + b * hop < all && row0 + 4 * ((i0 + b * hop) & 31) < p.N); };
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b)
+#pragma unroll
+      for (int q = 0; q < kMost; ++q) {
+        const int i = i0 + b * hop;
+        const uint32_t at = base + place(i >> 5, i & 31) * 4;
+        if (q < p.split && live(b)) x[b][q] = kMost == 1 ? ld_shared4(at) : ld_cluster(at, q);
+        else x[b][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      const int i = i0 + b * hop;
+      float4 v = x[b][0];
+#pragma unroll
+      for (int q = 1; q < kMost; ++q) { v.x += x[b][q].x; v.y += x[b][q].y; v.z += x[b][q].z; v.w += x[b][q].w; }
+      if (live(b)) store4(p, tok0 + (i >> 5), row0 + 4 * (i & 31), v);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -363,12 +388,15 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
   if (!C::kTokM && p.split == 1) return;
 
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
-  // With many outputs without the warp that has just given tensor memory back (256 x 4,096 x 8,192: 13.8 -> 13.7 us); with
+  // With many outputs without the warp that has just given tensor memory back (128 x 4,096 x 8,192 on two CTAs: 13.5 -> 13.3 us); with
   // few the others would take a turn more (16 x 4,096 x 8,192: 8.2 -> 8.5).
   constexpr int kStore = NT >= 64 ? C::kThreads - 32 : C::kThreads;
-  for (int i = rank * kStore + threadIdx.x; threadIdx.x < kStore && i < tokens * (kTile / 4); i += p.split * kStore) {
-    const int t = i >> 5, quad = i & 31, r = tile * kTile + 4 * quad;
-    if (r < p.N) store4(p, tok0 + t, r, sum_cluster<8>(base + place(t, quad) * 4, p.split));
+  if (threadIdx.x < kStore) {
+    const int row0 = tile * kTile;
+    if (C::kTokM && p.split == 1) join_sums<1, 8>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
+    else if (p.split == 2) join_sums<2, 4>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
+    else if (p.split <= 4) join_sums<4, 1>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
+    else join_sums<8, 1>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
   }
   // No CTA ends while another reads its sums: every read above has come back before the store that its thread made of it,
   // so that no order among memory accesses is asked for (1 x 1,280 x 4,096: 4.2 -> 3.9 us, 16 4.6 -> 4.1).
@@ -808,31 +836,31 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 }
 
 // What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
-// between CTAs, 2.5 more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
-// fits to calls whose weights come from memory; what they choose was within 5 % of the fastest at all of 61 sizes of 16
+// between CTAs, some more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
+// fits to calls whose weights come from memory; what they choose was within 4 % of the fastest at 60 of 61 sizes of 16
 // to 1,024 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 21.2 / 13.7 / 19.3; pairs on 1 / 2 / 3 30.0 / 21.9 / 20.3;
-//   256 x 10,240 x 4,096: rows 28.5 / 28.7, pairs 19.1 / 32.8; 512 x 4,096 x 8,192: rows 22.1 / 26.3, pairs 30.0 / 22.7;
-//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.9 / 17.3 / 15.4 / 18.7, two 16.9 / 12.4 / 11.4 / 16.3;
-//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 11.2 / 9.7 / 9.6, two per SM on 6 / 8 11.1 / 10.7;
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 18.8 / 13.1 / 19.4; pairs on 1 / 2 / 3 30.0 / 21.9 / 20.1;
+//   256 x 10,240 x 4,096: rows 23.4 / 27.1, pairs 19.1 / 32.7; 512 x 4,096 x 8,192: rows 19.1 / 25.0, pairs 29.9 / 22.4;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.9 / 16.8 / 15.3 / 18.7, two 17.2 / 12.3 / 11.4 / 16.4;
+//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 10.9 / 9.6 / 9.6, two per SM on 6 / 8 11.2 / 10.8;
 //   16 x 1,280 x 4,096 on 8 4.0 and 4.4; 64 x 28,672 x 4,096 on 1 27.0 and 22.5.
 struct FormCost {
   float launch, block, sums;
 };
-static float form_us(const FormCost& c, const LinearArgs& a, int64_t clusters, int at_once, int split, bool restart) {
+static float form_us(const FormCost& c, const LinearArgs& a, int64_t clusters, int at_once, int split, float restart) {
   const int64_t waves = (clusters + at_once - 1) / at_once;
   const int KB = (a.K + kTile - 1) / kTile;
   const float sums = split > 1 ? c.sums * static_cast<float>(split) : 0.f;
   const float us = static_cast<float>(waves) * (static_cast<float>((KB + split - 1) / split) * c.block + sums);
   const float bytes = static_cast<float>(a.N) * static_cast<float>(a.K) / 7.0e6f + sums;
-  return c.launch + (us > bytes ? us : bytes) + 2.5f * static_cast<float>(restart ? waves - 1 : 0);
+  return c.launch + (us > bytes ? us : bytes) + restart * static_cast<float>(waves - 1);
 }
 
 template <int NT, bool kDeep>
 struct RowsForm {
   using C = RowsCfg<NT, kDeep>;
   static constexpr size_t kSmem = C::kTotal + 1024;
-  static constexpr FormCost kCost = NT == 128 ? FormCost{6.0f, 0.24f, 0.2f}
+  static constexpr FormCost kCost = NT == 128 ? FormCost{6.5f, 0.19f, 0.18f}
                                   : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{5.2f, 0.2f, 0.2f})
                                           : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.45f, 0.2f} : FormCost{5.7f, 0.45f, 0.19f});
   // The number of CTAs that share a tile's K, and what the call then costs.
@@ -844,7 +872,7 @@ struct RowsForm {
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
       const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem);
-      const float t = form_us(kCost, a, tiles, at_once, s, true) - (s > 1 ? 0.9f : 0.f);
+      const float t = form_us(kCost, a, tiles, at_once, s, C::kCtas == 1 ? 5.f : 2.5f) - (s > 1 ? 0.9f : 0.f);
       if (split == 0 || t <= us) {
         split = s;
         us = t;
@@ -895,7 +923,7 @@ struct PairForm {
     split = 0;
     for (int s = forced ? forced : 1; s <= (forced ? forced : 4) && s <= KB; ++s) {
       // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
-      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 2.f : 6.f / static_cast<float>(s)}, a, tiles(a), at_once(dev, s), s, s > 1);
+      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 2.f : 6.f / static_cast<float>(s)}, a, tiles(a), at_once(dev, s), s, s > 1 ? 2.5f : 0.f);
       t += 1.1f * static_cast<float>((tiles(a) + at_once(dev, s) - 1) / at_once(dev, s));
       if (split == 0 || t < us) {
         split = s;
