@@ -14,7 +14,7 @@
 // way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us, an empty launch
 // 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
 // 13.1 us); for prompts the products with the sums' way back beside them (8,191 x
-// 10,240 x 4,096: 237 us, 2.9 PFLOP/s; 265 in a run of a second, where the board's
+// 10,240 x 4,096: 233 us, 2.95 PFLOP/s; 258 in a run of a second, where the board's
 // power limit takes the clock to 1.75 GHz).
 #include <cstdlib>
 #include <cstring>
@@ -411,11 +411,11 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
 // product of scales per block of K serves its 128 outputs. With few tiles, `split`
 // pairs of a cluster share a tile's K, and each finishes every split-th 16 columns
 // from the sums that the others copy there; otherwise a pair walks over the tiles.
-// A block takes some 830 cycles; without reading its sums back 710, as far as the
-// power limit lets the products go (8,191 x 10,240 x 4,096: 237 and 204 us).
+// A block takes some 810 cycles; without reading its sums back 710, as far as the
+// power limit lets the products go (8,191 x 10,240 x 4,096: 233 and 204 us).
 struct PairCfg {
   static constexpr int kTok = 128, kOut = 256;                        // a CTA's tokens, a tile's weight rows
-  static constexpr int kStages = 6, kAcc = 2;
+  static constexpr int kStages = 5, kAcc = 2;
   static constexpr uint32_t kStage = 2 * 128 * 128;
   static constexpr uint32_t oOut = kStages * kStage, kOutBuf = 32 * 128;   // 128 bytes of 32 rows per warp on their way out
   static constexpr uint32_t oBars = oOut + 8 * kOutBuf;
@@ -432,9 +432,9 @@ struct PairCfg {
 constexpr int pair_share(int part, int split) { return (PairCfg::kUnits - part + split - 1) / split; }   // units of a pair
 constexpr bool pair_sums_fit(int split) {             // those that leave a CTA, and those that come
   const int most = pair_share(0, split);
-  return 2 * (split - 1) * most * PairCfg::kUnit <= PairCfg::kStages * PairCfg::kStage;
+  return 2 * (split - 1) * most * PairCfg::kUnit <= PairCfg::oBars;
 }
-static_assert(pair_sums_fit(2) && pair_sums_fit(3) && pair_sums_fit(4), "the others' sums fit into the stages");
+static_assert(pair_sums_fit(2) && pair_sums_fit(3) && pair_sums_fit(4), "the others' sums fit into the stages and the buffers behind them");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -634,18 +634,26 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     const uint32_t free0 = cluster_addr(acc_free(0), lead_rank);
     const uint32_t out_at = base + C::oOut + (warp - 4) * C::kOutBuf;
     const int blocks = (p.N + 127) / 128;
-    int n = 0;
-    for (int i = first; i < tiles; i += clusters) {
-      int tm, tn;
+    int n = 0, tm, tn;
+    const float* sa = nullptr;
+    const float* sw = nullptr;
+    float s_next = 0.f, w_next = 0.f;
+    auto token = [&]() { return static_cast<int64_t>(tm) * 2 * C::kTok + half * C::kTok + sub * 32 + lane; };
+    auto enter = [&](int i) {                 // the tile's places; its first scales on their way, in front of the last tile's stores
       pair_tile(p, i, tm, tn);
-      const int64_t t = static_cast<int64_t>(tm) * 2 * C::kTok + half * C::kTok + sub * 32 + lane;
       const int wb = tn * 2 + g < blocks ? tn * 2 + g : blocks - 1;   // (a half without weight rows: any scale)
-      const float* sa = p.sa + (t < p.T ? t : 0) * p.KB;
-      const float* sw = p.sw + static_cast<int64_t>(wb) * p.KB;
+      sa = p.sa + (token() < p.T ? token() : 0) * p.KB;
+      sw = p.sw + static_cast<int64_t>(wb) * p.KB;
+      s_next = sa[kb0];
+      w_next = sw[kb0];
+    };
+    enter(first);
+    for (int i = first; i < tiles; i += clusters) {
+      const int64_t t = token();
+      const int n0 = tn * C::kOut + g * 128;
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      float s_next = sa[kb0], w_next = sw[kb0];
       // 32 columns at a time, the next ones on their way while the last are added, the next block's first among them
       float x[2][32];
       ok = ok && warp_wait(acc_full(n & 1), (n >> 1) & 1);
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           for (int u = 0; u < 32; u += 2) fma2(acc[32 * c + u], acc[32 * c + u + 1], x[c & 1][u], x[c & 1][u + 1], f);
         }
       }
-      const int n0 = tn * C::kOut + g * 128;
+      if (i + clusters < tiles) enter(i + clusters);
       if (p.split == 1 && p.boxed) {
         // 128 bytes of every row at a time, swizzled as the tensor map has them
         const int row0 = static_cast<int>(t) - lane;
@@ -732,7 +740,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         if (warp == 4 && lane == 0) mbar_arrive_expect_tx(got_bar, (p.split - 1) * own * C::kUnit);
         smem_to_async();
         tmem_fence_before();
-        cluster_sync_all();                 // every CTA's sums are written, and the stages behind them free
+        cluster_sync_all();                 // every CTA's sums are written, and what lies behind them is free
         if (warp == 4 && lane < p.split && lane != part) {
           const int slot = part < lane ? part : part - 1;
           const uint32_t to = 2 * lane + half;
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
                   acc[16 * u + 4 * c + 2] += v.z; acc[16 * u + 4 * c + 3] += v.w;
                 }
               }
-              if (t < p.T) store16(p, t, tn * C::kOut + 16 * unit(u), acc + 16 * u);
+              if (t < p.T) store16(p, t, n0 + 16 * u, acc + 16 * u);
             }
           }
         }
