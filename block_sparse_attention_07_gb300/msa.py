@@ -9,6 +9,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import dataclasses
 import math
 import os
@@ -196,6 +197,21 @@ class IndexCache:
         return _IndexCache(self.dtype, _ptr(self.keys), _ptr(self.scale), _ptr(self.block_scale), self.global_scale)
 
 
+@functools.cache
+def _bare(name):
+    """The entry point without declared argument types: it takes converted arguments as they are."""
+    fn = lib[name]
+    fn.restype = ctypes.c_int
+    return fn
+
+
+def _converted(kind, arg):
+    """An argument converted to its declared type, as ctypes would for every call."""
+    if isinstance(arg, ctypes.c_void_p):
+        arg = arg.value
+    return kind.from_param(arg)
+
+
 class Prepared:
     """A library call whose arguments were marshalled once; calling it launches again.
 
@@ -203,13 +219,15 @@ class Prepared:
     alive by the caller. Launches on the stream that was given, or current,
     when it was made. Used on launch-bound paths (the same call issued every
     decode step)."""
-    __slots__ = ("fn", "args", "keep", "what")
+    __slots__ = ("fn", "args", "keep", "what", "_bare", "_raw")
 
     def __init__(self, fn, args, keep, what):
         self.fn, self.args, self.keep, self.what = fn, args, keep, what
+        # The arguments as the call passes them, for a function object that converts none: 0.5 to 1 us less per call.
+        self._bare, self._raw = _bare(fn.__name__), tuple(_converted(t, a) for t, a in zip(fn.argtypes, args, strict=True))
 
     def __call__(self):
-        st = self.fn(*self.args)
+        st = self._bare(*self._raw)
         if st != OK:
             raise MSAError(st, self.what)
 
