@@ -19,8 +19,9 @@
 // Bound by the rows' bytes: as many as possible are kept in flight, the queries of
 // a token (contiguous, whatever the token's stride) by bulk copies into a ring per
 // warp, with keys and values done while the first of them arrive. 8,191 tokens, 64 +
-// 4 + 4 heads, FP8 cache: 52.9 us, 5.5 TB/s (82 % of a copy's rate); 16,000 tokens
-// 94.7 us (89 %); 64 tokens 4.3 us, the host's time per launch. With fewer heads what
+// 4 + 4 heads, FP8 cache: 53.0 us, 5.5 TB/s (82 % of a copy's rate); 16,000 tokens
+// 94.0 us (90 %); 64 tokens, bf16 cache: 4.0 us, of which 0.7 pass until a kernel may
+// start and 0.5 each for positions and for rows. With fewer heads what
 // comes before a warp's queries (position, sines, slot, keys) shows: 16 + 1 + 1 heads
 // 21.2 us for 8,191 tokens (51 % of a copy's rate).
 //
@@ -57,7 +58,7 @@ struct RopeParams {
   float low;                   // mean squares below it are too small beside eps
   int H, I, R;
   int parts;                   // warps per token
-  uint64_t turn[kDim / 2];     // freq / 2 pi, in units of 2^-64 of a turn
+  alignas(16) uint64_t turn[kDim / 2];     // freq / 2 pi, in units of 2^-64 of a turn
 };
 
 __device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v) {
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
   const int part = static_cast<int>(wid - t * pp.parts);
   if (t >= p.T) return;
 
-  const int q_passes = nq / 4;
+  const int q_passes = pp.parts * 4 >= rows ? 0 : nq / 4;       // a warp with one pass loads its rows itself (64 tokens: 4.7 -> 4.6 us)
   const uint16_t* q_row = pp.q + t * pp.q_stride;
   const uint32_t rows_at = smem_addr(ring_rows) + warp * kRopeSlots * kRopeGroup;
   const uint32_t bars_at = smem_addr(ring_bars) + warp * kRopeSlots * 8;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
   }
   __syncwarp();
 
+  const int64_t slot = p.slots[t];
   // the lane's chunks, and which of its pairs turn: all or none of a chunk's
   const int n = pp.R / 16;
   const int ca = kPairs || l < n ? l : n + l, cb = kPairs || l >= n ? 8 + l : n + l;
@@ -170,16 +172,23 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
   {
     const int64_t pos = pp.positions[t];
     float c2[2], s2[2];
+    // pairs i and i + 1 of the lane
+    const int i = 2 * (lane >> 3);
+    const bool on = kPairs && i >= 4 ? turn_b : turn_a;
+    const int at = !kPairs ? 8 * l + i : i < 4 ? 4 * ca + i : 4 * cb + i - 4;
+    // Through an address, as memory: read as parameters, lanes at 32 places take 32 turns (64 tokens: 4.6 -> 4.0 us, whole
+    // heads 5.7 -> 4.3).
+    const uint64_t* tp = pp.turn;
+    asm volatile("" : "+l"(tp));
+    ulonglong2 two = make_ulonglong2(0, 0);
+    if (on) two = *reinterpret_cast<const ulonglong2*>(tp + at);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = 2 * (lane >> 3) + e;
-      const bool on = kPairs && i >= 4 ? turn_b : turn_a;
-      const int at = !kPairs ? 8 * l + i : i < 4 ? 4 * ca + i : 4 * cb + i - 4;
       c2[e] = 1.f;
       s2[e] = 0.f;
       if (on) {
-        const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * pp.turn[at]);   // modulo one turn
-        sincospif(static_cast<float>(turn) * 0x1p-63f, &s2[e], &c2[e]);                         // half turns in [-1, 1]
+        const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * (e ? two.y : two.x));   // modulo one turn
+        sincospif(static_cast<float>(turn) * 0x1p-63f, &s2[e], &c2[e]);                                 // half turns in [-1, 1]
         c2[e] *= pp.gain;
         s2[e] *= pp.gain;
       }
@@ -190,7 +199,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
       sn[i] = __shfl_sync(0xffffffffu, s2[i & 1], 8 * (i >> 1) + l);
     }
   }
-  const int64_t slot = p.slots[t];
   const int64_t page = slot / kBlock, off = slot % kBlock;
   const bool held = slot >= 0 && slot < p.num_slots;
   if (slot >= p.num_slots && part == 0 && lane == 0) set_flag(p.flags, MSA_FLAG_BAD_SLOT);
