@@ -11,8 +11,8 @@
 //
 // What bounds it: the weights' bytes where there are many and few tokens (64 x
 // 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
-// way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us, an empty launch
-// 3.1); in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
+// way between CTAs where there are few (1 x 1,280 x 4,096: 3.7 us);
+// in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
 // 13.1 us); for prompts the products with the sums' way back beside them (8,191 x
 // 10,240 x 4,096: 233 us, 2.95 PFLOP/s; 258 in a run of a second, where the board's
 // power limit takes the clock to 1.75 GHz).

@@ -19,8 +19,8 @@
 // contiguous) on their way to its own part of shared memory by bulk copies,
 // and does the keys and values while the first of them arrive. 8,191 tokens,
 // 64 + 4 + 4 heads, FP8 cache: 51.3 us, 5.7 TB/s (85 % of a copy's rate); with
-// loads into registers, two groups ahead, 59.2 us. 64 tokens: 4.3 us, the
-// host's time per launch. With fewer heads a warp has fewer groups than its part
+// loads into registers, two groups ahead, 59.2 us. 64 tokens, bf16 cache: 3.9
+// us. With fewer heads a warp has fewer groups than its part
 // holds, and what comes before the first of them (position, sines, slot, weights)
 // shows: 32 + 2 + 2 heads 34.6 us (63 % of a copy's rate), 16 + 1 + 1 29.9 (37 %).
 //
@@ -54,8 +54,8 @@ struct MropeParams {
   float eps;
   int H, I;
   int parts;                   // warps per token
-  uint64_t turn[kDim / 2];     // theta^(-2i/D) / 2 pi, in units of 2^-64 of a turn
-  uint8_t axis[kDim / 2];
+  alignas(16) uint64_t turn[kDim / 2];     // theta^(-2i/D) / 2 pi, in units of 2^-64 of a turn
+  alignas(16) uint8_t axis[kDim / 2];
 };
 
 // One half (8 values) of an NVFP4 row: a 16-value group belongs to two lanes.
@@ -123,6 +123,7 @@ __device__ __forceinline__ void store_idx16(const InsertParams& p, int64_t row, 
   if (l == 0) p.idx_scale[row] = s;
 }
 
+template <bool kFew>                      // all warps begin at one time
 __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_insert_kernel(const __grid_constant__ MropeParams pp) {
   __shared__ alignas(128) uint8_t ring_rows[kMropeWarps * kRingSlots * kPassBytes];
   __shared__ uint64_t ring_bars[kMropeWarps * kRingSlots];
@@ -157,12 +158,24 @@ __global__ void __launch_bounds__(32 * kMropeWarps, kMropeCtas) qk_norm_mrope_in
   // four lanes that use it
   float cs[8], sn[8];
   {
+    // Axes and frequencies of two pairs. Read as parameters, lanes at 32 places take 32 turns, which shows where all warps
+    // begin at one time: so through addresses, as memory (64 tokens, calls in a row: 6.6 -> 3.9 us, 512 9.8 -> 7.9). Where
+    // warps follow one another it does not, and spreads them (8,191 tokens: 52.0 as memory, 51.0 as parameters).
+    const int i = 8 * l + 2 * (lane >> 3);
+    uchar2 ax = make_uchar2(0, 0);
+    ulonglong2 two = make_ulonglong2(0, 0);
+    if (kFew) {
+      const uint64_t* turns = pp.turn;
+      const uint8_t* axes = pp.axis;
+      asm volatile("" : "+l"(turns), "+l"(axes));
+      ax = *reinterpret_cast<const uchar2*>(axes + i);
+      two = *reinterpret_cast<const ulonglong2*>(turns + i);
+    }
     float c2[2], s2[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = 8 * l + 2 * (lane >> 3) + e;
-      const int64_t pos = pp.positions[pp.axis[i] * pp.pos_stride + t];
-      const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * pp.turn[i]);   // modulo one turn
+      const int64_t pos = pp.positions[(!kFew ? pp.axis[i + e] : e ? ax.y : ax.x) * pp.pos_stride + t];
+      const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * (!kFew ? pp.turn[i + e] : e ? two.y : two.x));   // modulo one turn
       sincospif(static_cast<float>(turn) * 0x1p-63f, &s2[e], &c2[e]);                        // half turns in [-1, 1]
     }
 #pragma unroll
@@ -331,8 +344,9 @@ cudaError_t launch_qk_norm_mrope_insert(const PrologueArgs& a, const msa_rope_ax
   pp.parts = static_cast<int>(parts);
   const int64_t grid = (a.ins.T * parts + kMropeWarps - 1) / kMropeWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  const cudaError_t err = launch_pdl(qk_norm_mrope_insert_kernel, dim3(static_cast<unsigned>(grid)),
-                                     dim3(32 * kMropeWarps), 0, stream, pp);
+  const bool few = a.ins.T * parts <= kMropeWarps * kMropeCtas * sms;
+  const cudaError_t err = launch_pdl(few ? qk_norm_mrope_insert_kernel<true> : qk_norm_mrope_insert_kernel<false>,
+                                     dim3(static_cast<unsigned>(grid)), dim3(32 * kMropeWarps), 0, stream, pp);
   if (err != cudaSuccess) return err;
   rec->set("qk_norm_mrope_insert %s%s grid=%lld block=%d warps_per_token=%d heads=%d+%d+%d axes=%d",
            a.ins.kv_nvfp4 ? "nvfp4" : a.ins.kv_fp8 ? "fp8" : "bf16",

@@ -19,8 +19,8 @@
 // Bound by the rows' bytes: as many as possible are kept in flight, the queries of
 // a token (contiguous, whatever the token's stride) by bulk copies into a ring per
 // warp, with keys and values done while the first of them arrive. 8,191 tokens, 64 +
-// 4 + 4 heads, FP8 cache: 53.0 us, 5.5 TB/s (82 % of a copy's rate); 16,000 tokens
-// 94.0 us (90 %); 64 tokens, bf16 cache: 4.0 us, of which 0.7 pass until a kernel may
+// 4 + 4 heads, FP8 cache: 52.5 us, 5.6 TB/s (83 % of a copy's rate); 16,000 tokens
+// 93.7 us (90 %); 64 tokens, bf16 cache: 4.0 us, of which 0.7 pass until a kernel may
 // start and 0.5 each for positions and for rows. With fewer heads what
 // comes before a warp's queries (position, sines, slot, keys) shows: 16 + 1 + 1 heads
 // 21.2 us for 8,191 tokens (51 % of a copy's rate).
@@ -30,6 +30,7 @@
 // the frequency, 2^-24 of a turn at the largest 32-bit position and frequency 1.
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "rope_rows.cuh"
 
@@ -126,7 +127,7 @@ __device__ __forceinline__ void write_idx(const InsertParams& p, int64_t row, co
   if (l == 0) p.idx_scale[row] = s;
 }
 
-template <bool kPairs, bool kNorm>        // interleaved pairs (2i, 2i + 1); norms
+template <bool kPairs, bool kNorm, bool kFew>       // interleaved pairs (2i, 2i + 1); norms; all warps begin at one time
 __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_kernel(const __grid_constant__ RopeParams pp) {
   __shared__ alignas(128) uint8_t ring_rows[kRopeWarps * kRopeSlots * kRopeGroup];
   __shared__ alignas(16) uint8_t turn_rows[kRopeWarps * kRopeGroup];
@@ -176,12 +177,17 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) qkv_rope_insert_ke
     const int i = 2 * (lane >> 3);
     const bool on = kPairs && i >= 4 ? turn_b : turn_a;
     const int at = !kPairs ? 8 * l + i : i < 4 ? 4 * ca + i : 4 * cb + i - 4;
-    // Through an address, as memory: read as parameters, lanes at 32 places take 32 turns (64 tokens: 4.6 -> 4.0 us, whole
-    // heads 5.7 -> 4.3).
-    const uint64_t* tp = pp.turn;
-    asm volatile("" : "+l"(tp));
+    // Read as parameters, lanes at 32 places take 32 turns, which shows where all warps begin at one time: so through an
+    // address, as memory (64 tokens: 4.6 -> 4.0 us, whole heads 5.7 -> 4.3). Where warps follow one another it does not, and
+    // spreads them (8,191 tokens: 53.1 as memory, 52.4 as parameters).
     ulonglong2 two = make_ulonglong2(0, 0);
-    if (on) two = *reinterpret_cast<const ulonglong2*>(tp + at);
+    if (on && kFew) {
+      const uint64_t* turns = pp.turn;
+      asm volatile("" : "+l"(turns));
+      two = *reinterpret_cast<const ulonglong2*>(turns + at);
+    } else if (on) {
+      two = make_ulonglong2(pp.turn[at], pp.turn[at + 1]);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       c2[e] = 1.f;
@@ -382,8 +388,13 @@ cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, Dispa
   const int64_t grid = (a.ins.T * parts + kRopeWarps - 1) / kRopeWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const bool pairs = a.rope->layout == MSA_ROPE_INTERLEAVED;
-  const cudaError_t err = launch_pdl(pairs ? (a.wq ? qkv_rope_insert_kernel<true, true> : qkv_rope_insert_kernel<true, false>)
-                                           : (a.wq ? qkv_rope_insert_kernel<false, true> : qkv_rope_insert_kernel<false, false>),
+  const bool few = a.ins.T * parts <= kRopeWarps * kRopeCtas * sms;
+  auto pick = [&](auto all) {
+    constexpr bool kFew = decltype(all)::value;
+    return pairs ? (a.wq ? qkv_rope_insert_kernel<true, true, kFew> : qkv_rope_insert_kernel<true, false, kFew>)
+                 : (a.wq ? qkv_rope_insert_kernel<false, true, kFew> : qkv_rope_insert_kernel<false, false, kFew>);
+  };
+  const cudaError_t err = launch_pdl(few ? pick(std::true_type()) : pick(std::false_type()),
                                      dim3(static_cast<unsigned>(grid)), dim3(32 * kRopeWarps), 0, stream, pp);
   if (err != cudaSuccess) return err;
   rec->set("qkv_rope_insert %s%s %s%s dims=%d grid=%lld block=%d warps_per_token=%d heads=%d+%d+%d",
