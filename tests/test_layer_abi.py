@@ -256,3 +256,29 @@ def test_calls_without_tokens(m, monkeypatch):
                           heads[:, 76:] if idx else None, z(0, dt=torch.int32), z(0, dt=torch.int64), m.make_norm_rope(*w),
                           m.make_rope(), z(0, 64, 128, dt=bf), z(0, 4, 128, dt=bf) if idx else None, cache, index if idx else None, flags)
         assert m.last_dispatch() == "qkv_rope_insert empty"
+
+
+def test_prepared_calls_are_the_plain_ones(m, monkeypatch):
+    """A prepared call passes the same arguments, every time: addresses, missing ones, sizes, floats and host structs."""
+    monkeypatch.setattr(m, "_stream", lambda stream: None)
+    monkeypatch.setattr(m, "_want_on_device", lambda *a, **k: None)
+    for run, args in calls(m).values():
+        seen = []
+        monkeypatch.setattr(m, "_call", lambda fn, a, keep, what, prepare: seen.append((fn, a, keep, what)))
+        run(**args)
+        fn, a, keep, what = seen[0]
+        p = m.Prepared(fn, a, keep, what)
+        types = [ctypes.c_void_p if issubclass(t, ctypes._Pointer) else t for t in fn.argtypes]
+        got = []
+        probe = ctypes.CFUNCTYPE(ctypes.c_int, *types)(lambda *x: got.append(x) or 0)
+        bare = ctypes.CFUNCTYPE(ctypes.c_int)(ctypes.cast(probe, ctypes.c_void_p).value)
+        typed = ctypes.CFUNCTYPE(ctypes.c_int, *fn.argtypes)(ctypes.cast(probe, ctypes.c_void_p).value)
+        typed(*a)
+        p._bare = bare
+        p(), p()
+        assert len(got) == 3 and got[0] == got[1] == got[2]
+    bad = m.Prepared(m.lib.msa_add_norm_quant, (2, 120, FAKE, 120, None, None, 1, FAKE, 1e-6, FAKE, None, None, None), (), "norm")
+    for _ in range(2):
+        with pytest.raises(m.MSAError) as e:
+            bad()
+        assert e.value.status == m.ERR_UNSUPPORTED
