@@ -492,8 +492,8 @@ msa_status_t msa_paged_gqa_decode(const msa_dims_t* dims, const void* q, const m
  *   y = h / sqrt(mean(h^2) + eps) * weight, from the unrounded h; y = h with
  *       weight = NULL (which rounds an attention output for its projection);
  *   out = bf16(y), and per 128 values (the last group may be shorter)
- *   scales = max|y| / 448, codes = E4M3_RNE_satfinite(y * (1 / scale)), IEEE
- *       divisions; a group of zeros has scale 0 and codes 0.
+ *   scales = max|y| / 448, codes = E4M3_RNE_satfinite(y / scale), the codes of
+ *       IEEE divisions; a group of zeros has scale 0 and codes 0.
  * Squares beyond fp32's range are no limit: such rows are scaled by a power of
  * two. A group that holds a NaN or an infinity comes out as NaN where its scale
  * is applied; a row that holds one is NaN there after the norm, and zero where

@@ -8,7 +8,7 @@ fused projection, norm, rotary embedding and insert; the pages give no formulas.
 The readings are this project's:
 
 * h = x + r; y = h / sqrt(mean(h^2) + eps) * w; rows in 8 bits: per 128 values
-  s = max|y| / 448, code = E4M3(y * (1 / s)) (``quant_rows`` does that step in fp32
+  s = max|y| / 448, code = E4M3(y / s) (``quant_rows`` does that step in fp32
   with one rounding per operation, so that it is an exact function of y).
 * out[t, n] = sum_g sa[t, g] sw[n / 128, g] sum_{k in g} a[t, k] w[n, k].
 * rotary: pair i turns by position * freq_i, cosine and sine times a gain; pairs
@@ -43,9 +43,7 @@ def quant_rows(y):
         s = (np.max(np.abs(part), axis=1) / np.float32(448.0)).astype(np.float32)
         scales[:, g] = s
         for t in np.flatnonzero(s):
-            up = np.float32(2.0 ** 100 if s[t] < 2.0 ** -126 else 1.0)
-            inv = (np.float32(1.0) / (s[t] * up)).astype(np.float32)
-            codes[t, g * GROUP:(g + 1) * GROUP] = formats.e4m3_encode((part[t] * up * inv).astype(np.float32))
+            codes[t, g * GROUP:(g + 1) * GROUP] = formats.e4m3_encode((part[t] / s[t]).astype(np.float32))
     return codes, scales
 
 
