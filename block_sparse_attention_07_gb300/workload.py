@@ -332,13 +332,17 @@ class DeviceWorkload:
             pro = self._prologue_state()
             packed = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
             cut = [H, G, G] + ([I, I] if self.has_index else [])
-            st = self._layer = dict(
+            st = dict(
                 hidden=hidden, norm=1.0 + 0.1 * torch.randn(hidden, generator=gen, device=dev), w_in=weight(heads * D, hidden),
                 w_out=weight(hidden, H * D), x8=rows(hidden), o8=rows(H * D), packed=packed,
                 parts=list(packed.split(cut, 1)) + [None] * (5 - len(cut)), rope=msa.make_rope(D, synth.PROLOGUE_THETA),
                 positions=pro["positions"], nr=pro["nr"], q=pro["q_out"], q_idx=pro["idx_q_out"] if self.has_index else None)
             if not self.has_index:
                 st["ws"] = torch.empty(msa.paged_gqa_workspace_size(self.dims, self.cache.dtype), dtype=torch.uint8, device=dev)
+            # The weights are drawn and converted on the current stream, the step may run on another: once waited for here,
+            # every stream sees them, and what the allocator got back on the way is not written any more.
+            torch.cuda.current_stream(dev).synchronize()
+            self._layer = st
         return st
 
     def hidden_step(self, x, residual, y, stream=None, rope=None):
@@ -346,12 +350,12 @@ class DeviceWorkload:
         norm of ``x`` (bf16 [T, hidden], T the step's tokens; ``residual``, bf16 or fp32, is updated in place), the packed
         FP8 projection, norm + rotary embedding + insert on its rows, attention (block-sparse; over every cached token
         for a layer without an index cache), and the output projection into ``y`` (bf16 or fp32 [T, hidden]), which the
-        next norm adds. ``rope`` (``msa.make_rope``) replaces the workload's own rotary embedding. As with the other
-        steps, one at a time: the buffers are the workload's."""
+        next norm adds. ``rope`` (``msa.make_rope``) replaces the workload's own rotary embedding. As with the other steps, one at a time: the buffers are the workload's. The first call for a
+        hidden size builds them and waits for them."""
         if self.has_index and self.w.idx_dtype == "f32":
             raise ValueError("hidden_step takes an FP8 or NVFP4 index cache")
-        st = self._layer_state(int(x.shape[1]))
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        st = self._layer_state(int(x.shape[1]))
         msa.add_norm_quant(x, st["norm"], residual=residual, residual_out=residual, codes=st["x8"][0], scales=st["x8"][1],
                            eps=synth.PROLOGUE_EPS, stream=s)
         packed = st["packed"]

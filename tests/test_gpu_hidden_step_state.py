@@ -1,0 +1,52 @@
+"""What ``DeviceWorkload.hidden_step`` builds at its first call: whole before any stream uses it, and kept."""
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_attention_07_gb300 import synth
+from block_sparse_attention_07_gb300.workload import DeviceWorkload
+
+pytestmark = pytest.mark.gpu
+
+
+def build(kind="b32_32k", index=True):
+    w = synth.scaled(synth.WORKLOADS[kind], batch=3, ctx=700)
+    return DeviceWorkload(w, "cuda", lens=np.array([700, 129, 300], dtype=np.int32), index_cache=index)
+
+
+def rows(dw, hidden, seed):
+    T = 3 * dw.w.q_len
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    x, r = (torch.randn((T, hidden), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    return x, r, torch.zeros_like(x)
+
+
+def eager(kind, index, hidden, seed):
+    dw = build(kind, index)
+    x, r, y = rows(dw, hidden, seed)
+    dw.hidden_step(x, r, y)
+    torch.cuda.synchronize()
+    assert dw.check_flags() == 0 and y.any()
+    return r, y
+
+
+@pytest.mark.parametrize("kind,index", [("b32_32k", True), ("b32_32k", False), ("spec8", True)])
+@pytest.mark.parametrize("raw", [False, True])
+def test_first_call_on_another_stream(kind, index, raw):
+    """The weights are made on the current stream, late; the first step is on another one."""
+    want = eager(kind, index, 2064, 1)
+    dw = build(kind, index)
+    x, r, y = rows(dw, 2064, 1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(40_000_000)                      # some 20 ms in front of the weights
+    dw.hidden_step(x, r, y, stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1])
+    # the weights stay: again, after everything has come to rest
+    torch.cuda.synchronize()
+    x, r, y = rows(dw, 2064, 1)
+    dw.hidden_step(x, r, y)
+    torch.cuda.synchronize()
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
