@@ -345,17 +345,27 @@ class DeviceWorkload:
             self._layer = st
         return st
 
+    def prepare_hidden_step(self, hidden):
+        """Builds what ``hidden_step`` keeps for a hidden size: before a first step that is captured. Otherwise the first
+        step does it."""
+        self._layer_state(int(hidden))
+
     def hidden_step(self, x, residual, y, stream=None, rope=None):
         """One decode step of a layer's attention half, from hidden states to hidden states: the residual's addition and
         norm of ``x`` (bf16 [T, hidden], T the step's tokens; ``residual``, bf16 or fp32, is updated in place), the packed
         FP8 projection, norm + rotary embedding + insert on its rows, attention (block-sparse; over every cached token
         for a layer without an index cache), and the output projection into ``y`` (bf16 or fp32 [T, hidden]), which the
         next norm adds. ``rope`` (``msa.make_rope``) replaces the workload's own rotary embedding. As with the other steps, one at a time: the buffers are the workload's. The first call for a
-        hidden size builds them and waits for them."""
+        hidden size builds them and waits for them; before a capture that is ``prepare_hidden_step``."""
         if self.has_index and self.w.idx_dtype == "f32":
             raise ValueError("hidden_step takes an FP8 or NVFP4 index cache")
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        st = self._layer_state(int(x.shape[1]))
+        hidden = int(x.shape[1])
+        if getattr(self, "_layer", {}).get("hidden") != hidden:
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, self.device) if isinstance(s, int) else s):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("hidden_step: prepare_hidden_step comes before a first step that is captured")
+        st = self._layer_state(hidden)
         msa.add_norm_quant(x, st["norm"], residual=residual, residual_out=residual, codes=st["x8"][0], scales=st["x8"][1],
                            eps=synth.PROLOGUE_EPS, stream=s)
         packed = st["packed"]
@@ -382,7 +392,8 @@ class DeviceWorkload:
 
     def capture(self, fn) -> torch.cuda.CUDAGraph:
         """Captures ``fn(stream)`` (a step of this workload) into a CUDA graph;
-        ``graph.replay()`` then reruns its kernels with the same buffers."""
+        ``graph.replay()`` then reruns its kernels with the same buffers. What a step builds at its first call has to be
+        there: that is a step that has run, or ``prepare_hidden_step``."""
         g = torch.cuda.CUDAGraph()
         torch.cuda.synchronize(self.device)
         with torch.cuda.graph(g):

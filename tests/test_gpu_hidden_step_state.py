@@ -50,3 +50,19 @@ def test_first_call_on_another_stream(kind, index, raw):
     dw.hidden_step(x, r, y)
     torch.cuda.synchronize()
     assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
+
+
+def test_first_step_in_a_capture():
+    """Refused by name; with prepare_hidden_step in front, a captured first step is an eager one's bits."""
+    want = eager("spec8", False, 1040, 3)
+    dw = build("spec8", False)
+    x, r, y = rows(dw, 1040, 3)
+    r0 = r.clone()
+    with pytest.raises(RuntimeError, match="prepare_hidden_step"):
+        dw.capture(lambda s: dw.hidden_step(x, r, y, s))
+    assert torch.equal(r, r0)
+    dw.prepare_hidden_step(1040)
+    g = dw.capture(lambda s: dw.hidden_step(x, r, y, s))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
