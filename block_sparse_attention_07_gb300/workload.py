@@ -309,9 +309,11 @@ class DeviceWorkload:
 
     # ------------------------------------- from hidden states to hidden states --
     def _layer_state(self, hidden):
-        """Synthetic FP8 weights of the layer's projections (from the workload's seed) and the buffers of ``hidden_step``."""
-        st = getattr(self, "_layer", None)
-        if st is None or st["hidden"] != hidden:
+        """Synthetic FP8 weights of the layer's projections (from the workload's seed) and the buffers of ``hidden_step``:
+        one set per hidden size, kept as long as the workload, since a captured step has their addresses."""
+        states = self.__dict__.setdefault("_layers", {})
+        st = states.get(hidden)
+        if st is None:
             w, dev = self.w, self.device
             T, H, G, I, D = len(self.which) * w.q_len, w.n_heads, w.n_kv_heads, w.n_idx_heads, w.head_dim
             gen = torch.Generator(device=dev)
@@ -342,7 +344,8 @@ class DeviceWorkload:
             # The weights are drawn and converted on the current stream, the step may run on another: once waited for here,
             # every stream sees them, and what the allocator got back on the way is not written any more.
             torch.cuda.current_stream(dev).synchronize()
-            self._layer = st
+            states[hidden] = st
+        self._layer = st
         return st
 
     def prepare_hidden_step(self, hidden):
@@ -361,7 +364,7 @@ class DeviceWorkload:
             raise ValueError("hidden_step takes an FP8 or NVFP4 index cache")
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         hidden = int(x.shape[1])
-        if getattr(self, "_layer", {}).get("hidden") != hidden:
+        if hidden not in self.__dict__.get("_layers", {}):
             with torch.cuda.stream(torch.cuda.ExternalStream(s, self.device) if isinstance(s, int) else s):
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("hidden_step: prepare_hidden_step comes before a first step that is captured")

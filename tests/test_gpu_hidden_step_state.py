@@ -52,6 +52,29 @@ def test_first_call_on_another_stream(kind, index, raw):
     assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
 
 
+def test_first_call_for_another_hidden_size():
+    """A captured step keeps its weights and buffers while steps of other sizes are made."""
+    want = {h: eager("b32_32k", True, h, 2) for h in (2064, 4096, 1040)}
+    dw = build()
+    x, r, y = rows(dw, 2064, 2)
+    r0 = r.clone()
+    dw.prepare_hidden_step(2064)
+    g = dw.capture(lambda s: dw.hidden_step(x, r, y, s))
+    for h in (4096, 1040):
+        a = rows(dw, h, 2)
+        dw.hidden_step(*a)
+        torch.cuda.synchronize()
+        assert torch.equal(a[1], want[h][0]) and torch.equal(a[2], want[h][1])
+        fill = [torch.full((1 << 24,), float("nan"), device="cuda") for _ in range(8)]      # what was let go is reused
+        del fill
+        r.copy_(r0)
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r, want[2064][0]) and torch.equal(y, want[2064][1])
+    assert dw.check_flags() == 0
+
+
 def test_first_step_in_a_capture():
     """Refused by name; with prepare_hidden_step in front, a captured first step is an eager one's bits."""
     want = eager("spec8", False, 1040, 3)
