@@ -357,8 +357,9 @@ class DeviceWorkload:
         """One decode step of a layer's attention half, from hidden states to hidden states: the residual's addition and
         norm of ``x`` (bf16 [T, hidden], T the step's tokens; ``residual``, bf16 or fp32, is updated in place), the packed
         FP8 projection, norm + rotary embedding + insert on its rows, attention (block-sparse; over every cached token
-        for a layer without an index cache), and the output projection into ``y`` (bf16 or fp32 [T, hidden]), which the
-        next norm adds. ``rope`` (``msa.make_rope``) replaces the workload's own rotary embedding. As with the other steps, one at a time: the buffers are the workload's. The first call for a
+        for a layer without an index cache), and the output projection into ``y`` [T, hidden] (bf16, which the next norm
+        adds, or fp32, which no norm of this library reads). ``rope`` (``msa.make_rope``) replaces the workload's own
+        rotary embedding. As with the other steps, one at a time: the buffers are the workload's. The first call for a
         hidden size builds them and waits for them; before a capture that is ``prepare_hidden_step``."""
         if self.has_index and self.w.idx_dtype == "f32":
             raise ValueError("hidden_step takes an FP8 or NVFP4 index cache")

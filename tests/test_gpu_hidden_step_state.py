@@ -89,3 +89,14 @@ def test_first_step_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
+
+
+def test_outputs_in_fp32():
+    """An fp32 y holds what a bf16 one rounds."""
+    want = eager("b32_32k", True, 1040, 4)
+    dw = build()
+    x, r, y = rows(dw, 1040, 4)
+    y = y.float()
+    dw.hidden_step(x, r, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y.bfloat16(), want[1]) and not torch.equal(y, want[1].float())
