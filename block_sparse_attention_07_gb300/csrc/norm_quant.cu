@@ -301,11 +301,13 @@ static cudaError_t launch_few(const NormParams& p, int vpt, int rows, int thread
 }
 template <int kRes, int kMost>
 static cudaError_t launch_ring(const NormParams& p, int rows, int threads, int sms, int& grid, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(threads) * kRingRows * (1 + kRes) * kRingVpt * 16;
+  constexpr size_t per_thread = kRingRows * (1 + kRes) * kRingVpt * 16;
+  const size_t smem = threads * per_thread;
   const int room = static_cast<int>((220u << 10) / (smem + 2048)), ctas = room < 1024 / threads ? room : 1024 / threads;
   grid = rows < sms * ctas ? rows : sms * ctas;
-  const cudaError_t err = cudaFuncSetAttribute(add_norm_quant_ring_kernel<kRes, kMost>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The most that any width takes: the limit is the function's, and another thread's launch may come in between.
+  const cudaError_t err = cudaFuncSetAttribute(add_norm_quant_ring_kernel<kRes, kMost>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kMost * per_thread));
   if (err != cudaSuccess) return err;
   return launch_pdl(add_norm_quant_ring_kernel<kRes, kMost>, dim3(static_cast<unsigned>(grid)),
                     dim3(static_cast<unsigned>(threads)), smem, stream, p, rows);
