@@ -674,8 +674,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
             tmem_fence_before();
             if (lane == 0) mbar_arrive_relaxed(free0 + 8u * b);
             if (kb + 1 < kb1) {
-              if (ok && !mbar_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1)) ok = false;
-              __syncwarp();
+              ok = ok && warp_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1);     // one answer per warp: the next tile's wait votes
               tmem_fence_after();
               tmem_ld32(mine + (b ^ 1) * C::kOut, x[0]);
             }
