@@ -47,10 +47,11 @@ __device__ __forceinline__ void prefetch_2d(const void* tmap, int x, int y) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The same without order among memory accesses: it does not wait for the stores in front of it.
-__device__ __forceinline__ void cluster_meet_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
-}
+// The two halves of it: what a thread has read and written in front of the first is done for those behind the second. The
+// relaxed one is for a thread whose accesses another thread's release covers.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
@@ -125,35 +126,74 @@ __device__ __forceinline__ void store4(const LinearParams& p, int64_t t, int n, 
     if (n + u < p.N) store_out(p, t, n + u, e[u]);
 }
 
-// A CTA's share of a tile's outputs, from the sums of the first `split` <= kMost CTAs of its cluster, added in rank order.
-// Thread `me` of `threads` takes four outputs of a row, kAhead times at one time: with all the sums on their way together
-// a tile of 128 tokens by itself is 2.5 us shorter (128 x 10,240 x 4,096: 15.6 -> 13.0), with two CTAs 0.5 (256 x 4,096 x
-// 8,192: 13.7 -> 13.2); more CTAs have enough on their way with one (64 x 4,096 x 8,192 on four: 9.6 and 9.7).
-template <int kMost, int kAhead, typename Place>
-__device__ __forceinline__ void join_sums(const LinearParams& p, uint32_t base, Place place, int tokens, int tok0, int row0, int rank,
-                                          int me, int threads) {
-  const int hop = p.split * threads, all = tokens * (kTile / 4);
-  for (int i0 = rank * threads + me; i0 < all; i0 += kAhead * hop) {
-    if (kAhead == 1 && row0 + 4 * (i0 & 31) >= p.N) continue;
-    float4 x[kAhead][kMost];
-    auto live = [&](int b) { return kAhead == 1 || (i0 + b * hop < all && row0 + 4 * ((i0 + b * hop) & 31) < p.N); };
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b)
-#pragma unroll
-      for (int q = 0; q < kMost; ++q) {
-        const int i = i0 + b * hop;
-        const uint32_t at = base + place(i >> 5, i & 31) * 4;
-        if (q < p.split && live(b)) x[b][q] = kMost == 1 ? ld_shared4(at) : ld_cluster(at, q);
-        else x[b][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+// A tile's outputs from the sums of a CTA that has it by itself. Thread `me` of kThreads takes four outputs of a row, eight
+// times at one time: with all the sums on their way together 128 x 10,240 x 4,096 takes 13.0 us, one after the other 15.6.
+template <int kThreads, typename Place>
+__device__ __forceinline__ void store_sums(const LinearParams& p, uint32_t base, Place place, int tokens, int tok0, int row0, int me) {
+  constexpr int kAhead = 8;
+  const int all = tokens * (kTile / 4);
+  for (int i0 = me; i0 < all; i0 += kAhead * kThreads) {
+    float4 v[kAhead];
+    auto live = [&](int b) { return i0 + b * kThreads < all && row0 + 4 * ((i0 + b * kThreads) & 31) < p.N; };
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
-      const int i = i0 + b * hop;
-      float4 v = x[b][0];
-#pragma unroll
-      for (int q = 1; q < kMost; ++q) { v.x += x[b][q].x; v.y += x[b][q].y; v.z += x[b][q].z; v.w += x[b][q].w; }
-      if (live(b)) store4(p, tok0 + (i >> 5), row0 + 4 * (i & 31), v);
+      const int i = i0 + b * kThreads;
+      v[b] = live(b) ? ld_shared4(base + place(i >> 5, i & 31) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      const int i = i0 + b * kThreads;
+      if (live(b)) store4(p, tok0 + (i >> 5), row0 + 4 * (i & 31), v[b]);
+    }
+  }
+}
+
+// A CTA's share of a tile's outputs, from the sums of the `split` <= kMost CTAs of its cluster, added in rank order. Thread `me`
+// of kThreads takes four outputs of a row, kPer times, kAhead of them at one time: with two CTAs four are 0.5 us shorter than one
+// (256 x 4,096 x 8,192), more CTAs have enough on their way with one (64 x 4,096 x 8,192 on four: 9.6 and 9.7).
+// No CTA may end while another reads its sums, so behind its last read a thread arrives at the cluster's last meeting, with
+// release, which waits for what the thread has under way: so in front of its stores. With many outputs the releases of all warps
+// take long too (256 x 4,096 x 8,192 15.9 us); there the threads arrive at a barrier of the CTA, and one warp, which has
+// nothing else under way, behind that with release for all (13.6; without order, which holds on the hardware but is not
+// promised, 13.1; 64 x 10,240 x 4,096 11.8, 11.7, 11.3). With few outputs every thread by itself is shorter (16 x 1,280 x 4,096
+// 4.1 us, by one warp 4.3, without order 4.05).
+template <int kMost, int kAhead, int kTokens, int kThreads, bool kByOne, typename Place>
+__device__ __forceinline__ void join_sums(const LinearParams& p, uint32_t base, Place place, int tokens, int tok0, int row0, int rank,
+                                          int me) {
+  constexpr int kFewest = kMost / 2 + (kMost > 2);                    // the fewest CTAs that come here
+  constexpr int kPer = (kTokens * (kTile / 4) + kFewest * kThreads - 1) / (kFewest * kThreads);
+  const int hop = p.split * kThreads, all = tokens * (kTile / 4), i0 = rank * kThreads + me;
+  auto live = [&](int j) { return i0 + j * hop < all && row0 + 4 * ((i0 + j * hop) & 31) < p.N; };
+  float4 v[kPer];
+#pragma unroll
+  for (int j0 = 0; j0 < kPer; j0 += kAhead) {
+    float4 x[kAhead][kMost];
+#pragma unroll
+    for (int b = 0; b < kAhead && j0 + b < kPer; ++b)
+#pragma unroll
+      for (int q = 0; q < kMost; ++q) {
+        const int i = i0 + (j0 + b) * hop;
+        x[b][q] = q < p.split && live(j0 + b) ? ld_cluster(base + place(i >> 5, i & 31) * 4, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+    for (int b = 0; b < kAhead && j0 + b < kPer; ++b) {
+      float4& s = v[j0 + b];
+      s = x[b][0];
+#pragma unroll
+      for (int q = 1; q < kMost; ++q) { s.x += x[b][q].x; s.y += x[b][q].y; s.z += x[b][q].z; s.w += x[b][q].w; }
+    }
+  }
+  if (kByOne) {
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(kThreads + 32) : "memory");
+    cluster_arrive_relaxed();
+  } else {
+    cluster_arrive();
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = i0 + j * hop;
+    if (live(j)) store4(p, tok0 + (i >> 5), row0 + 4 * (i & 31), v[j]);
   }
 }
 
@@ -390,17 +430,26 @@ __global__ void __launch_bounds__(RowsCfg<NT, kDeep>::kThreads, RowsCfg<NT, kDee
   const int tokens = p.T - tok0 < NT ? p.T - tok0 : NT;
   // With many outputs without the warp that has just given tensor memory back (128 x 4,096 x 8,192 on two CTAs: 13.5 -> 13.3 us); with
   // few the others would take a turn more (16 x 4,096 x 8,192: 8.2 -> 8.5).
-  constexpr int kStore = NT >= 64 ? C::kThreads - 32 : C::kThreads;
-  if (threadIdx.x < kStore) {
-    const int row0 = tile * kTile;
-    if (C::kTokM && p.split == 1) join_sums<1, 8>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
-    else if (p.split == 2) join_sums<2, 4>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
-    else if (p.split <= 4) join_sums<4, 1>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
-    else join_sums<8, 1>(p, base, place, tokens, tok0, row0, rank, threadIdx.x, kStore);
+  constexpr bool kByOne = NT >= 64;
+  constexpr int kStore = kByOne ? C::kThreads - 32 : C::kThreads;
+  static_assert(C::kMmaWarp * 32 == C::kThreads - 32, "the warp that does not store");
+  const int row0 = tile * kTile, me = threadIdx.x;
+  if (C::kTokM && p.split == 1) {
+    if (me < kStore) store_sums<kStore>(p, base, place, tokens, tok0, row0, me);
+    return;
   }
-  // No CTA ends while another reads its sums: every read above has come back before the store that its thread made of it,
-  // so that no order among memory accesses is asked for (1 x 1,280 x 4,096: 4.2 -> 3.9 us, 16 4.6 -> 4.1).
-  if (p.split > 1) cluster_meet_relaxed();
+  if (me >= kStore) {
+    __syncwarp();
+    named_barrier(2, kStore + 32);          // the others have read
+    cluster_arrive();
+  } else if (p.split == 2) {
+    join_sums<2, 4, NT, kStore, kByOne>(p, base, place, tokens, tok0, row0, rank, me);
+  } else if (p.split <= 4) {
+    join_sums<4, 1, NT, kStore, kByOne>(p, base, place, tokens, tok0, row0, rank, me);
+  } else {
+    join_sums<8, 1, NT, kStore, kByOne>(p, base, place, tokens, tok0, row0, rank, me);
+  }
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -441,8 +490,36 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Waits on barriers that other CTAs of the cluster, their copies or their products arrive on: mbar_wait with the cluster as
+// scope. kData: shared memory that was written in front of the arrival is read or written again behind the wait, which a fence
+// for shared memory alone orders (an acquiring wait, for all memory: 8,191 x 10,240 x 4,096 235 -> 245 us). Without, the wait is
+// for execution alone: the order of tensor memory's reads and products is that of tcgen05's fences on both sides.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+template <bool kData>
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+  bool ok = try_wait_cluster(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    do {
+#pragma unroll 1
+      for (int k = 0; k < 64 && !ok; ++k) ok = try_wait_cluster(bar, parity);
+    } while (!ok && globaltimer_ns() - t0 <= kWaitLimitNs);
+  }
+  if (kData && ok) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return ok;
+}
+template <bool kData>
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity) {
+  return __all_sync(kEvery, mbar_wait_cluster<kData>(bar, parity)) != 0;
+}
 // Says that tensor memory has been read: what was read is in registers, and nothing was written that the other CTA
-// would have to see, so the arrival needs no release (whose fence costs a microsecond).
+// would have to see, so the arrival needs no release (whose fence costs a microsecond). The order of the reads and the next
+// products is that of tcgen05.fence::before_thread_sync in front of it and ::after_thread_sync behind the other CTA's wait.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t at) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
 }
@@ -584,7 +661,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           pair_tile(p, i, tm, tn);
           const int tok = tm * 2 * C::kTok + static_cast<int>(half) * C::kTok, row = tn * C::kOut + static_cast<int>(half) * 128;
           for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(empty(s), ph ^ 1u)) { ok = false; break; }
+            if (!mbar_wait_cluster<true>(empty(s), ph ^ 1u)) { ok = false; break; }
             const uint32_t at = base + s * C::kStage, bar = full0 + 8u * s;
             if (half == 0) mbar_arrive_expect_tx(full(s), 2 * C::kStage);
             tma_load_2d_pair(at, &ta, kb * 128, tok, bar);
@@ -594,7 +671,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         }
         // every stage has been read, so no copy is in flight, and no arrival from the products either
         for (int k = 0; k < C::kStages; ++k) {
-          if (!mbar_wait(empty(s), ph ^ 1u)) ok = false;
+          if (!mbar_wait_cluster<true>(empty(s), ph ^ 1u)) ok = false;
           if (++s == C::kStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) set_flag(p.flags, MSA_FLAG_TIMEOUT);
@@ -610,7 +687,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       for (int i = first; i < tiles && ok; i += clusters) {
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
           const int b = n & 1;
-          ok = warp_wait(full(s), ph) && (n < C::kAcc || warp_wait(acc_free(b), ((n >> 1) - 1) & 1));
+          ok = warp_wait_cluster<true>(full(s), ph) && (n < C::kAcc || warp_wait_cluster<false>(acc_free(b), ((n >> 1) - 1) & 1));
           if (!ok) break;
           tmem_fence_after();
           if (lead) {
@@ -656,7 +733,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
       // 32 columns at a time, the next ones on their way while the last are added, the next block's first among them
       float x[2][32];
-      ok = ok && warp_wait(acc_full(n & 1), (n >> 1) & 1);
+      ok = ok && warp_wait_cluster<false>(acc_full(n & 1), (n >> 1) & 1);
       tmem_fence_after();
       tmem_ld32(mine + (n & 1) * C::kOut, x[0]);
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
@@ -674,7 +751,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
             tmem_fence_before();
             if (lane == 0) mbar_arrive_relaxed(free0 + 8u * b);
             if (kb + 1 < kb1) {
-              ok = ok && warp_wait(acc_full(b ^ 1), ((n + 1) >> 1) & 1);     // one answer per warp: the next tile's wait votes
+              ok = ok && warp_wait_cluster<false>(acc_full(b ^ 1), ((n + 1) >> 1) & 1);     // one answer per warp: the next tile's wait votes
               tmem_fence_after();
               tmem_ld32(mine + (b ^ 1) * C::kOut, x[0]);
             }
@@ -747,7 +824,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
                           pair_share(lane, p.split) * C::kUnit, cluster_addr(got_bar, to));
         }
         __syncwarp();
-        if (!warp_wait(got_bar, 0)) {
+        if (!warp_wait_cluster<true>(got_bar, 0)) {
           ok = false;
         } else {
 #pragma unroll
