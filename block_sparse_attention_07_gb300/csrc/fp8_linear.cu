@@ -19,6 +19,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "at_once.h"
 #include "tcgen05.cuh"
 
 namespace msa {
@@ -891,13 +892,9 @@ static cudaError_t out_map(CUtensorMap* map, void* base, int64_t T, int64_t N, i
 // Clusters of n CTAs of a kernel that the device runs at one time, asked once per device: fewer than its SMs would
 // hold, 36 clusters of four and 15 of eight CTAs on 152 SMs. (It counts one CTA per SM for these kernels; where two
 // fit, there is room for twice as many.)
-struct AtOnce {
-  int of[64][9];
-};
 template <typename Kernel>
 static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int threads, size_t smem) {
-  if (dev < 0) return 1;
-  if (cache.of[dev][n] == 0) {
+  return cache.get(dev, n, [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n);
     cfg.blockDim = dim3(threads);
@@ -910,13 +907,12 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
     cfg.numAttrs = 1;
     int most = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess || most < 1) {
+        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      most = 1;
+      return -1;
     }
-    cache.of[dev][n] = most;
-  }
-  return cache.of[dev][n];
+    return most;
+  });
 }
 
 // What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
@@ -947,21 +943,15 @@ struct RowsForm {
   static constexpr FormCost kCost = NT == 128 ? FormCost{6.5f, 0.19f, 0.18f}
                                   : kDeep ? (NT == 16 ? FormCost{3.9f, 0.2f, 0.08f} : NT == 32 ? FormCost{4.1f, 0.215f, 0.1f} : FormCost{5.2f, 0.2f, 0.2f})
                                           : (NT == 16 ? FormCost{3.8f, 0.4f, 0.12f} : NT == 32 ? FormCost{4.6f, 0.45f, 0.2f} : FormCost{5.7f, 0.45f, 0.19f});
-  // The number of CTAs that share a tile's K, and what the call then costs.
+  // The number of CTAs that share a tile's K (0: the device has none to give), and what the call then costs.
   static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
     static AtOnce cache;
     const int64_t tiles = static_cast<int64_t>((a.N + kTile - 1) / kTile) * ((a.T + NT - 1) / NT);
     const int KB = (a.K + kTile - 1) / kTile;
-    forced = forced <= KB ? forced : 0;
-    split = 0;
-    for (int s = forced ? forced : 1; s <= (forced ? forced : 8) && s <= KB; ++s) {
-      const int at_once = C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem);
-      const float t = form_us(kCost, a, tiles, at_once, s, C::kCtas == 1 ? 5.f : 2.5f) - (s > 1 ? 0.9f : 0.f);
-      if (split == 0 || t <= us) {
-        split = s;
-        us = t;
-      }
-    }
+    split = cheapest_split(
+        KB < 8 ? KB : 8, forced, true,
+        [&](int s) { return C::kCtas * clusters_at_once(fp8_linear_rows_kernel<NT, kDeep>, cache, dev, s, C::kThreads, kSmem); },
+        [&](int s, int at_once) { return form_us(kCost, a, tiles, at_once, s, C::kCtas == 1 ? 5.f : 2.5f) - (s > 1 ? 0.9f : 0.f); }, us);
   }
   static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta;
@@ -985,10 +975,11 @@ struct RowsForm {
 template <int NT>
 static cudaError_t launch_rows(const LinearArgs& a, const LinearParams& p, int dev, int forced, cudaStream_t stream, DispatchRecord* rec) {
   int split[2];
-  float us[2];
+  float us[2] = {0.f, 0.f};
   RowsForm<NT, false>::plan(a, dev, forced, split[0], us[0]);
   RowsForm<NT, true>::plan(a, dev, forced, split[1], us[1]);
-  return us[1] < us[0] ? RowsForm<NT, true>::launch(a, p, split[1], stream, rec) : RowsForm<NT, false>::launch(a, p, split[0], stream, rec);
+  const bool deep = split[0] == 0 || (split[1] != 0 && us[1] < us[0]);       // (neither: the launch says what is wrong)
+  return deep ? RowsForm<NT, true>::launch(a, p, split[1] ? split[1] : 1, stream, rec) : RowsForm<NT, false>::launch(a, p, split[0], stream, rec);
 }
 
 struct PairForm {
@@ -1003,17 +994,13 @@ struct PairForm {
   }
   static void plan(const LinearArgs& a, int dev, int forced, int& split, float& us) {
     const int KB = (a.K + kTile - 1) / kTile;
-    forced = forced <= 4 && forced <= KB ? forced : 0;
-    split = 0;
-    for (int s = forced ? forced : 1; s <= (forced ? forced : 4) && s <= KB; ++s) {
-      // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
-      float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 2.f : 6.f / static_cast<float>(s)}, a, tiles(a), at_once(dev, s), s, s > 1 ? 2.5f : 0.f);
-      t += 1.1f * static_cast<float>((tiles(a) + at_once(dev, s) - 1) / at_once(dev, s));
-      if (split == 0 || t < us) {
-        split = s;
-        us = t;
-      }
-    }
+    split = cheapest_split(
+        KB < 4 ? KB : 4, forced, false, [&](int s) { return at_once(dev, s); },
+        [&](int s, int room) {
+          // a tile's outputs 1.1 us; the sums' way 4 us for two pairs, 6 for more
+          const float t = form_us(FormCost{4.9f, 0.3875f, s == 2 ? 2.f : 6.f / static_cast<float>(s)}, a, tiles(a), room, s, s > 1 ? 2.5f : 0.f);
+          return t + 1.1f * static_cast<float>((tiles(a) + room - 1) / room);
+        }, us);
   }
   static cudaError_t launch(const LinearArgs& a, LinearParams p, int dev, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta, to;
@@ -1033,7 +1020,8 @@ struct PairForm {
     p.split = split;
     err = cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    const int64_t clusters = split > 1 || tiles(a) < at_once(dev, 1) ? tiles(a) : at_once(dev, 1);
+    const int room = at_once(dev, 1);
+    const int64_t clusters = split > 1 || tiles(a) < room ? tiles(a) : room < 1 ? 1 : room;
     err = launch_pdl_cluster(fp8_linear_pair_kernel, dim3(static_cast<unsigned>(clusters * 2 * split)), dim3(C::kThreads), kSmem,
                              stream, 2 * split, tw, ta, to, p);
     if (err != cudaSuccess) return err;
@@ -1071,8 +1059,9 @@ cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream, Dispatch
   const bool rows_fit = (a.T + 127) / 128 <= 65535;                 // groups of tokens are a grid's y
   if (!pairs_only && rows_fit) RowsForm<128, true>::plan(a, dev, forced, rows_split, rows_us);
   if (!rows_only || !rows_fit) PairForm::plan(a, dev, forced, pair_split, pair_us);
-  if (pair_split == 0 || (rows_split != 0 && rows_us <= pair_us)) return RowsForm<128, true>::launch(a, p, rows_split, stream, rec);
-  return PairForm::launch(a, p, dev, pair_split, stream, rec);
+  if (rows_split != 0 && (pair_split == 0 || rows_us <= pair_us)) return RowsForm<128, true>::launch(a, p, rows_split, stream, rec);
+  if (pair_split != 0 || pairs_only || !rows_fit) return PairForm::launch(a, p, dev, pair_split ? pair_split : 1, stream, rec);
+  return RowsForm<128, true>::launch(a, p, 1, stream, rec);                   // (neither: the launch says what is wrong)
 }
 
 }  // namespace msa
