@@ -6,8 +6,10 @@
 //   out[t, n] = sum_g sa[t, g] sw[n / 128, g] sum_{k in g} a[t, k] w[n, k].
 // The inner sum is one tcgen05 product of K = 128 into tensor memory, fresh for
 // every block; the outer one is kept in fp32 registers, which read the block's
-// sums back and add them times their scales. Blocks of K beyond its end and rows
-// beyond the operands' arrive as zeros.
+// sums back and add them times their scales' product, an fp32 value: one fused
+// addition per sum (the scales one after the other would be two operations, for
+// the sake of products below 2^-126). Blocks of K beyond its end and rows beyond
+// the operands' arrive as zeros.
 //
 // What bounds it: the weights' bytes where there are many and few tokens (64 x
 // 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'

@@ -544,7 +544,7 @@ def add_norm_quant(x, weight, residual=None, residual_out=None, out=None, codes=
 
 def fp8_linear(a, a_scales, w, w_scales, out, flags, stream=None, prepare=False):
     """msa_fp8_linear: ``out`` [T, N] (bf16 or fp32, rows may lie apart) from codes ``a`` [T, K] and ``w`` [N, K] (uint8
-    E4M3) with their scales per 128 values and per 128 x 128 block."""
+    E4M3) with their scales per 128 values and per 128 x 128 block, whose products are fp32 values."""
     what = "msa_fp8_linear"
     for name, t in (("a", a), ("w", w), ("out", out)):
         if t is None or t.dim() != 2:

@@ -521,6 +521,10 @@ msa_status_t msa_add_norm_quant(int32_t num_tokens, int32_t width, const void* x
  * fp32 registers in a fixed order: results do not depend on timing. They do
  * depend, within fp32's rounding, on num_tokens and on the GPU's size, which set
  * how K is split.
+ * The product of the two scales is taken first, in fp32: below 2^-126 it is rounded
+ * to a multiple of 2^-149 (zero among them), above fp32's range it is infinite, and
+ * so is then the group's share, or NaN where its sum is zero. Scales whose products
+ * are zero or between 2^-126 and 2^128 meet neither.
  * A code that is NaN makes every output that it enters NaN.
  * a: E4M3 [T, K]; a_scales: fp32 [T, ceil(K / 128)]; w: E4M3 [N, K]; w_scales:
  * fp32 [ceil(N / 128), ceil(K / 128)]; all contiguous. out: MSA_BF16 or MSA_F32
