@@ -12,12 +12,14 @@
 // the operands' arrive as zeros.
 //
 // What bounds it: the weights' bytes where there are many and few tokens (64 x
-// 100,003 x 4,096 to fp32: 71.5 us, 5.9 TB/s); launch, first copies and the sums'
-// way between CTAs where there are few (1 x 1,280 x 4,096: 3.7 us);
+// 100,003 x 4,096 to fp32: 71.7 us, 6.1 TB/s with the outputs); launch, first copies
+// and the sums' way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us);
 // in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
-// 13.1 us); for prompts the products with the sums' way back beside them (8,191 x
-// 10,240 x 4,096: 233 us, 2.95 PFLOP/s; 258 in a run of a second, where the board's
-// power limit takes the clock to 1.75 GHz).
+// 13.4 us); from some 400 tokens to 2,048 the last wave of tiles, which costs as much
+// as a full one (512 x 10,240 x 4,096, 80 tiles on 76 pairs: 30.7 us); for prompts
+// the products with the sums' way back beside them (8,191 x 10,240 x 4,096: 234 us,
+// 2.94 PFLOP/s; 260 in a run of a second, where the board's power limit takes the
+// clock to 1.75 GHz).
 #include <cstdlib>
 #include <cstring>
 
@@ -919,13 +921,14 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 
 // What a form costs, in microseconds: `launch` and, for every wave of clusters, its blocks of K and the sums' way
 // between CTAs, some more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
-// fits to calls whose weights come from memory; what they choose was within 4 % of the fastest at 60 of 61 sizes of 16
-// to 1,024 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 18.8 / 13.1 / 19.4; pairs on 1 / 2 / 3 30.0 / 21.9 / 20.1;
-//   256 x 10,240 x 4,096: rows 23.4 / 27.1, pairs 19.1 / 32.7; 512 x 4,096 x 8,192: rows 19.1 / 25.0, pairs 29.9 / 22.4;
-//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, one per SM 11.9 / 16.8 / 15.3 / 18.7, two 17.2 / 12.3 / 11.4 / 16.4;
-//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 10.9 / 9.6 / 9.6, two per SM on 6 / 8 11.2 / 10.8;
-//   16 x 1,280 x 4,096 on 8 4.0 and 4.4; 64 x 28,672 x 4,096 on 1 27.0 and 22.5.
+// fits to calls whose weights come from memory; what they choose was within 4 % of the fastest of these forms and splits at
+// 67 of 68 sizes of 16 to 8,191 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 18.4 / 13.6 / 20.1; pairs on 1 / 2 / 3 29.6 / 21.4 / 19.4;
+//   256 x 10,240 x 4,096: rows 22.7 / 28.1, pairs 18.1 / 32.0; 512 x 4,096 x 8,192: rows 18.8 / 26.0, pairs 29.4 / 21.9;
+//   1,536 x 4,096 x 8,192: rows 55.2 / 73.3, pairs 53.7 / 62.7;
+//   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, the better of one and two per SM 11.6 / 12.2 / 11.7 / 17.2;
+//   64 x 4,096 x 8,192 on 2 / 3 / 4, one per SM 11.1 / 9.8 / 9.9, two per SM on 6 / 8 11.5 / 11.3;
+//   16 x 1,280 x 4,096 on 4 / 6 / 8 4.5 / 4.3 / 4.1; 64 x 28,672 x 4,096 on 1, one and two per SM 27.0 and 22.6.
 struct FormCost {
   float launch, block, sums;
 };

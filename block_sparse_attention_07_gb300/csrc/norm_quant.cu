@@ -12,7 +12,7 @@
 // every value is read once and written once: the mean takes one CTA barrier, a
 // scale's maximum four shuffles among the 16 lanes that hold its group. What
 // bounds it is bytes for many rows and the chain load - sum - barrier - store for
-// few (64 x 4,096: 2.3 us).
+// few (64 x 4,096: 2.9 us).
 #include <cstring>
 
 #include "msa_internal.h"
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(1024) add_norm_quant_kernel(const __grid_const
 
 // Many rows: CTAs that stay, rows strided over them, the weight in registers, and the next two rows on their way into a
 // ring in shared memory of which every thread has its own 16-byte places: it waits for its own copies only. 8,191 rows of
-// 4,096 / 8,192 / 16,384 values, bf16 residual, FP8 out: 40.5 / 73.9 / 138.8 us (86 / 94 / 100 % of a copy's rate), a CTA
-// per row 43.9 / 91.4 / 195.8.
+// 4,096 / 8,192 / 16,384 values, bf16 residual, FP8 out: 41.4 / 76.4 / 143.7 us (84 / 91 / 97 % of a copy's rate), a CTA
+// per row 45.1 / 98.5 / 204.1.
 constexpr int kRingVpt = 2, kRingRows = 3;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -335,9 +335,12 @@ cudaError_t launch_add_norm_quant(const NormArgs& a, cudaStream_t stream, Dispat
   const int chunks = a.width / 8;
   const int res = a.residual == nullptr ? 0 : a.residual_f32 ? 2 : 1;
   const int sms = device_sm_count();
-  // The ring from 2^23 values in rows of at least 4,096: 2,432 x 4,096 15.7 us both ways, 1,216 x 8,192 15.7 against 17.3,
-  // 700 x 12,288 14.5 against 19.1; 700 x 8,192 11.9 against 11.6, 30,000 x 1,024 41.1 against 38.7. An fp32 residual,
-  // 32 bytes per thread, is better loaded than copied: 8,191 x 4,096 57.1 us, by a ring 76.0.
+  // The ring from 2^23 values in rows of at least 4,096. Ring and CTA per row, us, bf16 residual: 2,432 x 4,096 16.1 and 16.1,
+  // 1,216 x 8,192 15.8 and 18.0, 700 x 12,288 14.8 and 19.6; 700 x 8,192 12.2 and 11.9, 30,000 x 1,024 41.8 and 39.5. Below
+  // 4,096 the two lie close together, by the number of values: 2^23 of them in rows of 2,048 / 2,560 / 3,584 / 4,080 14.7 and
+  // 13.5 / 14.9 and 13.8 / 14.7 and 14.4 / 15.4 and 14.2, 2^25 42.1 and 43.6 / 44.9 and 44.5 / 43.3 and 46.5 / 42.4 and 45.9
+  // (without a residual 24.8 and 24.0 / 26.4 and 24.6 / 25.1 and 25.6 / 24.3 and 24.9). An fp32 residual, 32 bytes per
+  // thread, is better loaded than copied: 8,191 x 4,096 57.1 us, by a ring 76.0.
   const bool many = res != 2 && a.width >= 4096 && static_cast<int64_t>(a.rows) * a.width >= (1ll << 23);
   const int vpt = many ? kRingVpt : chunks > 1024 ? 2 : 1;
   const int threads = ((chunks + vpt - 1) / vpt + 31) / 32 * 32;

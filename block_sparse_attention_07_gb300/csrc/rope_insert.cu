@@ -23,7 +23,7 @@
 // 93.7 us (90 %); 64 tokens, bf16 cache: 4.0 us, of which 0.7 pass until a kernel may
 // start and 0.5 each for positions and for rows. With fewer heads what
 // comes before a warp's queries (position, sines, slot, keys) shows: 16 + 1 + 1 heads
-// 21.2 us for 8,191 tokens (51 % of a copy's rate).
+// 20.3 us for 8,191 tokens (53 % of a copy's rate): a warp has one token, and four passes of queries behind that chain.
 //
 // Phases: freq / 2 pi modulo one is held as a 64-bit fraction of a turn, so that
 // position times it, modulo one turn, is one integer product: 2^-53 relative to
@@ -378,8 +378,13 @@ cudaError_t launch_qkv_rope_insert(const RopeArgs& a, cudaStream_t stream, Dispa
   }
   const int rows = a.H + 2 * a.ins.G + (a.idx_q ? 2 * a.I : 0);
   const int passes = (rows + 3) / 4;
-  // Warps per token: about 16 warps per SM for few tokens (as the multi-axis kernel, which measured it), two per token
-  // for some, one from 32 tokens per SM on (8,191 tokens: two 3 % slower; 16,000 tokens the same).
+  // Warps per token: about 16 warps per SM for few tokens, two per token for some, one from 32 tokens per SM on. Measured, 64
+  // + 4 + 4 heads, FP8 cache, us by warps per token (the rule's in parentheses): 64 tokens on 4 / 8 / 16 / (18) 5.1 / 4.5 / 4.1
+  // / (4.5); 512 on 3 / 4 / (5) / 6 / 8 10.3 / 8.8 / (8.3) / 8.0 / 8.3; 1,024 on 2 / (3) / 4 / 6 13.8 / (11.8) / 10.8 / 11.7;
+  // 2,048 on 1 / (2) / 3 22.9 / (16.3) / 18.3; 4,500 35.8 / (32.9) / 33.1; 4,864 on (1) / 2 (38.7) / 34.9; 8,191 (52.2) /
+  // 51.9. One KV head: 512 on 4 / (5) 4.9 / (5.1); 1,024 on 2 / (3) / 4 6.7 / (6.5) / 6.9; 2,048 on 1 / (2) 10.1 / (8.4);
+  // 3,000 10.9 / (11.1); 4,864 on (1) / 2 (15.0) / 15.1; 8,191 (20.3) / 22.3; 16,000 (35.1) / 39.1. So the change from two to
+  // one lies between that of few heads (some 18 tokens per SM) and that of many (over 50), and costs the latter 10 % there.
   const int64_t sms = device_sm_count();
   int64_t parts = a.ins.T >= 32 * sms ? 1 : (16 * sms + a.ins.T - 1) / a.ins.T;
   if (parts < 2 && a.ins.T < 32 * sms) parts = 2;
