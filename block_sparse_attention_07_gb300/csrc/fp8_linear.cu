@@ -15,7 +15,7 @@
 // 100,003 x 4,096 to fp32: 71.7 us, 6.1 TB/s with the outputs); launch, first copies
 // and the sums' way between CTAs where there are few (1 x 1,280 x 4,096: 3.8 us);
 // in between a block's chain of copy, product and sums (256 x 4,096 x 8,192:
-// 13.4 us); from some 400 tokens to 2,048 the last wave of tiles, which costs as much
+// 13.1 us); from some 400 tokens to 2,048 the last wave of tiles, which costs as much
 // as a full one (512 x 10,240 x 4,096, 80 tiles on 76 pairs: 30.7 us); for prompts
 // the products with the sums' way back beside them (8,191 x 10,240 x 4,096: 234 us,
 // 2.94 PFLOP/s; 260 in a run of a second, where the board's power limit takes the
@@ -158,14 +158,14 @@ __device__ __forceinline__ void store_sums(const LinearParams& p, uint32_t base,
 // (256 x 4,096 x 8,192), more CTAs have enough on their way with one (64 x 4,096 x 8,192 on four: 9.6 and 9.7).
 // No CTA may end while another reads its sums, so behind its last read a thread arrives at the cluster's last meeting, with
 // release, which waits for what the thread has under way: so in front of its stores. With many outputs the releases of all warps
-// take long too (256 x 4,096 x 8,192 15.9 us); there the threads arrive at a barrier of the CTA, and one warp, which has
-// nothing else under way, behind that with release for all (13.6; without order, which holds on the hardware but is not
-// promised, 13.1; 64 x 10,240 x 4,096 11.8, 11.7, 11.3). With few outputs every thread by itself is shorter (16 x 1,280 x 4,096
-// 4.1 us, by one warp 4.3, without order 4.05).
+// take long too (256 x 4,096 x 8,192 14.9 us); there the threads arrive at a barrier of the CTA, and one warp, which has
+// nothing else under way, behind that with release for all (13.1, as much as without order, which holds on the hardware but is
+// not promised; 64 x 10,240 x 4,096 11.8, 11.7, without order 11.4). With few outputs every thread by itself is shorter (16 x
+// 1,280 x 4,096 4.1 us, by one warp 4.3, without order 4.05).
 template <int kMost, int kAhead, int kTokens, int kThreads, bool kByOne, typename Place>
 __device__ __forceinline__ void join_sums(const LinearParams& p, uint32_t base, Place place, int tokens, int tok0, int row0, int rank,
                                           int me) {
-  constexpr int kFewest = kMost / 2 + (kMost > 2);                    // the fewest CTAs that come here
+  constexpr int kFewest = kMost == 2 ? 2 : kMost / 2 + 1;             // the fewest CTAs that come here
   constexpr int kPer = (kTokens * (kTile / 4) + kFewest * kThreads - 1) / (kFewest * kThreads);
   const int hop = p.split * kThreads, all = tokens * (kTile / 4), i0 = rank * kThreads + me;
   auto live = [&](int j) { return i0 + j * hop < all && row0 + 4 * ((i0 + j * hop) & 31) < p.N; };
@@ -923,7 +923,7 @@ static int clusters_at_once(Kernel kernel, AtOnce& cache, int dev, int n, int th
 // between CTAs, some more where CTAs follow one another; never less than the weights' bytes at 7 TB/s. The constants are
 // fits to calls whose weights come from memory; what they choose was within 4 % of the fastest of these forms and splits at
 // 67 of 68 sizes of 16 to 8,191 tokens, 1,280 to 28,672 weight rows and K of 1,024 to 8,192. Some of them (us):
-//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 18.4 / 13.6 / 20.1; pairs on 1 / 2 / 3 29.6 / 21.4 / 19.4;
+//   rows of 128 tokens: 256 x 4,096 x 8,192 on 1 / 2 / 4 CTAs 18.4 / 13.1 / 20.1; pairs on 1 / 2 / 3 29.6 / 21.4 / 19.4;
 //   256 x 10,240 x 4,096: rows 22.7 / 28.1, pairs 18.1 / 32.0; 512 x 4,096 x 8,192: rows 18.8 / 26.0, pairs 29.4 / 21.9;
 //   1,536 x 4,096 x 8,192: rows 55.2 / 73.3, pairs 53.7 / 62.7;
 //   64 x 10,240 x 4,096 on 1 / 2 / 3 / 4 CTAs, the better of one and two per SM 11.6 / 12.2 / 11.7 / 17.2;
