@@ -960,14 +960,13 @@ struct RowsForm {
   }
   static cudaError_t launch(const LinearArgs& a, LinearParams p, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta;
-    cudaError_t err;
+    cudaError_t err = cudaFuncSetAttribute(fp8_linear_rows_kernel<NT, kDeep>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;                  // (in front of the maps: see encode_fn)
     if ((err = rows_map(&tw, a.w, a.N, a.K, kTile)) != cudaSuccess) return err;
     if ((err = rows_map(&ta, a.a, a.T, a.K, NT)) != cudaSuccess) return err;
     const int64_t tiles = (a.N + kTile - 1) / kTile, groups = (a.T + NT - 1) / NT;
     if (groups > 65535) return cudaErrorInvalidValue;
     p.split = split;
-    err = cudaFuncSetAttribute(fp8_linear_rows_kernel<NT, kDeep>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (err != cudaSuccess) return err;
     err = launch_pdl_cluster(fp8_linear_rows_kernel<NT, kDeep>, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups)),
                              dim3(C::kThreads), kSmem, stream, split, tw, ta, p);
     if (err != cudaSuccess) return err;
@@ -1009,7 +1008,8 @@ struct PairForm {
   }
   static cudaError_t launch(const LinearArgs& a, LinearParams p, int dev, int split, cudaStream_t stream, DispatchRecord* rec) {
     CUtensorMap tw, ta, to;
-    cudaError_t err;
+    cudaError_t err = cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;                  // (in front of the maps: see encode_fn)
     if ((err = rows_map(&tw, a.w, a.N, a.K, 128)) != cudaSuccess) return err;
     if ((err = rows_map(&ta, a.a, a.T, a.K, 128)) != cudaSuccess) return err;
     const int64_t stride = a.out_stride * (a.out_f32 ? 4 : 2);
@@ -1023,8 +1023,6 @@ struct PairForm {
     p.group = rows < 1 ? 1 : rows > p.tiles_m ? p.tiles_m : static_cast<int>(rows);
     if (tiles(a) > INT32_MAX / 16) return cudaErrorInvalidValue;
     p.split = split;
-    err = cudaFuncSetAttribute(fp8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (err != cudaSuccess) return err;
     const int room = at_once(dev, 1);
     const int64_t clusters = split > 1 || tiles(a) < room ? tiles(a) : room < 1 ? 1 : room;
     err = launch_pdl_cluster(fp8_linear_pair_kernel, dim3(static_cast<unsigned>(clusters * 2 * split)), dim3(C::kThreads), kSmem,

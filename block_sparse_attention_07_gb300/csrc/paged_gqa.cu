@@ -1902,26 +1902,24 @@ static cudaError_t launch_tc(const PagedParams& p, int ctas, cudaStream_t stream
   CUtensorMap tk, tv;
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
-  cudaError_t err;
+  constexpr size_t smem = C::kTotal + 1024;
+  cudaError_t err = cudaFuncSetAttribute(paged_gqa_tc_kernel<kKv, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;                    // (in front of the maps: see encode_fn)
   const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
   if ((err = cache_map(&tk, p.k, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
   if ((err = cache_map(&tv, p.v, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
-  constexpr size_t smem = C::kTotal + 1024;
-  err = cudaFuncSetAttribute(paged_gqa_tc_kernel<kKv, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (err != cudaSuccess) return err;
   return launch_pdl(paged_gqa_tc_kernel<kKv, NR>, dim3(ctas), dim3(32 * C::kWarpsAll), smem, stream, tk, tv, p);
 }
 
 template <int kKv>
 static cudaError_t launch_many(const PagedParams& p, int ctas, cudaStream_t stream) {
   CUtensorMap tk, tv;
-  cudaError_t err;
+  constexpr size_t smem = RwCfg<kKv>::kTotal + 1024;
+  cudaError_t err = cudaFuncSetAttribute(paged_gqa_rows_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;                    // (in front of the maps: see encode_fn)
   const int64_t rows = static_cast<int64_t>(p.P) * p.G * kBlock;
   if ((err = cache_map(&tk, p.k, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
   if ((err = cache_map(&tv, p.v, rows, static_cast<msa_dtype_t>(kKv))) != cudaSuccess) return err;
-  constexpr size_t smem = RwCfg<kKv>::kTotal + 1024;
-  err = cudaFuncSetAttribute(paged_gqa_rows_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (err != cudaSuccess) return err;
   return launch_pdl(paged_gqa_rows_kernel<kKv>, dim3(ctas), dim3(32 * RwCfg<kKv>::kWarpsAll), smem, stream, tk, tv, p);
 }
 

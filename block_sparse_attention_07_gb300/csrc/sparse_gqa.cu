@@ -2836,10 +2836,13 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
   memset(&tv, 0, sizeof(tv));
   const int64_t cache_rows = static_cast<int64_t>(a.P) * a.G * kBlock;
   cudaError_t err;
-  if (!a.nvfp4) {
-    if ((err = make_kv_map(&tk, a.k, cache_rows, a.fp8 != 0)) != cudaSuccess) return err;
-    if ((err = make_kv_map(&tv, a.v, cache_rows, a.fp8 != 0)) != cudaSuccess) return err;
-  }
+  // A kernel's shared-memory limit, then the maps: their encoder needs a context that is current in the calling thread,
+  // which the runtime's call makes where it is the thread's first.
+  auto prepare = [&](auto kernel, size_t bytes) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) e = make_kv_map(&tk, a.k, cache_rows, a.fp8 != 0);
+    return e != cudaSuccess ? e : make_kv_map(&tv, a.v, cache_rows, a.fp8 != 0);
+  };
   // Work split. bf16 and FP8 pages (64 / 32 KB per block) stream best when
   // every CTA owns whole rows: no split-K partials, no merge. NVFP4 pages (18 KB) are latency
   // bound per block, so their item ranges are balanced exactly over all SMs
@@ -2866,8 +2869,7 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
       const size_t tsm = tu_layout(nw).total + 1024;
       const int64_t ngroups = static_cast<int64_t>(a.B) * a.G;
       const int TC = static_cast<int>(ngroups < sms ? ngroups : sms);
-      err = cudaFuncSetAttribute(sparse_gqa_union_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(tsm));
+      err = prepare(sparse_gqa_union_tc_kernel, tsm);
       if (err != cudaSuccess) return err;
       err = launch_pdl(sparse_gqa_union_tc_kernel, dim3(TC), dim3(32 * kTuWarps), tsm, stream, tk, tv, p);
       rec->set("%ssparse_gqa bf16_tma_tcgen05 union_of_positions grid=%d block=%d smem=%zu stages=%d groups=%lld",
@@ -2878,8 +2880,7 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
     const size_t usmem = un_layout(nw).total + 1024;
     const int64_t groups = static_cast<int64_t>(a.B) * a.G;
     const int UC = static_cast<int>(groups < sms ? groups : sms);
-    err = cudaFuncSetAttribute(sparse_gqa_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(usmem));
+    err = prepare(sparse_gqa_union_kernel, usmem);
     if (err != cudaSuccess) return err;
     err = launch_pdl(sparse_gqa_union_kernel, dim3(UC), dim3(32 * (1 + kUnWarps)), usmem, stream, tk, tv, p);
     rec->set("%ssparse_gqa bf16_tma_mma union_of_positions grid=%d block=%d smem=%zu stages=%d groups=%lld",
@@ -2890,7 +2891,7 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
   if (!a.nvfp4 && !a.fp8 && bf16_tcgen05_selected()) {
     // bf16 K/V on the tcgen05 kernel, when selected (whole rows)
     const size_t tsmem = tc_layout().total + 1024;
-    err = cudaFuncSetAttribute(sparse_gqa_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tsmem));
+    err = prepare(sparse_gqa_tc_kernel, tsmem);
     if (err != cudaSuccess) return err;
     err = launch_pdl(sparse_gqa_tc_kernel, dim3(C), dim3(32 * kTcWarps), tsmem, stream, tk, tv, p);
     rec->set("%ssparse_gqa bf16_tma_tcgen05 persistent whole_rows grid=%d block=%d smem=%zu stages=%d items=%lld",
@@ -2923,7 +2924,7 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
     return err != cudaSuccess ? err : cudaGetLastError();
   }
   auto kern = a.fp8 ? sparse_gqa_kernel<kKvFp8> : sparse_gqa_kernel<kKvBf16>;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  err = prepare(kern, smem);
   if (err != cudaSuccess) return err;
   err = launch_pdl(kern, dim3(C), dim3(32 * (1 + kCWarps)), smem, stream, tk, tv, p);
   rec->set("%ssparse_gqa %s persistent %s grid=%d block=%d smem=%zu stages=%d items=%lld",

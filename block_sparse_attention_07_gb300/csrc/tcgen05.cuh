@@ -106,7 +106,9 @@ __device__ __forceinline__ bool group_any(int id, bool vote) {
 }
 
 // cuTensorMapEncodeTiled from the driver, looked up through the runtime (the
-// library does not link libcuda).
+// library does not link libcuda). It needs a context that is current in the calling
+// thread, which a thread's first call of the runtime makes: a launcher sets its
+// kernel's attributes before it encodes.
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
