@@ -34,6 +34,7 @@ constexpr int kIdxStages = 3;       // 66.5 KB pages (FP8 keys, 4 heads), one CT
 constexpr int kIdxStagesFp4 = 3;    // 36 KB pages (NVFP4 keys, 4 heads), two CTAs per SM
 constexpr int kFp4CtasPerSm = 2;    // two independent pipelines per SM hide more of the per-page latency
 constexpr int kMaxIdxHeads = 4;
+constexpr int kMaxBatch = 4096;                   // the entry points refuse larger ones
 constexpr int kWarpsPerHead = 2;    // consumer warps per index head (each takes a share of the page's tokens)
 constexpr int kTilesPerWarp = kBlock / 16 / kWarpsPerHead;
 constexpr int kIdxThreads = 32 * (1 + kWarpsPerHead * kMaxIdxHeads);
@@ -636,14 +637,18 @@ cudaError_t launch_index_score(const IndexArgs& a, const InsertArgs* ins, cudaSt
   cudaError_t err;
   if (a.fp8 || a.fp4) {
     const int stages = a.fp4 ? kIdxStagesFp4 : kIdxStages;
-    const size_t stage = a.fp4 ? static_cast<size_t>(a.I) * (key_bytes_per_head<true>() + scale_bytes_per_head<true>())
-                               : static_cast<size_t>(a.I) * (key_bytes_per_head<false>() + scale_bytes_per_head<false>());
-    const size_t smem = stages * stage + 2 * stages * 8 + stages * 4 +
-                        stages * kMaxIdxHeads * (kWarpsPerHead * 8 * 4 + 4) + stages * 4 + (a.B + 1) * 4;
+    const size_t head = a.fp4 ? key_bytes_per_head<true>() + scale_bytes_per_head<true>()
+                              : key_bytes_per_head<false>() + scale_bytes_per_head<false>();
+    auto bytes = [&](int heads, int batch) {
+      return stages * heads * head + 2 * stages * 8 + stages * 4 + stages * kMaxIdxHeads * (kWarpsPerHead * 8 * 4 + 4) +
+             stages * 4 + static_cast<size_t>(batch + 1) * 4;
+    };
+    const size_t smem = bytes(a.I, a.B);
     auto kern = !a.fp4 ? index_score_fp8_kernel<kIdxStages, false, false>
                 : a.Q == 1 ? index_score_fp8_kernel<kIdxStagesFp4, true, true>
                            : index_score_fp8_kernel<kIdxStagesFp4, true, false>;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The most that any call takes: the limit is the function's, and another thread's launch may come in between.
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(kMaxIdxHeads, kMaxBatch)));
     if (err != cudaSuccess) return err;
     const int grid = a.fp4 ? kFp4CtasPerSm * sms : sms;
     const int block = 32 * (1 + kWarpsPerHead * a.I);
@@ -653,9 +658,10 @@ cudaError_t launch_index_score(const IndexArgs& a, const InsertArgs* ins, cudaSt
              !a.fp4 ? "fp8_mma_f16" : a.Q == 1 ? "nvfp4_group_cols_mma_f16" : "nvfp4_mma_f16", grid, block, smem,
              stages, a.Q, a.I);
   } else {
-    const size_t smem = ((static_cast<size_t>(a.B) + 1) * 4 + 15) / 16 * 16 + 8 * kDim * 4 + 4 * 8 * 4;
+    auto bytes = [](int batch) { return ((static_cast<size_t>(batch) + 1) * 4 + 15) / 16 * 16 + 8 * kDim * 4 + 4 * 8 * 4; };
+    const size_t smem = bytes(a.B);
     err = cudaFuncSetAttribute(index_score_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
+                               static_cast<int>(bytes(kMaxBatch)));
     if (err != cudaSuccess) return err;
     const int grid = sms * 8;                   // grid-stride over (request, block, head) tasks
     err = launch_pdl(index_score_f32_kernel, dim3(grid), dim3(kBlock), smem, stream, p);

@@ -2869,7 +2869,8 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
       const size_t tsm = tu_layout(nw).total + 1024;
       const int64_t ngroups = static_cast<int64_t>(a.B) * a.G;
       const int TC = static_cast<int>(ngroups < sms ? ngroups : sms);
-      err = prepare(sparse_gqa_union_tc_kernel, tsm);
+      // (the most that any table's width takes: the limit is the function's, and another thread's launch may come between)
+      err = prepare(sparse_gqa_union_tc_kernel, tu_layout(kUnMaxNB / 32).total + 1024);
       if (err != cudaSuccess) return err;
       err = launch_pdl(sparse_gqa_union_tc_kernel, dim3(TC), dim3(32 * kTuWarps), tsm, stream, tk, tv, p);
       rec->set("%ssparse_gqa bf16_tma_tcgen05 union_of_positions grid=%d block=%d smem=%zu stages=%d groups=%lld",
@@ -2880,7 +2881,7 @@ cudaError_t launch_sparse_gqa(const GqaArgs& a, cudaStream_t stream, DispatchRec
     const size_t usmem = un_layout(nw).total + 1024;
     const int64_t groups = static_cast<int64_t>(a.B) * a.G;
     const int UC = static_cast<int>(groups < sms ? groups : sms);
-    err = prepare(sparse_gqa_union_kernel, usmem);
+    err = prepare(sparse_gqa_union_kernel, un_layout(kUnMaxNB / 32).total + 1024);
     if (err != cudaSuccess) return err;
     err = launch_pdl(sparse_gqa_union_kernel, dim3(UC), dim3(32 * (1 + kUnWarps)), usmem, stream, tk, tv, p);
     rec->set("%ssparse_gqa bf16_tma_mma union_of_positions grid=%d block=%d smem=%zu stages=%d groups=%lld",
