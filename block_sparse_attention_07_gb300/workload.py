@@ -366,8 +366,9 @@ class DeviceWorkload:
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         hidden = int(x.shape[1])
         if hidden not in self.__dict__.get("_layers", {}):
+            capturing = torch.cuda.is_current_stream_capturing()         # (where the state would be built, or the step's own)
             with torch.cuda.stream(torch.cuda.ExternalStream(s, self.device) if isinstance(s, int) else s):
-                if torch.cuda.is_current_stream_capturing():
+                if capturing or torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("hidden_step: prepare_hidden_step comes before a first step that is captured")
         st = self._layer_state(hidden)
         msa.add_norm_quant(x, st["norm"], residual=residual, residual_out=residual, codes=st["x8"][0], scales=st["x8"][1],

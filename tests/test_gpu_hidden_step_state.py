@@ -100,3 +100,18 @@ def test_outputs_in_fp32():
     dw.hidden_step(x, r, y)
     torch.cuda.synchronize()
     assert torch.equal(y.bfloat16(), want[1]) and not torch.equal(y, want[1].float())
+
+
+def test_first_call_by_the_default_streams_number():
+    """Stream 0 by its number, and a first call on another stream inside a capture of the current one: refused by name."""
+    want = eager("b32_32k", False, 1040, 5)
+    dw = build("b32_32k", False)
+    x, r, y = rows(dw, 1040, 5)
+    r0 = r.clone()
+    side = torch.cuda.Stream()
+    with pytest.raises(RuntimeError, match="prepare_hidden_step"):
+        dw.capture(lambda s: dw.hidden_step(x, r, y, side))
+    assert torch.equal(r, r0)
+    dw.hidden_step(x, r, y, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1]) and dw.check_flags() == 0
