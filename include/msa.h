@@ -49,6 +49,8 @@
  *     local block is p / BS.
  *   - The dispatch record (msa_get_last_dispatch) is thread-local and names
  *     the kernel variant and launch shape that actually ran.
+ *   - Host threads may call at one time, whatever sizes they pass. What calls
+ *     on several streams may not share is said at the call.
  */
 #ifndef MSA_H_
 #define MSA_H_
